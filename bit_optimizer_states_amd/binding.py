@@ -18,8 +18,10 @@ LIB_PATH = os.path.join(_HERE, "libqb.so")
 QB_OK, QB_EINVAL, QB_EALIGN, QB_EUNSUPPORTED, QB_EHIP, QB_EWORKSPACE, QB_EINIT = range(7)
 QB_F32, QB_F16, QB_BF16 = 0, 1, 2
 QB_DYN8, QB_NF4, QB_FP4, QB_UDYN8 = 0, 1, 2, 3
+QB_I32, QB_I64 = 0, 1
 QB_ADAMW, QB_ADAM, QB_LION, QB_SGD, QB_RMSPROP, QB_LAMB, QB_LARS = range(7)
 
+_INDEX = {torch.int32: QB_I32, torch.int64: QB_I64}
 _DTYPE = {torch.float32: QB_F32, torch.float16: QB_F16, torch.bfloat16: QB_BF16}
 
 
@@ -127,6 +129,23 @@ def lib():
         L.qb_multi_tensor_quantize.argtypes = [ctypes.POINTER(qb_quant_tensor), i32, i32, i32, i32, i32, vp, sz, vp]
         L.qb_multi_tensor_quantize_workspace_bytes.argtypes = [ctypes.POINTER(qb_quant_tensor), i32, i32]
         L.qb_multi_tensor_quantize_workspace_bytes.restype = sz
+        f64 = ctypes.c_double
+        L.qb_embedding.argtypes = [vp, i32, i64, i64, vp, i32, i64, f64, vp, i32, vp]
+        L.qb_dequant_embedding.argtypes = [vp, vp, ctypes.POINTER(qb_dq), i32, i32, i64, i64, vp, i32, i64, f64, vp,
+                                           i32, vp]
+        L.qb_embedding_backward.argtypes = [vp, i32, vp, i32, i64, i64, i64, f64, i64, i32, vp, i32, vp, sz, vp]
+        L.qb_layer_norm.argtypes = [vp, i32, i64, i64, vp, vp, i32, f64, vp, vp, vp, vp]
+        L.qb_layer_norm_backward.argtypes = [vp, vp, i32, i64, i64, vp, i32, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+        L.qb_stable_embedding.argtypes = [vp, i32, i64, i64, vp, i32, i64, f64, vp, vp, i32, f64, vp, i32, vp]
+        L.qb_stable_embedding_backward.argtypes = [vp, i32, vp, i32, i64, i64, vp, i32, i64, f64, vp, i32, f64, i64,
+                                                   i32, vp, i32, vp, vp, vp, sz, vp]
+        for f in (L.qb_embedding, L.qb_dequant_embedding, L.qb_embedding_backward, L.qb_layer_norm,
+                  L.qb_layer_norm_backward, L.qb_stable_embedding, L.qb_stable_embedding_backward):
+            f.restype = ctypes.c_int
+        for f, args in ((L.qb_embedding_workspace_bytes, [i64, i64, i64]), (L.qb_layer_norm_workspace_bytes, [i64, i64]),
+                        (L.qb_stable_embedding_workspace_bytes, [i64, i64, i64])):
+            f.argtypes = args
+            f.restype = sz
         for f in (L.qb_quantize, L.qb_dequantize, L.qb_adamw8bit_step, L.qb_multi_tensor_step,
                   L.qb_multi_tensor_step_noalloc,
                   L.qb_multi_tensor_dequantize, L.qb_multi_tensor_quantize, L.qb_optimizer8bit_step,
@@ -364,6 +383,164 @@ def qb_multi_tensor_dequantize(table, count, code, blocksize, blocksize2, ydt, w
     _check(lib().qb_multi_tensor_dequantize(table, int(count), int(code), int(blocksize), int(blocksize2), int(ydt),
                                             _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
            "qb_multi_tensor_dequantize")
+
+
+# ---------------------------------------------------------------------------
+# Row-wise layers.  These take the sizes from the tensors, so the shapes are
+# checked here; ids (int32 or int64) and the leading dimensions of the token
+# arrays may have any shape, as long as the token counts agree.
+# ---------------------------------------------------------------------------
+
+def _index(ids):
+    try:
+        return _INDEX[ids.dtype]
+    except KeyError:
+        raise TypeError(f"ids must be int32 or int64, not {ids.dtype}") from None
+
+
+def _matrix(t, name):
+    if t.dim() < 1 or t.shape[-1] == 0:
+        raise ValueError(f"{name}: rows of at least one element expected")
+    return t.numel() // t.shape[-1], t.shape[-1]
+
+
+def _expect(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _row_stream(stream, t):
+    """The stream argument, or torch's current stream of the tensor's device."""
+    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else _stream(stream)
+
+
+def _row_call(name, t, *args):
+    """Calls an entry point with the tensor's device current (kernels start on the current device)."""
+    f = getattr(lib(), name)
+    if t.device.index == torch.cuda.current_device():
+        status = f(*args)
+    else:
+        with torch.cuda.device(t.device):
+            status = f(*args)
+    _check(status, name)
+
+
+def _norm_weights(dim, wdt_default, *weights):
+    """The dtype shared by the norm's weights (and their gradients)."""
+    wdt = None
+    for w in weights:
+        if w is not None:
+            _expect(w.numel() == dim, f"norm weights of {dim} elements expected")
+            _expect(wdt is None or w.dtype == wdt, "the norm's weights and their gradients must share a dtype")
+            wdt = w.dtype
+    return wdt_default if wdt is None else _DTYPE.get(wdt, -1)
+
+
+def qb_embedding(table, ids, y, scale=1.0, stream=None):
+    """y[t] = scale * table[ids[t]]; zero rows for ids outside the table."""
+    rows, dim = _matrix(table, "table")
+    n, ydim = _matrix(y, "y")
+    _expect(ydim == dim and n == ids.numel(), f"y of [{ids.numel()}, {dim}] expected")
+    _same_device(y, table, ids)
+    _row_call("qb_embedding", y, _ptr(table), _dtype(table), rows, dim, _ptr(ids), _index(ids), n, float(scale),
+              _ptr(y), _dtype(y), _row_stream(stream, y))
+
+
+def qb_dequant_embedding(codes, absmax, dq, code, blocksize, rows, ids, y, scale=1.0, stream=None):
+    """qb_embedding from a quantized table of `rows` rows of y.shape[-1]
+    elements (codes and absmax or dq as for qb_dequantize)."""
+    n, dim = _matrix(y, "y")
+    _expect(n == ids.numel(), f"y of [{ids.numel()}, dim] expected")
+    total, nb = int(rows) * dim, -(-int(rows) * dim // max(int(blocksize), 1))
+    _expect(codes.numel() >= (total if code == QB_DYN8 else (total + 1) // 2), "codes of the whole table expected")
+    _expect(absmax is None or absmax.numel() >= nb, f"absmax of {nb} blocks expected")
+    _same_device(y, codes, absmax, ids)
+    _row_call("qb_dequant_embedding", y, _ptr(codes), _ptr(absmax), ctypes.byref(dq) if dq is not None else None,
+              int(code), int(blocksize), int(rows), dim, _ptr(ids), _index(ids), n, float(scale), _ptr(y), _dtype(y),
+              _row_stream(stream, y))
+
+
+def qb_embedding_workspace_bytes(n, rows, dim):
+    return lib().qb_embedding_workspace_bytes(int(n), int(rows), int(dim))
+
+
+def qb_embedding_backward(dy, ids, dtable, ws, scale=1.0, padding_id=-1, accumulate=False, stream=None):
+    """dtable[v] = scale * the sum of dy[t] over the tokens with ids[t] = v."""
+    rows, dim = _matrix(dtable, "dtable")
+    n, gdim = _matrix(dy, "dy")
+    _expect(gdim == dim and n == ids.numel(), f"dy of [{ids.numel()}, {dim}] expected")
+    _same_device(dtable, dy, ids, ws)
+    _row_call("qb_embedding_backward", dtable, _ptr(dy), _dtype(dy), _ptr(ids), _index(ids), n, rows, dim,
+              float(scale), int(padding_id), int(accumulate), _ptr(dtable), _dtype(dtable), _ptr(ws),
+              ws.numel() * ws.element_size(), _row_stream(stream, dtable))
+
+
+def qb_layer_norm(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
+    """Layer norm of the last dimension of x (gamma, beta: [dim] or None; mean,
+    rstd: fp32 outputs or None)."""
+    n, dim = _matrix(x, "x")
+    _expect(y.shape == x.shape and y.dtype == x.dtype, "y like x expected")
+    for t in (mean, rstd):
+        _expect(t is None or (t.numel() == n and t.dtype == torch.float32), f"{n} fp32 statistics expected")
+    wdt = _norm_weights(dim, _dtype(x), gamma, beta)
+    _same_device(x, gamma, beta, y, mean, rstd)
+    _row_call("qb_layer_norm", x, _ptr(x), _dtype(x), n, dim, _ptr(gamma), _ptr(beta), wdt, float(eps), _ptr(y),
+              _ptr(mean), _ptr(rstd), _row_stream(stream, x))
+
+
+def qb_layer_norm_workspace_bytes(n, dim):
+    return lib().qb_layer_norm_workspace_bytes(int(n), int(dim))
+
+
+def qb_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws=None, accumulate=False, stream=None):
+    """dx, dgamma, dbeta (each may be None) from the forward call's x, mean and
+    rstd; ws is needed for dgamma or dbeta."""
+    n, dim = _matrix(x, "x")
+    _expect(dy.shape == x.shape and dy.dtype == x.dtype, "dy like x expected")
+    _expect(dx is None or (dx.shape == x.shape and dx.dtype == x.dtype), "dx like x expected")
+    for t in (mean, rstd):
+        _expect(t.numel() == n and t.dtype == torch.float32, f"{n} fp32 statistics expected")
+    wdt = _norm_weights(dim, _dtype(x), gamma, dgamma, dbeta)
+    _same_device(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, ws)
+    _row_call("qb_layer_norm_backward", x, _ptr(dy), _ptr(x), _dtype(x), n, dim, _ptr(gamma), wdt, _ptr(mean),
+              _ptr(rstd), _ptr(dx), _ptr(dgamma), _ptr(dbeta), int(accumulate), _ptr(ws),
+              0 if ws is None else ws.numel() * ws.element_size(), _row_stream(stream, x))
+
+
+def qb_stable_embedding(table, ids, gamma, beta, eps, y, scale=1.0, stream=None):
+    """y[t] = layer norm of scale * table[ids[t]]; zero rows for ids outside the table."""
+    rows, dim = _matrix(table, "table")
+    n, ydim = _matrix(y, "y")
+    _expect(ydim == dim and n == ids.numel(), f"y of [{ids.numel()}, {dim}] expected")
+    wdt = _norm_weights(dim, _dtype(table), gamma, beta)
+    _same_device(y, table, ids, gamma, beta)
+    _row_call("qb_stable_embedding", y, _ptr(table), _dtype(table), rows, dim, _ptr(ids), _index(ids), n,
+              float(scale), _ptr(gamma), _ptr(beta), wdt, float(eps), _ptr(y), _dtype(y), _row_stream(stream, y))
+
+
+def qb_stable_embedding_workspace_bytes(n, rows, dim):
+    return lib().qb_stable_embedding_workspace_bytes(int(n), int(rows), int(dim))
+
+
+def qb_stable_embedding_backward(dy, table, ids, gamma, eps, dtable, dgamma, dbeta, ws, scale=1.0, padding_id=-1,
+                                 accumulate=False, stream=None):
+    """dtable, dgamma and dbeta (the latter two may be None) of qb_stable_embedding."""
+    rows, dim = _matrix(table, "table")
+    n, gdim = _matrix(dy, "dy")
+    _expect(gdim == dim and n == ids.numel(), f"dy of [{ids.numel()}, {dim}] expected")
+    _expect(dtable.shape == table.shape, "dtable like table expected")
+    wdt = _norm_weights(dim, _dtype(table), gamma, dgamma, dbeta)
+    _same_device(dtable, dy, table, ids, gamma, dgamma, dbeta, ws)
+    _row_call("qb_stable_embedding_backward", dtable, _ptr(dy), _dtype(dy), _ptr(table), _dtype(table), rows, dim,
+              _ptr(ids), _index(ids), n, float(scale), _ptr(gamma), wdt, float(eps), int(padding_id),
+              int(accumulate), _ptr(dtable), _dtype(dtable), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
+              ws.numel() * ws.element_size(), _row_stream(stream, dtable))
 
 
 def qb_code_table_bytes():

@@ -1,0 +1,434 @@
+// qb_embedding.hip -- embedding lookup from dense and from quantized tables, and
+// the gradient of the table by sorted tokens.
+//
+// Lookup: y_t = scale * W[id_t], one binary32 multiply and one rounding.  Bound
+// by HBM: the rows that are used are read, y is written.
+//
+// Gradient: dW[v] = scale * (sum of dy_t over the tokens t with id_t = v).  The
+// tokens are first ordered by id (k_order), so that every sum is taken by one
+// wave in ascending order of the tokens: no atomics on floating-point values,
+// the same bits on every run.  An id with more tokens than a chunk holds is summed
+// chunk by chunk by many waves (k_chunk_sums) and joined in chunk order.  The
+// last kernel writes every row of the table once, zeros included.
+#include "qb_token_sums.h"
+
+namespace qb {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// lookup
+// ---------------------------------------------------------------------------
+
+// `lanes` (a power of two) threads share a token, 256 / lanes tokens a workgroup.
+template <int TDT, int YDT, bool TAIL>
+__global__ __launch_bounds__(256) void k_embedding(IdArgs a, const void* __restrict__ table, float scale,
+                                                   void* __restrict__ y, int log2lanes)
+{
+    const int lane = threadIdx.x & ((1 << log2lanes) - 1);
+    const int64_t t = ((int64_t)blockIdx.x << (8 - log2lanes)) + (threadIdx.x >> log2lanes);
+    if (t >= a.n) return;
+    const int dim = a.dim, units = (dim + 7) >> 3;
+    const int64_t id = load_id(a.ids, a.id64, t);
+    const bool found = (uint64_t)id < (uint64_t)a.rows;
+    const char* const row = static_cast<const char*>(table) + (found ? id : 0) * dim * elem_bytes(TDT);
+    char* const yrow = static_cast<char*>(y) + t * dim * elem_bytes(YDT);
+    for (int unit = lane; unit < units; unit += 1 << log2lanes) {
+        float o[8];
+        if (found) {
+            const Unit<TDT> u = load_row_unit<TDT, TAIL, false>(row, unit, units, dim);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = unit_at<TDT>(u, j) * scale;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+        }
+        store_row_unit<YDT, TAIL, true>(yrow, unit, units, dim, o);
+    }
+}
+
+// Threads that share a token: enough for one unit each, at most a workgroup.
+int lanes_log2(int units)
+{
+    int k = 3;
+    while (k < 8 && (1 << k) < units) ++k;
+    return k;
+}
+
+template <int TDT, int YDT>
+hipError_t embedding_as(const IdArgs& a, const void* table, float scale, void* y, hipStream_t s)
+{
+    const int k = lanes_log2((a.dim + 7) / 8);
+    return launch_rows(a.n, 256 >> k, [&](int64_t t0, int64_t m, int grid) {
+        const IdArgs b = ids_from(a, t0, m);
+        void* const out = static_cast<char*>(y) + t0 * a.dim * elem_bytes(YDT);
+        return a.dim % 8 ? launch_kernel(k_embedding<TDT, YDT, true>, grid, s, b, table, scale, out, k)
+                         : launch_kernel(k_embedding<TDT, YDT, false>, grid, s, b, table, scale, out, k);
+    });
+}
+
+template <int TDT>
+hipError_t embedding_y(const IdArgs& a, const void* table, float scale, void* y, int ydt, hipStream_t s)
+{
+    if (ydt == DT_F32) return embedding_as<TDT, DT_F32>(a, table, scale, y, s);
+    if (ydt == DT_F16) return embedding_as<TDT, DT_F16>(a, table, scale, y, s);
+    return embedding_as<TDT, DT_BF16>(a, table, scale, y, s);
+}
+
+// ---------------------------------------------------------------------------
+// lookup in a quantized table
+// ---------------------------------------------------------------------------
+
+// The table [rows, dim] is quantized as one flat tensor, so a block may span
+// rows.  TAIL: dim is no multiple of 8, rows may begin inside a byte or a
+// block, and every element finds its own code and block; otherwise a unit of 8
+// elements is 4 or 8 aligned bytes of codes with one scale (blocks hold 64
+// elements or more).
+template <int BITS, int YDT, bool DQ, bool TAIL>
+__global__ __launch_bounds__(256) void k_dequant_embedding(IdArgs a, DequantDesc d, int log2B, int log2B2, int code4,
+                                                           const QbTables* __restrict__ tab, float scale,
+                                                           void* __restrict__ y, int log2lanes)
+{
+    __shared__ float s_val[BITS == 8 ? 256 : 16];
+    __shared__ float s_dyn[DQ && BITS == 4 ? 256 : 1];
+    if constexpr (BITS == 8) s_val[threadIdx.x] = tab->dyn8[threadIdx.x];
+    else if (threadIdx.x < 16) s_val[threadIdx.x] = (code4 == 0 ? tab->nf4 : tab->fp4)[threadIdx.x];
+    if constexpr (DQ && BITS == 4) s_dyn[threadIdx.x] = tab->dyn8[threadIdx.x];
+    const float mu = DQ ? gld<float>(d.offset) : 0.0f;
+    __syncthreads();
+
+    const int lane = threadIdx.x & ((1 << log2lanes) - 1);
+    const int64_t t = ((int64_t)blockIdx.x << (8 - log2lanes)) + (threadIdx.x >> log2lanes);
+    if (t >= a.n) return;
+    const int dim = a.dim, units = (dim + 7) >> 3;
+    const int64_t id = load_id(a.ids, a.id64, t);
+    const bool found = (uint64_t)id < (uint64_t)a.rows;
+    const int64_t first = (found ? id : 0) * dim;
+    char* const yrow = static_cast<char*>(y) + t * dim * elem_bytes(YDT);
+    auto block_scale = [&](int64_t b) -> float {
+        if constexpr (DQ) {
+            const float c = (BITS == 8 ? s_val : s_dyn)[gld<uint8_t>(d.c2 + b)];
+            return c * gld<float>(d.absmax2 + (b >> log2B2)) + mu;
+        } else {
+            return gld<float>(d.absmax + b);
+        }
+    };
+    for (int unit = lane; unit < units; unit += 1 << log2lanes) {
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+        const int64_t e = first + (int64_t)unit * 8;
+        if (found) {
+            if constexpr (!TAIL) {
+                const float sc = block_scale(e >> log2B);
+                uint32_t w0, w1 = 0;
+                if constexpr (BITS == 8) {
+                    const u32x2 w = gld<u32x2>(d.codes + e);
+                    w0 = w.x;
+                    w1 = w.y;
+                } else {
+                    w0 = gld<uint32_t>(d.codes + (e >> 1));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint32_t c;
+                    if constexpr (BITS == 8) c = ((j < 4 ? w0 : w1) >> (8 * (j & 3))) & 0xFFu;
+                    else c = (w0 >> (8 * (j >> 1) + ((j & 1) ? 0 : 4))) & 15u;      // element 2k in the high nibble
+                    o[j] = s_val[c] * sc * scale;
+                }
+            } else {
+                const int left = dim - unit * 8;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (j < left) {
+                        const int64_t i = e + j;
+                        uint32_t c;
+                        if constexpr (BITS == 8) c = gld<uint8_t>(d.codes + i);
+                        else c = (gld<uint8_t>(d.codes + (i >> 1)) >> ((i & 1) ? 0 : 4)) & 15u;
+                        o[j] = s_val[c] * block_scale(i >> log2B) * scale;
+                    }
+                }
+            }
+        }
+        store_row_unit<YDT, TAIL, true>(yrow, unit, units, dim, o);
+    }
+}
+
+int log2_of(int v)
+{
+    int k = 0;
+    while ((1 << k) < v) ++k;
+    return k;
+}
+
+template <int BITS, int YDT, bool DQ>
+hipError_t dequant_embedding_as(const IdArgs& a, const DequantDesc& d, int code4, int B, int B2, const QbTables* tab,
+                                float scale, void* y, hipStream_t s)
+{
+    const int k = lanes_log2((a.dim + 7) / 8);
+    return launch_rows(a.n, 256 >> k, [&](int64_t t0, int64_t m, int grid) {
+        const IdArgs b = ids_from(a, t0, m);
+        void* const out = static_cast<char*>(y) + t0 * a.dim * elem_bytes(YDT);
+        return a.dim % 8 ? launch_kernel(k_dequant_embedding<BITS, YDT, DQ, true>, grid, s, b, d, log2_of(B),
+                                         log2_of(B2), code4, tab, scale, out, k)
+                         : launch_kernel(k_dequant_embedding<BITS, YDT, DQ, false>, grid, s, b, d, log2_of(B),
+                                         log2_of(B2), code4, tab, scale, out, k);
+    });
+}
+
+template <int BITS, bool DQ>
+hipError_t dequant_embedding_y(const IdArgs& a, const DequantDesc& d, int code4, int B, int B2, const QbTables* tab,
+                               float scale, void* y, int ydt, hipStream_t s)
+{
+    if (ydt == DT_F32) return dequant_embedding_as<BITS, DT_F32, DQ>(a, d, code4, B, B2, tab, scale, y, s);
+    if (ydt == DT_F16) return dequant_embedding_as<BITS, DT_F16, DQ>(a, d, code4, B, B2, tab, scale, y, s);
+    return dequant_embedding_as<BITS, DT_BF16, DQ>(a, d, code4, B, B2, tab, scale, y, s);
+}
+
+// ---------------------------------------------------------------------------
+// order of the tokens by id
+// ---------------------------------------------------------------------------
+
+// One workgroup per class of ids (OrderArgs).  It walks all n ids twice: the
+// first time it counts its own entries, per wave (each wave owns one contiguous
+// stretch of the tokens), and the tokens of lower classes, whose number is where
+// its part of the list begins; the second time it places its tokens.  A wave
+// takes the tokens of its stretch in order and gives equal ids of one step
+// consecutive places by their lane, so the order is stable and no workgroup waits
+// for another.  The ids are read from L2 by every workgroup: n * classes reads,
+// 5 us at 16k tokens, in exchange for one launch and no atomics in memory.
+template <bool ID64>
+__global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs o)
+{
+    extern __shared__ int32_t s_cnt[];                 // [kOrderWaves][per]
+    __shared__ int32_t s_below[kOrderWaves], s_wave[kOrderWaves];
+    constexpr int UN = 8;                              // loads in flight per lane
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int32_t cls = (int32_t)blockIdx.x, mask = (1 << o.log2g) - 1, per = o.per;
+    for (int i = threadIdx.x; i < kOrderWaves * per; i += kOrderWaves * 64) s_cnt[i] = 0;
+    __syncthreads();
+
+    const int64_t stretch = ((a.n + kOrderWaves - 1) / kOrderWaves + 63) / 64 * 64;
+    const int64_t first = wave * stretch;
+    const int64_t last = first + stretch < a.n ? first + stretch : a.n;
+    int32_t* const cnt = s_cnt + wave * per;
+    // id of token t, or -1 beyond the stretch or outside the table
+    auto id_at = [&](int64_t t) -> int32_t {
+        if (t >= last) return -1;
+        if constexpr (ID64) {
+            const int64_t id = gld<int64_t>(static_cast<const int64_t*>(a.ids) + t);
+            return (uint64_t)id < (uint64_t)a.rows ? (int32_t)id : -1;
+        } else {
+            const int32_t id = gld<int32_t>(static_cast<const int32_t*>(a.ids) + t);
+            return (uint64_t)(int64_t)id < (uint64_t)a.rows ? id : -1;
+        }
+    };
+
+    int32_t below = 0;
+    for (int64_t t0 = first; t0 < last; t0 += 64 * UN) {
+        int32_t id[UN];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) id[k] = id_at(t0 + k * 64 + lane);
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            if (id[k] >= 0) {
+                const int32_t c = id[k] & mask;
+                below += c < cls ? 1 : 0;
+                if (c == cls) atomicAdd(&cnt[id[k] >> o.log2g], 1);
+            }
+        }
+    }
+    for (int step = 1; step < 64; step *= 2) below += __shfl_xor(below, step);
+    if (lane == 0) s_below[wave] = below;
+    __syncthreads();
+
+    // exclusive scan over the entries: thread j owns entry j (per <= kOrderPerMax)
+    int32_t base = 0;
+#pragma unroll
+    for (int w = 0; w < kOrderWaves; ++w) base += s_below[w];
+    const int j = threadIdx.x;
+    int32_t total = 0;
+    if (j < per)
+        for (int w = 0; w < kOrderWaves; ++w) total += s_cnt[w * per + j];
+    int32_t incl = total;
+    for (int step = 1; step < 64; step *= 2) {
+        const int32_t up = __shfl_up(incl, step);
+        if (lane >= step) incl += up;
+    }
+    if (lane == 63) s_wave[wave] = incl;
+    __syncthreads();
+    int32_t before = 0;
+    for (int w = 0; w < wave; ++w) before += s_wave[w];
+    if (j < per) {
+        int32_t run = base + before + incl - total;
+        o.start[(int64_t)cls * per + j] = run;
+        for (int w = 0; w < kOrderWaves; ++w) {
+            const int32_t c = s_cnt[w * per + j];
+            s_cnt[w * per + j] = run;
+            run += c;
+        }
+        if (cls == mask && j == per - 1) o.start[((int64_t)cls + 1) * per] = run;
+    }
+    __syncthreads();
+
+    for (int64_t t0 = first; t0 < last; t0 += 64 * UN) {
+        int32_t id[UN];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) id[k] = id_at(t0 + k * 64 + lane);
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            const bool mine = id[k] >= 0 && (id[k] & mask) == cls;
+            unsigned long long todo = __ballot(mine);
+            while (todo) {
+                const int lead = __builtin_ctzll(todo);
+                const int32_t e = __builtin_amdgcn_readlane(id[k], lead);
+                const unsigned long long same = __ballot(mine && id[k] == e);
+                int32_t at = 0;
+                if (lane == lead) at = atomicAdd(&cnt[e >> o.log2g], (int32_t)__popcll(same));
+                at = __builtin_amdgcn_readlane(at, lead);
+                if (mine && id[k] == e)
+                    o.order[at + __popcll(same & ((1ull << lane) - 1))] = (int32_t)(t0 + k * 64 + lane);
+                todo &= ~same;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gradient of the table
+// ---------------------------------------------------------------------------
+
+// One wave per chunk and 64 units.  Of a chunk's tokens only the first and the
+// last id can have more tokens than a chunk.
+template <int GDT, bool TAIL>
+__global__ __launch_bounds__(256) void k_chunk_sums(IdArgs a, OrderArgs o, const void* __restrict__ dy,
+                                                    float* __restrict__ part, int32_t chunk, int32_t slices)
+{
+    const int lane = threadIdx.x % 64;
+    const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int32_t c = (int32_t)(w / slices), unit = (int32_t)(w % slices) * 64 + lane;
+    const int32_t found = o.start[(int64_t(1) << o.log2g) * o.per];        // tokens inside the table
+    const int64_t begin = (int64_t)c * chunk;
+    if (begin >= found) return;
+    const int32_t b = (int32_t)begin, e = found - b < chunk ? found : b + chunk;
+    const int dim = a.dim, units = (dim + 7) >> 3;
+    const int64_t padded = (int64_t)units * 8;
+    int64_t before = -1;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const int64_t v = load_id(a.ids, a.id64, o.order[side == 0 ? b : e - 1]);
+        if (v == before) break;
+        before = v;
+        const int64_t s = slot_of(v, o);
+        const int32_t v0 = o.start[s], v1 = o.start[s + 1];
+        if (v1 - v0 <= chunk) continue;
+        float sum[8] = {};
+        sum_tokens<GDT, TAIL, 8>(o.order, v0 > b ? v0 : b, v1 < e ? v1 : e, dy, unit, units, dim, sum);
+        if (unit < units) {
+            float* const p = part + (2 * (int64_t)c + (v0 > b ? 1 : 0)) * padded + (int64_t)unit * 8;
+            gst<f32x4>(p, f32x4{sum[0], sum[1], sum[2], sum[3]});
+            gst<f32x4>(p + 4, f32x4{sum[4], sum[5], sum[6], sum[7]});
+        }
+    }
+}
+
+// One wave per table row and 64 units (walking the table where a launch cannot hold as many).
+template <int GDT, bool TAIL>
+__global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, const void* __restrict__ dy,
+                                                    const float* __restrict__ part, int32_t chunk, int32_t slices,
+                                                    float scale, int64_t pad, int accumulate, void* __restrict__ dtable,
+                                                    int ddt)
+{
+    const int lane = threadIdx.x % 64;
+    const int dim = a.dim, units = (dim + 7) >> 3;
+    for (int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64); w < a.rows * slices;
+         w += (int64_t)gridDim.x * 4) {
+        const int64_t v = w / slices;
+        const int unit = (int)(w % slices) * 64 + lane;
+        const int64_t s = slot_of(v, o);
+        const int32_t v0 = o.start[s], v1 = v == pad ? v0 : o.start[s + 1];
+        if (accumulate && v0 == v1) continue;
+        float sum[8] = {};
+        if (v1 - v0 > chunk) sum_chunks<8>(part, chunk, v0, v1, unit, units, (int64_t)units * 8, sum);
+        else sum_tokens<GDT, TAIL, 4>(o.order, v0, v1, dy, unit, units, dim, sum);
+        char* const row = static_cast<char*>(dtable) + v * dim * (ddt == DT_F32 ? 4 : 2);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] *= scale;
+        if (accumulate) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < unit_count(unit, dim)) sum[j] += load1_rt(ddt, row, (int64_t)unit * 8 + j);
+        }
+        store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, sum);
+    }
+}
+
+template <int GDT>
+hipError_t chunk_sums_as(const IdArgs& a, const OrderArgs& o, const void* dy, float* part, hipStream_t s)
+{
+    const int32_t slices = (a.dim + 511) / 512;
+    const int64_t grid = (chunk_count(a.n) * slices + 3) / 4;
+    if (grid >= (int64_t(1) << 24)) return hipErrorInvalidValue;
+    return a.dim % 8 ? launch_kernel(k_chunk_sums<GDT, true>, (int)grid, s, a, o, dy, part, chunk_tokens(a.n), slices)
+                     : launch_kernel(k_chunk_sums<GDT, false>, (int)grid, s, a, o, dy, part, chunk_tokens(a.n), slices);
+}
+
+template <int GDT>
+hipError_t table_grad_as(const IdArgs& a, const OrderArgs& o, const void* dy, const float* part, float scale,
+                         int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s)
+{
+    const int32_t slices = (a.dim + 511) / 512;
+    const int64_t waves = (a.rows * slices + 3) / 4, most = int64_t(1) << 22;
+    auto go = [&](auto kernel) {
+        return launch_kernel(kernel, (int)(waves < most ? waves : most), s, a, o, dy, part, chunk_tokens(a.n), slices, scale, pad,
+                             accumulate ? 1 : 0, dtable, ddt);
+    };
+    return a.dim % 8 ? go(k_table_grad<GDT, true>) : go(k_table_grad<GDT, false>);
+}
+
+}  // namespace
+
+hipError_t launch_embedding(const IdArgs& a, const void* table, int tdt, float scale, void* y, int ydt, hipStream_t s)
+{
+    if (tdt == DT_F32) return embedding_y<DT_F32>(a, table, scale, y, ydt, s);
+    if (tdt == DT_F16) return embedding_y<DT_F16>(a, table, scale, y, ydt, s);
+    return embedding_y<DT_BF16>(a, table, scale, y, ydt, s);
+}
+
+hipError_t launch_dequant_embedding(const IdArgs& a, const DequantDesc& t, int bits, int code4, int B, int B2,
+                                    float scale, void* y, int ydt, hipStream_t s)
+{
+    const QbTables* tab = device_tables();
+    if (!tab) return hipErrorNotInitialized;
+    const bool dq = t.c2 != nullptr;
+    if (bits == 8)
+        return dq ? dequant_embedding_y<8, true>(a, t, code4, B, B2, tab, scale, y, ydt, s)
+                  : dequant_embedding_y<8, false>(a, t, code4, B, B2, tab, scale, y, ydt, s);
+    return dq ? dequant_embedding_y<4, true>(a, t, code4, B, B2, tab, scale, y, ydt, s)
+              : dequant_embedding_y<4, false>(a, t, code4, B, B2, tab, scale, y, ydt, s);
+}
+
+hipError_t launch_order(const IdArgs& a, const OrderArgs& o, hipStream_t s)
+{
+    const size_t lds = (size_t)kOrderWaves * o.per * sizeof(int32_t);
+    return a.id64 ? launch_kernel_lds(k_order<true>, 1 << o.log2g, kOrderWaves * 64, lds, s, a, o)
+                  : launch_kernel_lds(k_order<false>, 1 << o.log2g, kOrderWaves * 64, lds, s, a, o);
+}
+
+hipError_t launch_chunk_sums(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part, hipStream_t s)
+{
+    if (a.n == 0) return hipSuccess;
+    if (gdt == DT_F32) return chunk_sums_as<DT_F32>(a, o, dy, part, s);
+    if (gdt == DT_F16) return chunk_sums_as<DT_F16>(a, o, dy, part, s);
+    return chunk_sums_as<DT_BF16>(a, o, dy, part, s);
+}
+
+hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, const float* part,
+                             float scale, int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s)
+{
+    if (gdt == DT_F32) return table_grad_as<DT_F32>(a, o, dy, part, scale, pad, accumulate, dtable, ddt, s);
+    if (gdt == DT_F16) return table_grad_as<DT_F16>(a, o, dy, part, scale, pad, accumulate, dtable, ddt, s);
+    return table_grad_as<DT_BF16>(a, o, dy, part, scale, pad, accumulate, dtable, ddt, s);
+}
+
+}  // namespace qb

@@ -1,0 +1,143 @@
+// qb_layers.h -- internal launchers of the row-wise layers: embedding lookup
+// (dense and quantized tables) and its gradient, layer norm, and the stable
+// embedding that joins them.  Argument checks are done by the callers in
+// qb_layers_api.cpp.
+#pragma once
+#include "qb_launch.h"
+
+namespace qb {
+
+// Longest row of the kernels that hold a row in registers (256 threads x 8
+// units x 8 elements).
+constexpr int64_t kRowRegMax = 16384;
+
+// Token ids of a lookup: n ids of 32 or 64 bits into a table of `rows` rows of
+// `dim` elements.
+struct IdArgs {
+    const void* ids;
+    int64_t n;
+    int64_t rows;
+    int32_t id64;
+    int32_t dim;
+};
+
+// Order of the tokens of a gradient.  Ids are dealt into 2^log2g classes, class
+// = id mod 2^log2g, entry = id >> log2g (`per` entries a class): frequent
+// tokens have small ids in common vocabularies, and neighbouring ids land in
+// different classes.  start[class * per + entry] .. start[... + 1] is the range of
+// the id's tokens in `order`, which lists their positions in ascending order.
+struct OrderArgs {
+    int32_t* start;      // [classes * per + 1]
+    int32_t* order;      // [n]
+    int32_t log2g;
+    int32_t per;
+};
+
+constexpr int kOrderWaves = 16;            // waves of the ordering kernel
+constexpr int kOrderPerMax = 1000;         // entries of a class: one per thread, 16 x 1000 counters in 64 KB of LDS
+
+// Classes for a table of `rows` rows: 256 (one workgroup per CU), more where a
+// class would hold over kOrderPerMax entries, fewer for tiny tables.
+constexpr int32_t order_log2g(int64_t rows)
+{
+    int32_t g = 0;
+    while (g < 8 && (int64_t(1) << g) < rows) ++g;
+    while (((rows + (int64_t(1) << g) - 1) >> g) > kOrderPerMax) ++g;
+    return g;
+}
+constexpr int64_t order_per(int64_t rows) { return (rows + (int64_t(1) << order_log2g(rows)) - 1) >> order_log2g(rows); }
+
+// Tokens per chunk of the ordered list: an id with more tokens than this is
+// summed chunk by chunk, then joined.  About half the square root of n, so that
+// an id that holds every token takes as many steps within a chunk as in the
+// join.
+constexpr int32_t chunk_tokens(int64_t n)
+{
+    int32_t c = 32;
+    while (c < 512 && (int64_t)c * c * 4 < n) c *= 2;
+    return c;
+}
+constexpr int64_t chunk_count(int64_t n) { return (n + chunk_tokens(n) - 1) / chunk_tokens(n); }
+constexpr int64_t padded_dim(int64_t dim) { return (dim + 7) / 8 * 8; }
+
+// Workgroups whose partial sums of the norm's weight gradients are joined.
+constexpr int kNormPartsMax = 512;
+
+// Rows [t0, t0 + m) of n in one launch each: a launch holds at most 2^21
+// workgroups (workgroups times threads stay below 2^32), `per_wg` rows apiece.
+template <class Launch>
+hipError_t launch_rows(int64_t n, int64_t per_wg, Launch launch)
+{
+    const int64_t most = per_wg << 21;
+    for (int64_t t0 = 0; t0 < n; t0 += most) {
+        const int64_t m = n - t0 < most ? n - t0 : most;
+        const hipError_t e = launch(t0, m, (int)((m + per_wg - 1) / per_wg));
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// The ids from token t0 on.
+inline IdArgs ids_from(const IdArgs& a, int64_t t0, int64_t m)
+{
+    IdArgs b = a;
+    if (a.ids) b.ids = static_cast<const char*>(a.ids) + t0 * (a.id64 ? 8 : 4);
+    b.n = m;
+    return b;
+}
+
+hipError_t launch_embedding(const IdArgs& a, const void* table, int tdt, float scale, void* y, int ydt,
+                            hipStream_t s);
+
+// Table as codes (bits 8: dynamic code; 4: code4 0 NF4, 1 FP4) with block size
+// B, and absmax (plain) or c2 / absmax2 / offset (nested, block size B2).
+hipError_t launch_dequant_embedding(const IdArgs& a, const DequantDesc& t, int bits, int code4, int B, int B2,
+                                    float scale, void* y, int ydt, hipStream_t s);
+
+// start, order of the ids.
+hipError_t launch_order(const IdArgs& a, const OrderArgs& o, hipStream_t s);
+
+// Sums of dy over the chunks' tokens of ids that have more tokens than a chunk:
+// part[2 * chunk] for an id whose tokens begin at or before the chunk's first,
+// part[2 * chunk + 1] for one whose tokens begin inside the chunk (rows of
+// padded_dim binary32).
+hipError_t launch_chunk_sums(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part,
+                             hipStream_t s);
+
+// dtable[v] = scale * sum of dy over the tokens of v (+ dtable[v] with
+// accumulate); pad: an id that takes no gradient, or -1.
+hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, const float* part,
+                             float scale, int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s);
+
+struct NormArgs {
+    const void* gamma;      // nullptr: ones
+    const void* beta;       // nullptr: zeros
+    int wdt;
+    float eps;
+};
+
+hipError_t launch_layer_norm(const void* x, int xdt, int64_t n, int64_t dim, const NormArgs& w, void* y, float* mean,
+                             float* rstd, hipStream_t s);
+hipError_t launch_stable_embedding(const IdArgs& a, const void* table, int tdt, float scale, const NormArgs& w,
+                                   void* y, int ydt, hipStream_t s);
+
+// Workgroups (and partial sums) of the backward passes.
+int layer_norm_parts(int64_t n, int64_t dim);
+int stable_parts(int64_t n, int64_t rows);
+
+// dx, and the partial sums part[g][2][padded_dim] of dgamma and dbeta over
+// layer_norm_parts(n, dim) workgroups (part nullptr: not wanted).
+hipError_t launch_layer_norm_grad(const void* dy, const void* x, int xdt, int64_t n, int64_t dim, const void* gamma,
+                                  int wdt, const float* mean, const float* rstd, void* dx, float* part,
+                                  hipStream_t s);
+
+// As launch_table_grad for the table below a layer norm, with the partial sums of dgamma and dbeta.
+hipError_t launch_stable_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, const float* chunk_part,
+                              const void* table, int tdt, float scale, const NormArgs& w, int64_t pad,
+                              bool accumulate, void* dtable, int ddt, float* part, int parts, hipStream_t s);
+
+// dgamma, dbeta (either may be nullptr) = the sum of `parts` partial sums.
+hipError_t launch_join_parts(const float* part, int parts, int64_t dim, bool accumulate, void* dgamma, void* dbeta,
+                             int wdt, hipStream_t s);
+
+}  // namespace qb

@@ -1,0 +1,280 @@
+// qb_layers_api.cpp -- the C ABI of the row-wise layers (embedding lookup, layer
+// norm, stable embedding) declared in include/qb.h: argument validation,
+// workspace layout and dispatch.  Nothing is enqueued unless every argument
+// checks out.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "qb.h"
+#include "qb_layers.h"
+
+namespace {
+
+using namespace qb;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool valid_dtype(qb_dtype d) { return d == QB_F32 || d == QB_F16 || d == QB_BF16; }
+bool valid_index(qb_index i) { return i == QB_I32 || i == QB_I64; }
+bool pow2_block(int32_t b) { return b >= 64 && b <= 4096 && (b & (b - 1)) == 0; }
+bool is4(qb_code c) { return c == QB_NF4 || c == QB_FP4; }
+size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+constexpr int64_t kIndexMax = int64_t(1) << 31;      // tokens, rows
+constexpr int64_t kDimMax = int64_t(1) << 24;        // elements of a table's row
+constexpr int64_t kGradRowsMax = int64_t(1) << 26;   // rows of a table that takes a gradient
+
+qb_status hip_status(hipError_t e)
+{
+    if (e == hipSuccess) return QB_OK;
+    if (e == hipErrorNotInitialized) return QB_EINIT;
+    return QB_EHIP;
+}
+
+bool valid_lookup(int64_t n, int64_t rows, int64_t dim, qb_index idt, double scale)
+{
+    return n >= 0 && n < kIndexMax && rows >= 0 && rows < kIndexMax && dim >= 1 && dim < kDimMax && valid_index(idt) &&
+           std::isfinite(scale) && std::isfinite((float)scale);
+}
+
+IdArgs id_args(const void* ids, qb_index idt, int64_t n, int64_t rows, int64_t dim)
+{
+    return IdArgs{ids, n, rows, idt == QB_I64 ? 1 : 0, (int32_t)dim};
+}
+
+// An eps that stays positive in binary32: a row of equal values then has a finite rstd.
+bool valid_eps(double eps) { return std::isfinite(eps) && (float)eps > 0.0f && std::isfinite((float)eps); }
+
+// Workspace of a table's gradient: start, order, the chunks' sums; then (stable)
+// the partial sums of dgamma and dbeta.
+struct GradLayout {
+    size_t order, chunks, parts, bytes;
+};
+
+GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim, int parts)
+{
+    GradLayout l;
+    const int64_t entries = (order_per(rows) << order_log2g(rows)) + 1;
+    l.order = round_up((size_t)entries * sizeof(int32_t), 256);
+    l.chunks = l.order + round_up((size_t)n * sizeof(int32_t), 256);
+    l.parts = l.chunks + (size_t)(2 * chunk_count(n) * padded_dim(dim)) * sizeof(float);
+    l.bytes = l.parts + (size_t)parts * 2 * (size_t)padded_dim(dim) * sizeof(float);
+    return l;
+}
+
+bool valid_grad_sizes(int64_t n, int64_t rows, int64_t dim)
+{
+    return n >= 0 && n < kIndexMax && rows >= 0 && rows <= kGradRowsMax && dim >= 1 && dim < kDimMax;
+}
+
+// Checks shared by the two gradients of a table.
+qb_status check_table_grad(const void* dy, qb_dtype gdt, const void* ids, qb_index idt, int64_t n, int64_t rows,
+                           int64_t dim, double scale, int64_t padding_id, const void* dtable, qb_dtype ddt)
+{
+    if (!valid_lookup(n, rows, dim, idt, scale) || !valid_grad_sizes(n, rows, dim) || !valid_dtype(gdt) ||
+        !valid_dtype(ddt) || padding_id < -1 || padding_id >= kIndexMax)
+        return QB_EINVAL;
+    if (n > 0 && (!dy || !ids)) return QB_EINVAL;
+    if (rows > 0 && !dtable) return QB_EINVAL;
+    if (!aligned16(dy) || !aligned16(ids) || !aligned16(dtable)) return QB_EALIGN;
+    return QB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qb_status qb_embedding(const void* table, qb_dtype tdt, int64_t rows, int64_t dim, const void* ids, qb_index idt,
+                       int64_t n, double scale, void* y, qb_dtype ydt, void* stream)
+{
+    if (!valid_lookup(n, rows, dim, idt, scale) || !valid_dtype(tdt) || !valid_dtype(ydt)) return QB_EINVAL;
+    if (n == 0) return QB_OK;
+    if ((rows > 0 && !table) || !ids || !y) return QB_EINVAL;
+    if (!aligned16(table) || !aligned16(ids) || !aligned16(y)) return QB_EALIGN;
+    return hip_status(launch_embedding(id_args(ids, idt, n, rows, dim), table, (int)tdt, (float)scale, y, (int)ydt,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+qb_status qb_dequant_embedding(const uint8_t* codes, const float* absmax, const qb_dq* dq, qb_code code,
+                               int32_t blocksize, int64_t rows, int64_t dim, const void* ids, qb_index idt, int64_t n,
+                               double scale, void* y, qb_dtype ydt, void* stream)
+{
+    if (!valid_lookup(n, rows, dim, idt, scale) || !valid_dtype(ydt) || (code != QB_DYN8 && !is4(code)) ||
+        !pow2_block(blocksize))
+        return QB_EINVAL;
+    if (n == 0) return QB_OK;
+    if (!ids || !y) return QB_EINVAL;
+    if (!aligned16(ids) || !aligned16(y) || !aligned16(codes) || !aligned16(absmax)) return QB_EALIGN;
+    DequantDesc d{};
+    if (rows > 0) {
+        if (!codes) return QB_EINVAL;
+        if ((rows * dim + blocksize - 1) / blocksize >= kIndexMax) return QB_EINVAL;
+        if (dq) {
+            if (absmax || !dq->codes || !dq->absmax2 || !dq->offset || !pow2_block(dq->blocksize2)) return QB_EINVAL;
+            if (!aligned16(dq->codes) || !aligned16(dq->absmax2) || !aligned16(dq->offset)) return QB_EALIGN;
+        } else if (!absmax) {
+            return QB_EINVAL;
+        }
+    }
+    if (!device_tables()) return QB_EINIT;
+    if (rows == 0)                     // every id is outside the table
+        return hip_status(launch_embedding(id_args(ids, idt, n, 0, dim), nullptr, QB_F32, 0.0f, y, (int)ydt,
+                                           static_cast<hipStream_t>(stream)));
+    d.codes = codes;
+    d.absmax = absmax;
+    d.c2 = dq ? dq->codes : nullptr;
+    d.absmax2 = dq ? dq->absmax2 : nullptr;
+    d.offset = dq ? dq->offset : nullptr;
+    return hip_status(launch_dequant_embedding(id_args(ids, idt, n, rows, dim), d, is4(code) ? 4 : 8,
+                                               code == QB_FP4 ? 1 : 0, blocksize, dq ? dq->blocksize2 : 256,
+                                               (float)scale, y, (int)ydt, static_cast<hipStream_t>(stream)));
+}
+
+size_t qb_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim)
+{
+    return valid_grad_sizes(n, rows, dim) ? grad_layout(n, rows, dim, 0).bytes : 0;
+}
+
+qb_status qb_embedding_backward(const void* dy, qb_dtype gdt, const void* ids, qb_index idt, int64_t n, int64_t rows,
+                                int64_t dim, double scale, int64_t padding_id, int32_t accumulate, void* dtable,
+                                qb_dtype ddt, void* ws, size_t ws_bytes, void* stream)
+{
+    qb_status st = check_table_grad(dy, gdt, ids, idt, n, rows, dim, scale, padding_id, dtable, ddt);
+    if (st != QB_OK) return st;
+    if (accumulate != 0 && accumulate != 1) return QB_EINVAL;
+    if (rows == 0 || (n == 0 && accumulate)) return QB_OK;
+    if (!ws) return QB_EINVAL;
+    if (!aligned16(ws)) return QB_EALIGN;
+    const GradLayout l = grad_layout(n, rows, dim, 0);
+    if (ws_bytes < l.bytes) return QB_EWORKSPACE;
+    char* const w = static_cast<char*>(ws);
+    const IdArgs a = id_args(ids, idt, n, rows, dim);
+    const OrderArgs o{reinterpret_cast<int32_t*>(w), reinterpret_cast<int32_t*>(w + l.order), order_log2g(rows),
+                      (int32_t)order_per(rows)};
+    float* const part = reinterpret_cast<float*>(w + l.chunks);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = launch_order(a, o, s);
+    if (e == hipSuccess) e = launch_chunk_sums(a, o, dy, (int)gdt, part, s);
+    if (e == hipSuccess)
+        e = launch_table_grad(a, o, dy, (int)gdt, part, (float)scale, padding_id, accumulate != 0, dtable, (int)ddt, s);
+    return hip_status(e);
+}
+
+qb_status qb_layer_norm(const void* x, qb_dtype xdt, int64_t n, int64_t dim, const void* gamma, const void* beta,
+                        qb_dtype wdt, double eps, void* y, float* mean, float* rstd, void* stream)
+{
+    if (n < 0 || n >= kIndexMax || dim < 1 || dim >= kIndexMax || !valid_dtype(xdt) || !valid_dtype(wdt) ||
+        !valid_eps(eps))
+        return QB_EINVAL;
+    if (wdt != QB_F32 && wdt != xdt) return QB_EUNSUPPORTED;
+    if (n > INT64_MAX / 8 / dim) return QB_EINVAL;
+    if (n == 0) return QB_OK;
+    if (!x || !y) return QB_EINVAL;
+    if (!aligned16(x) || !aligned16(gamma) || !aligned16(beta) || !aligned16(y) || !aligned16(mean) || !aligned16(rstd))
+        return QB_EALIGN;
+    return hip_status(launch_layer_norm(x, (int)xdt, n, dim, NormArgs{gamma, beta, (int)wdt, (float)eps}, y, mean, rstd,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+size_t qb_layer_norm_workspace_bytes(int64_t n, int64_t dim)
+{
+    if (n < 0 || n >= kIndexMax || dim < 1 || dim >= kIndexMax) return 0;
+    const int64_t parts = n < kNormPartsMax ? (n > 0 ? n : 1) : kNormPartsMax;
+    return (size_t)(parts * 2 * padded_dim(dim)) * sizeof(float);
+}
+
+qb_status qb_layer_norm_backward(const void* dy, const void* x, qb_dtype xdt, int64_t n, int64_t dim,
+                                 const void* gamma, qb_dtype wdt, const float* mean, const float* rstd, void* dx,
+                                 void* dgamma, void* dbeta, int32_t accumulate, void* ws, size_t ws_bytes,
+                                 void* stream)
+{
+    if (n < 0 || n >= kIndexMax || dim < 1 || dim >= kIndexMax || !valid_dtype(xdt) || !valid_dtype(wdt) ||
+        (accumulate != 0 && accumulate != 1))
+        return QB_EINVAL;
+    if (wdt != QB_F32 && wdt != xdt) return QB_EUNSUPPORTED;
+    if (n > INT64_MAX / 8 / dim) return QB_EINVAL;
+    const bool weights = dgamma || dbeta;
+    if (n == 0 && (!weights || accumulate)) return QB_OK;
+    if (!dx && !weights) return QB_OK;
+    if (n > 0 && (!dy || !x || !mean || !rstd)) return QB_EINVAL;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(gamma) || !aligned16(mean) || !aligned16(rstd) ||
+        !aligned16(dx) || !aligned16(dgamma) || !aligned16(dbeta))
+        return QB_EALIGN;
+    if (weights) {
+        if (!ws) return QB_EINVAL;
+        if (!aligned16(ws)) return QB_EALIGN;
+        if (ws_bytes < qb_layer_norm_workspace_bytes(n, dim)) return QB_EWORKSPACE;
+    }
+    float* const part = weights ? static_cast<float*>(ws) : nullptr;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (n > 0) {
+        const hipError_t e = launch_layer_norm_grad(dy, x, (int)xdt, n, dim, gamma, (int)wdt, mean, rstd, dx, part, s);
+        if (e != hipSuccess) return hip_status(e);
+    }
+    return hip_status(launch_join_parts(part, n > 0 ? layer_norm_parts(n, dim) : 0, dim, accumulate != 0, dgamma, dbeta,
+                                        (int)wdt, s));
+}
+
+qb_status qb_stable_embedding(const void* table, qb_dtype tdt, int64_t rows, int64_t dim, const void* ids,
+                              qb_index idt, int64_t n, double scale, const void* gamma, const void* beta, qb_dtype wdt,
+                              double eps, void* y, qb_dtype ydt, void* stream)
+{
+    if (!valid_lookup(n, rows, dim, idt, scale) || !valid_dtype(tdt) || !valid_dtype(ydt) || !valid_dtype(wdt) ||
+        !valid_eps(eps))
+        return QB_EINVAL;
+    if (dim > kRowRegMax || (wdt != QB_F32 && wdt != tdt)) return QB_EUNSUPPORTED;
+    if (n == 0) return QB_OK;
+    if ((rows > 0 && !table) || !ids || !y) return QB_EINVAL;
+    if (!aligned16(table) || !aligned16(ids) || !aligned16(gamma) || !aligned16(beta) || !aligned16(y))
+        return QB_EALIGN;
+    return hip_status(launch_stable_embedding(id_args(ids, idt, n, rows, dim), table, (int)tdt, (float)scale,
+                                              NormArgs{gamma, beta, (int)wdt, (float)eps}, y, (int)ydt,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+size_t qb_stable_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim)
+{
+    if (!valid_grad_sizes(n, rows, dim) || dim > kRowRegMax) return 0;
+    return grad_layout(n, rows, dim, stable_parts(n, rows)).bytes;
+}
+
+qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void* table, qb_dtype tdt, int64_t rows,
+                                       int64_t dim, const void* ids, qb_index idt, int64_t n, double scale,
+                                       const void* gamma, qb_dtype wdt, double eps, int64_t padding_id,
+                                       int32_t accumulate, void* dtable, qb_dtype ddt, void* dgamma, void* dbeta,
+                                       void* ws, size_t ws_bytes, void* stream)
+{
+    qb_status st = check_table_grad(dy, gdt, ids, idt, n, rows, dim, scale, padding_id, dtable, ddt);
+    if (st != QB_OK) return st;
+    if (!valid_dtype(tdt) || !valid_dtype(wdt) || !valid_eps(eps) || (accumulate != 0 && accumulate != 1))
+        return QB_EINVAL;
+    if (dim > kRowRegMax || (wdt != QB_F32 && wdt != tdt)) return QB_EUNSUPPORTED;
+    if (rows > 0 && n > 0 && !table) return QB_EINVAL;
+    if (!aligned16(table) || !aligned16(gamma) || !aligned16(dgamma) || !aligned16(dbeta)) return QB_EALIGN;
+    if (n == 0 && accumulate) return QB_OK;
+    if (!ws) return QB_EINVAL;
+    if (!aligned16(ws)) return QB_EALIGN;
+    const int parts = stable_parts(n, rows);
+    const GradLayout l = grad_layout(n, rows, dim, parts);
+    if (ws_bytes < l.bytes) return QB_EWORKSPACE;
+    char* const w = static_cast<char*>(ws);
+    const IdArgs a = id_args(ids, idt, n, rows, dim);
+    const OrderArgs o{reinterpret_cast<int32_t*>(w), reinterpret_cast<int32_t*>(w + l.order), order_log2g(rows),
+                      (int32_t)order_per(rows)};
+    float* const chunks = reinterpret_cast<float*>(w + l.chunks);
+    float* const part = reinterpret_cast<float*>(w + l.parts);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    if (rows > 0) {
+        e = launch_order(a, o, s);
+        if (e == hipSuccess) e = launch_chunk_sums(a, o, dy, (int)gdt, chunks, s);
+        if (e == hipSuccess)
+            e = launch_stable_grad(a, o, dy, (int)gdt, chunks, table, (int)tdt, (float)scale,
+                                   NormArgs{gamma, nullptr, (int)wdt, (float)eps}, padding_id, accumulate != 0, dtable,
+                                   (int)ddt, part, parts, s);
+    }
+    if (e == hipSuccess) e = launch_join_parts(part, parts, dim, accumulate != 0, dgamma, dbeta, (int)wdt, s);
+    return hip_status(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,400 @@
+// qb_norm.hip -- layer norm (forward) and its backward pass with the reduction
+// of the weight's gradient.
+//
+// Backward, with h = (x - mean) * rstd and g = dy * gamma:
+//   dx = rstd * (g - mean(g) - h * mean(g h)),  dgamma = sum_rows dy h,
+//   dbeta = sum_rows dy.
+// One kernel reads dy and x once: a fixed set of workgroups walks the rows, each
+// thread keeping binary32 sums of dy h and dy for its own columns in registers;
+// at the end a workgroup joins its waves' sums in LDS and writes one partial
+// row, and a second kernel adds the partial rows.  Every sum has a fixed order:
+// the same bits on every run.
+#include "qb_norm_kernels.h"
+
+namespace qb {
+
+namespace {
+
+// Rows too long for registers (dim > kRowRegMax): one workgroup of 1024
+// threads per row reads it three times (the second and third time from L2).
+constexpr int kLongThreads = 1024;
+
+template <int XDT, int WDT>
+__global__ __launch_bounds__(kLongThreads) void k_norm_long(const void* __restrict__ x, int64_t dim,
+                                                            const void* __restrict__ gamma,
+                                                            const void* __restrict__ beta, float eps,
+                                                            void* __restrict__ y, float* __restrict__ mean_out,
+                                                            float* __restrict__ rstd_out)
+{
+    __shared__ float s_slot[3 * (kLongThreads / 64)];
+    const int64_t t = blockIdx.x;
+    const char* const xrow = static_cast<const char*>(x) + t * dim * elem_bytes(XDT);
+    char* const yrow = static_cast<char*>(y) + t * dim * elem_bytes(XDT);
+    const int64_t whole = dim / 8;
+    const int left = (int)(dim % 8);
+
+    float sum = 0.0f;
+    for (int64_t u = threadIdx.x; u < whole; u += kLongThreads) {
+        const Unit<XDT> w = load_unit8<XDT, false>(xrow, u * 8);
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += unit_at<XDT>(w, j);
+        sum += s;
+    }
+    if ((int)threadIdx.x < left) sum += load1<XDT>(xrow, whole * 8 + threadIdx.x);
+    const float m0 = row_sum<kLongThreads>(sum, s_slot) / (float)dim;
+    float sd = 0.0f, sq = 0.0f;
+    for (int64_t u = threadIdx.x; u < whole; u += kLongThreads) {
+        const Unit<XDT> w = load_unit8<XDT, false>(xrow, u * 8);
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float d = unit_at<XDT>(w, j) - m0;
+            a += d;
+            b = __builtin_fmaf(d, d, b);
+        }
+        sd += a;
+        sq += b;
+    }
+    if ((int)threadIdx.x < left) {
+        const float d = load1<XDT>(xrow, whole * 8 + threadIdx.x) - m0;
+        sd += d;
+        sq = __builtin_fmaf(d, d, sq);
+    }
+    row_sum2<kLongThreads>(sd, sq, s_slot + kLongThreads / 64);
+    const float c = sd / (float)dim;
+    const float mean = m0 + c;
+    const float rstd = inv_deviation(sq / (float)dim - c * c, eps);
+    if (threadIdx.x == 0) {
+        if (mean_out) mean_out[t] = mean;
+        if (rstd_out) rstd_out[t] = rstd;
+    }
+    for (int64_t u = threadIdx.x; u < whole; u += kLongThreads) {
+        const Unit<XDT> w = load_unit8<XDT, false>(xrow, u * 8);
+        Unit<WDT> gu, bu;
+        if (gamma) gu = load_unit8<WDT, false>(gamma, u * 8);
+        if (beta) bu = load_unit8<WDT, false>(beta, u * 8);
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            o[j] = __builtin_fmaf((unit_at<XDT>(w, j) - mean) * rstd, gamma ? unit_at<WDT>(gu, j) : 1.0f,
+                                  beta ? unit_at<WDT>(bu, j) : 0.0f);
+        store_unit8<XDT, true>(yrow, u * 8, o);
+    }
+    if ((int)threadIdx.x < left) {
+        const int64_t i = whole * 8 + threadIdx.x;
+        store1<XDT>(yrow, i,
+                    __builtin_fmaf((load1<XDT>(xrow, i) - mean) * rstd, gamma ? load1<WDT>(gamma, i) : 1.0f,
+                                   beta ? load1<WDT>(beta, i) : 0.0f));
+    }
+}
+
+template <int XDT, int WDT>
+hipError_t layer_norm_as(const void* x, int64_t n, int64_t dim, const NormArgs& w, void* y, float* mean, float* rstd,
+                         hipStream_t s)
+{
+    if (dim > kRowRegMax)
+        return launch_rows(n, 1, [&](int64_t t0, int64_t, int grid) {
+            const int64_t at = t0 * dim * elem_bytes(XDT);
+            return launch_kernel_nt(k_norm_long<XDT, WDT>, grid, kLongThreads, s, static_cast<const char*>(x) + at, dim,
+                                    w.gamma, w.beta, w.eps, static_cast<char*>(y) + at, mean ? mean + t0 : nullptr,
+                                    rstd ? rstd + t0 : nullptr);
+        });
+    const IdArgs a{nullptr, n, n, 0, (int32_t)dim};
+    return norm_dim<XDT, XDT, WDT, false>(x, a, 1.0f, w, y, mean, rstd, s);
+}
+
+// Backward pass.  NT threads: NT / TPR rows at a time.  LDS (dynamic): gamma in
+// binary32 while the rows are walked, then the joined sums, padded_dim floats.
+template <int XDT, int WDT, int TPR, int VPT, bool TAIL, int NT>
+__global__ __launch_bounds__(NT) void k_norm_grad(const void* __restrict__ dy, const void* __restrict__ x, int64_t n,
+                                                  int dim, const void* __restrict__ gamma,
+                                                  const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
+                                                  void* __restrict__ dx, float* __restrict__ part)
+{
+    extern __shared__ __align__(16) float s_cols[];
+    constexpr int GROUPS = NT / TPR;
+    constexpr int SLOT = TPR <= 64 ? 1 : 2 * (TPR / 64);
+    __shared__ float s_slot[2][GROUPS][SLOT];
+    const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    const int units = (dim + 7) >> 3, padded = units * 8;
+    for (int c = threadIdx.x; c < padded; c += NT) s_cols[c] = (gamma && c < dim) ? load1<WDT>(gamma, c) : 1.0f;
+    __syncthreads();
+
+    float accg[VPT][8] = {}, accb[VPT][8] = {};
+    const float inv = 1.0f / (float)dim;
+    int buf = 0;
+    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < n; t0 += (int64_t)gridDim.x * GROUPS) {
+        const int64_t t = t0 + grp;
+        const bool live = t < n;
+        const int64_t row = (live ? t : n - 1) * dim * elem_bytes(XDT);
+        const char* const xrow = static_cast<const char*>(x) + row;
+        const char* const grow = static_cast<const char*>(dy) + row;
+        Unit<XDT> xu[VPT], du[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            du[k] = load_row_unit<XDT, TAIL, true>(grow, k * TPR + lane, units, dim);
+            xu[k] = load_row_unit<XDT, TAIL, true>(xrow, k * TPR + lane, units, dim);
+        }
+        const float m = mean_in[live ? t : n - 1], r = rstd_in[live ? t : n - 1];
+        // Units beyond the row, and rows beyond the last, take a dy of zero (and an x that is read: finite
+        // wherever the row is).
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int unit = k * TPR + lane;
+            if (!live || unit >= units) {
+#pragma unroll
+                for (int j = 0; j < (XDT == DT_F32 ? 8 : 4); ++j) du[k].w[j] = xu[k].w[j] = 0u;
+            }
+            const float* const gam = s_cols + (unit < units ? unit : 0) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = unit_at<XDT>(du[k], j);
+                const float h = (unit_at<XDT>(xu[k], j) - m) * r;
+                const float g = d * gam[j];
+                s1 += g;
+                s2 = __builtin_fmaf(g, h, s2);
+                accg[k][j] = (TPR < 64 && !live) ? accg[k][j] : __builtin_fmaf(d, h, accg[k][j]);
+                accb[k][j] += d;
+            }
+        }
+        row_sum2<TPR>(s1, s2, s_slot[buf][grp]);
+        buf ^= 1;
+        if (dx && live) {
+            const float c1 = s1 * inv, c2 = s2 * inv;
+            char* const orow = static_cast<char*>(dx) + row;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int unit = k * TPR + lane;
+                const float* const gam = s_cols + (unit < units ? unit : 0) * 8;
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float h = (unit_at<XDT>(xu[k], j) - m) * r;
+                    const float g = unit_at<XDT>(du[k], j) * gam[j];
+                    o[j] = r * (g - __builtin_fmaf(h, c2, c1));
+                }
+                store_row_unit<XDT, TAIL, true>(orow, unit, units, dim, o);
+            }
+        }
+    }
+    if (!part) return;
+
+    // Join: the threads that hold the same columns take turns, one unit each at a time.
+    if constexpr (TPR == 16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            accg[0][j] += __shfl_xor(accg[0][j], 16);
+            accg[0][j] += __shfl_xor(accg[0][j], 32);
+            accb[0][j] += __shfl_xor(accb[0][j], 16);
+            accb[0][j] += __shfl_xor(accb[0][j], 32);
+        }
+    }
+    constexpr int JT = TPR < 64 ? 64 : TPR;          // threads that hold one set of columns
+    constexpr int SETS = NT / JT;
+    const int set = threadIdx.x / JT;
+    const bool mine = TPR >= 64 || threadIdx.x % 64 < TPR;
+    float* const out = part + (int64_t)blockIdx.x * 2 * padded;
+    auto join = [&](float (&acc)[VPT][8], float* dst) {
+        __syncthreads();
+#pragma unroll
+        for (int turn = 0; turn < SETS; ++turn) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int unit = k * TPR + lane;
+                if (mine && unit < units && k % SETS == (set + turn) % SETS) {
+                    float* const p = s_cols + unit * 8;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) p[j] = turn == 0 ? acc[k][j] : p[j] + acc[k][j];
+                }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x * 4; c < padded; c += NT * 4)
+            *reinterpret_cast<float4*>(dst + c) = *reinterpret_cast<const float4*>(s_cols + c);
+    };
+    join(accg, out);
+    join(accb, out + padded);
+}
+
+// Long rows: dx by one workgroup per row, which reads the row twice ...
+template <int XDT, int WDT>
+__global__ __launch_bounds__(kLongThreads) void k_norm_grad_long(const void* __restrict__ dy,
+                                                                 const void* __restrict__ x, int64_t dim,
+                                                                 const void* __restrict__ gamma,
+                                                                 const float* __restrict__ mean_in,
+                                                                 const float* __restrict__ rstd_in,
+                                                                 void* __restrict__ dx)
+{
+    __shared__ float s_slot[2 * (kLongThreads / 64)];
+    const int64_t t = blockIdx.x, row = t * dim * elem_bytes(XDT);
+    const char* const xrow = static_cast<const char*>(x) + row;
+    const char* const grow = static_cast<const char*>(dy) + row;
+    char* const orow = static_cast<char*>(dx) + row;
+    const float m = mean_in[t], r = rstd_in[t];
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int64_t i = threadIdx.x; i < dim; i += kLongThreads) {
+        const float g = load1<XDT>(grow, i) * (gamma ? load1<WDT>(gamma, i) : 1.0f);
+        s1 += g;
+        s2 = __builtin_fmaf(g, (load1<XDT>(xrow, i) - m) * r, s2);
+    }
+    row_sum2<kLongThreads>(s1, s2, s_slot);
+    const float c1 = s1 / (float)dim, c2 = s2 / (float)dim;
+    for (int64_t i = threadIdx.x; i < dim; i += kLongThreads) {
+        const float g = load1<XDT>(grow, i) * (gamma ? load1<WDT>(gamma, i) : 1.0f);
+        store1<XDT>(orow, i, r * (g - __builtin_fmaf((load1<XDT>(xrow, i) - m) * r, c2, c1)));
+    }
+}
+
+// ... and the column sums apart: workgroup (b % parts) takes the rows t = part,
+// part + parts, ... of 256 columns.
+template <int XDT>
+__global__ __launch_bounds__(256) void k_norm_cols(const void* __restrict__ dy, const void* __restrict__ x, int64_t n,
+                                                   int64_t dim, const float* __restrict__ mean_in,
+                                                   const float* __restrict__ rstd_in, float* __restrict__ part,
+                                                   int parts)
+{
+    const int p = blockIdx.x % parts;
+    const int64_t c = (int64_t)(blockIdx.x / parts) * 256 + threadIdx.x, padded = (dim + 7) / 8 * 8;
+    if (c >= padded) return;
+    float sg = 0.0f, sb = 0.0f;
+    if (c < dim) {
+        for (int64_t t = p; t < n; t += parts) {
+            const float d = load1<XDT>(dy, t * dim + c);
+            sg = __builtin_fmaf(d, (load1<XDT>(x, t * dim + c) - mean_in[t]) * rstd_in[t], sg);
+            sb += d;
+        }
+    }
+    float* const out = part + (int64_t)p * 2 * padded;
+    out[c] = sg;
+    out[padded + c] = sb;
+}
+
+constexpr int kLongParts = 64;
+
+template <int XDT, int WDT, bool TAIL>
+hipError_t grad_as(const void* dy, const void* x, int64_t n, int dim, const void* gamma, const float* mean,
+                   const float* rstd, void* dx, float* part, hipStream_t s)
+{
+    const int units = (dim + 7) / 8;
+    const int grid = layer_norm_parts(n, dim);
+    const size_t lds = (size_t)units * 8 * sizeof(float);
+    auto go = [&](auto kernel, int threads) {
+        return launch_kernel_lds(kernel, grid, threads, lds, s, dy, x, n, dim, gamma, mean, rstd, dx, part);
+    };
+    if (units <= 16) return go(k_norm_grad<XDT, WDT, 16, 1, TAIL, 512>, 512);
+    if (units <= 64) return go(k_norm_grad<XDT, WDT, 64, 1, TAIL, 512>, 512);
+    if (units <= 128) return go(k_norm_grad<XDT, WDT, 64, 2, TAIL, 512>, 512);
+    if (units <= 256) return go(k_norm_grad<XDT, WDT, 64, 4, TAIL, 512>, 512);
+    if (units <= 512) return go(k_norm_grad<XDT, WDT, 256, 2, TAIL, 512>, 512);
+    if (units <= 1024) return go(k_norm_grad<XDT, WDT, 256, 4, TAIL, 512>, 512);
+    return go(k_norm_grad<XDT, WDT, 512, 4, TAIL, 512>, 512);
+}
+
+template <int XDT, int WDT>
+hipError_t layer_norm_grad_as(const void* dy, const void* x, int64_t n, int64_t dim, const void* gamma,
+                              const float* mean, const float* rstd, void* dx, float* part, hipStream_t s)
+{
+    if (dim > kRowRegMax) {
+        if (dx) {
+            const hipError_t e = launch_rows(n, 1, [&](int64_t t0, int64_t, int grid) {
+                const int64_t at = t0 * dim * elem_bytes(XDT);
+                return launch_kernel_nt(k_norm_grad_long<XDT, WDT>, grid, kLongThreads, s,
+                                        static_cast<const char*>(dy) + at, static_cast<const char*>(x) + at, dim,
+                                        gamma, mean + t0, rstd + t0, static_cast<char*>(dx) + at);
+            });
+            if (e != hipSuccess) return e;
+        }
+        if (!part) return hipSuccess;
+        const int parts = layer_norm_parts(n, dim);
+        const int64_t grid = (padded_dim(dim) + 255) / 256 * parts;
+        if (grid >= (int64_t(1) << 24)) return hipErrorInvalidValue;
+        return launch_kernel(k_norm_cols<XDT>, (int)grid, s, dy, x, n, dim, mean, rstd, part, parts);
+    }
+    return dim % 8 ? grad_as<XDT, WDT, true>(dy, x, n, (int)dim, gamma, mean, rstd, dx, part, s)
+                   : grad_as<XDT, WDT, false>(dy, x, n, (int)dim, gamma, mean, rstd, dx, part, s);
+}
+
+// dgamma, dbeta = the sum of the partial rows.  A workgroup takes 64 of the 2 *
+// padded columns: 16 lanes of 4 columns, the partial rows dealt to 16 threads
+// each, joined in LDS.
+__global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ part, int parts, int64_t dim,
+                                                    int64_t padded, int accumulate, void* __restrict__ dgamma,
+                                                    void* __restrict__ dbeta, int wdt)
+{
+    __shared__ f32x4 s_sum[16][16];
+    const int l = threadIdx.x % 16, q = threadIdx.x / 16;
+    const int64_t c = (int64_t)blockIdx.x * 64 + l * 4;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < 2 * padded) {
+        const float* p = part + c;
+#pragma unroll 4
+        for (int g = q; g < parts; g += 16) sum += gld<f32x4>(p + (int64_t)g * 2 * padded);
+    }
+    s_sum[q][l] = sum;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        const int64_t cc = (int64_t)blockIdx.x * 64 + threadIdx.x;
+        float v = 0.0f;
+#pragma unroll
+        for (int g = 0; g < 16; ++g) v += s_sum[g][threadIdx.x / 4][threadIdx.x % 4];
+        if (cc < 2 * padded) {
+            void* const out = cc < padded ? dgamma : dbeta;
+            const int64_t i = cc < padded ? cc : cc - padded;
+            if (out && i < dim) {
+                if (accumulate) v += load1_rt(wdt, out, i);
+                store1_rt(wdt, out, i, v);
+            }
+        }
+    }
+}
+
+}  // namespace
+
+int layer_norm_parts(int64_t n, int64_t dim)
+{
+    if (dim > kRowRegMax) return (int)(n < kLongParts ? n : kLongParts);
+    const int64_t units = (dim + 7) / 8;
+    const int64_t groups = units <= 16 ? 32 : units <= 256 ? 8 : units <= 1024 ? 2 : 1;     // rows a workgroup takes at once
+    const int64_t g = (n + groups - 1) / groups;
+    return (int)(g < kNormPartsMax ? g : kNormPartsMax);
+}
+
+hipError_t launch_layer_norm(const void* x, int xdt, int64_t n, int64_t dim, const NormArgs& w, void* y, float* mean,
+                             float* rstd, hipStream_t s)
+{
+    if (w.wdt == DT_F32) {
+        if (xdt == DT_F32) return layer_norm_as<DT_F32, DT_F32>(x, n, dim, w, y, mean, rstd, s);
+        if (xdt == DT_F16) return layer_norm_as<DT_F16, DT_F32>(x, n, dim, w, y, mean, rstd, s);
+        return layer_norm_as<DT_BF16, DT_F32>(x, n, dim, w, y, mean, rstd, s);
+    }
+    if (w.wdt != xdt) return hipErrorInvalidValue;
+    if (xdt == DT_F16) return layer_norm_as<DT_F16, DT_F16>(x, n, dim, w, y, mean, rstd, s);
+    return layer_norm_as<DT_BF16, DT_BF16>(x, n, dim, w, y, mean, rstd, s);
+}
+
+hipError_t launch_layer_norm_grad(const void* dy, const void* x, int xdt, int64_t n, int64_t dim, const void* gamma,
+                                  int wdt, const float* mean, const float* rstd, void* dx, float* part, hipStream_t s)
+{
+    if (wdt == DT_F32) {
+        if (xdt == DT_F32) return layer_norm_grad_as<DT_F32, DT_F32>(dy, x, n, dim, gamma, mean, rstd, dx, part, s);
+        if (xdt == DT_F16) return layer_norm_grad_as<DT_F16, DT_F32>(dy, x, n, dim, gamma, mean, rstd, dx, part, s);
+        return layer_norm_grad_as<DT_BF16, DT_F32>(dy, x, n, dim, gamma, mean, rstd, dx, part, s);
+    }
+    if (wdt != xdt) return hipErrorInvalidValue;
+    if (xdt == DT_F16) return layer_norm_grad_as<DT_F16, DT_F16>(dy, x, n, dim, gamma, mean, rstd, dx, part, s);
+    return layer_norm_grad_as<DT_BF16, DT_BF16>(dy, x, n, dim, gamma, mean, rstd, dx, part, s);
+}
+
+hipError_t launch_join_parts(const float* part, int parts, int64_t dim, bool accumulate, void* dgamma, void* dbeta,
+                             int wdt, hipStream_t s)
+{
+    if (!dgamma && !dbeta) return hipSuccess;
+    const int64_t padded = padded_dim(dim), grid = (2 * padded + 63) / 64;
+    if (grid >= (int64_t(1) << 24)) return hipErrorInvalidValue;
+    return launch_kernel(k_join_parts, (int)grid, s, part, parts, dim, padded, accumulate ? 1 : 0, dgamma, dbeta,
+                         wdt);
+}
+
+}  // namespace qb

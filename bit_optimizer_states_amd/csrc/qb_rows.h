@@ -1,0 +1,192 @@
+// qb_rows.h -- device helpers of the row-wise layers (embedding lookup, layer
+// norm): rows are cut into units of 8 elements, one unit per lane and step.
+#pragma once
+#include "qb_device.h"
+#include "qb_layers.h"
+
+namespace qb {
+
+// Rows start at any multiple of the element size (dim may be odd), so units are
+// accessed through vector types of element alignment: the GLOBAL instructions
+// take them as they are (gfx950 runs in unaligned-access mode), and an aligned
+// row costs the same as through aligned types.
+typedef u32x4 __attribute__((aligned(2))) u32x4_a2;
+typedef f32x4 __attribute__((aligned(4))) f32x4_a4;
+
+// The raw bits of one unit: 16 bytes of a 16-bit type, 32 of binary32.
+template <int DT>
+struct Unit {
+    uint32_t w[DT == DT_F32 ? 8 : 4];
+};
+
+constexpr int elem_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
+
+template <int DT, bool NT>
+__device__ __forceinline__ Unit<DT> load_unit8(const void* row, int64_t elem)
+{
+    Unit<DT> u;
+    const char* p = static_cast<const char*>(row) + elem * elem_bytes(DT);
+#pragma unroll
+    for (int h = 0; h < (DT == DT_F32 ? 2 : 1); ++h) {
+        const QB_G u32x4_a2* q = (const QB_G u32x4_a2*)(p + 16 * h);
+        u32x4 v;
+        if constexpr (NT) v = __builtin_nontemporal_load(q);
+        else v = *q;
+        u.w[4 * h] = v.x; u.w[4 * h + 1] = v.y; u.w[4 * h + 2] = v.z; u.w[4 * h + 3] = v.w;
+    }
+    return u;
+}
+
+template <int DT>
+__device__ __forceinline__ float unit_at(const Unit<DT>& u, int j)
+{
+    if constexpr (DT == DT_F32) return ffrom(u.w[j]);
+    else return (j & 1) ? half_hi<DT>(u.w[j >> 1]) : half_lo<DT>(u.w[j >> 1]);
+}
+
+// The unit of a row's last `left` (1 .. 7) elements; the others are zero.
+template <int DT>
+__device__ __forceinline__ Unit<DT> load_part8(const void* row, int64_t elem, int left)
+{
+    Unit<DT> u;
+#pragma unroll
+    for (int j = 0; j < (DT == DT_F32 ? 8 : 4); ++j) u.w[j] = 0u;
+    const char* p = static_cast<const char*>(row) + elem * elem_bytes(DT);
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+        if (j < left) {
+            if constexpr (DT == DT_F32) u.w[j] = gld<uint32_t>(p + 4 * j);
+            else u.w[j >> 1] |= (uint32_t)gld<uint16_t>(p + 2 * j) << (16 * (j & 1));
+        }
+    }
+    return u;
+}
+
+// Unit number `unit` of a row of `dim` elements.  TAIL: dim is no multiple of 8,
+// so the last unit is partial.  A unit beyond the row (unit >= ceil(dim / 8))
+// reads unit 0 instead (its caller masks it), so that no load is under a branch
+// where there is no tail.
+template <int DT, bool TAIL, bool NT>
+__device__ __forceinline__ Unit<DT> load_row_unit(const void* row, int unit, int units, int dim)
+{
+    if constexpr (!TAIL) {
+        return load_unit8<DT, NT>(row, (int64_t)(unit < units ? unit : 0) * 8);
+    } else {
+        const int u = unit < units ? unit : 0;
+        const int left = dim - u * 8;
+        if (left >= 8) return load_unit8<DT, NT>(row, (int64_t)u * 8);
+        return load_part8<DT>(row, (int64_t)u * 8, left);
+    }
+}
+
+template <int DT, bool NT>
+__device__ __forceinline__ void store_unit8(void* row, int64_t elem, const float* v)
+{
+    char* p = static_cast<char*>(row) + elem * elem_bytes(DT);
+    if constexpr (DT == DT_F32) {
+        f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+        QB_G f32x4_a4* q = (QB_G f32x4_a4*)p;
+        if constexpr (NT) {
+            __builtin_nontemporal_store(a, q);
+            __builtin_nontemporal_store(b, q + 1);
+        } else {
+            q[0] = a;
+            q[1] = b;
+        }
+    } else {
+        u32x4 a = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+        QB_G u32x4_a2* q = (QB_G u32x4_a2*)p;
+        if constexpr (NT) __builtin_nontemporal_store(a, q);
+        else *q = a;
+    }
+}
+
+// Stores unit `unit` of a row (nothing beyond the row, a partial last unit element by element).
+template <int DT, bool TAIL, bool NT>
+__device__ __forceinline__ void store_row_unit(void* row, int unit, int units, int dim, const float* v)
+{
+    if (unit >= units) return;
+    if constexpr (TAIL) {
+        const int left = dim - unit * 8;
+        if (left < 8) {
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (j < left) store1<DT>(row, (int64_t)unit * 8 + j, v[j]);
+            return;
+        }
+    }
+    store_unit8<DT, NT>(row, (int64_t)unit * 8, v);
+}
+
+// The same with the type known at run time only (uniform).
+template <bool TAIL, bool NT>
+__device__ __forceinline__ void store_row_unit_rt(int dt, void* row, int unit, int units, int dim, const float* v)
+{
+    if (dt == DT_F32) store_row_unit<DT_F32, TAIL, NT>(row, unit, units, dim, v);
+    else if (dt == DT_F16) store_row_unit<DT_F16, TAIL, NT>(row, unit, units, dim, v);
+    else store_row_unit<DT_BF16, TAIL, NT>(row, unit, units, dim, v);
+}
+
+__device__ __forceinline__ float load1_rt(int dt, const void* p, int64_t i)
+{
+    return dt == DT_F32 ? load1<DT_F32>(p, i) : dt == DT_F16 ? load1<DT_F16>(p, i) : load1<DT_BF16>(p, i);
+}
+
+__device__ __forceinline__ void store1_rt(int dt, void* p, int64_t i, float v)
+{
+    if (dt == DT_F32) store1<DT_F32>(p, i, v);
+    else if (dt == DT_F16) store1<DT_F16>(p, i, v);
+    else store1<DT_BF16>(p, i, v);
+}
+
+// Number of elements of unit `unit` that lie in the row: 8, or fewer at its end, or none beyond it.
+__device__ __forceinline__ int unit_count(int unit, int dim)
+{
+    const int left = dim - unit * 8;
+    return left < 0 ? 0 : left > 8 ? 8 : left;
+}
+
+// Token id number t (32- or 64-bit ids) as 64 bits.
+__device__ __forceinline__ int64_t load_id(const void* ids, int id64, int64_t t)
+{
+    return id64 ? gld<int64_t>(static_cast<const int64_t*>(ids) + t)
+                : (int64_t)gld<int32_t>(static_cast<const int32_t*>(ids) + t);
+}
+
+// Sum over aligned groups of L lanes (16 or 64), the same bits in every lane
+// of the group: four steps within a row of 16 lanes, then the four rows' sums
+// in row order.  All 64 lanes must be active.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v)
+{
+    return v + ffrom((uint32_t)__builtin_amdgcn_mov_dpp((int)fbits(v), CTRL, 0xF, 0xF, false));
+}
+
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+    static_assert(L == 16 || L == 64, "row of 16 lanes or whole wave");
+    v = dpp_add<0xB1>(v);      // quad_perm [1,0,3,2]
+    v = dpp_add<0x4E>(v);      // quad_perm [2,3,0,1]
+    v = dpp_add<0x141>(v);     // row_half_mirror
+    v = dpp_add<0x140>(v);     // row_mirror
+    if constexpr (L == 64) {
+        const int b = (int)fbits(v);
+        const float r0 = ffrom((uint32_t)__builtin_amdgcn_readlane(b, 0));
+        const float r1 = ffrom((uint32_t)__builtin_amdgcn_readlane(b, 16));
+        const float r2 = ffrom((uint32_t)__builtin_amdgcn_readlane(b, 32));
+        const float r3 = ffrom((uint32_t)__builtin_amdgcn_readlane(b, 48));
+        v = (r0 + r1) + (r2 + r3);
+    }
+    return v;
+}
+
+// Workgroup barrier that orders LDS accesses only: global loads and stores stay in flight across it.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+}  // namespace qb

@@ -1,8 +1,9 @@
 /*
  * qb.h -- C ABI of libqb: block-wise dynamic quantization, nested quantization
  * of the block constants, the fused 8-bit AdamW step and its sibling 8-bit
- * optimizers (with paged states), user codes, and the product of a 4-bit
- * layer, for AMD Instinct MI355X (gfx950).
+ * optimizers (with paged states), user codes, the product of a 4-bit layer, and
+ * the stable embedding layer (embedding lookup, layer norm, their gradients),
+ * for AMD Instinct MI355X (gfx950).
  *
  * The method: a tensor is cut into blocks of `blocksize` consecutive elements;
  * every block is scaled by its own absolute maximum and each scaled value is
@@ -71,6 +72,9 @@ typedef enum {
 } qb_status;
 
 typedef enum { QB_F32 = 0, QB_F16 = 1, QB_BF16 = 2 } qb_dtype;
+
+/* Type of token ids (the row-wise layers below). */
+typedef enum { QB_I32 = 0, QB_I64 = 1 } qb_index;
 
 typedef enum { QB_DYN8 = 0, QB_NF4 = 1, QB_FP4 = 2, QB_UDYN8 = 3 } qb_code;
 
@@ -572,6 +576,144 @@ size_t qb_multi_tensor_workspace_bytes(int32_t count);
  * per tensor.  0 when hp, tensors or a size is invalid. */
 size_t qb_optimizer_workspace_bytes(const qb_optim_hparams* hp, const qb_tensor* tensors, int32_t count,
                                     int32_t blocksize);
+
+/*
+ * The row-wise layers: embedding lookup, layer norm, and the stable embedding
+ * that joins them (page "Py之bitsandbytes", section 1, lists a stable embedding
+ * layer next to the 8-bit optimizers: an embedding followed by layer norm, whose
+ * table keeps 32-bit optimizer state).  Common to these calls:
+ *   - Matrices are row-major and dense: a table [rows, dim], tokens [n, dim].
+ *     Rows may begin at any element (dim may be odd); the arrays themselves are
+ *     16-byte aligned.
+ *   - Token ids: n int32 or int64 values (idt).  An id outside [0, rows) names
+ *     no row: its output row is zero and it takes no gradient.  This serves
+ *     padded batches (id -1) and shards of a vocabulary (ids shifted by the
+ *     shard's first row).  With rows == 0 the table may be NULL.
+ *   - Arithmetic, sums and statistics are binary32; each output is rounded once
+ *     to its dtype.  Every sum is added in a fixed order: the same inputs give
+ *     the same bits on every run.  NaN and infinities propagate as in the
+ *     formulas: into the rows (and, for the sums over rows, columns) that they
+ *     enter, into no others.
+ *   - n == 0: the forward calls do nothing; the backward calls write the
+ *     gradient of no tokens (zeros) unless they accumulate.
+ *   - Outputs must not overlap inputs or each other.
+ *   - accumulate (0 or 1): add the gradient to what the outputs hold (read in
+ *     their dtype, added in binary32, rounded once) instead of overwriting them.
+ *   - Limits: n, rows < 2^31; dim < 2^24 for tables (2^31 for layer norm); the
+ *     backward calls take tables of at most 2^26 rows.
+ */
+
+/*
+ * qb_embedding -- y[t] = ydt(scale * table[ids[t]]): one binary32 multiply, one
+ * rounding.
+ *   table   [rows, dim] of dtype tdt.     ids  [n] of type idt.
+ *   scale   finite (in binary32 too).     y    [n, dim] of dtype ydt.
+ * One kernel.
+ */
+qb_status qb_embedding(const void* table, qb_dtype tdt, int64_t rows, int64_t dim, const void* ids, qb_index idt,
+                       int64_t n, double scale, void* y, qb_dtype ydt, void* stream);
+
+/*
+ * qb_dequant_embedding -- qb_embedding with the table [rows, dim] held as
+ * block-wise codes, as qb_quantize writes them for its rows * dim elements
+ * (blocks may span rows; an odd dim begins every other row inside a byte):
+ * y[t] = ydt(scale * w) with w the binary32 value of qb_dequantize, two rounded
+ * multiplies.  Only the rows that ids name are decoded (the embedding of a
+ * 4-bit model: page "Bitsandbytes", section Normal Float 4 (NF4)).
+ *   codes, absmax, dq, code, blocksize   as for qb_dequantize (dq->ws is not used);
+ *           the table has fewer than 2^31 blocks.
+ * One kernel.  The first call on a device that needs the library's constant
+ * tables uploads them: make one before capturing a graph.
+ */
+qb_status qb_dequant_embedding(const uint8_t* codes, const float* absmax, const qb_dq* dq, qb_code code,
+                               int32_t blocksize, int64_t rows, int64_t dim, const void* ids, qb_index idt, int64_t n,
+                               double scale, void* y, qb_dtype ydt, void* stream);
+
+/*
+ * qb_embedding_backward -- the gradient of the table,
+ *   dtable[v] = scale * (sum of dy[t] over the tokens t with ids[t] = v),
+ * zero for an id without tokens.  The tokens are sorted by id first, and each
+ * row's sum runs over them in order.
+ *   dy          [n, dim] of dtype gdt.
+ *   padding_id  an id that takes no gradient (its row is zero, or left as it is
+ *               with accumulate); -1 for none.
+ *   dtable      [rows, dim] of dtype ddt, every row written (with accumulate:
+ *               only the rows of ids that have tokens are read and written).
+ *   ws          device workspace of qb_embedding_workspace_bytes(n, rows, dim)
+ *               bytes, 16-byte aligned; holds nothing between calls, and must not
+ *               be shared by calls that may overlap in time.
+ * Three kernels on `stream`; no memory operations, so it may be captured.
+ */
+qb_status qb_embedding_backward(const void* dy, qb_dtype gdt, const void* ids, qb_index idt, int64_t n, int64_t rows,
+                                int64_t dim, double scale, int64_t padding_id, int32_t accumulate, void* dtable,
+                                qb_dtype ddt, void* ws, size_t ws_bytes, void* stream);
+size_t qb_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim);
+
+/*
+ * qb_layer_norm -- per row x of n rows of dim elements
+ *   mean = sum x / dim,  var = sum (x - mean)^2 / dim,  rstd = 1 / sqrt(var + eps),
+ *   y = xdt((x - mean) * rstd * gamma + beta).
+ *   x, y         [n, dim] of dtype xdt.
+ *   gamma, beta  [dim] of dtype wdt, each may be NULL (ones, zeros).  wdt is
+ *                QB_F32 or xdt (else QB_EUNSUPPORTED).
+ *   eps          positive and finite in binary32.
+ *   mean, rstd   [n] fp32 out, each may be NULL; qb_layer_norm_backward takes them.
+ * One kernel.
+ */
+qb_status qb_layer_norm(const void* x, qb_dtype xdt, int64_t n, int64_t dim, const void* gamma, const void* beta,
+                        qb_dtype wdt, double eps, void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * qb_layer_norm_backward -- with h = (x - mean) * rstd and g = dy * gamma:
+ *   dx = rstd * (g - (sum g) / dim - h * (sum g h) / dim)   per row,
+ *   dgamma = sum over rows of dy * h,  dbeta = sum over rows of dy.
+ *   dy, x, dx      [n, dim] of dtype xdt.      mean, rstd  [n] as qb_layer_norm wrote them.
+ *   gamma          [dim] of dtype wdt, or NULL (ones).
+ *   dx, dgamma, dbeta   each may be NULL (not wanted); dgamma, dbeta [dim] of
+ *                  dtype wdt.
+ *   accumulate     applies to dgamma and dbeta; dx is overwritten.
+ *   ws             device workspace of qb_layer_norm_workspace_bytes(n, dim)
+ *                  bytes, 16-byte aligned; needed for dgamma or dbeta only.
+ * Two kernels (dx alone: one; rows over 16384 elements: three).
+ */
+qb_status qb_layer_norm_backward(const void* dy, const void* x, qb_dtype xdt, int64_t n, int64_t dim,
+                                 const void* gamma, qb_dtype wdt, const float* mean, const float* rstd, void* dx,
+                                 void* dgamma, void* dbeta, int32_t accumulate, void* ws, size_t ws_bytes,
+                                 void* stream);
+size_t qb_layer_norm_workspace_bytes(int64_t n, int64_t dim);
+
+/*
+ * qb_stable_embedding -- layer norm of an embedding's rows in one kernel:
+ * y[t] = ydt(layer_norm(scale * table[ids[t]])), the lookup in binary32 (not
+ * rounded in between).  Arguments as qb_embedding and qb_layer_norm; wdt is
+ * QB_F32 or tdt, and dim at most 16384 (else QB_EUNSUPPORTED).  The row of an id
+ * outside the table is zero (beta is not added).
+ */
+qb_status qb_stable_embedding(const void* table, qb_dtype tdt, int64_t rows, int64_t dim, const void* ids,
+                              qb_index idt, int64_t n, double scale, const void* gamma, const void* beta, qb_dtype wdt,
+                              double eps, void* y, qb_dtype ydt, void* stream);
+
+/*
+ * qb_stable_embedding_backward -- the gradients of qb_stable_embedding.  The
+ * tokens of an id v share their row and its statistics, so with S_v = sum of
+ * dy[t] over them, h the normalized row and g = S_v * gamma:
+ *   dtable[v] = scale * rstd * (g - (sum g) / dim - h * (sum g h) / dim),
+ *   dgamma = sum over ids of S_v * h,  dbeta = sum over ids of S_v.
+ * The statistics are taken anew from the table, which must hold what the
+ * forward call read.
+ *   padding_id   an id whose table row takes no gradient (its tokens still
+ *                count in dgamma and dbeta); -1 for none.
+ *   dgamma, dbeta   [dim] of dtype wdt, each may be NULL.
+ *   ws           device workspace of qb_stable_embedding_workspace_bytes(n, rows,
+ *                dim) bytes, as for qb_embedding_backward.
+ * Other arguments as qb_embedding_backward and qb_stable_embedding.  Four kernels.
+ */
+qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void* table, qb_dtype tdt, int64_t rows,
+                                       int64_t dim, const void* ids, qb_index idt, int64_t n, double scale,
+                                       const void* gamma, qb_dtype wdt, double eps, int64_t padding_id,
+                                       int32_t accumulate, void* dtable, qb_dtype ddt, void* dgamma, void* dbeta,
+                                       void* ws, size_t ws_bytes, void* stream);
+size_t qb_stable_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim);
 
 /*
  * qb_codebook -- host: copy the decode table of `code` (indexed by stored code)
