@@ -388,8 +388,30 @@ def qb_multi_tensor_dequantize(table, count, code, blocksize, blocksize2, ydt, w
 # ---------------------------------------------------------------------------
 # Row-wise layers.  These take the sizes from the tensors, so the shapes are
 # checked here; ids (int32 or int64) and the leading dimensions of the token
-# arrays may have any shape, as long as the token counts agree.
+# arrays may have any shape, as long as the token counts agree.  The tensors of
+# a call share a device, which need not be the current one; the default stream
+# is torch's current stream of that device.  A decoding step is a few
+# microseconds on the GPU, so the checks are kept cheap (one call of each
+# tensor method).
 # ---------------------------------------------------------------------------
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _at(t, device):
+    """Data pointer of a contiguous tensor on `device`, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("torch tensor expected")
+    d = t.get_device()
+    if d != device or d < 0:
+        raise ValueError("device tensor expected" if d < 0 or device < 0 else f"tensors on devices {device} and {d}")
+    if not t.is_contiguous():
+        raise ValueError("contiguous tensor expected")
+    return t.data_ptr()
+
 
 def _index(ids):
     try:
@@ -398,72 +420,81 @@ def _index(ids):
         raise TypeError(f"ids must be int32 or int64, not {ids.dtype}") from None
 
 
-def _matrix(t, name):
-    if t.dim() < 1 or t.shape[-1] == 0:
-        raise ValueError(f"{name}: rows of at least one element expected")
-    return t.numel() // t.shape[-1], t.shape[-1]
+def _tokens(t, dim, name, ids=None):
+    """Rows of a token array, whose last dimension must be `dim`, one per id."""
+    shape = t.shape
+    if dim == 0 or shape[-1] != dim:
+        raise ValueError(f"{name} with rows of {dim} (at least one) elements expected")
+    n = t.numel() // dim
+    if ids is not None and ids.numel() != n:
+        raise ValueError(f"{name} of {ids.numel()} rows expected")
+    return n
 
 
-def _expect(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _table(t, name):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} of [rows, dim] expected")
+    return shape
 
 
-def _same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-
-
-def _row_stream(stream, t):
-    """The stream argument, or torch's current stream of the tensor's device."""
-    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else _stream(stream)
-
-
-def _row_call(name, t, *args):
-    """Calls an entry point with the tensor's device current (kernels start on the current device)."""
-    f = getattr(lib(), name)
-    if t.device.index == torch.cuda.current_device():
-        status = f(*args)
-    else:
-        with torch.cuda.device(t.device):
-            status = f(*args)
-    _check(status, name)
-
-
-def _norm_weights(dim, wdt_default, *weights):
+def _weights_dtype(dim, default, *weights):
     """The dtype shared by the norm's weights (and their gradients)."""
-    wdt = None
+    dtype = None
     for w in weights:
         if w is not None:
-            _expect(w.numel() == dim, f"norm weights of {dim} elements expected")
-            _expect(wdt is None or w.dtype == wdt, "the norm's weights and their gradients must share a dtype")
-            wdt = w.dtype
-    return wdt_default if wdt is None else _DTYPE.get(wdt, -1)
+            if w.numel() != dim:
+                raise ValueError(f"norm weights of {dim} elements expected")
+            if dtype is None:
+                dtype = w.dtype
+            elif w.dtype != dtype:
+                raise ValueError("the norm's weights and their gradients must share a dtype")
+    if dtype is None:
+        return default
+    try:
+        return _DTYPE[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {dtype}") from None
+
+
+def _row_call(name, device, stream, *args):
+    """Calls an entry point with the tensors' device current (kernels start on the current device)."""
+    f = getattr(_lib, name)
+    s = _raw_stream(device) if stream is None else _stream(stream)
+    if device == torch.cuda.current_device():
+        status = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, s)
+    if status != QB_OK:
+        raise QbError(status, name)
 
 
 def qb_embedding(table, ids, y, scale=1.0, stream=None):
     """y[t] = scale * table[ids[t]]; zero rows for ids outside the table."""
-    rows, dim = _matrix(table, "table")
-    n, ydim = _matrix(y, "y")
-    _expect(ydim == dim and n == ids.numel(), f"y of [{ids.numel()}, {dim}] expected")
-    _same_device(y, table, ids)
-    _row_call("qb_embedding", y, _ptr(table), _dtype(table), rows, dim, _ptr(ids), _index(ids), n, float(scale),
-              _ptr(y), _dtype(y), _row_stream(stream, y))
+    lib()
+    rows, dim = _table(table, "table")
+    n = _tokens(y, dim, "y", ids)
+    d = y.get_device()
+    _row_call("qb_embedding", d, stream, _at(table, d), _dtype(table), rows, dim, _at(ids, d), _index(ids), n, scale,
+              _at(y, d), _dtype(y))
 
 
 def qb_dequant_embedding(codes, absmax, dq, code, blocksize, rows, ids, y, scale=1.0, stream=None):
     """qb_embedding from a quantized table of `rows` rows of y.shape[-1]
     elements (codes and absmax or dq as for qb_dequantize)."""
-    n, dim = _matrix(y, "y")
-    _expect(n == ids.numel(), f"y of [{ids.numel()}, dim] expected")
-    total, nb = int(rows) * dim, -(-int(rows) * dim // max(int(blocksize), 1))
-    _expect(codes.numel() >= (total if code == QB_DYN8 else (total + 1) // 2), "codes of the whole table expected")
-    _expect(absmax is None or absmax.numel() >= nb, f"absmax of {nb} blocks expected")
-    _same_device(y, codes, absmax, ids)
-    _row_call("qb_dequant_embedding", y, _ptr(codes), _ptr(absmax), ctypes.byref(dq) if dq is not None else None,
-              int(code), int(blocksize), int(rows), dim, _ptr(ids), _index(ids), n, float(scale), _ptr(y), _dtype(y),
-              _row_stream(stream, y))
+    lib()
+    dim = y.shape[-1]
+    n = _tokens(y, dim, "y", ids)
+    total = rows * dim
+    if codes.numel() < (total if code == QB_DYN8 else (total + 1) // 2):
+        raise ValueError("codes of the whole table expected")
+    if absmax is not None and absmax.numel() * blocksize < total:
+        raise ValueError(f"absmax of {-(-total // blocksize)} blocks expected")
+    d = y.get_device()
+    _row_call("qb_dequant_embedding", d, stream, _at(codes, d), _at(absmax, d),
+              ctypes.byref(dq) if dq is not None else None, code, blocksize, rows, dim, _at(ids, d), _index(ids), n,
+              scale, _at(y, d), _dtype(y))
 
 
 def qb_embedding_workspace_bytes(n, rows, dim):
@@ -472,26 +503,38 @@ def qb_embedding_workspace_bytes(n, rows, dim):
 
 def qb_embedding_backward(dy, ids, dtable, ws, scale=1.0, padding_id=-1, accumulate=False, stream=None):
     """dtable[v] = scale * the sum of dy[t] over the tokens with ids[t] = v."""
-    rows, dim = _matrix(dtable, "dtable")
-    n, gdim = _matrix(dy, "dy")
-    _expect(gdim == dim and n == ids.numel(), f"dy of [{ids.numel()}, {dim}] expected")
-    _same_device(dtable, dy, ids, ws)
-    _row_call("qb_embedding_backward", dtable, _ptr(dy), _dtype(dy), _ptr(ids), _index(ids), n, rows, dim,
-              float(scale), int(padding_id), int(accumulate), _ptr(dtable), _dtype(dtable), _ptr(ws),
-              ws.numel() * ws.element_size(), _row_stream(stream, dtable))
+    lib()
+    rows, dim = _table(dtable, "dtable")
+    n = _tokens(dy, dim, "dy", ids)
+    d = dtable.get_device()
+    _row_call("qb_embedding_backward", d, stream, _at(dy, d), _dtype(dy), _at(ids, d), _index(ids), n, rows, dim, scale,
+              padding_id, accumulate, _at(dtable, d), _dtype(dtable), _at(ws, d), ws.numel() * ws.element_size())
+
+
+def _statistics(n, *stats):
+    for t in stats:
+        if t is not None and (t.numel() != n or t.dtype != torch.float32):
+            raise ValueError(f"{n} fp32 statistics expected")
+
+
+def _like(t, x, name):
+    if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+        raise ValueError(f"{name} like x expected")
 
 
 def qb_layer_norm(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
     """Layer norm of the last dimension of x (gamma, beta: [dim] or None; mean,
     rstd: fp32 outputs or None)."""
-    n, dim = _matrix(x, "x")
-    _expect(y.shape == x.shape and y.dtype == x.dtype, "y like x expected")
-    for t in (mean, rstd):
-        _expect(t is None or (t.numel() == n and t.dtype == torch.float32), f"{n} fp32 statistics expected")
-    wdt = _norm_weights(dim, _dtype(x), gamma, beta)
-    _same_device(x, gamma, beta, y, mean, rstd)
-    _row_call("qb_layer_norm", x, _ptr(x), _dtype(x), n, dim, _ptr(gamma), _ptr(beta), wdt, float(eps), _ptr(y),
-              _ptr(mean), _ptr(rstd), _row_stream(stream, x))
+    lib()
+    dim = x.shape[-1]
+    n = _tokens(x, dim, "x")
+    _like(y, x, "y")
+    _statistics(n, mean, rstd)
+    xdt = _dtype(x)
+    wdt = _weights_dtype(dim, xdt, gamma, beta)
+    d = x.get_device()
+    _row_call("qb_layer_norm", d, stream, _at(x, d), xdt, n, dim, _at(gamma, d), _at(beta, d), wdt, eps, _at(y, d),
+              _at(mean, d), _at(rstd, d))
 
 
 def qb_layer_norm_workspace_bytes(n, dim):
@@ -501,27 +544,30 @@ def qb_layer_norm_workspace_bytes(n, dim):
 def qb_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws=None, accumulate=False, stream=None):
     """dx, dgamma, dbeta (each may be None) from the forward call's x, mean and
     rstd; ws is needed for dgamma or dbeta."""
-    n, dim = _matrix(x, "x")
-    _expect(dy.shape == x.shape and dy.dtype == x.dtype, "dy like x expected")
-    _expect(dx is None or (dx.shape == x.shape and dx.dtype == x.dtype), "dx like x expected")
-    for t in (mean, rstd):
-        _expect(t.numel() == n and t.dtype == torch.float32, f"{n} fp32 statistics expected")
-    wdt = _norm_weights(dim, _dtype(x), gamma, dgamma, dbeta)
-    _same_device(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, ws)
-    _row_call("qb_layer_norm_backward", x, _ptr(dy), _ptr(x), _dtype(x), n, dim, _ptr(gamma), wdt, _ptr(mean),
-              _ptr(rstd), _ptr(dx), _ptr(dgamma), _ptr(dbeta), int(accumulate), _ptr(ws),
-              0 if ws is None else ws.numel() * ws.element_size(), _row_stream(stream, x))
+    lib()
+    dim = x.shape[-1]
+    n = _tokens(x, dim, "x")
+    _like(dy, x, "dy")
+    _like(dx, x, "dx")
+    _statistics(n, mean, rstd)
+    xdt = _dtype(x)
+    wdt = _weights_dtype(dim, xdt, gamma, dgamma, dbeta)
+    d = x.get_device()
+    _row_call("qb_layer_norm_backward", d, stream, _at(dy, d), _at(x, d), xdt, n, dim, _at(gamma, d), wdt, _at(mean, d),
+              _at(rstd, d), _at(dx, d), _at(dgamma, d), _at(dbeta, d), accumulate, _at(ws, d),
+              0 if ws is None else ws.numel() * ws.element_size())
 
 
 def qb_stable_embedding(table, ids, gamma, beta, eps, y, scale=1.0, stream=None):
     """y[t] = layer norm of scale * table[ids[t]]; zero rows for ids outside the table."""
-    rows, dim = _matrix(table, "table")
-    n, ydim = _matrix(y, "y")
-    _expect(ydim == dim and n == ids.numel(), f"y of [{ids.numel()}, {dim}] expected")
-    wdt = _norm_weights(dim, _dtype(table), gamma, beta)
-    _same_device(y, table, ids, gamma, beta)
-    _row_call("qb_stable_embedding", y, _ptr(table), _dtype(table), rows, dim, _ptr(ids), _index(ids), n,
-              float(scale), _ptr(gamma), _ptr(beta), wdt, float(eps), _ptr(y), _dtype(y), _row_stream(stream, y))
+    lib()
+    rows, dim = _table(table, "table")
+    n = _tokens(y, dim, "y", ids)
+    tdt = _dtype(table)
+    wdt = _weights_dtype(dim, tdt, gamma, beta)
+    d = y.get_device()
+    _row_call("qb_stable_embedding", d, stream, _at(table, d), tdt, rows, dim, _at(ids, d), _index(ids), n, scale,
+              _at(gamma, d), _at(beta, d), wdt, eps, _at(y, d), _dtype(y))
 
 
 def qb_stable_embedding_workspace_bytes(n, rows, dim):
@@ -531,16 +577,17 @@ def qb_stable_embedding_workspace_bytes(n, rows, dim):
 def qb_stable_embedding_backward(dy, table, ids, gamma, eps, dtable, dgamma, dbeta, ws, scale=1.0, padding_id=-1,
                                  accumulate=False, stream=None):
     """dtable, dgamma and dbeta (the latter two may be None) of qb_stable_embedding."""
-    rows, dim = _matrix(table, "table")
-    n, gdim = _matrix(dy, "dy")
-    _expect(gdim == dim and n == ids.numel(), f"dy of [{ids.numel()}, {dim}] expected")
-    _expect(dtable.shape == table.shape, "dtable like table expected")
-    wdt = _norm_weights(dim, _dtype(table), gamma, dgamma, dbeta)
-    _same_device(dtable, dy, table, ids, gamma, dgamma, dbeta, ws)
-    _row_call("qb_stable_embedding_backward", dtable, _ptr(dy), _dtype(dy), _ptr(table), _dtype(table), rows, dim,
-              _ptr(ids), _index(ids), n, float(scale), _ptr(gamma), wdt, float(eps), int(padding_id),
-              int(accumulate), _ptr(dtable), _dtype(dtable), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
-              ws.numel() * ws.element_size(), _row_stream(stream, dtable))
+    lib()
+    rows, dim = _table(table, "table")
+    n = _tokens(dy, dim, "dy", ids)
+    if dtable.shape != table.shape:
+        raise ValueError("dtable like table expected")
+    tdt = _dtype(table)
+    wdt = _weights_dtype(dim, tdt, gamma, dgamma, dbeta)
+    d = dtable.get_device()
+    _row_call("qb_stable_embedding_backward", d, stream, _at(dy, d), _dtype(dy), _at(table, d), tdt, rows, dim,
+              _at(ids, d), _index(ids), n, scale, _at(gamma, d), wdt, eps, padding_id, accumulate, _at(dtable, d),
+              _dtype(dtable), _at(dgamma, d), _at(dbeta, d), _at(ws, d), ws.numel() * ws.element_size())
 
 
 def qb_code_table_bytes():

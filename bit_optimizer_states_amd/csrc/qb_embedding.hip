@@ -4,12 +4,14 @@
 // Lookup: y_t = scale * W[id_t], one binary32 multiply and one rounding.  Bound
 // by HBM: the rows that are used are read, y is written.
 //
-// Gradient: dW[v] = scale * (sum of dy_t over the tokens t with id_t = v).  The
-// tokens are first ordered by id (k_order), so that every sum is taken by one
-// wave in ascending order of the tokens: no atomics on floating-point values,
-// the same bits on every run.  An id with more tokens than a chunk holds is summed
-// chunk by chunk by many waves (k_chunk_sums) and joined in chunk order.  The
-// last kernel writes every row of the table once, zeros included.
+// Gradient: dW[v] = scale * (sum of dy_t over the tokens t with id_t = v), in
+// three launches.  The tokens are ordered by id (k_order), so that every sum is
+// taken by one wave in ascending order of the tokens: no atomics on
+// floating-point values, the same bits on every run.  An id with more tokens than a
+// chunk holds is summed chunk by chunk by many waves, and in the same launch the
+// zero rows of the table are written, which keeps HBM busy meanwhile
+// (k_prepare_grad).  The last launch sums and writes the rows of the ids that
+// have tokens, and only those (k_table_grad).
 #include "qb_token_sums.h"
 
 namespace qb {
@@ -189,46 +191,51 @@ hipError_t dequant_embedding_y(const IdArgs& a, const DequantDesc& d, int code4,
 // order of the tokens by id
 // ---------------------------------------------------------------------------
 
-// One workgroup per class of ids (OrderArgs).  It walks all n ids twice: the
-// first time it counts its own entries, per wave (each wave owns one contiguous
-// stretch of the tokens), and the tokens of lower classes, whose number is where
-// its part of the list begins; the second time it places its tokens.  A wave
+// One workgroup per class of ids (OrderArgs).  It goes through all n ids twice:
+// the first time it counts its own entries, per wave (each wave owns one
+// contiguous stretch of the tokens), and the tokens of lower classes, whose number
+// is where its part of the list begins; the second time it places its tokens.  A wave
 // takes the tokens of its stretch in order and gives equal ids of one step
 // consecutive places by their lane, so the order is stable and no workgroup waits
-// for another.  The ids are read from L2 by every workgroup: n * classes reads,
-// 5 us at 16k tokens, in exchange for one launch and no atomics in memory.
+// for another.  The ids are read from L2 by every workgroup, n * classes reads in
+// exchange for one launch and no atomics in memory; up to 16384 tokens a wave
+// keeps its stretch in registers for the second time.
 template <bool ID64>
 __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs o)
 {
     extern __shared__ int32_t s_cnt[];                 // [kOrderWaves][per]
-    __shared__ int32_t s_below[kOrderWaves], s_wave[kOrderWaves];
-    constexpr int UN = 8;                              // loads in flight per lane
+    __shared__ int32_t s_below[kOrderWaves], s_wave[kOrderWaves], s_used[2][kOrderWaves];
+    constexpr int UN = 16;                             // loads in flight per lane
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     const int32_t cls = (int32_t)blockIdx.x, mask = (1 << o.log2g) - 1, per = o.per;
-    for (int i = threadIdx.x; i < kOrderWaves * per; i += kOrderWaves * 64) s_cnt[i] = 0;
-    __syncthreads();
 
     const int64_t stretch = ((a.n + kOrderWaves - 1) / kOrderWaves + 63) / 64 * 64;
     const int64_t first = wave * stretch;
     const int64_t last = first + stretch < a.n ? first + stretch : a.n;
     int32_t* const cnt = s_cnt + wave * per;
-    // id of token t, or -1 beyond the stretch or outside the table
-    auto id_at = [&](int64_t t) -> int32_t {
-        if (t >= last) return -1;
-        if constexpr (ID64) {
-            const int64_t id = gld<int64_t>(static_cast<const int64_t*>(a.ids) + t);
-            return (uint64_t)id < (uint64_t)a.rows ? (int32_t)id : -1;
-        } else {
-            const int32_t id = gld<int32_t>(static_cast<const int32_t*>(a.ids) + t);
-            return (uint64_t)(int64_t)id < (uint64_t)a.rows ? id : -1;
+    // ids of the tokens t0 + k * 64 + lane; -1 beyond the stretch or outside the table
+    int32_t id[UN];
+    auto load_ids = [&](int64_t t0) {
+        int64_t raw[UN];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            const int64_t t = t0 + k * 64 + lane;
+            const int64_t at = t < last ? t : last - 1;
+            if constexpr (ID64) raw[k] = gld<int64_t>(static_cast<const int64_t*>(a.ids) + at);
+            else raw[k] = gld<int32_t>(static_cast<const int32_t*>(a.ids) + at);
         }
+#pragma unroll
+        for (int k = 0; k < UN; ++k)
+            id[k] = t0 + k * 64 + lane < last && (uint64_t)raw[k] < (uint64_t)a.rows ? (int32_t)raw[k] : -1;
     };
+    const bool once = stretch <= 64 * UN;              // uniform: the stretch fits in registers
+    if (once && first < last) load_ids(first);
+    for (int i = threadIdx.x; i < kOrderWaves * per; i += kOrderWaves * 64) s_cnt[i] = 0;
+    __syncthreads();
 
     int32_t below = 0;
     for (int64_t t0 = first; t0 < last; t0 += 64 * UN) {
-        int32_t id[UN];
-#pragma unroll
-        for (int k = 0; k < UN; ++k) id[k] = id_at(t0 + k * 64 + lane);
+        if (!once) load_ids(t0);
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
             if (id[k] >= 0) {
@@ -255,7 +262,12 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
         const int32_t up = __shfl_up(incl, step);
         if (lane >= step) incl += up;
     }
-    if (lane == 63) s_wave[wave] = incl;
+    const unsigned long long some = __ballot(total > 0), many = __ballot(total > o.chunk);
+    if (lane == 63) {
+        s_wave[wave] = incl;
+        s_used[0][wave] = (int32_t)__popcll(some);
+        s_used[1][wave] = (int32_t)__popcll(many);
+    }
     __syncthreads();
     int32_t before = 0;
     for (int w = 0; w < wave; ++w) before += s_wave[w];
@@ -269,12 +281,15 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
         }
         if (cls == mask && j == per - 1) o.start[((int64_t)cls + 1) * per] = run;
     }
+    if (j < 2) {
+        int32_t used = 0;
+        for (int w = 0; w < kOrderWaves; ++w) used += s_used[j][w];
+        o.used[2 * (int64_t)cls + j] = used;
+    }
     __syncthreads();
 
     for (int64_t t0 = first; t0 < last; t0 += 64 * UN) {
-        int32_t id[UN];
-#pragma unroll
-        for (int k = 0; k < UN; ++k) id[k] = id_at(t0 + k * 64 + lane);
+        if (!once) load_ids(t0);
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
             const bool mine = id[k] >= 0 && (id[k] & mask) == cls;
@@ -298,19 +313,50 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
 // gradient of the table
 // ---------------------------------------------------------------------------
 
-// One wave per chunk and 64 units.  Of a chunk's tokens only the first and the
-// last id can have more tokens than a chunk.
-template <int GDT, bool TAIL>
-__global__ __launch_bounds__(256) void k_chunk_sums(IdArgs a, OrderArgs o, const void* __restrict__ dy,
-                                                    float* __restrict__ part, int32_t chunk, int32_t slices)
+// The lists of used and of long ids: one wave per class, which begins where the
+// lower classes' counts end.
+__device__ __forceinline__ void list_used(const OrderArgs& o, int64_t cls)
 {
     const int lane = threadIdx.x % 64;
-    const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int32_t c = (int32_t)(w / slices), unit = (int32_t)(w % slices) * 64 + lane;
+    const int64_t classes = int64_t(1) << o.log2g;
+    if (cls >= classes) return;
+    int32_t base = 0, lbase = 0;
+    for (int64_t c = lane; c < cls; c += 64) {
+        const u32x2 u = gld<u32x2>(o.used + 2 * c);
+        base += (int32_t)u.x;
+        lbase += (int32_t)u.y;
+    }
+    for (int step = 1; step < 64; step *= 2) {
+        base += __shfl_xor(base, step);
+        lbase += __shfl_xor(lbase, step);
+    }
+    const int32_t* const start = o.start + cls * o.per;
+    for (int32_t e0 = 0; e0 < o.per; e0 += 64) {
+        const int32_t e = e0 + lane;
+        const int32_t k = e < o.per ? gld<int32_t>(start + e + 1) - gld<int32_t>(start + e) : 0;
+        const unsigned long long some = __ballot(k > 0), many = __ballot(k > o.chunk), below = (1ull << lane) - 1;
+        const int32_t v = (int32_t)(((int64_t)e << o.log2g) + cls);
+        if (k > 0) o.list[base + __popcll(some & below)] = v;
+        if (k > o.chunk) o.longs[lbase + __popcll(many & below)] = v;
+        base += (int32_t)__popcll(some);
+        lbase += (int32_t)__popcll(many);
+    }
+    if (cls == classes - 1 && lane == 0) {
+        o.count[0] = base;
+        o.count[1] = lbase;
+    }
+}
+
+// One wave: a chunk's tokens, 64 units.  Only the first and the last id of a chunk
+// can have more tokens than a chunk.
+template <int GDT, bool TAIL>
+__device__ __forceinline__ void chunk_sums(const IdArgs& a, const OrderArgs& o, const void* dy, float* part,
+                                           int64_t c, int unit)
+{
+    const int32_t chunk = o.chunk;
     const int32_t found = o.start[(int64_t(1) << o.log2g) * o.per];        // tokens inside the table
-    const int64_t begin = (int64_t)c * chunk;
-    if (begin >= found) return;
-    const int32_t b = (int32_t)begin, e = found - b < chunk ? found : b + chunk;
+    if (c * chunk >= found) return;
+    const int32_t b = (int32_t)(c * chunk), e = found - b < chunk ? found : b + chunk;
     const int dim = a.dim, units = (dim + 7) >> 3;
     const int64_t padded = (int64_t)units * 8;
     int64_t before = -1;
@@ -322,66 +368,156 @@ __global__ __launch_bounds__(256) void k_chunk_sums(IdArgs a, OrderArgs o, const
         const int64_t s = slot_of(v, o);
         const int32_t v0 = o.start[s], v1 = o.start[s + 1];
         if (v1 - v0 <= chunk) continue;
-        float sum[8] = {};
-        sum_tokens<GDT, TAIL, 8>(o.order, v0 > b ? v0 : b, v1 < e ? v1 : e, dy, unit, units, dim, sum);
+        float sums[1][8] = {};
+        sum_tokens<GDT, TAIL, 64, 1, 8>(o.order, v0 > b ? v0 : b, v1 < e ? v1 : e, dy, unit, units, dim, sums);
+        const float(&sum)[8] = sums[0];
         if (unit < units) {
-            float* const p = part + (2 * (int64_t)c + (v0 > b ? 1 : 0)) * padded + (int64_t)unit * 8;
+            float* const p = part + (2 * c + (v0 > b ? 1 : 0)) * padded + (int64_t)unit * 8;
             gst<f32x4>(p, f32x4{sum[0], sum[1], sum[2], sum[3]});
             gst<f32x4>(p + 4, f32x4{sum[4], sum[5], sum[6], sum[7]});
         }
     }
 }
 
-// One wave per table row and 64 units (walking the table where a launch cannot hold as many).
+constexpr int kZeroRows = 16;           // table rows of a zero-filling workgroup
+
+template <int GDT, bool TAIL>
+__global__ __launch_bounds__(256) void k_prepare_grad(IdArgs a, OrderArgs o, const void* __restrict__ dy,
+                                                      float* __restrict__ part, int32_t slices, int32_t list_wgs,
+                                                      int32_t chunk_wgs, int64_t pad,
+                                                      void* __restrict__ dtable, int ddt)
+{
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    int64_t wg = blockIdx.x;
+    if (wg < list_wgs) {
+        list_used(o, wg * 4 + wave);
+        return;
+    }
+    wg -= list_wgs;
+    if (wg < chunk_wgs) {
+        const int64_t w = wg * 4 + wave;
+        chunk_sums<GDT, TAIL>(a, o, dy, part, w / slices, (int)(w % slices) * 64 + lane);
+        return;
+    }
+    // zero rows, walking the table where a launch cannot hold as many workgroups
+    wg -= chunk_wgs;
+    const int dim = a.dim, units = (dim + 7) >> 3;
+    const int64_t step = (int64_t)gridDim.x - list_wgs - chunk_wgs;
+    const float zero[8] = {};
+    for (int64_t v0 = wg * kZeroRows; v0 < a.rows; v0 += step * kZeroRows) {
+        const int64_t mine = v0 + lane;
+        bool empty = false;
+        if (lane < kZeroRows && mine < a.rows) {
+            const int64_t s = slot_of(mine, o);
+            empty = mine == pad || gld<int32_t>(o.start + s) == gld<int32_t>(o.start + s + 1);
+        }
+        for (unsigned long long todo = __ballot(empty); todo; todo &= todo - 1) {
+            char* const row = static_cast<char*>(dtable) + (v0 + __builtin_ctzll(todo)) * dim * (ddt == DT_F32 ? 4 : 2);
+            for (int unit = threadIdx.x; unit < units; unit += 256)
+                store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, zero);
+        }
+    }
+}
+
+// Joined sums of the long ids, 64 columns a wave, into the slot of the first
+// chunk (which no other wave reads in these columns).
+__global__ __launch_bounds__(256) void k_join_chunks(OrderArgs o, float* __restrict__ part, int64_t padded)
+{
+    const int lane = threadIdx.x % 64;
+    const int64_t groups = (padded + 63) / 64, tasks = (int64_t)o.count[1] * groups;
+    for (int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64); w < tasks;
+         w += (int64_t)gridDim.x * 4) {
+        const int64_t s = slot_of(o.longs[w / groups], o), col = w % groups * 64 + lane;
+        const int32_t first = o.start[s], last = o.start[s + 1];
+        if (col < padded)
+            part[chunk_slot(first / o.chunk, first, o.chunk) * padded + col] =
+                join_column(part, o.chunk, first, last, padded, col);
+    }
+}
+
+// Long ids first, one wave per 64 columns; then the other listed ids, one wave
+// per id and 64 units.  A wave looks its next 64 ids up at once (lane l the
+// l-th).
 template <int GDT, bool TAIL>
 __global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, const void* __restrict__ dy,
-                                                    const float* __restrict__ part, int32_t chunk, int32_t slices,
-                                                    float scale, int64_t pad, int accumulate, void* __restrict__ dtable,
-                                                    int ddt)
+                                                    const float* __restrict__ part, int32_t slices, float scale,
+                                                    int64_t pad, int accumulate, void* __restrict__ dtable, int ddt)
 {
     const int lane = threadIdx.x % 64;
     const int dim = a.dim, units = (dim + 7) >> 3;
-    for (int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64); w < a.rows * slices;
-         w += (int64_t)gridDim.x * 4) {
-        const int64_t v = w / slices;
-        const int unit = (int)(w % slices) * 64 + lane;
-        const int64_t s = slot_of(v, o);
-        const int32_t v0 = o.start[s], v1 = v == pad ? v0 : o.start[s + 1];
-        if (accumulate && v0 == v1) continue;
-        float sum[8] = {};
-        if (v1 - v0 > chunk) sum_chunks<8>(part, chunk, v0, v1, unit, units, (int64_t)units * 8, sum);
-        else sum_tokens<GDT, TAIL, 4>(o.order, v0, v1, dy, unit, units, dim, sum);
+    const int64_t padded = (int64_t)units * 8;
+    const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t step = (int64_t)gridDim.x * 4;
+    const int64_t groups = (dim + 63) / 64, joins = (int64_t)o.count[1] * groups;
+    for (int64_t w = wave; w < joins; w += step) {
+        const int64_t v = o.longs[w / groups], s = slot_of(v, o), col = w % groups * 64 + lane;
+        if (v == pad || col >= dim) continue;
+        float sum = join_column(part, o.chunk, o.start[s], o.start[s + 1], padded, col) * scale;
         char* const row = static_cast<char*>(dtable) + v * dim * (ddt == DT_F32 ? 4 : 2);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] *= scale;
-        if (accumulate) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < unit_count(unit, dim)) sum[j] += load1_rt(ddt, row, (int64_t)unit * 8 + j);
+        if (accumulate) sum += load1_rt(ddt, row, col);
+        store1_rt(ddt, row, col, sum);
+    }
+    const int64_t tasks = (int64_t)o.count[0] * slices;
+    for (int64_t w0 = wave; w0 < tasks; w0 += 64 * step) {
+        const int64_t mine = w0 + lane * step;
+        int32_t id = 0, lo = 0, hi = 0;
+        if (mine < tasks) {
+            id = gld<int32_t>(o.list + mine / slices);
+            const int64_t s = slot_of(id, o);
+            lo = gld<int32_t>(o.start + s);
+            hi = gld<int32_t>(o.start + s + 1);
         }
-        store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, sum);
+        for (int i = 0; i < 64 && w0 + i * step < tasks; ++i) {
+            const int64_t v = __builtin_amdgcn_readlane(id, i);
+            const int32_t first = __builtin_amdgcn_readlane(lo, i), last = __builtin_amdgcn_readlane(hi, i);
+            if (v == pad || last - first > o.chunk) continue;
+            const int unit = (int)((w0 + i * step) % slices) * 64 + lane;
+            float sums[1][8] = {};
+            float(&sum)[8] = sums[0];
+            sum_tokens<GDT, TAIL, 64, 1, 8>(o.order, first, last, dy, unit, units, dim, sums);
+            char* const row = static_cast<char*>(dtable) + v * dim * (ddt == DT_F32 ? 4 : 2);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] *= scale;
+            if (accumulate) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < unit_count(unit, dim)) sum[j] += load1_rt(ddt, row, (int64_t)unit * 8 + j);
+            }
+            store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, sum);
+        }
     }
 }
 
 template <int GDT>
-hipError_t chunk_sums_as(const IdArgs& a, const OrderArgs& o, const void* dy, float* part, hipStream_t s)
+hipError_t prepare_grad_as(const IdArgs& a, const OrderArgs& o, const void* dy, float* part, int64_t pad,
+                           bool accumulate, void* dtable, int ddt, hipStream_t s)
 {
     const int32_t slices = (a.dim + 511) / 512;
-    const int64_t grid = (chunk_count(a.n) * slices + 3) / 4;
-    if (grid >= (int64_t(1) << 24)) return hipErrorInvalidValue;
-    return a.dim % 8 ? launch_kernel(k_chunk_sums<GDT, true>, (int)grid, s, a, o, dy, part, chunk_tokens(a.n), slices)
-                     : launch_kernel(k_chunk_sums<GDT, false>, (int)grid, s, a, o, dy, part, chunk_tokens(a.n), slices);
+    const int64_t most = int64_t(1) << 22;
+    const int64_t list = ((int64_t(1) << o.log2g) + 3) / 4, chunks = (chunk_count(a.n) * slices + 3) / 4;
+    int64_t zeros = accumulate ? 0 : (a.rows + kZeroRows - 1) / kZeroRows;
+    if (chunks > most) return hipErrorInvalidValue;
+    if (zeros > most) zeros = most;
+    auto go = [&](auto kernel) {
+        return launch_kernel(kernel, (int)(list + chunks + zeros), s, a, o, dy, part, slices, (int32_t)list,
+                             (int32_t)chunks, pad, dtable, ddt);
+    };
+    return a.dim % 8 ? go(k_prepare_grad<GDT, true>) : go(k_prepare_grad<GDT, false>);
 }
+
+// 8 workgroups per CU at most: a wave of 64 units in flight needs few registers.
+constexpr int64_t kTableGradWgs = 2048;
 
 template <int GDT>
 hipError_t table_grad_as(const IdArgs& a, const OrderArgs& o, const void* dy, const float* part, float scale,
                          int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s)
 {
     const int32_t slices = (a.dim + 511) / 512;
-    const int64_t waves = (a.rows * slices + 3) / 4, most = int64_t(1) << 22;
+    // a long id has over chunk tokens and dim / 64 waves' work: never more than its tokens' own
+    const int64_t wgs = (a.n * slices + 3) / 4;
     auto go = [&](auto kernel) {
-        return launch_kernel(kernel, (int)(waves < most ? waves : most), s, a, o, dy, part, chunk_tokens(a.n), slices, scale, pad,
-                             accumulate ? 1 : 0, dtable, ddt);
+        return launch_kernel(kernel, (int)(wgs < kTableGradWgs ? wgs : kTableGradWgs), s, a, o, dy, part,
+                             slices, scale, pad, accumulate ? 1 : 0, dtable, ddt);
     };
     return a.dim % 8 ? go(k_table_grad<GDT, true>) : go(k_table_grad<GDT, false>);
 }
@@ -415,17 +551,26 @@ hipError_t launch_order(const IdArgs& a, const OrderArgs& o, hipStream_t s)
                   : launch_kernel_lds(k_order<false>, 1 << o.log2g, kOrderWaves * 64, lds, s, a, o);
 }
 
-hipError_t launch_chunk_sums(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part, hipStream_t s)
+hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part, int64_t pad,
+                               bool accumulate, void* dtable, int ddt, hipStream_t s)
 {
-    if (a.n == 0) return hipSuccess;
-    if (gdt == DT_F32) return chunk_sums_as<DT_F32>(a, o, dy, part, s);
-    if (gdt == DT_F16) return chunk_sums_as<DT_F16>(a, o, dy, part, s);
-    return chunk_sums_as<DT_BF16>(a, o, dy, part, s);
+    if (gdt == DT_F32) return prepare_grad_as<DT_F32>(a, o, dy, part, pad, accumulate, dtable, ddt, s);
+    if (gdt == DT_F16) return prepare_grad_as<DT_F16>(a, o, dy, part, pad, accumulate, dtable, ddt, s);
+    return prepare_grad_as<DT_BF16>(a, o, dy, part, pad, accumulate, dtable, ddt, s);
+}
+
+hipError_t launch_join_chunks(const IdArgs& a, const OrderArgs& o, float* part, hipStream_t s)
+{
+    if (a.n <= o.chunk) return hipSuccess;             // no id can have more tokens than a chunk
+    const int64_t padded = padded_dim(a.dim);
+    const int64_t wgs = (a.n / o.chunk * ((padded + 63) / 64) + 3) / 4;
+    return launch_kernel(k_join_chunks, (int)(wgs < kTableGradWgs ? wgs : kTableGradWgs), s, o, part, padded);
 }
 
 hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, const float* part,
                              float scale, int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s)
 {
+    if (a.n == 0) return hipSuccess;
     if (gdt == DT_F32) return table_grad_as<DT_F32>(a, o, dy, part, scale, pad, accumulate, dtable, ddt, s);
     if (gdt == DT_F16) return table_grad_as<DT_F16>(a, o, dy, part, scale, pad, accumulate, dtable, ddt, s);
     return table_grad_as<DT_BF16>(a, o, dy, part, scale, pad, accumulate, dtable, ddt, s);

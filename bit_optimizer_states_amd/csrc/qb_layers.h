@@ -26,11 +26,18 @@ struct IdArgs {
 // tokens have small ids in common vocabularies, and neighbouring ids land in
 // different classes.  start[class * per + entry] .. start[... + 1] is the range of
 // the id's tokens in `order`, which lists their positions in ascending order.
+// `list` holds the count[0] ids that have tokens, `longs` the count[1] ids that
+// have more than `chunk` of them.
 struct OrderArgs {
     int32_t* start;      // [classes * per + 1]
     int32_t* order;      // [n]
+    int32_t* used;       // [2 * classes] ids with tokens, and with more than a chunk, per class
+    int32_t* count;      // [2]
+    int32_t* list;       // [min(n, rows)]
+    int32_t* longs;      // [n / chunk + 1]
     int32_t log2g;
     int32_t per;
+    int32_t chunk;
 };
 
 constexpr int kOrderWaves = 16;            // waves of the ordering kernel
@@ -48,13 +55,14 @@ constexpr int32_t order_log2g(int64_t rows)
 constexpr int64_t order_per(int64_t rows) { return (rows + (int64_t(1) << order_log2g(rows)) - 1) >> order_log2g(rows); }
 
 // Tokens per chunk of the ordered list: an id with more tokens than this is
-// summed chunk by chunk, then joined.  About half the square root of n, so that
-// an id that holds every token takes as many steps within a chunk as in the
-// join.
+// summed chunk by chunk, then joined.
+#ifndef QB_CHUNK_MIN
+#define QB_CHUNK_MIN 32
+#endif
 constexpr int32_t chunk_tokens(int64_t n)
 {
-    int32_t c = 32;
-    while (c < 512 && (int64_t)c * c * 4 < n) c *= 2;
+    int32_t c = QB_CHUNK_MIN;
+    while (c < 512 && (int64_t)c * c * 16 < n) c *= 2;
     return c;
 }
 constexpr int64_t chunk_count(int64_t n) { return (n + chunk_tokens(n) - 1) / chunk_tokens(n); }
@@ -97,15 +105,22 @@ hipError_t launch_dequant_embedding(const IdArgs& a, const DequantDesc& t, int b
 // start, order of the ids.
 hipError_t launch_order(const IdArgs& a, const OrderArgs& o, hipStream_t s);
 
-// Sums of dy over the chunks' tokens of ids that have more tokens than a chunk:
-// part[2 * chunk] for an id whose tokens begin at or before the chunk's first,
-// part[2 * chunk + 1] for one whose tokens begin inside the chunk (rows of
-// padded_dim binary32).
-hipError_t launch_chunk_sums(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part,
-                             hipStream_t s);
+// Joins the chunks' sums of the long ids, each into the slot of its first chunk.
+hipError_t launch_join_chunks(const IdArgs& a, const OrderArgs& o, float* part, hipStream_t s);
+
+// The second step of a gradient, one launch of three kinds of workgroups:
+//  - the list of the ids that have tokens;
+//  - sums of dy over the chunks' tokens of ids that have more tokens than a
+//    chunk: part[2 * chunk] for an id whose tokens begin at or before the chunk's
+//    first, part[2 * chunk + 1] for one whose tokens begin inside the chunk (rows of
+//    padded_dim binary32);
+//  - zeros into the rows of dtable whose ids take no gradient: those without
+//    tokens, and pad (none with accumulate).
+hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part, int64_t pad,
+                               bool accumulate, void* dtable, int ddt, hipStream_t s);
 
 // dtable[v] = scale * sum of dy over the tokens of v (+ dtable[v] with
-// accumulate); pad: an id that takes no gradient, or -1.
+// accumulate) for the listed ids but pad.
 hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, const float* part,
                              float scale, int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s);
 

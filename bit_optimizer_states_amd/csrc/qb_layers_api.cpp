@@ -45,21 +45,34 @@ IdArgs id_args(const void* ids, qb_index idt, int64_t n, int64_t rows, int64_t d
 // An eps that stays positive in binary32: a row of equal values then has a finite rstd.
 bool valid_eps(double eps) { return std::isfinite(eps) && (float)eps > 0.0f && std::isfinite((float)eps); }
 
-// Workspace of a table's gradient: start, order, the chunks' sums; then (stable)
-// the partial sums of dgamma and dbeta.
+// Workspace of a table's gradient: the arrays of OrderArgs, the chunks' sums; then
+// (stable) the partial sums of dgamma and dbeta.
 struct GradLayout {
-    size_t order, chunks, parts, bytes;
+    size_t order, used, list, longs, chunks, parts, bytes;
 };
 
 GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim, int parts)
 {
     GradLayout l;
-    const int64_t entries = (order_per(rows) << order_log2g(rows)) + 1;
+    const int64_t classes = int64_t(1) << order_log2g(rows), entries = classes * order_per(rows) + 1;
     l.order = round_up((size_t)entries * sizeof(int32_t), 256);
-    l.chunks = l.order + round_up((size_t)n * sizeof(int32_t), 256);
+    l.used = l.order + round_up((size_t)n * sizeof(int32_t), 256);
+    l.list = l.used + round_up((size_t)(2 * classes + 2) * sizeof(int32_t), 256);
+    l.longs = l.list + round_up((size_t)(n < rows ? n : rows) * sizeof(int32_t), 256);
+    l.chunks = l.longs + round_up((size_t)(n / chunk_tokens(n) + 1) * sizeof(int32_t), 256);
     l.parts = l.chunks + (size_t)(2 * chunk_count(n) * padded_dim(dim)) * sizeof(float);
     l.bytes = l.parts + (size_t)parts * 2 * (size_t)padded_dim(dim) * sizeof(float);
     return l;
+}
+
+OrderArgs order_args(void* ws, const GradLayout& l, int64_t n, int64_t rows)
+{
+    char* const w = static_cast<char*>(ws);
+    int32_t* const used = reinterpret_cast<int32_t*>(w + l.used);
+    return OrderArgs{reinterpret_cast<int32_t*>(w), reinterpret_cast<int32_t*>(w + l.order), used,
+                     used + (int64_t(2) << order_log2g(rows)), reinterpret_cast<int32_t*>(w + l.list),
+                     reinterpret_cast<int32_t*>(w + l.longs), order_log2g(rows), (int32_t)order_per(rows),
+                     chunk_tokens(n)};
 }
 
 bool valid_grad_sizes(int64_t n, int64_t rows, int64_t dim)
@@ -147,14 +160,13 @@ qb_status qb_embedding_backward(const void* dy, qb_dtype gdt, const void* ids, q
     if (!aligned16(ws)) return QB_EALIGN;
     const GradLayout l = grad_layout(n, rows, dim, 0);
     if (ws_bytes < l.bytes) return QB_EWORKSPACE;
-    char* const w = static_cast<char*>(ws);
     const IdArgs a = id_args(ids, idt, n, rows, dim);
-    const OrderArgs o{reinterpret_cast<int32_t*>(w), reinterpret_cast<int32_t*>(w + l.order), order_log2g(rows),
-                      (int32_t)order_per(rows)};
-    float* const part = reinterpret_cast<float*>(w + l.chunks);
+    const OrderArgs o = order_args(ws, l, n, rows);
+    float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + l.chunks);
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = launch_order(a, o, s);
-    if (e == hipSuccess) e = launch_chunk_sums(a, o, dy, (int)gdt, part, s);
+    if (e == hipSuccess)
+        e = launch_prepare_grad(a, o, dy, (int)gdt, part, padding_id, accumulate != 0, dtable, (int)ddt, s);
     if (e == hipSuccess)
         e = launch_table_grad(a, o, dy, (int)gdt, part, (float)scale, padding_id, accumulate != 0, dtable, (int)ddt, s);
     return hip_status(e);
@@ -259,15 +271,16 @@ qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void*
     if (ws_bytes < l.bytes) return QB_EWORKSPACE;
     char* const w = static_cast<char*>(ws);
     const IdArgs a = id_args(ids, idt, n, rows, dim);
-    const OrderArgs o{reinterpret_cast<int32_t*>(w), reinterpret_cast<int32_t*>(w + l.order), order_log2g(rows),
-                      (int32_t)order_per(rows)};
+    const OrderArgs o = order_args(ws, l, n, rows);
     float* const chunks = reinterpret_cast<float*>(w + l.chunks);
     float* const part = reinterpret_cast<float*>(w + l.parts);
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = hipSuccess;
     if (rows > 0) {
         e = launch_order(a, o, s);
-        if (e == hipSuccess) e = launch_chunk_sums(a, o, dy, (int)gdt, chunks, s);
+        if (e == hipSuccess)
+            e = launch_prepare_grad(a, o, dy, (int)gdt, chunks, padding_id, accumulate != 0, dtable, (int)ddt, s);
+        if (e == hipSuccess) e = launch_join_chunks(a, o, chunks, s);
         if (e == hipSuccess)
             e = launch_stable_grad(a, o, dy, (int)gdt, chunks, table, (int)tdt, (float)scale,
                                    NormArgs{gamma, nullptr, (int)wdt, (float)eps}, padding_id, accumulate != 0, dtable,

@@ -4,6 +4,12 @@
 #include "qb_device.h"
 #include "qb_layers.h"
 
+#ifndef QB_NT32L
+#define QB_NT32L 0
+#endif
+#ifndef QB_NT32S
+#define QB_NT32S 0
+#endif
 namespace qb {
 
 // Rows start at any multiple of the element size (dim may be odd), so units are
@@ -30,7 +36,7 @@ __device__ __forceinline__ Unit<DT> load_unit8(const void* row, int64_t elem)
     for (int h = 0; h < (DT == DT_F32 ? 2 : 1); ++h) {
         const QB_G u32x4_a2* q = (const QB_G u32x4_a2*)(p + 16 * h);
         u32x4 v;
-        if constexpr (NT) v = __builtin_nontemporal_load(q);
+        if constexpr (NT && (DT != DT_F32 || QB_NT32L)) v = __builtin_nontemporal_load(q);
         else v = *q;
         u.w[4 * h] = v.x; u.w[4 * h + 1] = v.y; u.w[4 * h + 2] = v.z; u.w[4 * h + 3] = v.w;
     }
@@ -62,20 +68,40 @@ __device__ __forceinline__ Unit<DT> load_part8(const void* row, int64_t elem, in
     return u;
 }
 
-// Unit number `unit` of a row of `dim` elements.  TAIL: dim is no multiple of 8,
-// so the last unit is partial.  A unit beyond the row (unit >= ceil(dim / 8))
-// reads unit 0 instead (its caller masks it), so that no load is under a branch
-// where there is no tail.
+// Elements `by` (0 .. 7) and up of a unit, moved to the front; zeros follow.
+template <int DT>
+__device__ __forceinline__ void shift_unit(Unit<DT>& u, int by)
+{
+    constexpr int W = DT == DT_F32 ? 8 : 4;
+    const int words = DT == DT_F32 ? by : by >> 1;
+#pragma unroll
+    for (int step = W / 2; step > 0; step /= 2)
+#pragma unroll
+        for (int j = 0; j < W; ++j) u.w[j] = (words & step) ? (j + step < W ? u.w[j + step] : 0u) : u.w[j];
+    if constexpr (DT != DT_F32) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) u.w[j] = __builtin_amdgcn_alignbit(j + 1 < W ? u.w[j + 1] : 0u, u.w[j], (by & 1) * 16);
+    }
+}
+
+// Unit number `unit` of a row of `dim` elements.  A unit beyond the row (unit >=
+// ceil(dim / 8)) reads unit 0 instead (its caller masks it), so that no load
+// is under a branch.  TAIL: dim is no multiple of 8; the partial last unit is read as
+// the row's last 8 elements and shifted, for the same reason (element by element
+// the one lane that holds it took a chain of up to 7 loads while its wave
+// waited).  Only rows of fewer than 8 elements are read one by one.
 template <int DT, bool TAIL, bool NT>
 __device__ __forceinline__ Unit<DT> load_row_unit(const void* row, int unit, int units, int dim)
 {
+    const int e = (unit < units ? unit : 0) * 8;
     if constexpr (!TAIL) {
-        return load_unit8<DT, NT>(row, (int64_t)(unit < units ? unit : 0) * 8);
+        return load_unit8<DT, NT>(row, e);
     } else {
-        const int u = unit < units ? unit : 0;
-        const int left = dim - u * 8;
-        if (left >= 8) return load_unit8<DT, NT>(row, (int64_t)u * 8);
-        return load_part8<DT>(row, (int64_t)u * 8, left);
+        if (dim < 8) return load_part8<DT>(row, 0, dim);
+        const int at = e < dim - 8 ? e : dim - 8;
+        Unit<DT> u = load_unit8<DT, NT>(row, at);
+        shift_unit<DT>(u, e - at);
+        return u;
     }
 }
 
@@ -86,7 +112,7 @@ __device__ __forceinline__ void store_unit8(void* row, int64_t elem, const float
     if constexpr (DT == DT_F32) {
         f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
         QB_G f32x4_a4* q = (QB_G f32x4_a4*)p;
-        if constexpr (NT) {
+        if constexpr (NT && QB_NT32S) {
             __builtin_nontemporal_store(a, q);
             __builtin_nontemporal_store(b, q + 1);
         } else {

@@ -4,6 +4,7 @@
 // built with -fsanitize=address,undefined.  The launchers below stand in for the
 // HIP sources: they enqueue nothing and check that what they are given lies
 // inside the workspace.  Exits non-zero on the first unexpected status.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -53,8 +54,13 @@ hipError_t launch_order(const IdArgs& a, const OrderArgs& o, hipStream_t)
     inside(o.order, (double)a.n * 4);
     return done();
 }
-hipError_t launch_chunk_sums(const IdArgs& a, const OrderArgs&, const void*, int, float* part, hipStream_t)
+hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void*, int, float* part, int64_t, bool,
+                               void*, int, hipStream_t)
 {
+    inside(o.used, (double)(int64_t(2) << o.log2g) * 4);
+    inside(o.count, 8);
+    inside(o.longs, (double)(a.n / o.chunk + 1) * 4);
+    inside(o.list, (double)(a.n < a.rows ? a.n : a.rows) * 4);
     inside(part, 2.0 * (double)chunk_count(a.n) * (double)padded_dim(a.dim) * 4);
     return done();
 }
@@ -63,6 +69,7 @@ hipError_t launch_table_grad(const IdArgs&, const OrderArgs&, const void*, int, 
 {
     return done();
 }
+hipError_t launch_join_chunks(const IdArgs&, const OrderArgs&, float*, hipStream_t) { return done(); }
 hipError_t launch_layer_norm(const void*, int, int64_t, int64_t, const NormArgs&, void*, float*, float*, hipStream_t)
 {
     return done();
@@ -73,7 +80,7 @@ hipError_t launch_stable_embedding(const IdArgs&, const void*, int, float, const
 }
 // the number of workgroups is the HIP sources' choice, at most one per row and kNormPartsMax
 int layer_norm_parts(int64_t n, int64_t) { return (int)(n < kNormPartsMax ? n : kNormPartsMax); }
-int stable_parts(int64_t, int64_t rows) { return rows == 0 ? 0 : kNormPartsMax; }
+int stable_parts(int64_t n, int64_t rows) { return (int)std::min<int64_t>(kNormPartsMax, std::min(n, rows)); }
 hipError_t launch_layer_norm_grad(const void*, const void*, int, int64_t n, int64_t dim, const void*, int,
                                   const float*, const float*, void*, float* part, hipStream_t)
 {

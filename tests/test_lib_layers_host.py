@@ -140,9 +140,9 @@ def test_workspace_sizes(qb):
         assert L.qb_stable_embedding_workspace_bytes(n, rows, dim) == 0
     assert L.qb_stable_embedding_workspace_bytes(1, 10, 16385) == 0
     assert L.qb_layer_norm_workspace_bytes(-1, 8) == 0 and L.qb_layer_norm_workspace_bytes(8, 0) == 0
-    # order of the tokens (one word each), entries of the table, two rows of sums per chunk of 64 tokens
-    entries = 256 * 125 + 1
-    want = -(-4 * entries // 256) * 256 + 4 * 16384 + 2 * (16384 // 64) * 4096 * 4
+    # entries of the table, order of the tokens, used and long ids (per class and as lists), two rows of sums per
+    # chunk of 32 tokens
+    want = sum(-(-4 * words // 256) * 256 for words in (256 * 125 + 1, 16384, 514, 16384, 513)) + 2 * 512 * 4096 * 4
     assert L.qb_embedding_workspace_bytes(16384, 32000, 4096) == want
     # partial sums of dgamma and dbeta of at most 512 workgroups, rows padded to 8 elements
     assert L.qb_layer_norm_workspace_bytes(16384, 4093) == 512 * 2 * 4096 * 4
