@@ -436,8 +436,9 @@ __global__ __launch_bounds__(256) void k_join_chunks(OrderArgs o, float* __restr
 }
 
 // Long ids first, one wave per 64 columns; then the other listed ids, one wave
-// per id and 64 units.  A wave looks its next 64 ids up at once (lane l the
-// l-th).
+// per id and 64 units.  A wave looks its next 64 tasks up at once (lane l the
+// l-th), and reads the first token of the next one before it sums the current:
+// most ids have few tokens, and a wave is bound by the latency of its reads.
 template <int GDT, bool TAIL>
 __global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, const void* __restrict__ dy,
                                                     const float* __restrict__ part, int32_t slices, float scale,
@@ -460,21 +461,34 @@ __global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, const
     const int64_t tasks = (int64_t)o.count[0] * slices;
     for (int64_t w0 = wave; w0 < tasks; w0 += 64 * step) {
         const int64_t mine = w0 + lane * step;
-        int32_t id = 0, lo = 0, hi = 0;
+        int32_t id = 0, lo = 0, hi = 0, slice = 0, head = 0;
         if (mine < tasks) {
             id = gld<int32_t>(o.list + mine / slices);
+            slice = (int32_t)(mine % slices);
             const int64_t s = slot_of(id, o);
             lo = gld<int32_t>(o.start + s);
             hi = gld<int32_t>(o.start + s + 1);
+            head = gld<int32_t>(o.order + lo);
         }
-        for (int i = 0; i < 64 && w0 + i * step < tasks; ++i) {
+        auto load_head = [&](int i) {
+            const int32_t t = __builtin_amdgcn_readlane(head, i);
+            return load_row_unit<GDT, TAIL, true>(static_cast<const char*>(dy) + (int64_t)t * dim * elem_bytes(GDT),
+                                                  __builtin_amdgcn_readlane(slice, i) * 64 + lane, units, dim);
+        };
+        const int todo = tasks - w0 > 63 * step ? 64 : (int)((tasks - w0 + step - 1) / step);
+        Unit<GDT> next = load_head(0);
+        for (int i = 0; i < todo; ++i) {
+            const Unit<GDT> u = next;
+            if (i + 1 < todo) next = load_head(i + 1);
             const int64_t v = __builtin_amdgcn_readlane(id, i);
             const int32_t first = __builtin_amdgcn_readlane(lo, i), last = __builtin_amdgcn_readlane(hi, i);
             if (v == pad || last - first > o.chunk) continue;
-            const int unit = (int)((w0 + i * step) % slices) * 64 + lane;
-            float sums[1][8] = {};
+            const int unit = __builtin_amdgcn_readlane(slice, i) * 64 + lane;
+            float sums[1][8];
             float(&sum)[8] = sums[0];
-            sum_tokens<GDT, TAIL, 64, 1, 8>(o.order, first, last, dy, unit, units, dim, sums);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] = unit_at<GDT>(u, j);
+            sum_tokens<GDT, TAIL, 64, 1, 8>(o.order, first + 1, last, dy, unit, units, dim, sums);
             char* const row = static_cast<char*>(dtable) + v * dim * (ddt == DT_F32 ? 4 : 2);
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[j] *= scale;

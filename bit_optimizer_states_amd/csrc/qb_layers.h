@@ -69,7 +69,23 @@ constexpr int64_t chunk_count(int64_t n) { return (n + chunk_tokens(n) - 1) / ch
 constexpr int64_t padded_dim(int64_t dim) { return (dim + 7) / 8 * 8; }
 
 // Workgroups whose partial sums of the norm's weight gradients are joined.
-constexpr int kNormPartsMax = 512;
+constexpr int kNormPartsMax = 256;
+
+// Workgroups of T threads for a kernel that walks `tiles` tiles by the grid: as
+// many as are resident at once.
+template <int T, class Kernel>
+int persistent_grid_of(Kernel kernel, int64_t tiles)
+{
+    auto query = [](const void* k) -> int {
+        int per_cu = 0;
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, reinterpret_cast<Kernel>(const_cast<void*>(k)), T, 0) !=
+                hipSuccess || per_cu < 1)
+            per_cu = 1;
+        return per_cu;
+    };
+    const int cap = persistent_grid_cap(reinterpret_cast<const void*>(kernel), query);
+    return (int)(tiles < cap ? tiles : cap);
+}
 
 // Rows [t0, t0 + m) of n in one launch each: a launch holds at most 2^21
 // workgroups (workgroups times threads stay below 2^32), `per_wg` rows apiece.

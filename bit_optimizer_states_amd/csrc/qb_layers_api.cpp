@@ -42,8 +42,8 @@ IdArgs id_args(const void* ids, qb_index idt, int64_t n, int64_t rows, int64_t d
     return IdArgs{ids, n, rows, idt == QB_I64 ? 1 : 0, (int32_t)dim};
 }
 
-// An eps that stays positive in binary32: a row of equal values then has a finite rstd.
-bool valid_eps(double eps) { return std::isfinite(eps) && (float)eps > 0.0f && std::isfinite((float)eps); }
+// An eps that is a positive normal binary32: a row of equal values then has a finite rstd.
+bool valid_eps(double eps) { return std::isfinite(eps) && (float)eps >= 0x1p-126f && std::isfinite((float)eps); }
 
 // Workspace of a table's gradient: the arrays of OrderArgs, the chunks' sums; then
 // (stable) the partial sums of dgamma and dbeta.

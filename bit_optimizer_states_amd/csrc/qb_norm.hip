@@ -26,7 +26,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(const void* __restri
                                                             void* __restrict__ y, float* __restrict__ mean_out,
                                                             float* __restrict__ rstd_out)
 {
-    __shared__ float s_slot[3 * (kLongThreads / 64)];
+    __shared__ float s_slot[4 * (kLongThreads / 64)];
     const int64_t t = blockIdx.x;
     const char* const xrow = static_cast<const char*>(x) + t * dim * elem_bytes(XDT);
     char* const yrow = static_cast<char*>(y) + t * dim * elem_bytes(XDT);
@@ -42,7 +42,9 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(const void* __restri
         sum += s;
     }
     if ((int)threadIdx.x < left) sum += load1<XDT>(xrow, whole * 8 + threadIdx.x);
-    const float m0 = row_sum<kLongThreads>(sum, s_slot) / (float)dim;
+    float none = 0.0f;
+    row_sum2<kLongThreads>(sum, none, s_slot);
+    const float m0 = sum / (float)dim;
     float sd = 0.0f, sq = 0.0f;
     for (int64_t u = threadIdx.x; u < whole; u += kLongThreads) {
         const Unit<XDT> w = load_unit8<XDT, false>(xrow, u * 8);
@@ -61,7 +63,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(const void* __restri
         sd += d;
         sq = __builtin_fmaf(d, d, sq);
     }
-    row_sum2<kLongThreads>(sd, sq, s_slot + kLongThreads / 64);
+    row_sum2<kLongThreads>(sd, sq, s_slot + 2 * (kLongThreads / 64));
     const float c = sd / (float)dim;
     const float mean = m0 + c;
     const float rstd = inv_deviation(sq / (float)dim - c * c, eps);
@@ -115,35 +117,49 @@ __global__ __launch_bounds__(NT) void k_norm_grad(const void* __restrict__ dy, c
     extern __shared__ __align__(16) float s_cols[];
     constexpr int GROUPS = NT / TPR;
     constexpr int SLOT = TPR <= 64 ? 1 : 2 * (TPR / 64);
+    constexpr bool KEEP = VPT <= 2;          // h and g stay in registers for the second use
     __shared__ float s_slot[2][GROUPS][SLOT];
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int units = (dim + 7) >> 3, padded = units * 8;
-    for (int c = threadIdx.x; c < padded; c += NT) s_cols[c] = (gamma && c < dim) ? load1<WDT>(gamma, c) : 1.0f;
-    __syncthreads();
-
     float accg[VPT][8] = {}, accb[VPT][8] = {};
     const float inv = 1.0f / (float)dim;
     int buf = 0;
-    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < n; t0 += (int64_t)gridDim.x * GROUPS) {
-        const int64_t t = t0 + grp;
-        const bool live = t < n;
-        const int64_t row = (live ? t : n - 1) * dim * elem_bytes(XDT);
-        const char* const xrow = static_cast<const char*>(x) + row;
-        const char* const grow = static_cast<const char*>(dy) + row;
-        Unit<XDT> xu[VPT], du[VPT];
+    const int64_t step = (int64_t)gridDim.x * GROUPS;
+    Unit<XDT> xu[VPT], du[VPT];
+    float m, r;
+    auto load_next = [&](int64_t t) {
+        const int64_t at = t < n ? t : n - 1;
+        const char* const xrow = static_cast<const char*>(x) + at * dim * elem_bytes(XDT);
+        const char* const grow = static_cast<const char*>(dy) + at * dim * elem_bytes(XDT);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             du[k] = load_row_unit<XDT, TAIL, true>(grow, k * TPR + lane, units, dim);
             xu[k] = load_row_unit<XDT, TAIL, true>(xrow, k * TPR + lane, units, dim);
         }
-        const float m = mean_in[live ? t : n - 1], r = rstd_in[live ? t : n - 1];
+        m = mean_in[at];
+        r = rstd_in[at];
+    };
+    int64_t t0 = (int64_t)blockIdx.x * GROUPS;
+    load_next(t0 + grp);
+    for (int unit = threadIdx.x; unit < units; unit += NT) {
+        Unit<WDT> u;
+        if (gamma) u = load_row_unit<WDT, TAIL, false>(gamma, unit, units, dim);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_cols[unit * 8 + j] = gamma ? unit_at<WDT>(u, j) : 1.0f;
+    }
+    lds_barrier();
+    for (; t0 < n; t0 += step) {
+        const int64_t t = t0 + grp;
+        const bool live = t < n;
+        const int64_t row = t * dim * elem_bytes(XDT);
         // Units beyond the row, and rows beyond the last, take a dy of zero (and an x that is read: finite
         // wherever the row is).
         float s1 = 0.0f, s2 = 0.0f;
+        float hk[KEEP ? VPT : 1][8], gk[KEEP ? VPT : 1][8];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int unit = k * TPR + lane;
-            if (!live || unit >= units) {
+            if (!(whole_step<TPR>(k, dim) && t0 + GROUPS <= n) && (!live || unit >= units)) {
 #pragma unroll
                 for (int j = 0; j < (XDT == DT_F32 ? 8 : 4); ++j) du[k].w[j] = xu[k].w[j] = 0u;
             }
@@ -155,8 +171,12 @@ __global__ __launch_bounds__(NT) void k_norm_grad(const void* __restrict__ dy, c
                 const float g = d * gam[j];
                 s1 += g;
                 s2 = __builtin_fmaf(g, h, s2);
-                accg[k][j] = (TPR < 64 && !live) ? accg[k][j] : __builtin_fmaf(d, h, accg[k][j]);
+                accg[k][j] = __builtin_fmaf(d, h, accg[k][j]);
                 accb[k][j] += d;
+                if constexpr (KEEP) {
+                    hk[k][j] = h;
+                    gk[k][j] = g;
+                }
             }
         }
         row_sum2<TPR>(s1, s2, s_slot[buf][grp]);
@@ -171,13 +191,20 @@ __global__ __launch_bounds__(NT) void k_norm_grad(const void* __restrict__ dy, c
                 float o[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float h = (unit_at<XDT>(xu[k], j) - m) * r;
-                    const float g = unit_at<XDT>(du[k], j) * gam[j];
+                    float h, g;
+                    if constexpr (KEEP) {
+                        h = hk[k][j];
+                        g = gk[k][j];
+                    } else {
+                        h = (unit_at<XDT>(xu[k], j) - m) * r;
+                        g = unit_at<XDT>(du[k], j) * gam[j];
+                    }
                     o[j] = r * (g - __builtin_fmaf(h, c2, c1));
                 }
                 store_row_unit<XDT, TAIL, true>(orow, unit, units, dim, o);
             }
         }
+        if (t0 + step < n) load_next(t + step);
     }
     if (!part) return;
 
@@ -287,7 +314,7 @@ hipError_t grad_as(const void* dy, const void* x, int64_t n, int dim, const void
     if (units <= 64) return go(k_norm_grad<XDT, WDT, 64, 1, TAIL, 512>, 512);
     if (units <= 128) return go(k_norm_grad<XDT, WDT, 64, 2, TAIL, 512>, 512);
     if (units <= 256) return go(k_norm_grad<XDT, WDT, 64, 4, TAIL, 512>, 512);
-    if (units <= 512) return go(k_norm_grad<XDT, WDT, 256, 2, TAIL, 512>, 512);
+    if (units <= 512) return go(k_norm_grad<XDT, WDT, 256, 2, TAIL, 1024>, 1024);
     if (units <= 1024) return go(k_norm_grad<XDT, WDT, 256, 4, TAIL, 512>, 512);
     return go(k_norm_grad<XDT, WDT, 512, 4, TAIL, 512>, 512);
 }
@@ -317,20 +344,23 @@ hipError_t layer_norm_grad_as(const void* dy, const void* x, int64_t n, int64_t 
 }
 
 // dgamma, dbeta = the sum of the partial rows.  A workgroup takes 64 of the 2 *
-// padded columns: 16 lanes of 4 columns, the partial rows dealt to 16 threads
-// each, joined in LDS.
-__global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ part, int parts, int64_t dim,
-                                                    int64_t padded, int accumulate, void* __restrict__ dgamma,
-                                                    void* __restrict__ dbeta, int wdt)
+// padded columns: 16 lanes of 4 columns, the partial rows dealt to 32 threads
+// each (8 of 256 rows in flight at once), joined in LDS.
+constexpr int kJoinRows = 32;
+
+__global__ __launch_bounds__(16 * kJoinRows) void k_join_parts(const float* __restrict__ part, int parts, int64_t dim,
+                                                               int64_t padded, int accumulate,
+                                                               void* __restrict__ dgamma, void* __restrict__ dbeta,
+                                                               int wdt)
 {
-    __shared__ f32x4 s_sum[16][16];
+    __shared__ f32x4 s_sum[kJoinRows][16];
     const int l = threadIdx.x % 16, q = threadIdx.x / 16;
     const int64_t c = (int64_t)blockIdx.x * 64 + l * 4;
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < 2 * padded) {
         const float* p = part + c;
-#pragma unroll 4
-        for (int g = q; g < parts; g += 16) sum += gld<f32x4>(p + (int64_t)g * 2 * padded);
+#pragma unroll 8
+        for (int g = q; g < parts; g += kJoinRows) sum += gld<f32x4>(p + (int64_t)g * 2 * padded);
     }
     s_sum[q][l] = sum;
     __syncthreads();
@@ -338,7 +368,7 @@ __global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ pa
         const int64_t cc = (int64_t)blockIdx.x * 64 + threadIdx.x;
         float v = 0.0f;
 #pragma unroll
-        for (int g = 0; g < 16; ++g) v += s_sum[g][threadIdx.x / 4][threadIdx.x % 4];
+        for (int g = 0; g < kJoinRows; ++g) v += s_sum[g][threadIdx.x / 4][threadIdx.x % 4];
         if (cc < 2 * padded) {
             void* const out = cc < padded ? dgamma : dbeta;
             const int64_t i = cc < padded ? cc : cc - padded;
@@ -352,12 +382,21 @@ __global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ pa
 
 }  // namespace
 
+// Rows a workgroup of the backward kernel takes at once.
+int norm_grad_groups(int64_t dim)
+{
+    const int64_t units = (dim + 7) / 8;
+    return units <= 16 ? 32 : units <= 256 ? 8 : units <= 512 ? 4 : units <= 1024 ? 2 : 1;
+}
+
+// One workgroup per CU at most, and two rows at least per group of threads:
+// every workgroup writes two partial rows of binary32, which for few rows cost
+// more than the rows (1024 rows of 8192 16-bit elements: 23.6 us with 512
+// workgroups, 14.4 us of them without the partial rows).
 int layer_norm_parts(int64_t n, int64_t dim)
 {
     if (dim > kRowRegMax) return (int)(n < kLongParts ? n : kLongParts);
-    const int64_t units = (dim + 7) / 8;
-    const int64_t groups = units <= 16 ? 32 : units <= 256 ? 8 : units <= 1024 ? 2 : 1;     // rows a workgroup takes at once
-    const int64_t g = (n + groups - 1) / groups;
+    const int64_t per = 2 * norm_grad_groups(dim), g = (n + per - 1) / per;
     return (int)(g < kNormPartsMax ? g : kNormPartsMax);
 }
 
@@ -393,7 +432,7 @@ hipError_t launch_join_parts(const float* part, int parts, int64_t dim, bool acc
     if (!dgamma && !dbeta) return hipSuccess;
     const int64_t padded = padded_dim(dim), grid = (2 * padded + 63) / 64;
     if (grid >= (int64_t(1) << 24)) return hipErrorInvalidValue;
-    return launch_kernel(k_join_parts, (int)grid, s, part, parts, dim, padded, accumulate ? 1 : 0, dgamma, dbeta,
+    return launch_kernel_nt(k_join_parts, (int)grid, 16 * kJoinRows, s, part, parts, dim, padded, accumulate ? 1 : 0, dgamma, dbeta,
                          wdt);
 }
 

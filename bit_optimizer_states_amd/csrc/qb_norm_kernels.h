@@ -5,44 +5,24 @@
 // layer, an embedding followed by layer norm, next to the 8-bit optimizers):
 //   mean = sum x / dim,  var = sum (x - mean)^2 / dim,  rstd = 1/sqrt(var + eps),
 //   y = (x - mean) * rstd * gamma + beta.
-// The statistics take two passes over the registers that hold the row: the
-// sum, then the sums of d = x - mean and of d^2, from which the mean is
-// corrected by the residue of its own rounding, m = sum d / dim (var = sum d^2
-// / dim - m^2).  A row whose mean is large against its spread keeps its digits,
-// which sum x^2 - (sum x)^2 would cancel.  All sums are binary32.
+// The statistics take two passes over the registers that hold the row, so that
+// nothing cancels as sum x^2 - (sum x)^2 would.  All sums are binary32.
 //
-// One read and one write of every row: the kernel is bound by HBM.
+// One read and one write of every row: the kernel is bound by HBM, with the
+// vector ALU close behind (at 4096 16-bit elements about 250 instructions per
+// wave and row; a first version of 550 was bound by them, 50 us against 45 for
+// a copy of the same 268 MB), so uniform conditions are kept out of the lanes and
+// everything that depends on the row's length alone is computed once.
 #pragma once
+#include <type_traits>
+
 #include "qb_rows.h"
 
 namespace qb {
 
-// Sum over the TPR threads that share a row: within a wave by DPP, over the
-// row's waves through LDS (slot: TPR / 64 words that no other sum uses before
-// the next-but-one barrier).
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* slot)
-{
-    if constexpr (TPR <= 64) {
-        return lanes_sum<TPR>(v);
-    } else {
-        constexpr int W = TPR / 64;
-        v = lanes_sum<64>(v);
-        const int w = (threadIdx.x % TPR) / 64;
-        if (threadIdx.x % 64 == 0) slot[w] = v;
-        lds_barrier();
-        float s[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) s[i] = slot[i];
-#pragma unroll
-        for (int h = W / 2; h > 0; h /= 2)
-#pragma unroll
-            for (int i = 0; i < h; ++i) s[i] += s[i + h];
-        return s[0];
-    }
-}
-
-// Two sums with one barrier.
+// Two sums over the TPR threads that share a row, with one barrier: within a
+// wave by DPP, over the row's waves through LDS (slot: 2 * TPR / 64 words that no
+// other sum uses before the next-but-one barrier).
 template <int TPR>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float* slot)
 {
@@ -77,20 +57,65 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* slot)
     }
 }
 
-constexpr int row_slot_words(int tpr) { return tpr <= 64 ? 1 : 3 * (tpr / 64); }
+constexpr int row_slot_words(int tpr) { return tpr <= 64 ? 1 : 2 * (tpr / 64); }
 
-// 1/sqrt(var + eps); a variance that rounding took below zero is zero, a NaN stays one.
+// 1/sqrt(var + eps) by the hardware's reciprocal root (1 ulp); a variance that
+// rounding took below zero is zero, a NaN stays one.
 __device__ __forceinline__ float inv_deviation(float var, float eps)
 {
-    return 1.0f / __builtin_sqrtf((var < 0.0f ? 0.0f : var) + eps);
+    return __builtin_amdgcn_rsqf((var < 0.0f ? 0.0f : var) + eps);
 }
 
-// Mean and 1/sqrt(var + eps) of a row of `dim` elements spread over TPR
-// threads, unit k * TPR + lane in x[k] (zeros beyond the row).
+// What depends on the length of a row alone: the numbers of elements that the
+// TPR / 64 waves of a row hold, and reciprocals.
 template <int TPR, int VPT>
-__device__ __forceinline__ void row_stats(const float (&x)[VPT][8], int lane, int dim, float eps, float* slot,
-                                          float* mean, float* rstd)
+struct RowShape {
+    static constexpr int L = TPR < 64 ? TPR : 64, W = TPR < 64 ? 1 : TPR / 64;
+    float held[W];           // elements of each wave
+    float inv_mine;          // 1 / elements of this wave (0 where it has none)
+    float inv_dim;
+    int wave;
+
+    __device__ __forceinline__ RowShape(int lane, int dim)
+    {
+        wave = W == 1 ? 0 : __builtin_amdgcn_readfirstlane(lane / 64);
+        float mine = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int left = dim - (k * TPR + w * L) * 8;
+                n += left < 0 ? 0 : left > L * 8 ? L * 8 : left;
+            }
+            held[w] = (float)n;
+            mine = w == wave ? held[w] : mine;
+        }
+        inv_mine = mine > 0.0f ? 1.0f / mine : 0.0f;
+        inv_dim = 1.0f / (float)dim;
+    }
+};
+
+// Whether all TPR lanes' units of step k are whole (uniform).
+template <int TPR>
+__device__ __forceinline__ bool whole_step(int k, int dim)
 {
+    return (k + 1) * TPR * 8 <= dim;
+}
+
+// Mean and 1/sqrt(var + eps) of a row spread over TPR threads, unit k * TPR +
+// lane in x[k] (zeros beyond the row).  Each wave takes the mean and the squared
+// deviation of its own elements, which are then joined over the row's waves (one
+// barrier) as those of parts of a sample:
+//   mean = sum n_w mean_w / dim,  M2 = sum (M2_w + n_w (mean_w - mean)^2).
+// EXACT (binary32 rows): a wave's mean is corrected by the mean of the rounded
+// differences, so that a row whose mean is large against its spread keeps its
+// digits; 16-bit elements have no such digits.
+template <int TPR, int VPT, bool EXACT>
+__device__ __forceinline__ void row_stats(const float (&x)[VPT][8], const RowShape<TPR, VPT>& shape, int lane, int dim,
+                                          float eps, float* slot, float* mean, float* rstd)
+{
+    constexpr int L = RowShape<TPR, VPT>::L, W = RowShape<TPR, VPT>::W;
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
@@ -98,121 +123,167 @@ __device__ __forceinline__ void row_stats(const float (&x)[VPT][8], int lane, in
         const float b = (x[k][4] + x[k][5]) + (x[k][6] + x[k][7]);
         s += a + b;
     }
-    const float m0 = row_sum<TPR>(s, slot) / (float)dim;
+    const float m0 = lanes_sum<L>(s) * shape.inv_mine;
     float sd = 0.0f, sq = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int cnt = unit_count(k * TPR + lane, dim);
         float ud = 0.0f, uq = 0.0f;
-        if (cnt == 8) {
+        if (whole_step<TPR>(k, dim)) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float d = x[k][j] - m0;
-                ud += d;
+                if constexpr (EXACT) ud += d;
                 uq = __builtin_fmaf(d, d, uq);
             }
         } else {
+            const int cnt = unit_count(k * TPR + lane, dim);
 #pragma unroll
-            for (int j = 0; j < 7; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const float d = j < cnt ? x[k][j] - m0 : 0.0f;
-                ud += d;
+                if constexpr (EXACT) ud += d;
                 uq = __builtin_fmaf(d, d, uq);
             }
         }
-        sd += ud;
+        if constexpr (EXACT) sd += ud;
         sq += uq;
     }
-    row_sum2<TPR>(sd, sq, slot + (TPR <= 64 ? 0 : TPR / 64));
-    const float c = sd / (float)dim;
-    *mean = m0 + c;
-    *rstd = inv_deviation(sq / (float)dim - c * c, eps);
+    float m2 = lanes_sum<L>(sq), m = m0;
+    if constexpr (EXACT) {
+        sd = lanes_sum<L>(sd);
+        const float c = sd * shape.inv_mine;
+        m = m0 + c;
+        m2 -= sd * c;
+    }
+    if constexpr (W > 1) {
+        if (threadIdx.x % 64 == 0) {
+            slot[2 * shape.wave] = m;
+            slot[2 * shape.wave + 1] = m2;
+        }
+        lds_barrier();
+        // differences from wave 0's mean (it holds elements in every row): the join keeps
+        // the digits that the waves' means share.  A wave without elements has mean 0, weight 0.
+        const float m00 = slot[0];
+        float dm = 0.0f, dq = 0.0f, q = slot[1];
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+            const float d = slot[2 * i] - m00, nd = shape.held[i] * d;
+            dm += nd;
+            dq = __builtin_fmaf(nd, d, dq);
+            q += slot[2 * i + 1];
+        }
+        const float shift = dm * shape.inv_dim;
+        m = m00 + shift;
+        m2 = q + (dq - dm * shift);
+    }
+    *mean = m;
+    *rstd = inv_deviation(m2 * shape.inv_dim, eps);
 }
 
-// One row per TPR threads, 256 threads a workgroup.  GATHER: row t is scale *
-// table[ids[t]] (zeros out where the id is outside the table).
+// Threads of a workgroup: a row that waves share has one to itself.
+constexpr int norm_threads(int tpr) { return tpr > 64 ? tpr : 256; }
+
+// TPR threads to a row; the workgroups walk the rows by the grid, gamma and beta
+// stay in registers (EARLY) and the next row is read before the current one is
+// reduced.  GATHER: row t is scale * table[ids[t]] (zeros out where the id is
+// outside the table); the id is read one row further ahead.
 template <int XDT, int YDT, int WDT, int TPR, int VPT, bool TAIL, bool GATHER>
-__global__ __launch_bounds__(256) void k_norm(const void* __restrict__ x, IdArgs a, float scale,
-                                              const void* __restrict__ gamma, const void* __restrict__ beta, float eps,
-                                              void* __restrict__ y, float* __restrict__ mean_out,
-                                              float* __restrict__ rstd_out)
+__global__ __launch_bounds__(norm_threads(TPR)) void k_norm(const void* __restrict__ x, IdArgs a, float scale,
+                                                            const void* __restrict__ gamma,
+                                                            const void* __restrict__ beta, float eps,
+                                                            void* __restrict__ y, float* __restrict__ mean_out,
+                                                            float* __restrict__ rstd_out)
 {
-    constexpr int RPB = 256 / TPR;
-    // gamma and beta are read with the row where registers allow, else after the statistics
+    constexpr int RPB = norm_threads(TPR) / TPR;
     constexpr bool EARLY = VPT <= 2;
     __shared__ float s_slot[RPB][row_slot_words(TPR)];
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-    const int64_t t = (int64_t)blockIdx.x * RPB + grp;
     const int dim = a.dim, units = (dim + 7) >> 3;
-    bool live = t < a.n;
-    if constexpr (TPR >= 64) {
-        if (!live) return;             // a whole wave, or the whole workgroup where its waves meet at barriers
-    }
-    char* const yrow = static_cast<char*>(y) + t * dim * elem_bytes(YDT);
-    const char* xrow = nullptr;
-    bool found = live;
-    if constexpr (GATHER) {
-        const int64_t id = live ? load_id(a.ids, a.id64, t) : -1;
-        found = (uint64_t)id < (uint64_t)a.rows;
-        if (found) xrow = static_cast<const char*>(x) + id * dim * elem_bytes(XDT);
-    } else {
-        if (found) xrow = static_cast<const char*>(x) + t * dim * elem_bytes(XDT);
-    }
+    const int64_t step = (int64_t)gridDim.x * RPB;
 
-    float v[VPT][8];
-    Unit<WDT> gu[VPT], bu[VPT];
-    {
-        Unit<XDT> xu[VPT];
-        if (found) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) xu[k] = load_row_unit<XDT, TAIL, !GATHER>(xrow, k * TPR + lane, units, dim);
+    // row t's id (its own number without GATHER), or -1 where it has no row to read
+    auto id_of = [&](int64_t t) -> int64_t {
+        if constexpr (GATHER) {
+            const int64_t id = t < a.n ? load_id(a.ids, a.id64, t) : -1;
+            return (uint64_t)id < (uint64_t)a.rows ? id : -1;
+        } else {
+            return t < a.n ? t : -1;
         }
-        if constexpr (EARLY) {
-            if (gamma) {
+    };
+    Unit<XDT> xu[VPT] = {};
+    auto load_row = [&](int64_t id) {
+        if (id >= 0) {
+            const char* const row = static_cast<const char*>(x) + id * dim * elem_bytes(XDT);
 #pragma unroll
-                for (int k = 0; k < VPT; ++k)
-                    gu[k] = load_row_unit<WDT, TAIL, false>(gamma, k * TPR + lane, units, dim);
-            }
-            if (beta) {
-#pragma unroll
-                for (int k = 0; k < VPT; ++k)
-                    bu[k] = load_row_unit<WDT, TAIL, false>(beta, k * TPR + lane, units, dim);
-            }
+            for (int k = 0; k < VPT; ++k) xu[k] = load_row_unit<XDT, TAIL, !GATHER>(row, k * TPR + lane, units, dim);
         }
+    };
+    int64_t base = (int64_t)blockIdx.x * RPB;
+    int64_t id = id_of(base + grp), id1 = GATHER ? id_of(base + step + grp) : 0;
+    load_row(id);
+    const RowShape<TPR, VPT> shape(lane, dim);
+    float g[VPT][8], b[VPT][8];
+    auto load_weights = [&](int k) {
+        Unit<WDT> gu, bu;
+        if (gamma) gu = load_row_unit<WDT, TAIL, false>(gamma, k * TPR + lane, units, dim);
+        if (beta) bu = load_row_unit<WDT, TAIL, false>(beta, k * TPR + lane, units, dim);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            g[k][j] = gamma ? unit_at<WDT>(gu, j) : 1.0f;
+            b[k][j] = beta ? unit_at<WDT>(bu, j) : 0.0f;
+        }
+    };
+    if constexpr (EARLY) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) load_weights(k);
+    }
+    for (; base < a.n; base += step) {
+        const int64_t t = base + grp;
+        const bool found = id >= 0;
+        float v[VPT][8];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const bool in = found && k * TPR + lane < units;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float w = unit_at<XDT>(xu[k], j);
-                v[k][j] = in ? (GATHER ? w * scale : w) : 0.0f;
+                v[k][j] = GATHER ? w * scale : w;
+            }
+            if (!whole_step<TPR>(k, dim) && k * TPR + lane >= units) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
             }
         }
-    }
-    float mean, rstd;
-    row_stats<TPR, VPT>(v, lane, dim, eps, s_slot[grp], &mean, &rstd);
-    if (!live) return;
-    if (lane == 0) {
-        if (mean_out) mean_out[t] = mean;
-        if (rstd_out) rstd_out[t] = rstd;
-    }
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int unit = k * TPR + lane;
-        if constexpr (!EARLY) {
-            if (gamma) gu[k] = load_row_unit<WDT, TAIL, false>(gamma, unit, units, dim);
-            if (beta) bu[k] = load_row_unit<WDT, TAIL, false>(beta, unit, units, dim);
+        if constexpr (GATHER) {
+            id = id1;
+            id1 = id_of(base + 2 * step + grp);
+        } else {
+            id = id_of(base + step + grp);
         }
-        float o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float g = gamma ? unit_at<WDT>(gu[k], j) : 1.0f;
-            const float b = beta ? unit_at<WDT>(bu[k], j) : 0.0f;
-            o[j] = __builtin_fmaf((v[k][j] - mean) * rstd, g, b);
-            if (GATHER && !found) o[j] = 0.0f;
+        load_row(id);
+        float mean = 0.0f, rstd = 0.0f;
+        if (TPR < 64 || found) row_stats<TPR, VPT, XDT == DT_F32>(v, shape, lane, dim, eps, s_slot[grp], &mean, &rstd);
+        if (t >= a.n) continue;
+        if (lane == 0) {
+            if (mean_out) mean_out[t] = mean;
+            if (rstd_out) rstd_out[t] = rstd;
         }
-        store_row_unit<YDT, TAIL, true>(yrow, unit, units, dim, o);
+        char* const yrow = static_cast<char*>(y) + t * dim * elem_bytes(YDT);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            if constexpr (!EARLY) load_weights(k);
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = __builtin_fmaf((v[k][j] - mean) * rstd, g[k][j], b[k][j]);
+            if (GATHER && !found) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+            }
+            store_row_unit<YDT, TAIL, true>(yrow, k * TPR + lane, units, dim, o);
+        }
     }
 }
+
+template <int N>
+using threads_c = std::integral_constant<int, N>;
 
 // Threads and units per row.  Up to 128 elements 16 lanes share a row, up to
 // 2048 one wave (no barrier), beyond that a workgroup.
@@ -221,21 +292,19 @@ hipError_t norm_as(const void* x, const IdArgs& a, float scale, const NormArgs& 
                    hipStream_t s)
 {
     const int units = (a.dim + 7) / 8;
-    auto go = [&](auto kernel, int tpr) {
-        return launch_rows(a.n, 256 / tpr, [&](int64_t t0, int64_t m, int grid) {
-            const void* const in = GATHER ? x : static_cast<const char*>(x) + t0 * a.dim * elem_bytes(XDT);
-            return launch_kernel(kernel, grid, s, in, ids_from(a, t0, m), scale, w.gamma, w.beta, w.eps,
-                                 static_cast<char*>(y) + t0 * a.dim * elem_bytes(YDT), mean ? mean + t0 : nullptr,
-                                 rstd ? rstd + t0 : nullptr);
-        });
+    auto go = [&](auto kernel, auto tpr) {
+        constexpr int T = norm_threads(decltype(tpr)::value), RPB = T / decltype(tpr)::value;
+        const int64_t tiles = (a.n + RPB - 1) / RPB;
+        const int grid = tiles <= 256 ? (int)tiles : persistent_grid_of<T>(kernel, tiles);
+        return launch_kernel_nt(kernel, grid, T, s, x, a, scale, w.gamma, w.beta, w.eps, y, mean, rstd);
     };
-    if (units <= 16) return go(k_norm<XDT, YDT, WDT, 16, 1, TAIL, GATHER>, 16);
-    if (units <= 64) return go(k_norm<XDT, YDT, WDT, 64, 1, TAIL, GATHER>, 64);
-    if (units <= 128) return go(k_norm<XDT, YDT, WDT, 64, 2, TAIL, GATHER>, 64);
-    if (units <= 256) return go(k_norm<XDT, YDT, WDT, 64, 4, TAIL, GATHER>, 64);
-    if (units <= 512) return go(k_norm<XDT, YDT, WDT, 256, 2, TAIL, GATHER>, 256);
-    if (units <= 1024) return go(k_norm<XDT, YDT, WDT, 256, 4, TAIL, GATHER>, 256);
-    if (units <= 2048) return go(k_norm<XDT, YDT, WDT, 256, 8, TAIL, GATHER>, 256);
+    if (units <= 16) return go(k_norm<XDT, YDT, WDT, 16, 1, TAIL, GATHER>, threads_c<16>{});
+    if (units <= 64) return go(k_norm<XDT, YDT, WDT, 64, 1, TAIL, GATHER>, threads_c<64>{});
+    if (units <= 128) return go(k_norm<XDT, YDT, WDT, 64, 2, TAIL, GATHER>, threads_c<64>{});
+    if (units <= 256) return go(k_norm<XDT, YDT, WDT, 64, 4, TAIL, GATHER>, threads_c<64>{});
+    if (units <= 512) return go(k_norm<XDT, YDT, WDT, 256, 2, TAIL, GATHER>, threads_c<256>{});
+    if (units <= 1024) return go(k_norm<XDT, YDT, WDT, 512, 2, TAIL, GATHER>, threads_c<512>{});
+    if (units <= 2048) return go(k_norm<XDT, YDT, WDT, 1024, 2, TAIL, GATHER>, threads_c<1024>{});
     return hipErrorInvalidValue;
 }
 

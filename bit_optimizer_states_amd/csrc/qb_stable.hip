@@ -10,6 +10,8 @@
 // the norm's backward pass runs once per used id instead of once per token, and
 // no [tokens, dim] intermediate is written: the bytes are those of the plain
 // embedding's gradient plus the used rows of W.
+#include <type_traits>
+
 #include "qb_norm_kernels.h"
 #include "qb_token_sums.h"
 
@@ -34,6 +36,8 @@ hipError_t stable_y(const IdArgs& a, const void* table, float scale, const NormA
     return stable_as<TDT, DT_BF16>(a, table, scale, w, y, s);
 }
 
+constexpr int kStableParts = 512;        // workgroups of the gradient, two per CU
+
 struct StableGradArgs {
     const void* dy;
     const float* chunk_part;
@@ -47,7 +51,8 @@ struct StableGradArgs {
 };
 
 // TPR threads (one workgroup) to a listed id; a workgroup walks the list by
-// the grid and looks its next 64 ids up at once (lane l the l-th).
+// the grid, looks its next 64 ids up at once (lane l the l-th), and reads the
+// next id's row and first token before it works on the current one.
 template <int GDT, int TDT, int TPR, int VPT, bool TAIL>
 __global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, StableGradArgs p)
 {
@@ -57,34 +62,67 @@ __global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, Stab
     const int tid = threadIdx.x, lane = tid % 64;
     const int32_t count = o.count[0], step = (int32_t)gridDim.x;
     float gam[VPT][8], accg[VPT][8] = {}, accb[VPT][8] = {};
+    auto load_gamma = [&](auto wdt) {
+        constexpr int WDT = decltype(wdt)::value;
+        Unit<WDT> u[VPT];
 #pragma unroll
-    for (int k = 0; k < VPT; ++k)
+        for (int k = 0; k < VPT; ++k) u[k] = load_row_unit<WDT, TAIL, false>(p.gamma, k * TPR + tid, units, dim);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = (k * TPR + tid) * 8 + j;
-            gam[k][j] = c >= dim ? 0.0f : p.gamma ? load1_rt(p.wdt, p.gamma, c) : 1.0f;
-        }
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) gam[k][j] = unit_at<WDT>(u[k], j);
+    };
+    if (!p.gamma) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) gam[k][j] = 1.0f;
+    } else if (p.wdt == DT_F32) {
+        load_gamma(std::integral_constant<int, DT_F32>{});
+    } else {
+        load_gamma(std::integral_constant<int, TDT>{});
+    }
 
+    const RowShape<TPR, VPT> shape(tid, dim);
     for (int64_t i0 = blockIdx.x; i0 < count; i0 += 64 * (int64_t)step) {
         const int64_t at = i0 + lane * (int64_t)step;
-        int32_t id = 0, lo = 0, hi = 0;
+        int32_t id = 0, lo = 0, hi = 0, head = 0;
         if (at < count) {
             id = gld<int32_t>(o.list + at);
             const int64_t s = slot_of(id, o);
             lo = gld<int32_t>(o.start + s);
             hi = gld<int32_t>(o.start + s + 1);
+            head = gld<int32_t>(o.order + lo);
         }
-        for (int i = 0; i < 64 && i0 + i * (int64_t)step < count; ++i) {
+        const int todo = count - i0 > 63 * (int64_t)step ? 64 : (int)((count - i0 + step - 1) / step);
+        Unit<TDT> wnext[VPT];
+        Unit<GDT> dnext[VPT];
+        // an id's row and its first token's dy
+        auto load_next = [&](int i) {
+            const char* const wrow =
+                static_cast<const char*>(p.table) + (int64_t)__builtin_amdgcn_readlane(id, i) * dim * elem_bytes(TDT);
+            const char* const drow =
+                static_cast<const char*>(p.dy) + (int64_t)__builtin_amdgcn_readlane(head, i) * dim * elem_bytes(GDT);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                wnext[k] = load_row_unit<TDT, TAIL, true>(wrow, k * TPR + tid, units, dim);
+                dnext[k] = load_row_unit<GDT, TAIL, true>(drow, k * TPR + tid, units, dim);
+            }
+        };
+        load_next(0);
+        for (int i = 0; i < todo; ++i) {
             const int64_t v = __builtin_amdgcn_readlane(id, i);
             const int32_t first = __builtin_amdgcn_readlane(lo, i), last = __builtin_amdgcn_readlane(hi, i);
-
-            // the id's row
-            const char* const wrow = static_cast<const char*>(p.table) + v * dim * elem_bytes(TDT);
             Unit<TDT> wu[VPT];
+            float sum[VPT][8];
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) wu[k] = load_row_unit<TDT, TAIL, true>(wrow, k * TPR + tid, units, dim);
+            for (int k = 0; k < VPT; ++k) {
+                wu[k] = wnext[k];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[k][j] = unit_at<GDT>(dnext[k], j);
+            }
+            if (i + 1 < todo) load_next(i + 1);
             // S_v
-            float sum[VPT][8] = {};
             if (last - first > o.chunk) {              // joined before, in the slot of its first chunk
                 const float* const q = p.chunk_part + chunk_slot(first / o.chunk, first, o.chunk) * padded;
 #pragma unroll
@@ -98,24 +136,28 @@ __global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, Stab
                     }
                 }
             } else {
-                sum_tokens<GDT, TAIL, TPR, VPT, 4>(o.order, first, last, p.dy, tid, units, dim, sum);
+                sum_tokens<GDT, TAIL, TPR, VPT, 4>(o.order, first + 1, last, p.dy, tid, units, dim, sum);
             }
             // the statistics of its norm
             float x[VPT][8];
 #pragma unroll
-            for (int k = 0; k < VPT; ++k)
+            for (int k = 0; k < VPT; ++k) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[k][j] = k * TPR + tid < units ? unit_at<TDT>(wu[k], j) * p.scale : 0.0f;
+                for (int j = 0; j < 8; ++j) x[k][j] = unit_at<TDT>(wu[k], j) * p.scale;
+                if (!whole_step<TPR>(k, dim) && k * TPR + tid >= units) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[k][j] = sum[k][j] = 0.0f;
+                }
+            }
             float mean, rstd;
-            row_stats<TPR, VPT>(x, tid, dim, p.eps, s_slot, &mean, &rstd);
+            row_stats<TPR, VPT, TDT == DT_F32>(x, shape, tid, dim, p.eps, s_slot, &mean, &rstd);
 
             float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
             for (int k = 0; k < VPT; ++k)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float d = k * TPR + tid < units ? sum[k][j] : 0.0f;
+                    const float d = sum[k][j];
                     const float h = (x[k][j] - mean) * rstd, g = d * gam[k][j];
                     sum[k][j] = g;
                     x[k][j] = h;
@@ -126,7 +168,7 @@ __global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, Stab
                 }
             row_sum2<TPR>(s1, s2, s_slot + row_slot_words(TPR));
             if (v == p.pad) continue;                  // its row takes no gradient
-            const float c1 = s1 / (float)dim, c2 = s2 / (float)dim, f = p.scale * rstd;
+            const float c1 = s1 * shape.inv_dim, c2 = s2 * shape.inv_dim, f = p.scale * rstd;
             char* const row = static_cast<char*>(p.dtable) + v * dim * (p.ddt == DT_F32 ? 4 : 2);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
@@ -194,11 +236,11 @@ hipError_t launch_stable_embedding(const IdArgs& a, const void* table, int tdt, 
     return stable_y<DT_BF16>(a, table, scale, w, y, ydt, s);
 }
 
-// Two workgroups per CU, no more than ids that can have tokens.
+// No more workgroups than ids that can have tokens.
 int stable_parts(int64_t n, int64_t rows)
 {
     const int64_t most = n < rows ? n : rows;
-    return (int)(most < kNormPartsMax ? most : kNormPartsMax);
+    return (int)(most < kStableParts ? most : kStableParts);
 }
 
 hipError_t launch_stable_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, const float* chunk_part,

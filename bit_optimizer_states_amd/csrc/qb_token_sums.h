@@ -73,14 +73,14 @@ __device__ __forceinline__ float join_column(const float* part, int32_t chunk, i
     float sum = gld<float>(part + chunk_slot(c, first, chunk) * padded + col);
     ++c;
     const float* p = part + 2 * (int64_t)c * padded + col;         // later chunks begin with this id's tokens
-    for (; c + UN <= c1 + 1; c += UN, p += 2 * UN * padded) {
+    for (; c <= c1; c += UN, p += 2 * UN * padded) {
         float v[UN];
 #pragma unroll
-        for (int q = 0; q < UN; ++q) v[q] = gld<float>(p + 2 * q * padded);
+        for (int q = 0; q < UN; ++q) v[q] = gld<float>(p + 2 * (int64_t)(c + q <= c1 ? q : c1 - c) * padded);
 #pragma unroll
-        for (int q = 0; q < UN; ++q) sum += v[q];
+        for (int q = 0; q < UN; ++q)
+            if (c + q <= c1) sum += v[q];
     }
-    for (; c <= c1; ++c, p += 2 * padded) sum += gld<float>(p);
     return sum;
 }
 

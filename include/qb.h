@@ -656,7 +656,7 @@ size_t qb_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim);
  *   x, y         [n, dim] of dtype xdt.
  *   gamma, beta  [dim] of dtype wdt, each may be NULL (ones, zeros).  wdt is
  *                QB_F32 or xdt (else QB_EUNSUPPORTED).
- *   eps          positive and finite in binary32.
+ *   eps          finite and positive, a normal number in binary32 too (at least 2^-126).
  *   mean, rstd   [n] fp32 out, each may be NULL; qb_layer_norm_backward takes them.
  * One kernel.
  */

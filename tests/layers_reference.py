@@ -35,25 +35,32 @@ def statistics(x, eps):
     return mean, var, 1.0 / np.sqrt(var + eps)
 
 
-def normalized(x, eps):
-    """h = (x - mean) * rstd, rstd, the error of the kernels' h and of rstd.
+def normalized(x, eps, exact):
+    """h = (x - mean) * rstd, mean, rstd, and the kernels' errors of h, mean and rstd.
 
-    The mean is corrected by the mean of the rounded differences d, so it is off
-    by its own rounding u |mean| and by the error (L + 2) u mean|x - mean| of that
-    correction; mean|x - mean| * rstd <= 1.  var, as sum d^2 / dim - correction^2, is
-    off by (L + 6) u relative, rstd by half of that and 3 u of the root and the
-    quotient; the difference and the product round twice."""
+    exact (binary32 rows): the mean is corrected by the mean of the rounded
+    differences d, so it is off by its own rounding u |mean| and by the error
+    (L + 2) u mean|x - mean| of that correction (mean|x - mean| <= sqrt(var)).
+    Otherwise (16-bit rows) it is the sum's, off by (L + 2) u mean|x|, and the
+    squared deviation, taken around it, is too large by the square of that.
+    var is off by (L + 6) u relative besides, rstd by half of all that and by 3 u of
+    the hardware's reciprocal root (1 ulp = 2 u) and its argument; the
+    difference and the product of h round once each."""
     mean, var, rstd = statistics(x, eps)
     h = (x - mean[:, None]) * rstd[:, None]
-    e_rstd = ((L + 6) / 2 + 3) * U
-    e_mean = U * np.abs(mean) + (L + 2) * U * np.sqrt(var)
-    e_h = (e_mean * rstd)[:, None] + np.abs(h) * (e_rstd + 2 * U)
-    return h, mean, rstd, e_h, e_mean, e_rstd * rstd
+    if exact:
+        e_mean = U * np.abs(mean) + (L + 2) * U * np.sqrt(var)
+        e_rel = np.full_like(mean, ((L + 6) / 2 + 3) * U)
+    else:
+        e_mean = (L + 2) * U * np.abs(x).mean(1)
+        e_rel = ((L + 6) / 2 + 3) * U + (e_mean * rstd) ** 2 / 2
+    e_h = (e_mean * rstd)[:, None] + np.abs(h) * (e_rel[:, None] + 2 * U)
+    return h, mean, rstd, e_h, e_mean, e_rel * rstd
 
 
-def layer_norm(x, gamma, beta, eps):
-    """y and the error of the kernels' binary32 y."""
-    h, mean, rstd, e_h, e_mean, e_rstd = normalized(x, eps)
+def layer_norm(x, gamma, beta, eps, exact):
+    """y, the error of the kernels' binary32 y, and the statistics with theirs."""
+    h, mean, rstd, e_h, e_mean, e_rstd = normalized(x, eps, exact)
     g = np.ones(x.shape[1]) if gamma is None else gamma
     b = np.zeros(x.shape[1]) if beta is None else beta
     y = h * g + b

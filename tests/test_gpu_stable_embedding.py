@@ -24,7 +24,7 @@ def weights(dim, wdt, seed):
 def check_forward(table, ids, gamma, beta, scale, y):
     x = lookup(table, ids, scale, F32)
     want, err, *_ = ref.layer_norm(ref.f64(x), None if gamma is None else ref.f64(gamma),
-                                   None if beta is None else ref.f64(beta), float(np.float32(EPS)))
+                                   None if beta is None else ref.f64(beta), float(np.float32(EPS)), table.dtype == F32)
     out = ((ids < 0) | (ids >= table.shape[0])).cpu().numpy()
     want[out], err[out] = 0, 0
     ref.assert_close(y, want, err, f"y {list(y.shape)}")
@@ -34,7 +34,7 @@ def check_backward(dy, table, ids, gamma, scale, dtable, dgamma, dbeta, padding_
     rows, dim = table.shape
     s, e_s, k = ref.token_sums(ref.f64(dy), ids.tolist(), rows)
     x = ref.f64(table.float() * torch.tensor(scale, dtype=F32, device=DEV))
-    h, _, rstd, e_h, _, e_r = ref.normalized(x, float(np.float32(EPS)))
+    h, _, rstd, e_h, _, e_r = ref.normalized(x, float(np.float32(EPS)), table.dtype == F32)
     g = np.ones(dim) if gamma is None else ref.f64(gamma)
     want, err = ref.norm_grad(s, e_s, h, e_h, rstd, e_r, g)
     sc = abs(float(np.float32(scale)))
