@@ -35,17 +35,20 @@ __global__ __launch_bounds__(256) void k_embedding(IdArgs a, const void* __restr
     const bool found = (uint64_t)id < (uint64_t)a.rows;
     const char* const row = static_cast<const char*>(table) + (found ? id : 0) * dim * elem_bytes(TDT);
     char* const yrow = static_cast<char*>(y) + t * dim * elem_bytes(YDT);
-    for (int unit = lane; unit < units; unit += 1 << log2lanes) {
-        float o[8];
+    const int step = 1 << log2lanes;
+    for (int unit = lane; unit < units; unit += 2 * step) {
+        float o[2][8] = {};
         if (found) {
-            const Unit<TDT> u = load_row_unit<TDT, TAIL, false>(row, unit, units, dim);
+            Unit<TDT> u[2];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = unit_at<TDT>(u, j) * scale;
-        } else {
+            for (int q = 0; q < 2; ++q) u[q] = load_row_unit<TDT, TAIL, false>(row, unit + q * step, units, dim);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[q][j] = unit_at<TDT>(u[q], j) * scale;
         }
-        store_row_unit<YDT, TAIL, true>(yrow, unit, units, dim, o);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) store_row_unit<YDT, TAIL, true>(yrow, unit + q * step, units, dim, o[q]);
     }
 }
 
@@ -359,27 +362,30 @@ __device__ __forceinline__ void chunk_sums(const IdArgs& a, const OrderArgs& o, 
     const int32_t b = (int32_t)(c * chunk), e = found - b < chunk ? found : b + chunk;
     const int dim = a.dim, units = (dim + 7) >> 3;
     const int64_t padded = (int64_t)units * 8;
-    int64_t before = -1;
+    // both sides' look-ups at once: each is a chain of three dependent reads
+    const int32_t t0 = o.order[b], t1 = o.order[e - 1];
+    const int64_t id[2] = {load_id(a.ids, a.id64, t0), load_id(a.ids, a.id64, t1)};
+    const int64_t s[2] = {slot_of(id[0], o), slot_of(id[1], o)};
+    const int32_t lo[2] = {o.start[s[0]], o.start[s[1]]}, hi[2] = {o.start[s[0] + 1], o.start[s[1] + 1]};
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-        const int64_t v = load_id(a.ids, a.id64, o.order[side == 0 ? b : e - 1]);
-        if (v == before) break;
-        before = v;
-        const int64_t s = slot_of(v, o);
-        const int32_t v0 = o.start[s], v1 = o.start[s + 1];
+        if (side == 1 && id[1] == id[0]) break;
+        const int32_t v0 = lo[side], v1 = hi[side];
         if (v1 - v0 <= chunk) continue;
         float sums[1][8] = {};
         sum_tokens<GDT, TAIL, 64, 1, 8>(o.order, v0 > b ? v0 : b, v1 < e ? v1 : e, dy, unit, units, dim, sums);
-        const float(&sum)[8] = sums[0];
         if (unit < units) {
             float* const p = part + (2 * c + (v0 > b ? 1 : 0)) * padded + (int64_t)unit * 8;
-            gst<f32x4>(p, f32x4{sum[0], sum[1], sum[2], sum[3]});
-            gst<f32x4>(p + 4, f32x4{sum[4], sum[5], sum[6], sum[7]});
+            gst<f32x4>(p, f32x4{sums[0][0], sums[0][1], sums[0][2], sums[0][3]});
+            gst<f32x4>(p + 4, f32x4{sums[0][4], sums[0][5], sums[0][6], sums[0][7]});
         }
     }
 }
 
-constexpr int kZeroRows = 16;           // table rows of a zero-filling workgroup
+#ifndef QB_ZR
+#define QB_ZR 16
+#endif
+constexpr int kZeroRows = QB_ZR;           // table rows of a zero-filling workgroup
 
 template <int GDT, bool TAIL>
 __global__ __launch_bounds__(256) void k_prepare_grad(IdArgs a, OrderArgs o, const void* __restrict__ dy,

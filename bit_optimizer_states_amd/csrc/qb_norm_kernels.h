@@ -57,7 +57,7 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* slot)
     }
 }
 
-constexpr int row_slot_words(int tpr) { return tpr <= 64 ? 1 : 2 * (tpr / 64); }
+constexpr int row_slot_words(int tpr) { return tpr <= 64 ? 1 : 3 * (tpr / 64); }
 
 // 1/sqrt(var + eps) by the hardware's reciprocal root (1 ulp); a variance that
 // rounding took below zero is zero, a NaN stays one.
@@ -147,32 +147,36 @@ __device__ __forceinline__ void row_stats(const float (&x)[VPT][8], const RowSha
         if constexpr (EXACT) sd += ud;
         sq += uq;
     }
-    float m2 = lanes_sum<L>(sq), m = m0;
+    float m2 = lanes_sum<L>(sq), c = 0.0f;
     if constexpr (EXACT) {
         sd = lanes_sum<L>(sd);
-        const float c = sd * shape.inv_mine;
-        m = m0 + c;
+        c = sd * shape.inv_mine;               // the wave's mean is m0 + c, not rounded to one binary32 here
         m2 -= sd * c;
     }
+    float m = m0 + c;
     if constexpr (W > 1) {
+        constexpr int S = EXACT ? 3 : 2;
         if (threadIdx.x % 64 == 0) {
-            slot[2 * shape.wave] = m;
-            slot[2 * shape.wave + 1] = m2;
+            slot[S * shape.wave] = m0;
+            slot[S * shape.wave + 1] = m2;
+            if constexpr (EXACT) slot[S * shape.wave + 2] = c;
         }
         lds_barrier();
         // differences from wave 0's mean (it holds elements in every row): the join keeps
         // the digits that the waves' means share.  A wave without elements has mean 0, weight 0.
-        const float m00 = slot[0];
+        const float m00 = slot[0], c00 = EXACT ? slot[2] : 0.0f;
         float dm = 0.0f, dq = 0.0f, q = slot[1];
 #pragma unroll
         for (int i = 1; i < W; ++i) {
-            const float d = slot[2 * i] - m00, nd = shape.held[i] * d;
+            float d = slot[S * i] - m00;
+            if constexpr (EXACT) d += slot[S * i + 2] - c00;
+            const float nd = shape.held[i] * d;
             dm += nd;
             dq = __builtin_fmaf(nd, d, dq);
-            q += slot[2 * i + 1];
+            q += slot[S * i + 1];
         }
         const float shift = dm * shape.inv_dim;
-        m = m00 + shift;
+        m = m00 + (c00 + shift);
         m2 = q + (dq - dm * shift);
     }
     *mean = m;

@@ -41,8 +41,10 @@ def normalized(x, eps, exact):
     exact (binary32 rows): the mean is corrected by the mean of the rounded
     differences d, so it is off by its own rounding u |mean| and by the error
     (L + 2) u mean|x - mean| of that correction (mean|x - mean| <= sqrt(var)).
-    Otherwise (16-bit rows) it is the sum's, off by (L + 2) u mean|x|, and the
-    squared deviation, taken around it, is too large by the square of that.
+    Otherwise (16-bit rows) it is the sum's, off by e = (L + 2) u mean|x|.  The
+    squared deviations of a row's waves, taken around such means, are joined as
+    if these were exact: off by 2 e |d_w| + e^2 for a wave whose mean lies d_w from the
+    row's, and the mean of |d_w| over the waves is at most sqrt(var).
     var is off by (L + 6) u relative besides, rstd by half of all that and by 3 u of
     the hardware's reciprocal root (1 ulp = 2 u) and its argument; the
     difference and the product of h round once each."""
@@ -53,7 +55,7 @@ def normalized(x, eps, exact):
         e_rel = np.full_like(mean, ((L + 6) / 2 + 3) * U)
     else:
         e_mean = (L + 2) * U * np.abs(x).mean(1)
-        e_rel = ((L + 6) / 2 + 3) * U + (e_mean * rstd) ** 2 / 2
+        e_rel = ((L + 6) / 2 + 3) * U + e_mean * rstd + (e_mean * rstd) ** 2 / 2
     e_h = (e_mean * rstd)[:, None] + np.abs(h) * (e_rel[:, None] + 2 * U)
     return h, mean, rstd, e_h, e_mean, e_rel * rstd
 

@@ -148,11 +148,13 @@ def test_rows_of_equal_values_and_far_means():
     """A constant row has h = 0 up to the mean's rounding; a mean that is large
     against the spread keeps its digits."""
     L = qb()
-    for dim in (100, 1001, 4096, 16385):
-        x = torch.full((4, dim), 3.0, device=DEV)
+    for dim in (100, 1001, 2500, 4096, 7000, 16383, 16385):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(dim)
+        x = torch.full((40, dim), 3.0, device=DEV)
         x[1] = -1000.1
         x[2] = 0.0
-        x[3] = 1e4 + torch.randn(dim, device=DEV)
+        x[3:] = 1e4 + torch.randn(37, dim, device=DEV, generator=g)
         y, mean, rstd = forward(L, x, None, None)
         check_forward(x, None, None, y, mean, rstd)
         assert (y[2] == 0).all() and abs(mean[0].item() - 3.0) <= 3.0 * ref.U * 2
