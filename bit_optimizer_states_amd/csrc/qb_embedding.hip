@@ -284,6 +284,7 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
         }
         if (cls == mask && j == per - 1) o.start[((int64_t)cls + 1) * per] = run;
     }
+    if (cls == 0 && j == 0) o.count[1] = 0;            // k_table_grad counts long ids in it
     if (j < 2) {
         int32_t used = 0;
         for (int w = 0; w < kOrderWaves; ++w) used += s_used[j][w];
@@ -304,8 +305,11 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
                 int32_t at = 0;
                 if (lane == lead) at = atomicAdd(&cnt[e >> o.log2g], (int32_t)__popcll(same));
                 at = __builtin_amdgcn_readlane(at, lead);
-                if (mine && id[k] == e)
-                    o.order[at + __popcll(same & ((1ull << lane) - 1))] = (int32_t)(t0 + k * 64 + lane);
+                if (mine && id[k] == e) {
+                    const int32_t p = at + (int32_t)__popcll(same & ((1ull << lane) - 1));
+                    o.order[p] = (int32_t)(t0 + k * 64 + lane);
+                    o.key[p] = e;
+                }
                 todo &= ~same;
             }
         }
@@ -339,7 +343,11 @@ __device__ __forceinline__ void list_used(const OrderArgs& o, int64_t cls)
         const int32_t k = e < o.per ? gld<int32_t>(start + e + 1) - gld<int32_t>(start + e) : 0;
         const unsigned long long some = __ballot(k > 0), many = __ballot(k > o.chunk), below = (1ull << lane) - 1;
         const int32_t v = (int32_t)(((int64_t)e << o.log2g) + cls);
-        if (k > 0) o.list[base + __popcll(some & below)] = v;
+        if (k > 0) {
+            const int32_t lo = gld<int32_t>(start + e);
+            const u32x4 entry = {(uint32_t)v, (uint32_t)lo, (uint32_t)(lo + k), gld<uint32_t>(o.order + lo)};
+            gst<u32x4>(o.list + 4 * ((int64_t)base + __popcll(some & below)), entry);
+        }
         if (k > o.chunk) o.longs[lbase + __popcll(many & below)] = v;
         base += (int32_t)__popcll(some);
         lbase += (int32_t)__popcll(many);
@@ -382,10 +390,30 @@ __device__ __forceinline__ void chunk_sums(const IdArgs& a, const OrderArgs& o, 
     }
 }
 
-#ifndef QB_ZR
-#define QB_ZR 16
-#endif
-constexpr int kZeroRows = QB_ZR;           // table rows of a zero-filling workgroup
+constexpr int kZeroRows = 16;           // table rows of a zero-filling workgroup
+
+// One workgroup of 256 threads: zeros into the empty ones of kZeroRows rows at a
+// time, workgroup wg of wgs.
+template <bool TAIL>
+__device__ __forceinline__ void zero_rows(const IdArgs& a, const OrderArgs& o, int64_t wg, int64_t wgs, int64_t pad,
+                                          void* dtable, int ddt)
+{
+    const int lane = threadIdx.x % 64, dim = a.dim, units = (dim + 7) >> 3;
+    const float zero[8] = {};
+    for (int64_t v0 = wg * kZeroRows; v0 < a.rows; v0 += wgs * kZeroRows) {
+        const int64_t mine = v0 + lane;
+        bool empty = false;
+        if (lane < kZeroRows && mine < a.rows) {
+            const int64_t s = slot_of(mine, o);
+            empty = mine == pad || gld<int32_t>(o.start + s) == gld<int32_t>(o.start + s + 1);
+        }
+        for (unsigned long long todo = __ballot(empty); todo; todo &= todo - 1) {
+            char* const row = static_cast<char*>(dtable) + (v0 + __builtin_ctzll(todo)) * dim * (ddt == DT_F32 ? 4 : 2);
+            for (int unit = threadIdx.x; unit < units; unit += 256)
+                store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, zero);
+        }
+    }
+}
 
 template <int GDT, bool TAIL>
 __global__ __launch_bounds__(256) void k_prepare_grad(IdArgs a, OrderArgs o, const void* __restrict__ dy,
@@ -405,24 +433,8 @@ __global__ __launch_bounds__(256) void k_prepare_grad(IdArgs a, OrderArgs o, con
         chunk_sums<GDT, TAIL>(a, o, dy, part, w / slices, (int)(w % slices) * 64 + lane);
         return;
     }
-    // zero rows, walking the table where a launch cannot hold as many workgroups
     wg -= chunk_wgs;
-    const int dim = a.dim, units = (dim + 7) >> 3;
-    const int64_t step = (int64_t)gridDim.x - list_wgs - chunk_wgs;
-    const float zero[8] = {};
-    for (int64_t v0 = wg * kZeroRows; v0 < a.rows; v0 += step * kZeroRows) {
-        const int64_t mine = v0 + lane;
-        bool empty = false;
-        if (lane < kZeroRows && mine < a.rows) {
-            const int64_t s = slot_of(mine, o);
-            empty = mine == pad || gld<int32_t>(o.start + s) == gld<int32_t>(o.start + s + 1);
-        }
-        for (unsigned long long todo = __ballot(empty); todo; todo &= todo - 1) {
-            char* const row = static_cast<char*>(dtable) + (v0 + __builtin_ctzll(todo)) * dim * (ddt == DT_F32 ? 4 : 2);
-            for (int unit = threadIdx.x; unit < units; unit += 256)
-                store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, zero);
-        }
-    }
+    zero_rows<TAIL>(a, o, wg, (int64_t)gridDim.x - list_wgs - chunk_wgs, pad, dtable, ddt);
 }
 
 // Joined sums of the long ids, 64 columns a wave, into the slot of the first
@@ -441,70 +453,131 @@ __global__ __launch_bounds__(256) void k_join_chunks(OrderArgs o, float* __restr
     }
 }
 
-// Long ids first, one wave per 64 columns; then the other listed ids, one wave
-// per id and 64 units.  A wave looks its next 64 tasks up at once (lane l the
-// l-th), and reads the first token of the next one before it sums the current:
-// most ids have few tokens, and a wave is bound by the latency of its reads.
+struct TableGradArgs {
+    const void* dy;
+    float* part;
+    void* dtable;
+    int64_t pad;
+    float scale;
+    int32_t accumulate, ddt, slices, work, zeros;
+};
+
+// One wave: the ordered tokens from c * chunk on, 64 units.  It sums, in order,
+//  - the ids whose tokens begin in its chunk and are no more than a chunk: their rows
+//    are written when their last token is added (up to one chunk further on);
+//  - the chunk's tokens of long ids, into the chunk's partial rows.
+// Lane l holds token c * chunk + l (two chunks are at most the 64 lanes) with the
+// range of its id; UN tokens' units are in flight while UN are added, whatever
+// ids they belong to.
 template <int GDT, bool TAIL>
-__global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, const void* __restrict__ dy,
-                                                    const float* __restrict__ part, int32_t slices, float scale,
-                                                    int64_t pad, int accumulate, void* __restrict__ dtable, int ddt)
+__device__ __forceinline__ void sum_chunk_rows(const IdArgs& a, const OrderArgs& o, const TableGradArgs& p, int64_t c,
+                                               int slice)
+{
+    constexpr int UN = GDT == DT_F32 ? 4 : 8;
+    const int lane = threadIdx.x % 64, dim = a.dim, units = (dim + 7) >> 3, unit = slice * 64 + lane;
+    const int32_t found = o.start[(int64_t(1) << o.log2g) * o.per];
+    if (c * o.chunk >= found) return;
+    const int32_t b = (int32_t)(c * o.chunk), at = b + lane;
+    const bool valid = at < found && lane < 2 * o.chunk;
+    const int32_t t = valid ? gld<int32_t>(o.order + at) : 0, id = valid ? gld<int32_t>(o.key + at) : 0;
+    int32_t lo = 0, hi = 0;
+    if (valid) {
+        const int64_t s = slot_of(id, o);
+        lo = gld<int32_t>(o.start + s);
+        hi = gld<int32_t>(o.start + s + 1);
+    }
+    const bool is_long = hi - lo > o.chunk;
+    const int32_t stop = is_long && hi > b + o.chunk ? b + o.chunk : hi;      // end of the id's tokens here
+    const bool mine = valid && (is_long ? at < b + o.chunk : lo >= b && lo < b + o.chunk);
+    const unsigned long long todo = __ballot(mine), ends = __ballot(mine && at == stop - 1);
+    const unsigned long long longs = __ballot(mine && is_long);
+    if (slice == 0 && mine && is_long && lo == at) o.longs[atomicAdd(&o.count[1], 1)] = id;
+    if (!todo) return;
+    const int i1 = 64 - __builtin_clzll(todo);
+    int i = __builtin_ctzll(todo);
+    Unit<GDT> u[UN];
+    auto load = [&](int k) {
+#pragma unroll
+        for (int q = 0; q < UN; ++q) {
+            // (a token beyond the last is read as the last: no branch, the same lines)
+            const int32_t row = __builtin_amdgcn_readlane(t, k + q < i1 ? k + q : i1 - 1);
+            u[q] = load_row_unit<GDT, TAIL, true>(static_cast<const char*>(p.dy) + (int64_t)row * dim * elem_bytes(GDT),
+                                                  unit, units, dim);
+        }
+    };
+    load(i);
+    float sum[8] = {};
+    for (; i < i1; i += UN) {
+        float v[UN][8];
+#pragma unroll
+        for (int q = 0; q < UN; ++q)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[q][j] = unit_at<GDT>(u[q], j);
+        if (i + UN < i1) load(i + UN);
+#pragma unroll
+        for (int q = 0; q < UN; ++q) {
+            if (i + q >= i1) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += v[q][j];
+            if (!((ends >> (i + q)) & 1)) continue;
+            if ((longs >> (i + q)) & 1) {
+                const int64_t padded = (int64_t)units * 8;
+                float* const out = p.part + chunk_slot((int32_t)c, __builtin_amdgcn_readlane(lo, i + q), o.chunk) * padded +
+                                   (int64_t)unit * 8;
+                if (unit < units) {
+                    gst<f32x4>(out, f32x4{sum[0], sum[1], sum[2], sum[3]});
+                    gst<f32x4>(out + 4, f32x4{sum[4], sum[5], sum[6], sum[7]});
+                }
+            } else {
+                const int64_t v0 = __builtin_amdgcn_readlane(id, i + q);
+                if (v0 != p.pad) {
+                    char* const row = static_cast<char*>(p.dtable) + v0 * dim * (p.ddt == DT_F32 ? 4 : 2);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] *= p.scale;
+                    if (p.accumulate) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < unit_count(unit, dim)) sum[j] += load1_rt(p.ddt, row, (int64_t)unit * 8 + j);
+                    }
+                    store_row_unit_rt<TAIL, true>(p.ddt, row, unit, units, dim, sum);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+        }
+    }
+}
+
+// Workgroups that sum (p.work of them, four waves each) and workgroups that
+// write zero rows (p.zeros) take turns while both last, so that waves that wait
+// for reads run beside waves that only write.
+template <int GDT, bool TAIL>
+__global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, TableGradArgs p)
+{
+    const int64_t b = blockIdx.x, both = p.work < p.zeros ? p.work : p.zeros;
+    const bool zero = b < 2 * both ? (b & 1) != 0 : p.work == both;
+    const int64_t wg = b < 2 * both ? b >> 1 : b - both;
+    if (zero) {
+        zero_rows<TAIL>(a, o, wg, p.zeros, p.pad, p.dtable, p.ddt);
+    } else {
+        const int64_t w = wg * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        sum_chunk_rows<GDT, TAIL>(a, o, p, w / p.slices, (int)(w % p.slices));
+    }
+}
+
+// The rows of the long ids, one wave per 64 columns.
+__global__ __launch_bounds__(256) void k_long_rows(OrderArgs o, int dim, TableGradArgs p)
 {
     const int lane = threadIdx.x % 64;
-    const int dim = a.dim, units = (dim + 7) >> 3;
-    const int64_t padded = (int64_t)units * 8;
-    const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int64_t step = (int64_t)gridDim.x * 4;
-    const int64_t groups = (dim + 63) / 64, joins = (int64_t)o.count[1] * groups;
-    for (int64_t w = wave; w < joins; w += step) {
+    const int64_t padded = (dim + 7) / 8 * 8, groups = (dim + 63) / 64, tasks = (int64_t)o.count[1] * groups;
+    for (int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64); w < tasks;
+         w += (int64_t)gridDim.x * 4) {
         const int64_t v = o.longs[w / groups], s = slot_of(v, o), col = w % groups * 64 + lane;
-        if (v == pad || col >= dim) continue;
-        float sum = join_column(part, o.chunk, o.start[s], o.start[s + 1], padded, col) * scale;
-        char* const row = static_cast<char*>(dtable) + v * dim * (ddt == DT_F32 ? 4 : 2);
-        if (accumulate) sum += load1_rt(ddt, row, col);
-        store1_rt(ddt, row, col, sum);
-    }
-    const int64_t tasks = (int64_t)o.count[0] * slices;
-    for (int64_t w0 = wave; w0 < tasks; w0 += 64 * step) {
-        const int64_t mine = w0 + lane * step;
-        int32_t id = 0, lo = 0, hi = 0, slice = 0, head = 0;
-        if (mine < tasks) {
-            id = gld<int32_t>(o.list + mine / slices);
-            slice = (int32_t)(mine % slices);
-            const int64_t s = slot_of(id, o);
-            lo = gld<int32_t>(o.start + s);
-            hi = gld<int32_t>(o.start + s + 1);
-            head = gld<int32_t>(o.order + lo);
-        }
-        auto load_head = [&](int i) {
-            const int32_t t = __builtin_amdgcn_readlane(head, i);
-            return load_row_unit<GDT, TAIL, true>(static_cast<const char*>(dy) + (int64_t)t * dim * elem_bytes(GDT),
-                                                  __builtin_amdgcn_readlane(slice, i) * 64 + lane, units, dim);
-        };
-        const int todo = tasks - w0 > 63 * step ? 64 : (int)((tasks - w0 + step - 1) / step);
-        Unit<GDT> next = load_head(0);
-        for (int i = 0; i < todo; ++i) {
-            const Unit<GDT> u = next;
-            if (i + 1 < todo) next = load_head(i + 1);
-            const int64_t v = __builtin_amdgcn_readlane(id, i);
-            const int32_t first = __builtin_amdgcn_readlane(lo, i), last = __builtin_amdgcn_readlane(hi, i);
-            if (v == pad || last - first > o.chunk) continue;
-            const int unit = __builtin_amdgcn_readlane(slice, i) * 64 + lane;
-            float sums[1][8];
-            float(&sum)[8] = sums[0];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] = unit_at<GDT>(u, j);
-            sum_tokens<GDT, TAIL, 64, 1, 8>(o.order, first + 1, last, dy, unit, units, dim, sums);
-            char* const row = static_cast<char*>(dtable) + v * dim * (ddt == DT_F32 ? 4 : 2);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] *= scale;
-            if (accumulate) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < unit_count(unit, dim)) sum[j] += load1_rt(ddt, row, (int64_t)unit * 8 + j);
-            }
-            store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, sum);
-        }
+        if (v == p.pad || col >= dim) continue;
+        float sum = join_column(p.part, o.chunk, o.start[s], o.start[s + 1], padded, col) * p.scale;
+        char* const row = static_cast<char*>(p.dtable) + v * dim * (p.ddt == DT_F32 ? 4 : 2);
+        if (p.accumulate) sum += load1_rt(p.ddt, row, col);
+        store1_rt(p.ddt, row, col, sum);
     }
 }
 
@@ -525,21 +598,28 @@ hipError_t prepare_grad_as(const IdArgs& a, const OrderArgs& o, const void* dy, 
     return a.dim % 8 ? go(k_prepare_grad<GDT, true>) : go(k_prepare_grad<GDT, false>);
 }
 
-// 8 workgroups per CU at most: a wave of 64 units in flight needs few registers.
-constexpr int64_t kTableGradWgs = 2048;
+// Workgroups for the columns of the long ids, 8 per CU at most.
+int long_wgs(const IdArgs& a, const OrderArgs& o)
+{
+    const int64_t wgs = (a.n / o.chunk * ((a.dim + 63) / 64) + 3) / 4;
+    return (int)(wgs < 2048 ? wgs : 2048);
+}
 
 template <int GDT>
-hipError_t table_grad_as(const IdArgs& a, const OrderArgs& o, const void* dy, const float* part, float scale,
-                         int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s)
+hipError_t table_grad_as(const IdArgs& a, const OrderArgs& o, TableGradArgs p, hipStream_t s)
 {
-    const int32_t slices = (a.dim + 511) / 512;
-    // a long id has over chunk tokens and dim / 64 waves' work: never more than its tokens' own
-    const int64_t wgs = (a.n * slices + 3) / 4;
-    auto go = [&](auto kernel) {
-        return launch_kernel(kernel, (int)(wgs < kTableGradWgs ? wgs : kTableGradWgs), s, a, o, dy, part,
-                             slices, scale, pad, accumulate ? 1 : 0, dtable, ddt);
-    };
-    return a.dim % 8 ? go(k_table_grad<GDT, true>) : go(k_table_grad<GDT, false>);
+    const int64_t most = int64_t(1) << 22, work = (chunk_count(a.n) * ((a.dim + 511) / 512) + 3) / 4;
+    int64_t zeros = p.accumulate ? 0 : (a.rows + kZeroRows - 1) / kZeroRows;
+    if (work > most) return hipErrorInvalidValue;
+    if (zeros > most) zeros = most;
+    p.slices = (a.dim + 511) / 512;
+    p.work = (int32_t)work;
+    p.zeros = (int32_t)zeros;
+    if (work + zeros == 0) return hipSuccess;
+    const hipError_t e = a.dim % 8 ? launch_kernel(k_table_grad<GDT, true>, (int)(work + zeros), s, a, o, p)
+                                   : launch_kernel(k_table_grad<GDT, false>, (int)(work + zeros), s, a, o, p);
+    if (e != hipSuccess || a.n <= o.chunk) return e;       // no id can be long
+    return launch_kernel(k_long_rows, long_wgs(a, o), s, o, a.dim, p);
 }
 
 }  // namespace
@@ -567,8 +647,7 @@ hipError_t launch_dequant_embedding(const IdArgs& a, const DequantDesc& t, int b
 hipError_t launch_order(const IdArgs& a, const OrderArgs& o, hipStream_t s)
 {
     const size_t lds = (size_t)kOrderWaves * o.per * sizeof(int32_t);
-    return a.id64 ? launch_kernel_lds(k_order<true>, 1 << o.log2g, kOrderWaves * 64, lds, s, a, o)
-                  : launch_kernel_lds(k_order<false>, 1 << o.log2g, kOrderWaves * 64, lds, s, a, o);
+    return launch_kernel_lds(a.id64 ? k_order<true> : k_order<false>, 1 << o.log2g, kOrderWaves * 64, lds, s, a, o);
 }
 
 hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part, int64_t pad,
@@ -581,19 +660,17 @@ hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void* 
 
 hipError_t launch_join_chunks(const IdArgs& a, const OrderArgs& o, float* part, hipStream_t s)
 {
-    if (a.n <= o.chunk) return hipSuccess;             // no id can have more tokens than a chunk
-    const int64_t padded = padded_dim(a.dim);
-    const int64_t wgs = (a.n / o.chunk * ((padded + 63) / 64) + 3) / 4;
-    return launch_kernel(k_join_chunks, (int)(wgs < kTableGradWgs ? wgs : kTableGradWgs), s, o, part, padded);
+    if (a.n <= o.chunk) return hipSuccess;             // no id can be long
+    return launch_kernel(k_join_chunks, long_wgs(a, o), s, o, part, padded_dim(a.dim));
 }
 
-hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, const float* part,
-                             float scale, int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s)
+hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part, float scale,
+                             int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s)
 {
-    if (a.n == 0) return hipSuccess;
-    if (gdt == DT_F32) return table_grad_as<DT_F32>(a, o, dy, part, scale, pad, accumulate, dtable, ddt, s);
-    if (gdt == DT_F16) return table_grad_as<DT_F16>(a, o, dy, part, scale, pad, accumulate, dtable, ddt, s);
-    return table_grad_as<DT_BF16>(a, o, dy, part, scale, pad, accumulate, dtable, ddt, s);
+    const TableGradArgs p{dy, part, dtable, pad, scale, accumulate ? 1 : 0, ddt, 0, 0, 0};
+    if (gdt == DT_F32) return table_grad_as<DT_F32>(a, o, p, s);
+    if (gdt == DT_F16) return table_grad_as<DT_F16>(a, o, p, s);
+    return table_grad_as<DT_BF16>(a, o, p, s);
 }
 
 }  // namespace qb

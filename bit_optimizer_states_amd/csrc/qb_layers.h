@@ -25,15 +25,17 @@ struct IdArgs {
 // = id mod 2^log2g, entry = id >> log2g (`per` entries a class): frequent
 // tokens have small ids in common vocabularies, and neighbouring ids land in
 // different classes.  start[class * per + entry] .. start[... + 1] is the range of
-// the id's tokens in `order`, which lists their positions in ascending order.
-// `list` holds the count[0] ids that have tokens, `longs` the count[1] ids that
-// have more than `chunk` of them.
+// the id's tokens in `order`, which lists their positions in ascending order;
+// `key` lists their ids.
+// `list` holds the count[0] ids that have tokens, each as {id, begin, end, first
+// position}, `longs` the count[1] ids that have more than `chunk` tokens.
 struct OrderArgs {
     int32_t* start;      // [classes * per + 1]
     int32_t* order;      // [n]
+    int32_t* key;        // [n]
     int32_t* used;       // [2 * classes] ids with tokens, and with more than a chunk, per class
     int32_t* count;      // [2]
-    int32_t* list;       // [min(n, rows)]
+    int32_t* list;       // [4 * min(n, rows)]
     int32_t* longs;      // [n / chunk + 1]
     int32_t log2g;
     int32_t per;
@@ -55,16 +57,11 @@ constexpr int32_t order_log2g(int64_t rows)
 constexpr int64_t order_per(int64_t rows) { return (rows + (int64_t(1) << order_log2g(rows)) - 1) >> order_log2g(rows); }
 
 // Tokens per chunk of the ordered list: an id with more tokens than this is
-// summed chunk by chunk, then joined.
-#ifndef QB_CHUNK_MIN
-#define QB_CHUNK_MIN 32
+// summed chunk by chunk, then joined.  Two chunks fit the lanes of a wave.
+#ifndef QB_CHUNK_AT
+#define QB_CHUNK_AT 16384
 #endif
-constexpr int32_t chunk_tokens(int64_t n)
-{
-    int32_t c = QB_CHUNK_MIN;
-    while (c < 512 && (int64_t)c * c * 16 < n) c *= 2;
-    return c;
-}
+constexpr int32_t chunk_tokens(int64_t n) { return n < QB_CHUNK_AT ? 16 : 32; }
 constexpr int64_t chunk_count(int64_t n) { return (n + chunk_tokens(n) - 1) / chunk_tokens(n); }
 constexpr int64_t padded_dim(int64_t dim) { return (dim + 7) / 8 * 8; }
 
@@ -118,13 +115,14 @@ hipError_t launch_embedding(const IdArgs& a, const void* table, int tdt, float s
 hipError_t launch_dequant_embedding(const IdArgs& a, const DequantDesc& t, int bits, int code4, int B, int B2,
                                     float scale, void* y, int ydt, hipStream_t s);
 
-// start, order of the ids.
+// start, order, key of the ids.
 hipError_t launch_order(const IdArgs& a, const OrderArgs& o, hipStream_t s);
 
 // Joins the chunks' sums of the long ids, each into the slot of its first chunk.
 hipError_t launch_join_chunks(const IdArgs& a, const OrderArgs& o, float* part, hipStream_t s);
 
-// The second step of a gradient, one launch of three kinds of workgroups:
+// The second step of a stable embedding's gradient, one launch of three kinds of
+// workgroups:
 //  - the list of the ids that have tokens;
 //  - sums of dy over the chunks' tokens of ids that have more tokens than a
 //    chunk: part[2 * chunk] for an id whose tokens begin at or before the chunk's
@@ -136,9 +134,10 @@ hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void* 
                                bool accumulate, void* dtable, int ddt, hipStream_t s);
 
 // dtable[v] = scale * sum of dy over the tokens of v (+ dtable[v] with
-// accumulate) for the listed ids but pad.
-hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, const float* part,
-                             float scale, int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s);
+// accumulate), zeros for the other rows: one launch, and one that joins the long
+// ids' sums (part as above).
+hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part, float scale,
+                             int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s);
 
 struct NormArgs {
     const void* gamma;      // nullptr: ones

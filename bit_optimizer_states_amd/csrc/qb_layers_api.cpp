@@ -48,7 +48,7 @@ bool valid_eps(double eps) { return std::isfinite(eps) && (float)eps >= 0x1p-126
 // Workspace of a table's gradient: the arrays of OrderArgs, the chunks' sums; then
 // (stable) the partial sums of dgamma and dbeta.
 struct GradLayout {
-    size_t order, used, list, longs, chunks, parts, bytes;
+    size_t order, key, used, list, longs, chunks, parts, bytes;
 };
 
 GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim, int parts)
@@ -56,9 +56,10 @@ GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim, int parts)
     GradLayout l;
     const int64_t classes = int64_t(1) << order_log2g(rows), entries = classes * order_per(rows) + 1;
     l.order = round_up((size_t)entries * sizeof(int32_t), 256);
-    l.used = l.order + round_up((size_t)n * sizeof(int32_t), 256);
+    l.key = l.order + round_up((size_t)n * sizeof(int32_t), 256);
+    l.used = l.key + round_up((size_t)n * sizeof(int32_t), 256);
     l.list = l.used + round_up((size_t)(2 * classes + 2) * sizeof(int32_t), 256);
-    l.longs = l.list + round_up((size_t)(n < rows ? n : rows) * sizeof(int32_t), 256);
+    l.longs = l.list + round_up((size_t)(n < rows ? n : rows) * 4 * sizeof(int32_t), 256);
     l.chunks = l.longs + round_up((size_t)(n / chunk_tokens(n) + 1) * sizeof(int32_t), 256);
     l.parts = l.chunks + (size_t)(2 * chunk_count(n) * padded_dim(dim)) * sizeof(float);
     l.bytes = l.parts + (size_t)parts * 2 * (size_t)padded_dim(dim) * sizeof(float);
@@ -69,7 +70,8 @@ OrderArgs order_args(void* ws, const GradLayout& l, int64_t n, int64_t rows)
 {
     char* const w = static_cast<char*>(ws);
     int32_t* const used = reinterpret_cast<int32_t*>(w + l.used);
-    return OrderArgs{reinterpret_cast<int32_t*>(w), reinterpret_cast<int32_t*>(w + l.order), used,
+    return OrderArgs{reinterpret_cast<int32_t*>(w), reinterpret_cast<int32_t*>(w + l.order),
+                     reinterpret_cast<int32_t*>(w + l.key), used,
                      used + (int64_t(2) << order_log2g(rows)), reinterpret_cast<int32_t*>(w + l.list),
                      reinterpret_cast<int32_t*>(w + l.longs), order_log2g(rows), (int32_t)order_per(rows),
                      chunk_tokens(n)};
@@ -165,8 +167,6 @@ qb_status qb_embedding_backward(const void* dy, qb_dtype gdt, const void* ids, q
     float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + l.chunks);
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = launch_order(a, o, s);
-    if (e == hipSuccess)
-        e = launch_prepare_grad(a, o, dy, (int)gdt, part, padding_id, accumulate != 0, dtable, (int)ddt, s);
     if (e == hipSuccess)
         e = launch_table_grad(a, o, dy, (int)gdt, part, (float)scale, padding_id, accumulate != 0, dtable, (int)ddt, s);
     return hip_status(e);

@@ -52,21 +52,26 @@ hipError_t launch_order(const IdArgs& a, const OrderArgs& o, hipStream_t)
     if (classes * o.per < (double)a.rows || o.per > kOrderPerMax || o.per < 1) ++failures;
     inside(o.start, (classes * o.per + 1) * 4);
     inside(o.order, (double)a.n * 4);
+    inside(o.key, (double)a.n * 4);
+    if (o.chunk < 1 || o.chunk > 32) ++failures;       // two chunks are one wave's lanes
     return done();
 }
-hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void*, int, float* part, int64_t, bool,
-                               void*, int, hipStream_t)
+hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void*, int, float* part, int64_t,
+                               bool, void*, int, hipStream_t)
 {
     inside(o.used, (double)(int64_t(2) << o.log2g) * 4);
     inside(o.count, 8);
     inside(o.longs, (double)(a.n / o.chunk + 1) * 4);
-    inside(o.list, (double)(a.n < a.rows ? a.n : a.rows) * 4);
+    inside(o.list, (double)(a.n < a.rows ? a.n : a.rows) * 16);
     inside(part, 2.0 * (double)chunk_count(a.n) * (double)padded_dim(a.dim) * 4);
     return done();
 }
-hipError_t launch_table_grad(const IdArgs&, const OrderArgs&, const void*, int, const float*, float, int64_t, bool,
+hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void*, int, float* part, float, int64_t, bool,
                              void*, int, hipStream_t)
 {
+    inside(o.count, 8);
+    inside(o.longs, (double)(a.n / o.chunk + 1) * 4);
+    inside(part, 2.0 * (double)chunk_count(a.n) * (double)padded_dim(a.dim) * 4);
     return done();
 }
 hipError_t launch_join_chunks(const IdArgs&, const OrderArgs&, float*, hipStream_t) { return done(); }

@@ -140,9 +140,9 @@ def test_workspace_sizes(qb):
         assert L.qb_stable_embedding_workspace_bytes(n, rows, dim) == 0
     assert L.qb_stable_embedding_workspace_bytes(1, 10, 16385) == 0
     assert L.qb_layer_norm_workspace_bytes(-1, 8) == 0 and L.qb_layer_norm_workspace_bytes(8, 0) == 0
-    # entries of the table, order of the tokens, used and long ids (per class and as lists), two rows of sums per
+    # entries of the table, order and ids of the tokens, used and long ids (per class and as lists), two rows of sums per
     # chunk of 32 tokens
-    want = sum(-(-4 * words // 256) * 256 for words in (256 * 125 + 1, 16384, 514, 16384, 513)) + 2 * 512 * 4096 * 4
+    want = sum(-(-4 * words // 256) * 256 for words in (256 * 125 + 1, 16384, 16384, 514, 4 * 16384, 513)) + 2 * 512 * 4096 * 4
     assert L.qb_embedding_workspace_bytes(16384, 32000, 4096) == want
     # partial sums of dgamma and dbeta of at most 256 workgroups, rows padded to 8 elements
     assert L.qb_layer_norm_workspace_bytes(16384, 4093) == 256 * 2 * 4096 * 4
