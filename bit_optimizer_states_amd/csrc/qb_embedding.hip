@@ -548,19 +548,18 @@ __device__ __forceinline__ void sum_chunk_rows(const IdArgs& a, const OrderArgs&
     }
 }
 
-// Workgroups that sum (p.work of them, four waves each) and workgroups that
-// write zero rows (p.zeros) take turns while both last, so that waves that wait
-// for reads run beside waves that only write.
+// p.work workgroups that sum (four waves each), then p.zeros that write zero
+// rows: the summing waves, which wait for chains of reads, start first and the
+// writes fill the time around them (16384 tokens of natural frequencies into [32000,
+// 4096] bf16: 80 us; taking turns 86, in two launches 54 + 33).
 template <int GDT, bool TAIL>
 __global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, TableGradArgs p)
 {
-    const int64_t b = blockIdx.x, both = p.work < p.zeros ? p.work : p.zeros;
-    const bool zero = b < 2 * both ? (b & 1) != 0 : p.work == both;
-    const int64_t wg = b < 2 * both ? b >> 1 : b - both;
-    if (zero) {
-        zero_rows<TAIL>(a, o, wg, p.zeros, p.pad, p.dtable, p.ddt);
+    const int64_t b = blockIdx.x;
+    if (b >= p.work) {
+        zero_rows<TAIL>(a, o, b - p.work, p.zeros, p.pad, p.dtable, p.ddt);
     } else {
-        const int64_t w = wg * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        const int64_t w = b * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
         sum_chunk_rows<GDT, TAIL>(a, o, p, w / p.slices, (int)(w % p.slices));
     }
 }

@@ -39,21 +39,10 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* slot)
             slot[2 * w + 1] = b;
         }
         lds_barrier();
-        float s[W], t[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            s[i] = slot[2 * i];
-            t[i] = slot[2 * i + 1];
-        }
-#pragma unroll
-        for (int h = W / 2; h > 0; h /= 2)
-#pragma unroll
-            for (int i = 0; i < h; ++i) {
-                s[i] += s[i + h];
-                t[i] += t[i + h];
-            }
-        a = s[0];
-        b = t[0];
+        // lane l takes wave l % W's sums: two reads and log2 W steps for all of them
+        const int l = threadIdx.x % W;
+        a = group_sum<W>(slot[2 * l]);
+        b = group_sum<W>(slot[2 * l + 1]);
     }
 }
 
@@ -71,7 +60,7 @@ __device__ __forceinline__ float inv_deviation(float var, float eps)
 template <int TPR, int VPT>
 struct RowShape {
     static constexpr int L = TPR < 64 ? TPR : 64, W = TPR < 64 ? 1 : TPR / 64;
-    float held[W];           // elements of each wave
+    float held;              // elements of wave (lane % W)
     float inv_mine;          // 1 / elements of this wave (0 where it has none)
     float inv_dim;
     int wave;
@@ -80,6 +69,7 @@ struct RowShape {
     {
         wave = W == 1 ? 0 : __builtin_amdgcn_readfirstlane(lane / 64);
         float mine = 0.0f;
+        held = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             int n = 0;
@@ -88,8 +78,8 @@ struct RowShape {
                 const int left = dim - (k * TPR + w * L) * 8;
                 n += left < 0 ? 0 : left > L * 8 ? L * 8 : left;
             }
-            held[w] = (float)n;
-            mine = w == wave ? held[w] : mine;
+            held = w == lane % W ? (float)n : held;
+            mine = w == wave ? (float)n : mine;
         }
         inv_mine = mine > 0.0f ? 1.0f / mine : 0.0f;
         inv_dim = 1.0f / (float)dim;
@@ -164,17 +154,13 @@ __device__ __forceinline__ void row_stats(const float (&x)[VPT][8], const RowSha
         lds_barrier();
         // differences from wave 0's mean (it holds elements in every row): the join keeps
         // the digits that the waves' means share.  A wave without elements has mean 0, weight 0.
+        // Lane l takes wave l % W.
+        const int l = threadIdx.x % W;
         const float m00 = slot[0], c00 = EXACT ? slot[2] : 0.0f;
-        float dm = 0.0f, dq = 0.0f, q = slot[1];
-#pragma unroll
-        for (int i = 1; i < W; ++i) {
-            float d = slot[S * i] - m00;
-            if constexpr (EXACT) d += slot[S * i + 2] - c00;
-            const float nd = shape.held[i] * d;
-            dm += nd;
-            dq = __builtin_fmaf(nd, d, dq);
-            q += slot[S * i + 1];
-        }
+        float d = slot[S * l] - m00;
+        if constexpr (EXACT) d += slot[S * l + 2] - c00;
+        const float nd = shape.held * d;
+        const float dm = group_sum<W>(nd), dq = group_sum<W>(nd * d), q = group_sum<W>(slot[S * l + 1]);
         const float shift = dm * shape.inv_dim;
         m = m00 + (c00 + shift);
         m2 = q + (dq - dm * shift);

@@ -215,6 +215,18 @@ __device__ __forceinline__ float lanes_sum(float v)
     return v;
 }
 
+// Sum over aligned groups of W lanes (a power of two up to 16), the same bits in
+// every lane of the group.
+template <int W>
+__device__ __forceinline__ float group_sum(float v)
+{
+    if constexpr (W >= 2) v = dpp_add<0xB1>(v);
+    if constexpr (W >= 4) v = dpp_add<0x4E>(v);
+    if constexpr (W >= 8) v = dpp_add<0x141>(v);
+    if constexpr (W >= 16) v = dpp_add<0x140>(v);
+    return v;
+}
+
 // Workgroup barrier that orders LDS accesses only: global loads and stores stay in flight across it.
 __device__ __forceinline__ void lds_barrier()
 {
