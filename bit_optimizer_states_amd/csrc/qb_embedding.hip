@@ -390,8 +390,6 @@ __device__ __forceinline__ void chunk_sums(const IdArgs& a, const OrderArgs& o, 
     }
 }
 
-constexpr int kZeroRows = 16;           // table rows of a zero-filling workgroup
-
 // One workgroup of 256 threads: zeros into the empty ones of kZeroRows rows at a
 // time, workgroup wg of wgs.
 template <bool TAIL>
@@ -597,6 +595,38 @@ hipError_t prepare_grad_as(const IdArgs& a, const OrderArgs& o, const void* dy, 
     return a.dim % 8 ? go(k_prepare_grad<GDT, true>) : go(k_prepare_grad<GDT, false>);
 }
 
+// Few tokens: workgroup (t, slice) of 256 units works if token t is the first of
+// its id; workgroups beyond the tokens' write zero rows.
+template <int GDT, bool TAIL>
+__global__ __launch_bounds__(256) void k_table_grad_direct(IdArgs a, const void* __restrict__ dy, float scale, int64_t pad,
+                                                           int accumulate, void* __restrict__ dtable, int ddt,
+                                                           int32_t slices)
+{
+    const DirectIds ids(a);
+    const int dim = a.dim, units = (dim + 7) >> 3;
+    const int64_t work = a.n * slices;
+    if (blockIdx.x >= work) {
+        zero_unnamed<TAIL, 256>(a, ids, (blockIdx.x - work) * kZeroRows, pad, dtable, ddt);
+        return;
+    }
+    const int t = (int)(blockIdx.x / slices), unit = (int)(blockIdx.x % slices) * 256 + threadIdx.x;
+    const int32_t v = ids.of(t);
+    const unsigned long long m0 = ids.tokens(0, v), m1 = ids.tokens(1, v);
+    if (v < 0 || v == pad || (m0 ? __builtin_ctzll(m0) : 64 + __builtin_ctzll(m1)) != t) return;
+    float sum[1][8] = {};
+    sum_masked<GDT, TAIL, 256, 1, 8>(m0, 0, dy, unit, units, dim, sum);
+    sum_masked<GDT, TAIL, 256, 1, 8>(m1, 1, dy, unit, units, dim, sum);
+    char* const row = static_cast<char*>(dtable) + (int64_t)v * dim * (ddt == DT_F32 ? 4 : 2);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[0][j] *= scale;
+    if (accumulate) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < unit_count(unit, dim)) sum[0][j] += load1_rt(ddt, row, (int64_t)unit * 8 + j);
+    }
+    store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, sum[0]);
+}
+
 // Workgroups for the columns of the long ids, 8 per CU at most.
 int long_wgs(const IdArgs& a, const OrderArgs& o)
 {
@@ -655,6 +685,19 @@ hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void* 
     if (gdt == DT_F32) return prepare_grad_as<DT_F32>(a, o, dy, part, pad, accumulate, dtable, ddt, s);
     if (gdt == DT_F16) return prepare_grad_as<DT_F16>(a, o, dy, part, pad, accumulate, dtable, ddt, s);
     return prepare_grad_as<DT_BF16>(a, o, dy, part, pad, accumulate, dtable, ddt, s);
+}
+
+hipError_t launch_table_grad_direct(const IdArgs& a, const void* dy, int gdt, float scale, int64_t pad,
+                                    bool accumulate, void* dtable, int ddt, hipStream_t s)
+{
+    const int64_t slices = (a.dim + 2047) / 2048, grid = a.n * slices + direct_zero_wgs(a.rows, accumulate);
+    auto go = [&](auto kernel) {
+        return launch_kernel(kernel, (int)grid, s, a, dy, scale, pad, accumulate ? 1 : 0, dtable, ddt, (int32_t)slices);
+    };
+    const bool tail = a.dim % 8 != 0;
+    if (gdt == DT_F32) return tail ? go(k_table_grad_direct<DT_F32, true>) : go(k_table_grad_direct<DT_F32, false>);
+    if (gdt == DT_F16) return tail ? go(k_table_grad_direct<DT_F16, true>) : go(k_table_grad_direct<DT_F16, false>);
+    return tail ? go(k_table_grad_direct<DT_BF16, true>) : go(k_table_grad_direct<DT_BF16, false>);
 }
 
 hipError_t launch_join_chunks(const IdArgs& a, const OrderArgs& o, float* part, hipStream_t s)

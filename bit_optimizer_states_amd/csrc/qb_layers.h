@@ -139,6 +139,14 @@ hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void* 
 hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part, float scale,
                              int64_t pad, bool accumulate, void* dtable, int ddt, hipStream_t s);
 
+// Up to kDirectTokens tokens take no ordering: one launch, in which the first token
+// of each id sums the id's tokens (a wave holds all ids in two registers a lane).
+// A call of few tokens is bound by its launches, about 2.5 us each on the host.
+constexpr int64_t kDirectTokens = 128;
+constexpr bool takes_direct(int64_t n, int64_t rows) { return n > 0 && n <= kDirectTokens && rows < (int64_t(1) << 24); }
+hipError_t launch_table_grad_direct(const IdArgs& a, const void* dy, int gdt, float scale, int64_t pad,
+                                    bool accumulate, void* dtable, int ddt, hipStream_t s);
+
 struct NormArgs {
     const void* gamma;      // nullptr: ones
     const void* beta;       // nullptr: zeros
@@ -165,6 +173,11 @@ hipError_t launch_layer_norm_grad(const void* dy, const void* x, int xdt, int64_
 hipError_t launch_stable_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, const float* chunk_part,
                               const void* table, int tdt, float scale, const NormArgs& w, int64_t pad,
                               bool accumulate, void* dtable, int ddt, float* part, int parts, hipStream_t s);
+
+// The same for up to kDirectTokens tokens, with one partial sum per token.
+hipError_t launch_stable_grad_direct(const IdArgs& a, const void* dy, int gdt, const void* table, int tdt, float scale,
+                                     const NormArgs& w, int64_t pad, bool accumulate, void* dtable, int ddt,
+                                     float* part, hipStream_t s);
 
 // dgamma, dbeta (either may be nullptr) = the sum of `parts` partial sums.
 hipError_t launch_join_parts(const float* part, int parts, int64_t dim, bool accumulate, void* dgamma, void* dbeta,

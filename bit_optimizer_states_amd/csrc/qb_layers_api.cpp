@@ -163,9 +163,12 @@ qb_status qb_embedding_backward(const void* dy, qb_dtype gdt, const void* ids, q
     const GradLayout l = grad_layout(n, rows, dim, 0);
     if (ws_bytes < l.bytes) return QB_EWORKSPACE;
     const IdArgs a = id_args(ids, idt, n, rows, dim);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (takes_direct(n, rows))
+        return hip_status(launch_table_grad_direct(a, dy, (int)gdt, (float)scale, padding_id, accumulate != 0, dtable,
+                                                   (int)ddt, s));
     const OrderArgs o = order_args(ws, l, n, rows);
     float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + l.chunks);
-    hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = launch_order(a, o, s);
     if (e == hipSuccess)
         e = launch_table_grad(a, o, dy, (int)gdt, part, (float)scale, padding_id, accumulate != 0, dtable, (int)ddt, s);
@@ -275,16 +278,19 @@ qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void*
     float* const chunks = reinterpret_cast<float*>(w + l.chunks);
     float* const part = reinterpret_cast<float*>(w + l.parts);
     hipStream_t s = static_cast<hipStream_t>(stream);
+    const NormArgs norm{gamma, nullptr, (int)wdt, (float)eps};
     hipError_t e = hipSuccess;
-    if (rows > 0) {
+    if (rows > 0 && takes_direct(n, rows)) {
+        e = launch_stable_grad_direct(a, dy, (int)gdt, table, (int)tdt, (float)scale, norm, padding_id, accumulate != 0,
+                                      dtable, (int)ddt, part, s);
+    } else if (rows > 0) {
         e = launch_order(a, o, s);
         if (e == hipSuccess)
             e = launch_prepare_grad(a, o, dy, (int)gdt, chunks, padding_id, accumulate != 0, dtable, (int)ddt, s);
         if (e == hipSuccess) e = launch_join_chunks(a, o, chunks, s);
         if (e == hipSuccess)
             e = launch_stable_grad(a, o, dy, (int)gdt, chunks, table, (int)tdt, (float)scale,
-                                   NormArgs{gamma, nullptr, (int)wdt, (float)eps}, padding_id, accumulate != 0, dtable,
-                                   (int)ddt, part, parts, s);
+                                   norm, padding_id, accumulate != 0, dtable, (int)ddt, part, parts, s);
     }
     if (e == hipSuccess) e = launch_join_parts(part, parts, dim, accumulate != 0, dgamma, dbeta, (int)wdt, s);
     return hip_status(e);

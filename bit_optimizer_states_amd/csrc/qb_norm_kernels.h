@@ -20,30 +20,40 @@
 
 namespace qb {
 
-// Two sums over the TPR threads that share a row, with one barrier: within a
-// wave by DPP, over the row's waves through LDS (slot: 2 * TPR / 64 words that no
-// other sum uses before the next-but-one barrier).
+// Two sums over the TPR threads that share a row: within a wave by DPP, then
+// over the row's waves through LDS (slot: 2 * TPR / 64 words that no other sum uses
+// before the next-but-one barrier), in two parts with a barrier between them.
 template <int TPR>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float* slot)
+__device__ __forceinline__ void put_sum2(float& a, float& b, float* slot)
 {
-    if constexpr (TPR <= 64) {
-        a = lanes_sum<TPR>(a);
-        b = lanes_sum<TPR>(b);
-    } else {
-        constexpr int W = TPR / 64;
-        a = lanes_sum<64>(a);
-        b = lanes_sum<64>(b);
+    constexpr int L = TPR < 64 ? TPR : 64;
+    a = lanes_sum<L>(a);
+    b = lanes_sum<L>(b);
+    if (TPR > 64 && threadIdx.x % 64 == 0) {
         const int w = (threadIdx.x % TPR) / 64;
-        if (threadIdx.x % 64 == 0) {
-            slot[2 * w] = a;
-            slot[2 * w + 1] = b;
-        }
-        lds_barrier();
+        slot[2 * w] = a;
+        slot[2 * w + 1] = b;
+    }
+}
+
+template <int TPR>
+__device__ __forceinline__ void join_sum2(float& a, float& b, const float* slot)
+{
+    if constexpr (TPR > 64) {
         // lane l takes wave l % W's sums: two reads and log2 W steps for all of them
+        constexpr int W = TPR / 64;
         const int l = threadIdx.x % W;
         a = group_sum<W>(slot[2 * l]);
         b = group_sum<W>(slot[2 * l + 1]);
     }
+}
+
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float* slot)
+{
+    put_sum2<TPR>(a, b, slot);
+    if constexpr (TPR > 64) lds_barrier();
+    join_sum2<TPR>(a, b, slot);
 }
 
 constexpr int row_slot_words(int tpr) { return tpr <= 64 ? 1 : 3 * (tpr / 64); }
@@ -95,17 +105,21 @@ __device__ __forceinline__ bool whole_step(int k, int dim)
 
 // Mean and 1/sqrt(var + eps) of a row spread over TPR threads, unit k * TPR +
 // lane in x[k] (zeros beyond the row).  Each wave takes the mean and the squared
-// deviation of its own elements, which are then joined over the row's waves (one
-// barrier) as those of parts of a sample:
+// deviation of its own elements (wave_stats), which are then joined over the row's
+// waves (join_stats, behind one barrier) as those of parts of a sample:
 //   mean = sum n_w mean_w / dim,  M2 = sum (M2_w + n_w (mean_w - mean)^2).
 // EXACT (binary32 rows): a wave's mean is corrected by the mean of the rounded
 // differences, so that a row whose mean is large against its spread keeps its
 // digits; 16-bit elements have no such digits.
+struct WaveStats {
+    float m0, c, m2;          // mean m0 + c (not rounded to one binary32), squared deviation
+};
+
 template <int TPR, int VPT, bool EXACT>
-__device__ __forceinline__ void row_stats(const float (&x)[VPT][8], const RowShape<TPR, VPT>& shape, int lane, int dim,
-                                          float eps, float* slot, float* mean, float* rstd)
+__device__ __forceinline__ WaveStats wave_stats(const float (&x)[VPT][8], const RowShape<TPR, VPT>& shape, int lane,
+                                                int dim)
 {
-    constexpr int L = RowShape<TPR, VPT>::L, W = RowShape<TPR, VPT>::W;
+    constexpr int L = RowShape<TPR, VPT>::L;
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
@@ -137,21 +151,34 @@ __device__ __forceinline__ void row_stats(const float (&x)[VPT][8], const RowSha
         if constexpr (EXACT) sd += ud;
         sq += uq;
     }
-    float m2 = lanes_sum<L>(sq), c = 0.0f;
+    WaveStats w{m0, 0.0f, lanes_sum<L>(sq)};
     if constexpr (EXACT) {
         sd = lanes_sum<L>(sd);
-        c = sd * shape.inv_mine;               // the wave's mean is m0 + c, not rounded to one binary32 here
-        m2 -= sd * c;
+        w.c = sd * shape.inv_mine;
+        w.m2 -= sd * w.c;
     }
-    float m = m0 + c;
+    return w;
+}
+
+// Leaves a wave's share in the row's slot (row_slot_words(TPR) words).
+template <int TPR, int VPT, bool EXACT>
+__device__ __forceinline__ void put_stats(const WaveStats& w, const RowShape<TPR, VPT>& shape, float* slot)
+{
+    constexpr int S = EXACT ? 3 : 2;
+    if (RowShape<TPR, VPT>::W > 1 && threadIdx.x % 64 == 0) {
+        slot[S * shape.wave] = w.m0;
+        slot[S * shape.wave + 1] = w.m2;
+        if constexpr (EXACT) slot[S * shape.wave + 2] = w.c;
+    }
+}
+
+template <int TPR, int VPT, bool EXACT>
+__device__ __forceinline__ void join_stats(const WaveStats& w, const RowShape<TPR, VPT>& shape, float eps,
+                                           const float* slot, float* mean, float* rstd)
+{
+    constexpr int W = RowShape<TPR, VPT>::W, S = EXACT ? 3 : 2;
+    float m = w.m0 + w.c, m2 = w.m2;
     if constexpr (W > 1) {
-        constexpr int S = EXACT ? 3 : 2;
-        if (threadIdx.x % 64 == 0) {
-            slot[S * shape.wave] = m0;
-            slot[S * shape.wave + 1] = m2;
-            if constexpr (EXACT) slot[S * shape.wave + 2] = c;
-        }
-        lds_barrier();
         // differences from wave 0's mean (it holds elements in every row): the join keeps
         // the digits that the waves' means share.  A wave without elements has mean 0, weight 0.
         // Lane l takes wave l % W.
@@ -167,6 +194,16 @@ __device__ __forceinline__ void row_stats(const float (&x)[VPT][8], const RowSha
     }
     *mean = m;
     *rstd = inv_deviation(m2 * shape.inv_dim, eps);
+}
+
+template <int TPR, int VPT, bool EXACT>
+__device__ __forceinline__ void row_stats(const float (&x)[VPT][8], const RowShape<TPR, VPT>& shape, int lane, int dim,
+                                          float eps, float* slot, float* mean, float* rstd)
+{
+    const WaveStats w = wave_stats<TPR, VPT, EXACT>(x, shape, lane, dim);
+    put_stats<TPR, VPT, EXACT>(w, shape, slot);
+    if constexpr (TPR > 64) lds_barrier();
+    join_stats<TPR, VPT, EXACT>(w, shape, eps, slot, mean, rstd);
 }
 
 // Threads of a workgroup: a row that waves share has one to itself.

@@ -32,20 +32,36 @@ struct StableGradArgs {
     int32_t wdt, ddt, accumulate;
 };
 
-// TPR threads (one workgroup) to a listed id; a workgroup walks the list by
-// the grid, looks its next 64 ids up at once (lane l the l-th), and reads the
-// next id's row and first token before it works on the current one.
+// Work on single ids by a whole workgroup: TPR threads, unit k * TPR + tid in
+// register k, the sums of dgamma and dbeta over the workgroup's ids.
 template <int GDT, int TDT, int TPR, int VPT, bool TAIL>
-__global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, StableGradArgs p)
-{
-    __shared__ float s_slot[2 * row_slot_words(TPR)];
-    const int dim = a.dim, units = (dim + 7) >> 3;
-    const int64_t padded = (int64_t)units * 8;
-    const int tid = threadIdx.x, lane = tid % 64;
-    const int32_t count = o.count[0], step = (int32_t)gridDim.x;
+struct StableRows {
+    const IdArgs& a;
+    const StableGradArgs& p;
+    float* slot;
+    const int dim, units, tid;
+    const RowShape<TPR, VPT> shape;
     float gam[VPT][8], accg[VPT][8] = {}, accb[VPT][8] = {};
-    auto load_gamma = [&](auto wdt) {
-        constexpr int WDT = decltype(wdt)::value;
+
+    __device__ __forceinline__ StableRows(const IdArgs& a_, const StableGradArgs& p_, float* slot_)
+        : a(a_), p(p_), slot(slot_), dim(a_.dim), units((a_.dim + 7) >> 3), tid(threadIdx.x),
+          shape(threadIdx.x, a_.dim)
+    {
+        if (!p.gamma) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) gam[k][j] = 1.0f;
+        } else if (p.wdt == DT_F32) {
+            load_gamma<DT_F32>();
+        } else {
+            load_gamma<TDT>();
+        }
+    }
+
+    template <int WDT>
+    __device__ __forceinline__ void load_gamma()
+    {
         Unit<WDT> u[VPT];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) u[k] = load_row_unit<WDT, TAIL, false>(p.gamma, k * TPR + tid, units, dim);
@@ -53,19 +69,107 @@ __global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, Stab
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
             for (int j = 0; j < 8; ++j) gam[k][j] = unit_at<WDT>(u[k], j);
-    };
-    if (!p.gamma) {
+    }
+
+    __device__ __forceinline__ void load_table(Unit<TDT> (&w)[VPT], int64_t v)
+    {
+        const char* const row = static_cast<const char*>(p.table) + v * dim * elem_bytes(TDT);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) w[k] = load_row_unit<TDT, TAIL, true>(row, k * TPR + tid, units, dim);
+    }
+
+    // The id's row and its sum S_v: adds to dgamma and dbeta, writes dtable[v].
+    __device__ __forceinline__ void finish(int64_t v, const Unit<TDT> (&w)[VPT], float (&sum)[VPT][8])
+    {
+        float x[VPT][8];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[k][j] = unit_at<TDT>(w[k], j) * p.scale;
+            if (!whole_step<TPR>(k, dim) && k * TPR + tid >= units) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[k][j] = sum[k][j] = 0.0f;
+            }
+        }
+        float mean, rstd;
+        row_stats<TPR, VPT, TDT == DT_F32>(x, shape, tid, dim, p.eps, slot, &mean, &rstd);
+        float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) gam[k][j] = 1.0f;
-    } else if (p.wdt == DT_F32) {
-        load_gamma(std::integral_constant<int, DT_F32>{});
-    } else {
-        load_gamma(std::integral_constant<int, TDT>{});
+            for (int j = 0; j < 8; ++j) {
+                const float d = sum[k][j], h = (x[k][j] - mean) * rstd, g = d * gam[k][j];
+                sum[k][j] = g;
+                x[k][j] = h;
+                accg[k][j] = __builtin_fmaf(d, h, accg[k][j]);
+                accb[k][j] += d;
+                s1 += g;
+                s2 = __builtin_fmaf(g, h, s2);
+            }
+        row_sum2<TPR>(s1, s2, slot + row_slot_words(TPR));
+        if (v == p.pad) return;                        // its row takes no gradient
+        const float c1 = s1 * shape.inv_dim, c2 = s2 * shape.inv_dim, f = p.scale * rstd;
+        char* const row = static_cast<char*>(p.dtable) + v * dim * (p.ddt == DT_F32 ? 4 : 2);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int unit = k * TPR + tid;
+            float out[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[j] = f * (sum[k][j] - __builtin_fmaf(x[k][j], c2, c1));
+            if (p.accumulate) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < unit_count(unit, dim)) out[j] += load1_rt(p.ddt, row, (int64_t)unit * 8 + j);
+            }
+            store_row_unit_rt<TAIL, true>(p.ddt, row, unit, units, dim, out);
+        }
     }
 
-    const RowShape<TPR, VPT> shape(tid, dim);
+    __device__ __forceinline__ void load8f(const float* q, float (&v)[8])
+    {
+        const f32x4 lo = gld<f32x4>(q), hi = gld<f32x4>(q + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = lo[j];
+            v[4 + j] = hi[j];
+        }
+    }
+
+    __device__ __forceinline__ void store8f(float* q, const float (&v)[8])
+    {
+        gst<f32x4>(q, f32x4{v[0], v[1], v[2], v[3]});
+        gst<f32x4>(q + 4, f32x4{v[4], v[5], v[6], v[7]});
+    }
+
+    // The workgroup's partial sums.
+    __device__ __forceinline__ void put_parts(int64_t wg)
+    {
+        const int64_t padded = (int64_t)units * 8;
+        float* const out = p.part + wg * 2 * padded;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int unit = k * TPR + tid;
+            if (unit >= units) continue;
+            float* const q = out + (int64_t)unit * 8;
+            store8f(q, accg[k]);
+            store8f(q + padded, accb[k]);
+        }
+    }
+};
+
+// TPR threads (one workgroup) to a listed id; a workgroup walks the list by
+// the grid, looks its next 64 ids up at once (lane l the l-th), and reads the
+// next id's row and first token before it works on the current one.  (Two ids at a
+// time, sharing the barriers, spilled or halved the resident workgroups: 60 to 65 us
+// against 55 for 4300 ids of 4096 elements.)
+template <int GDT, int TDT, int TPR, int VPT, bool TAIL>
+__global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, StableGradArgs p)
+{
+    __shared__ float s_slot[2 * row_slot_words(TPR)];
+    StableRows<GDT, TDT, TPR, VPT, TAIL> r(a, p, s_slot);
+    const int lane = threadIdx.x % 64;
+    const int64_t padded = (int64_t)r.units * 8;
+    const int32_t count = o.count[0], step = (int32_t)gridDim.x;
     for (int64_t i0 = blockIdx.x; i0 < count; i0 += 64 * (int64_t)step) {
         const int64_t at = i0 + lane * (int64_t)step;
         int32_t id = 0, lo = 0, hi = 0, head = 0;
@@ -79,27 +183,23 @@ __global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, Stab
         const int todo = count - i0 > 63 * (int64_t)step ? 64 : (int)((count - i0 + step - 1) / step);
         Unit<TDT> wnext[VPT];
         Unit<GDT> dnext[VPT];
-        // an id's row and its first token's dy
         auto load_next = [&](int i) {
-            const char* const wrow =
-                static_cast<const char*>(p.table) + (int64_t)__builtin_amdgcn_readlane(id, i) * dim * elem_bytes(TDT);
-            const char* const drow =
-                static_cast<const char*>(p.dy) + (int64_t)__builtin_amdgcn_readlane(head, i) * dim * elem_bytes(GDT);
+            r.load_table(wnext, __builtin_amdgcn_readlane(id, i));
+            const char* const row =
+                static_cast<const char*>(p.dy) + (int64_t)__builtin_amdgcn_readlane(head, i) * r.dim * elem_bytes(GDT);
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                wnext[k] = load_row_unit<TDT, TAIL, true>(wrow, k * TPR + tid, units, dim);
-                dnext[k] = load_row_unit<GDT, TAIL, true>(drow, k * TPR + tid, units, dim);
-            }
+            for (int k = 0; k < VPT; ++k)
+                dnext[k] = load_row_unit<GDT, TAIL, true>(row, k * TPR + r.tid, r.units, r.dim);
         };
         load_next(0);
         for (int i = 0; i < todo; ++i) {
             const int64_t v = __builtin_amdgcn_readlane(id, i);
             const int32_t first = __builtin_amdgcn_readlane(lo, i), last = __builtin_amdgcn_readlane(hi, i);
-            Unit<TDT> wu[VPT];
+            Unit<TDT> w[VPT];
             float sum[VPT][8];
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                wu[k] = wnext[k];
+                w[k] = wnext[k];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[k][j] = unit_at<GDT>(dnext[k], j);
             }
@@ -108,94 +208,68 @@ __global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, Stab
             if (last - first > o.chunk) {              // joined before, in the slot of its first chunk
                 const float* const q = p.chunk_part + chunk_slot(first / o.chunk, first, o.chunk) * padded;
 #pragma unroll
-                for (int k = 0; k < VPT; ++k) {
-                    const int64_t c = (int64_t)(k * TPR + tid < units ? k * TPR + tid : 0) * 8;
-                    const f32x4 lo4 = gld<f32x4>(q + c), hi4 = gld<f32x4>(q + c + 4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        sum[k][j] = lo4[j];
-                        sum[k][4 + j] = hi4[j];
-                    }
-                }
+                for (int k = 0; k < VPT; ++k)
+                    r.load8f(q + (int64_t)(k * TPR + r.tid < r.units ? k * TPR + r.tid : 0) * 8, sum[k]);
             } else {
-                sum_tokens<GDT, TAIL, TPR, VPT, 4>(o.order, first + 1, last, p.dy, tid, units, dim, sum);
+                sum_tokens<GDT, TAIL, TPR, VPT, 4>(o.order, first + 1, last, p.dy, r.tid, r.units, r.dim, sum);
             }
-            // the statistics of its norm
-            float x[VPT][8];
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[k][j] = unit_at<TDT>(wu[k], j) * p.scale;
-                if (!whole_step<TPR>(k, dim) && k * TPR + tid >= units) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[k][j] = sum[k][j] = 0.0f;
-                }
-            }
-            float mean, rstd;
-            row_stats<TPR, VPT, TDT == DT_F32>(x, shape, tid, dim, p.eps, s_slot, &mean, &rstd);
-
-            float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-            for (int k = 0; k < VPT; ++k)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float d = sum[k][j];
-                    const float h = (x[k][j] - mean) * rstd, g = d * gam[k][j];
-                    sum[k][j] = g;
-                    x[k][j] = h;
-                    accg[k][j] = __builtin_fmaf(d, h, accg[k][j]);
-                    accb[k][j] += d;
-                    s1 += g;
-                    s2 = __builtin_fmaf(g, h, s2);
-                }
-            row_sum2<TPR>(s1, s2, s_slot + row_slot_words(TPR));
-            if (v == p.pad) continue;                  // its row takes no gradient
-            const float c1 = s1 * shape.inv_dim, c2 = s2 * shape.inv_dim, f = p.scale * rstd;
-            char* const row = static_cast<char*>(p.dtable) + v * dim * (p.ddt == DT_F32 ? 4 : 2);
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int unit = k * TPR + tid;
-                float out[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) out[j] = f * (sum[k][j] - __builtin_fmaf(x[k][j], c2, c1));
-                if (p.accumulate) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < unit_count(unit, dim)) out[j] += load1_rt(p.ddt, row, (int64_t)unit * 8 + j);
-                }
-                store_row_unit_rt<TAIL, true>(p.ddt, row, unit, units, dim, out);
-            }
+            r.finish(v, w, sum);
         }
     }
-    float* const out = p.part + (int64_t)blockIdx.x * 2 * padded;
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int unit = k * TPR + tid;
-        if (unit < units) {
-            float* const q = out + (int64_t)unit * 8;
-            gst<f32x4>(q, f32x4{accg[k][0], accg[k][1], accg[k][2], accg[k][3]});
-            gst<f32x4>(q + 4, f32x4{accg[k][4], accg[k][5], accg[k][6], accg[k][7]});
-            gst<f32x4>(q + padded, f32x4{accb[k][0], accb[k][1], accb[k][2], accb[k][3]});
-            gst<f32x4>(q + padded + 4, f32x4{accb[k][4], accb[k][5], accb[k][6], accb[k][7]});
-        }
-    }
+    r.put_parts(blockIdx.x);
 }
 
+// Few tokens: workgroup t works if token t is the first of its id, and writes
+// partial sums in any case; workgroups beyond the tokens' write zero rows.
+template <int GDT, int TDT, int TPR, int VPT, bool TAIL>
+__global__ __launch_bounds__(TPR) void k_stable_grad_direct(IdArgs a, StableGradArgs p)
+{
+    __shared__ float s_slot[2 * row_slot_words(TPR)];
+    const DirectIds ids(a);
+    if (blockIdx.x >= a.n) {
+        zero_unnamed<TAIL, TPR>(a, ids, (blockIdx.x - a.n) * kZeroRows, p.pad, p.dtable, p.ddt);
+        return;
+    }
+    StableRows<GDT, TDT, TPR, VPT, TAIL> r(a, p, s_slot);
+    const int t = (int)blockIdx.x;
+    const int32_t v = ids.of(t);
+    const unsigned long long m0 = ids.tokens(0, v), m1 = ids.tokens(1, v);
+    if (v >= 0 && (m0 ? __builtin_ctzll(m0) : 64 + __builtin_ctzll(m1)) == t) {
+        Unit<TDT> w[VPT];
+        r.load_table(w, v);
+        float sum[VPT][8] = {};
+        sum_masked<GDT, TAIL, TPR, VPT, 4>(m0, 0, p.dy, r.tid, r.units, r.dim, sum);
+        sum_masked<GDT, TAIL, TPR, VPT, 4>(m1, 1, p.dy, r.tid, r.units, r.dim, sum);
+        r.finish(v, w, sum);
+    }
+    r.put_parts(t);
+}
+
+template <int GDT, int TDT, int TPR, int VPT, bool TAIL>
+hipError_t stable_grad_tpr(const IdArgs& a, const OrderArgs* o, const StableGradArgs& p, int parts, hipStream_t s)
+{
+    if (!o)
+        return launch_kernel_nt(k_stable_grad_direct<GDT, TDT, TPR, VPT, TAIL>,
+                                (int)(a.n + direct_zero_wgs(a.rows, p.accumulate != 0)), TPR, s, a, p);
+    return launch_kernel_nt(k_stable_grad<GDT, TDT, TPR, VPT, TAIL>, parts, TPR, s, a, *o, p);
+}
+
+// One unit per thread up to 8192 elements: a workgroup of many waves hides the
+// latency of its reads with the few registers of each.  o nullptr: few tokens.
 template <int GDT, int TDT, bool TAIL>
-hipError_t stable_grad_as(const IdArgs& a, const OrderArgs& o, const StableGradArgs& p, int parts, hipStream_t s)
+hipError_t stable_grad_as(const IdArgs& a, const OrderArgs* o, const StableGradArgs& p, int parts, hipStream_t s)
 {
     const int units = (a.dim + 7) / 8;
-    auto go = [&](auto kernel, int threads) { return launch_kernel_nt(kernel, parts, threads, s, a, o, p); };
-    if (units <= 64) return go(k_stable_grad<GDT, TDT, 64, 1, TAIL>, 64);
-    if (units <= 256) return go(k_stable_grad<GDT, TDT, 256, 1, TAIL>, 256);
-    if (units <= 512) return go(k_stable_grad<GDT, TDT, 512, 1, TAIL>, 512);
-    if (units <= 1024) return go(k_stable_grad<GDT, TDT, 1024, 1, TAIL>, 1024);
-    if (units <= 2048) return go(k_stable_grad<GDT, TDT, 1024, 2, TAIL>, 1024);
+    if (units <= 64) return stable_grad_tpr<GDT, TDT, 64, 1, TAIL>(a, o, p, parts, s);
+    if (units <= 256) return stable_grad_tpr<GDT, TDT, 256, 1, TAIL>(a, o, p, parts, s);
+    if (units <= 512) return stable_grad_tpr<GDT, TDT, 512, 1, TAIL>(a, o, p, parts, s);
+    if (units <= 1024) return stable_grad_tpr<GDT, TDT, 1024, 1, TAIL>(a, o, p, parts, s);
+    if (units <= 2048) return stable_grad_tpr<GDT, TDT, 1024, 2, TAIL>(a, o, p, parts, s);
     return hipErrorInvalidValue;
 }
 
 template <int GDT>
-hipError_t stable_grad_t(const IdArgs& a, const OrderArgs& o, const StableGradArgs& p, int parts, int tdt,
+hipError_t stable_grad_t(const IdArgs& a, const OrderArgs* o, const StableGradArgs& p, int parts, int tdt,
                          hipStream_t s)
 {
     if (a.dim % 8) {
@@ -210,11 +284,20 @@ hipError_t stable_grad_t(const IdArgs& a, const OrderArgs& o, const StableGradAr
 
 }  // namespace
 
-// No more workgroups than ids that can have tokens.
+// No more workgroups than ids that can have tokens; one per token where these are few.
 int stable_parts(int64_t n, int64_t rows)
 {
+    if (takes_direct(n, rows)) return rows > 0 ? (int)n : 0;
     const int64_t most = n < rows ? n : rows;
     return (int)(most < kStableParts ? most : kStableParts);
+}
+
+template <typename... Args>
+static hipError_t stable_grad_g(int gdt, Args... args)
+{
+    if (gdt == DT_F32) return stable_grad_t<DT_F32>(args...);
+    if (gdt == DT_F16) return stable_grad_t<DT_F16>(args...);
+    return stable_grad_t<DT_BF16>(args...);
 }
 
 hipError_t launch_stable_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, const float* chunk_part,
@@ -224,9 +307,15 @@ hipError_t launch_stable_grad(const IdArgs& a, const OrderArgs& o, const void* d
     if (parts == 0) return hipSuccess;
     const StableGradArgs p{dy, chunk_part, table, w.gamma, dtable, part, pad, scale, w.eps,
                            w.wdt, ddt, accumulate ? 1 : 0};
-    if (gdt == DT_F32) return stable_grad_t<DT_F32>(a, o, p, parts, tdt, s);
-    if (gdt == DT_F16) return stable_grad_t<DT_F16>(a, o, p, parts, tdt, s);
-    return stable_grad_t<DT_BF16>(a, o, p, parts, tdt, s);
+    return stable_grad_g(gdt, a, &o, p, parts, tdt, s);
+}
+
+hipError_t launch_stable_grad_direct(const IdArgs& a, const void* dy, int gdt, const void* table, int tdt, float scale,
+                                     const NormArgs& w, int64_t pad, bool accumulate, void* dtable, int ddt,
+                                     float* part, hipStream_t s)
+{
+    const StableGradArgs p{dy, nullptr, table, w.gamma, dtable, part, pad, scale, w.eps, w.wdt, ddt, accumulate ? 1 : 0};
+    return stable_grad_g(gdt, a, (const OrderArgs*)nullptr, p, (int)a.n, tdt, s);
 }
 
 }  // namespace qb

@@ -6,6 +6,8 @@
 
 namespace qb {
 
+constexpr int kZeroRows = 16;           // table rows of a zero-filling workgroup
+
 // sum[k] += dy of the units k * TPR + tid over the R tokens whose positions lanes
 // i .. i + R - 1 hold, in order; the loads of all R rows are in flight together.
 template <int GDT, bool TAIL, int TPR, int VPT, int R>
@@ -87,6 +89,92 @@ __device__ __forceinline__ float join_column(const float* part, int32_t chunk, i
 __device__ __forceinline__ int64_t slot_of(int64_t v, const OrderArgs& o)
 {
     return (v & ((int64_t(1) << o.log2g) - 1)) * o.per + (v >> o.log2g);
+}
+
+// ---------------------------------------------------------------------------
+// few tokens: no ordering
+// ---------------------------------------------------------------------------
+
+// The ids of up to kDirectTokens tokens, held by every wave (lane l: tokens l and
+// 64 + l); ids outside the table are -1.
+struct DirectIds {
+    int32_t id[2];
+
+    __device__ __forceinline__ explicit DirectIds(const IdArgs& a)
+    {
+        const int lane = threadIdx.x % 64;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = h * 64 + lane;
+            const int64_t v = t < a.n ? load_id(a.ids, a.id64, t) : -1;
+            id[h] = (uint64_t)v < (uint64_t)a.rows ? (int32_t)v : -1;
+        }
+    }
+
+    // id of token t (uniform)
+    __device__ __forceinline__ int32_t of(int t) const
+    {
+        const int32_t a = __builtin_amdgcn_readlane(id[0], t & 63), b = __builtin_amdgcn_readlane(id[1], t & 63);
+        return t < 64 ? a : b;
+    }
+
+    // tokens of id v
+    __device__ __forceinline__ unsigned long long tokens(int h, int32_t v) const { return __ballot(id[h] == v); }
+};
+
+// sum[k] += dy of the units k * TPR + tid over the tokens of `mask` (bit l: token
+// 64 h + l), in order, UN tokens in flight.
+template <int GDT, bool TAIL, int TPR, int VPT, int UN>
+__device__ __forceinline__ void sum_masked(unsigned long long mask, int h, const void* dy, int tid, int units, int dim,
+                                           float (&sum)[VPT][8])
+{
+    while (mask) {
+        Unit<GDT> u[UN][VPT];
+        const int m = (int)__popcll(mask);
+        unsigned long long rest = mask;
+        int t = 0;
+#pragma unroll
+        for (int q = 0; q < UN; ++q) {
+            // (beyond the last token the last one again: no branch, the same lines)
+            t = rest ? h * 64 + __builtin_ctzll(rest) : t;
+            rest &= rest - 1;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                u[q][k] = load_row_unit<GDT, TAIL, true>(
+                    static_cast<const char*>(dy) + (int64_t)t * dim * elem_bytes(GDT), k * TPR + tid, units, dim);
+        }
+#pragma unroll
+        for (int q = 0; q < UN; ++q)
+            if (q < m)
+#pragma unroll
+                for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[k][j] += unit_at<GDT>(u[q][k], j);
+        mask = rest;
+    }
+}
+
+// One workgroup of THREADS threads: zeros into the rows of kZeroRows that no
+// token names, and into pad's.
+template <bool TAIL, int THREADS>
+__device__ __forceinline__ void zero_unnamed(const IdArgs& a, const DirectIds& ids, int64_t v0, int64_t pad, void* dtable,
+                                             int ddt)
+{
+    const int dim = a.dim, units = (dim + 7) >> 3;
+    const float zero[8] = {};
+    for (int i = 0; i < kZeroRows && v0 + i < a.rows; ++i) {
+        const int64_t v = v0 + i;
+        if (v != pad && (ids.tokens(0, (int32_t)v) | ids.tokens(1, (int32_t)v))) continue;
+        char* const row = static_cast<char*>(dtable) + v * dim * (ddt == DT_F32 ? 4 : 2);
+        for (int unit = threadIdx.x; unit < units; unit += THREADS)
+            store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, zero);
+    }
+}
+
+// Workgroups that zero the table in such a launch (0 with accumulate).
+inline int64_t direct_zero_wgs(int64_t rows, bool accumulate)
+{
+    return accumulate ? 0 : (rows + kZeroRows - 1) / kZeroRows;
 }
 
 }  // namespace qb

@@ -75,6 +75,18 @@ hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void*, i
     return done();
 }
 hipError_t launch_join_chunks(const IdArgs&, const OrderArgs&, float*, hipStream_t) { return done(); }
+hipError_t launch_table_grad_direct(const IdArgs& a, const void*, int, float, int64_t, bool, void*, int, hipStream_t)
+{
+    if (a.n < 1 || a.n > kDirectTokens || a.rows < 1) ++failures;
+    return done();
+}
+hipError_t launch_stable_grad_direct(const IdArgs& a, const void*, int, const void*, int, float, const NormArgs&, int64_t,
+                                     bool, void*, int, float* part, hipStream_t)
+{
+    if (a.n < 1 || a.n > kDirectTokens || a.rows < 1) ++failures;
+    inside(part, 2.0 * (double)a.n * (double)padded_dim(a.dim) * 4);
+    return done();
+}
 hipError_t launch_layer_norm(const void*, int, int64_t, int64_t, const NormArgs&, void*, float*, float*, hipStream_t)
 {
     return done();
@@ -85,7 +97,10 @@ hipError_t launch_stable_embedding(const IdArgs&, const void*, int, float, const
 }
 // the number of workgroups is the HIP sources' choice, at most one per row and kNormPartsMax
 int layer_norm_parts(int64_t n, int64_t) { return (int)(n < kNormPartsMax ? n : kNormPartsMax); }
-int stable_parts(int64_t n, int64_t rows) { return (int)std::min<int64_t>(kNormPartsMax, std::min(n, rows)); }
+int stable_parts(int64_t n, int64_t rows)
+{
+    return rows > 0 && takes_direct(n, rows) ? (int)n : (int)std::min<int64_t>(kNormPartsMax, std::min(n, rows));
+}
 hipError_t launch_layer_norm_grad(const void*, const void*, int, int64_t n, int64_t dim, const void*, int,
                                   const float*, const float*, void*, float* part, hipStream_t)
 {

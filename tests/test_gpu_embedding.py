@@ -146,7 +146,9 @@ def check_grad(dy, ids, rows, scale, ddt, got, padding_id=-1, old=None):
 @pytest.mark.parametrize("gdt,ddt", [(F32, F32), (BF16, BF16), (F16, F16), (BF16, F32), (F32, F16)])
 @pytest.mark.parametrize("n,rows,dim,kind", [(1, 1, 1, "uniform"), (5, 3, 7, "mixed"), (700, 300, 64, "zipf"),
                                              (300, 40, 1001, "mixed"), (150, 9, 520, "uniform"), (1000, 50, 72, "one"),
-                                             (333, 1000, 513, "zipf"), (40, 6, 4096, "mixed"), (6000, 700, 33, "zipf")])
+                                             (333, 1000, 513, "zipf"), (40, 6, 4096, "mixed"), (6000, 700, 33, "zipf"),
+                                             (128, 40, 2600, "zipf"), (129, 40, 520, "zipf"), (128, 5, 64, "one"),
+                                             (64, 300, 100, "mixed"), (65, 2, 9, "uniform")])
 def test_table_gradient(gdt, ddt, n, rows, dim, kind):
     L = qb()
     for idt in (torch.int32, torch.int64):
@@ -168,8 +170,12 @@ def test_table_gradient(gdt, ddt, n, rows, dim, kind):
 
 @pytest.mark.parametrize("ddt", [F32, F16, BF16])
 def test_table_gradient_accumulates_and_skips_padding(ddt):
-    L = qb()
-    n, rows, dim = 500, 90, 201
+    for n in (500, 100):
+        accumulates_and_skips_padding(qb(), n, ddt)
+
+
+def accumulates_and_skips_padding(L, n, ddt):
+    rows, dim = 90, 201
     dy = normal((n, dim), 1, 0.1, BF16)
     ids = make_ids(n, rows, 2, torch.int64, "zipf")
     pad = int(ids[0])

@@ -77,7 +77,9 @@ def backward(L, dy, table, ids, gamma, scale, ddt, wdt, **kw):
 @pytest.mark.parametrize("n,rows,dim,kind", [(1, 1, 1, "uniform"), (40, 9, 7, "mixed"), (300, 60, 64, "zipf"),
                                              (200, 300, 500, "mixed"), (333, 40, 1001, "zipf"), (200, 20, 2048, "one"),
                                              (64, 11, 4096, "mixed"), (50, 30, 2050, "uniform"), (41, 7, 8192, "mixed"),
-                                             (30, 5, 5003, "uniform"), (9, 3, 16384, "mixed"), (70, 4, 9001, "one")])
+                                             (30, 5, 5003, "uniform"), (9, 3, 16384, "mixed"), (70, 4, 9001, "one"),
+                                             (128, 40, 264, "zipf"), (129, 40, 264, "zipf"), (200, 5, 8192, "zipf"),
+                                             (150, 3, 16384, "zipf"), (140, 9, 5003, "one")])
 def test_forward_and_backward(tdt, ydt, ddt, wdt, n, rows, dim, kind):
     L = qb()
     idt = torch.int32 if n % 2 else torch.int64
@@ -98,8 +100,12 @@ def test_forward_and_backward(tdt, ydt, ddt, wdt, n, rows, dim, kind):
 
 def test_options_of_the_backward_pass():
     """No gamma, a padding id, accumulation, gradients left out."""
-    L = qb()
-    n, rows, dim = 400, 70, 333
+    for n in (400, 90):
+        options_of_the_backward_pass(qb(), n)
+
+
+def options_of_the_backward_pass(L, n):
+    rows, dim = 70, 333
     table = normal((rows, dim), 1, 0.05, BF16)
     gamma, beta = weights(dim, F32, 2)
     ids = make_ids(n, rows, 4, torch.int64, "zipf")
