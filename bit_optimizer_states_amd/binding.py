@@ -397,6 +397,7 @@ def qb_multi_tensor_dequantize(table, count, code, blocksize, blocksize2, ydt, w
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _at(t, device):
@@ -422,8 +423,7 @@ def _index(ids):
 
 def _tokens(t, dim, name, ids=None):
     """Rows of a token array, whose last dimension must be `dim`, one per id."""
-    shape = t.shape
-    if dim == 0 or shape[-1] != dim:
+    if dim == 0 or t.shape[-1] != dim:
         raise ValueError(f"{name} with rows of {dim} (at least one) elements expected")
     n = t.numel() // dim
     if ids is not None and ids.numel() != n:
@@ -461,7 +461,7 @@ def _row_call(name, device, stream, *args):
     """Calls an entry point with the tensors' device current (kernels start on the current device)."""
     f = getattr(_lib, name)
     s = _raw_stream(device) if stream is None else _stream(stream)
-    if device == torch.cuda.current_device():
+    if device == _current_device():
         status = f(*args, s)
     else:
         with torch.cuda.device(device):
@@ -490,7 +490,7 @@ def qb_dequant_embedding(codes, absmax, dq, code, blocksize, rows, ids, y, scale
     if codes.numel() < (total if code == QB_DYN8 else (total + 1) // 2):
         raise ValueError("codes of the whole table expected")
     if absmax is not None and absmax.numel() * blocksize < total:
-        raise ValueError(f"absmax of {-(-total // blocksize)} blocks expected")
+        raise ValueError("absmax of every block expected")
     d = y.get_device()
     _row_call("qb_dequant_embedding", d, stream, _at(codes, d), _at(absmax, d),
               ctypes.byref(dq) if dq is not None else None, code, blocksize, rows, dim, _at(ids, d), _index(ids), n,

@@ -427,8 +427,8 @@ __global__ __launch_bounds__(256) void k_prepare_grad(IdArgs a, OrderArgs o, con
     }
     wg -= list_wgs;
     if (wg < chunk_wgs) {
-        const int64_t w = wg * 4 + wave;
-        chunk_sums<GDT, TAIL>(a, o, dy, part, w / slices, (int)(w % slices) * 64 + lane);
+        for (int64_t w = wg * 4 + wave; w / slices * o.chunk < a.n; w += (int64_t)chunk_wgs * 4)
+            chunk_sums<GDT, TAIL>(a, o, dy, part, w / slices, (int)(w % slices) * 64 + lane);
         return;
     }
     wg -= chunk_wgs;
@@ -557,8 +557,9 @@ __global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, Table
     if (b >= p.work) {
         zero_rows<TAIL>(a, o, b - p.work, p.zeros, p.pad, p.dtable, p.ddt);
     } else {
-        const int64_t w = b * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-        sum_chunk_rows<GDT, TAIL>(a, o, p, w / p.slices, (int)(w % p.slices));
+        for (int64_t w = b * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64); w / p.slices * o.chunk < a.n;
+             w += (int64_t)p.work * 4)
+            sum_chunk_rows<GDT, TAIL>(a, o, p, w / p.slices, (int)(w % p.slices));
     }
 }
 
@@ -584,9 +585,10 @@ hipError_t prepare_grad_as(const IdArgs& a, const OrderArgs& o, const void* dy, 
 {
     const int32_t slices = (a.dim + 511) / 512;
     const int64_t most = int64_t(1) << 22;
-    const int64_t list = ((int64_t(1) << o.log2g) + 3) / 4, chunks = (chunk_count(a.n) * slices + 3) / 4;
+    const int64_t list = ((int64_t(1) << o.log2g) + 3) / 4;
+    int64_t chunks = (chunk_count(a.n) * slices + 3) / 4;
     int64_t zeros = accumulate ? 0 : (a.rows + kZeroRows - 1) / kZeroRows;
-    if (chunks > most) return hipErrorInvalidValue;
+    if (chunks > most) chunks = most;
     if (zeros > most) zeros = most;
     auto go = [&](auto kernel) {
         return launch_kernel(kernel, (int)(list + chunks + zeros), s, a, o, dy, part, slices, (int32_t)list,
@@ -637,9 +639,10 @@ int long_wgs(const IdArgs& a, const OrderArgs& o)
 template <int GDT>
 hipError_t table_grad_as(const IdArgs& a, const OrderArgs& o, TableGradArgs p, hipStream_t s)
 {
-    const int64_t most = int64_t(1) << 22, work = (chunk_count(a.n) * ((a.dim + 511) / 512) + 3) / 4;
+    const int64_t most = int64_t(1) << 22;
+    int64_t work = (chunk_count(a.n) * ((a.dim + 511) / 512) + 3) / 4;
     int64_t zeros = p.accumulate ? 0 : (a.rows + kZeroRows - 1) / kZeroRows;
-    if (work > most) return hipErrorInvalidValue;
+    if (work > most) work = most;
     if (zeros > most) zeros = most;
     p.slices = (a.dim + 511) / 512;
     p.work = (int32_t)work;

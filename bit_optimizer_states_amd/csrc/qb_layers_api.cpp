@@ -21,8 +21,9 @@ bool is4(qb_code c) { return c == QB_NF4 || c == QB_FP4; }
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 constexpr int64_t kIndexMax = int64_t(1) << 31;      // tokens, rows
-constexpr int64_t kDimMax = int64_t(1) << 24;        // elements of a table's row
+constexpr int64_t kDimMax = int64_t(1) << 24;        // elements of a row
 constexpr int64_t kGradRowsMax = int64_t(1) << 26;   // rows of a table that takes a gradient
+constexpr int64_t kGradTokensMax = int64_t(1) << 30; // tokens of a gradient
 
 qb_status hip_status(hipError_t e)
 {
@@ -79,7 +80,7 @@ OrderArgs order_args(void* ws, const GradLayout& l, int64_t n, int64_t rows)
 
 bool valid_grad_sizes(int64_t n, int64_t rows, int64_t dim)
 {
-    return n >= 0 && n < kIndexMax && rows >= 0 && rows <= kGradRowsMax && dim >= 1 && dim < kDimMax;
+    return n >= 0 && n <= kGradTokensMax && rows >= 0 && rows <= kGradRowsMax && dim >= 1 && dim < kDimMax;
 }
 
 // Checks shared by the two gradients of a table.
@@ -178,11 +179,10 @@ qb_status qb_embedding_backward(const void* dy, qb_dtype gdt, const void* ids, q
 qb_status qb_layer_norm(const void* x, qb_dtype xdt, int64_t n, int64_t dim, const void* gamma, const void* beta,
                         qb_dtype wdt, double eps, void* y, float* mean, float* rstd, void* stream)
 {
-    if (n < 0 || n >= kIndexMax || dim < 1 || dim >= kIndexMax || !valid_dtype(xdt) || !valid_dtype(wdt) ||
+    if (n < 0 || n >= kIndexMax || dim < 1 || dim >= kDimMax || !valid_dtype(xdt) || !valid_dtype(wdt) ||
         !valid_eps(eps))
         return QB_EINVAL;
     if (wdt != QB_F32 && wdt != xdt) return QB_EUNSUPPORTED;
-    if (n > INT64_MAX / 8 / dim) return QB_EINVAL;
     if (n == 0) return QB_OK;
     if (!x || !y) return QB_EINVAL;
     if (!aligned16(x) || !aligned16(gamma) || !aligned16(beta) || !aligned16(y) || !aligned16(mean) || !aligned16(rstd))
@@ -193,7 +193,7 @@ qb_status qb_layer_norm(const void* x, qb_dtype xdt, int64_t n, int64_t dim, con
 
 size_t qb_layer_norm_workspace_bytes(int64_t n, int64_t dim)
 {
-    if (n < 0 || n >= kIndexMax || dim < 1 || dim >= kIndexMax) return 0;
+    if (n < 0 || n >= kIndexMax || dim < 1 || dim >= kDimMax) return 0;
     const int64_t parts = n < kNormPartsMax ? (n > 0 ? n : 1) : kNormPartsMax;
     return (size_t)(parts * 2 * padded_dim(dim)) * sizeof(float);
 }
@@ -203,11 +203,10 @@ qb_status qb_layer_norm_backward(const void* dy, const void* x, qb_dtype xdt, in
                                  void* dgamma, void* dbeta, int32_t accumulate, void* ws, size_t ws_bytes,
                                  void* stream)
 {
-    if (n < 0 || n >= kIndexMax || dim < 1 || dim >= kIndexMax || !valid_dtype(xdt) || !valid_dtype(wdt) ||
+    if (n < 0 || n >= kIndexMax || dim < 1 || dim >= kDimMax || !valid_dtype(xdt) || !valid_dtype(wdt) ||
         (accumulate != 0 && accumulate != 1))
         return QB_EINVAL;
     if (wdt != QB_F32 && wdt != xdt) return QB_EUNSUPPORTED;
-    if (n > INT64_MAX / 8 / dim) return QB_EINVAL;
     const bool weights = dgamma || dbeta;
     if (n == 0 && (!weights || accumulate)) return QB_OK;
     if (!dx && !weights) return QB_OK;

@@ -599,8 +599,8 @@ size_t qb_optimizer_workspace_bytes(const qb_optim_hparams* hp, const qb_tensor*
  *   - Outputs must not overlap inputs or each other.
  *   - accumulate (0 or 1): add the gradient to what the outputs hold (read in
  *     their dtype, added in binary32, rounded once) instead of overwriting them.
- *   - Limits: n, rows < 2^31; dim < 2^24 for tables (2^31 for layer norm); the
- *     backward calls take tables of at most 2^26 rows.
+ *   - Limits: n, rows < 2^31; dim < 2^24; a table's gradient takes at most 2^30
+ *     tokens and 2^26 rows.
  */
 
 /*
@@ -642,7 +642,8 @@ qb_status qb_dequant_embedding(const uint8_t* codes, const float* absmax, const 
  *   ws          device workspace of qb_embedding_workspace_bytes(n, rows, dim)
  *               bytes, 16-byte aligned; holds nothing between calls, and must not
  *               be shared by calls that may overlap in time.
- * Three kernels on `stream`; no memory operations, so it may be captured.
+ * Up to three kernels on `stream` (one for up to 128 tokens); no memory
+ * operations, so it may be captured.
  */
 qb_status qb_embedding_backward(const void* dy, qb_dtype gdt, const void* ids, qb_index idt, int64_t n, int64_t rows,
                                 int64_t dim, double scale, int64_t padding_id, int32_t accumulate, void* dtable,
@@ -706,7 +707,8 @@ qb_status qb_stable_embedding(const void* table, qb_dtype tdt, int64_t rows, int
  *   dgamma, dbeta   [dim] of dtype wdt, each may be NULL.
  *   ws           device workspace of qb_stable_embedding_workspace_bytes(n, rows,
  *                dim) bytes, as for qb_embedding_backward.
- * Other arguments as qb_embedding_backward and qb_stable_embedding.  Four kernels.
+ * Other arguments as qb_embedding_backward and qb_stable_embedding.  Up to five
+ * kernels (two for up to 128 tokens).
  */
 qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void* table, qb_dtype tdt, int64_t rows,
                                        int64_t dim, const void* ids, qb_index idt, int64_t n, double scale,

@@ -127,20 +127,23 @@ int main()
     ws_begin = reinterpret_cast<char*>(uintptr_t(1) << 41);
     const int64_t top = (int64_t(1) << 31) - 1;
 
-    for (int64_t n : {int64_t(0), int64_t(1), int64_t(63), int64_t(5003), int64_t(1) << 20, top})
+    for (int64_t n : {int64_t(0), int64_t(1), int64_t(63), int64_t(128), int64_t(129), int64_t(5003), int64_t(1) << 20,
+                      int64_t(1) << 30, top})
         for (int64_t rows : {int64_t(0), int64_t(1), int64_t(2), int64_t(255), int64_t(257), int64_t(32000),
                              int64_t(256001), int64_t(1) << 26})
             for (int64_t dim : {int64_t(1), int64_t(8), int64_t(1001), int64_t(16384), (int64_t(1) << 24) - 1}) {
+                const bool takes = n <= int64_t(1) << 30;
                 ws_bytes = qb_embedding_workspace_bytes(n, rows, dim);
+                EXPECT(ws_bytes != 0, takes);
                 EXPECT(qb_embedding_backward(A, QB_BF16, B, QB_I64, n, rows, dim, 0.5, -1, 0, A, QB_F32, ws_begin,
-                                             ws_bytes, nullptr), QB_OK);
+                                             ws_bytes, nullptr), takes ? QB_OK : QB_EINVAL);
                 EXPECT(qb_embedding(A, QB_F32, rows, dim, B, QB_I32, n, 2.0, A, QB_F16, nullptr), QB_OK);
                 const bool fits = dim <= 16384;
                 ws_bytes = qb_stable_embedding_workspace_bytes(n, rows, dim);
-                EXPECT(ws_bytes != 0, fits);
+                EXPECT(ws_bytes != 0, fits && takes);
                 EXPECT(qb_stable_embedding_backward(A, QB_F16, B, QB_F32, rows, dim, B, QB_I32, n, 1.0, A, QB_F32, 1e-5,
                                                     3, 0, A, QB_F32, A, A, ws_begin, ws_bytes, nullptr),
-                       fits ? QB_OK : QB_EUNSUPPORTED);
+                       !takes ? QB_EINVAL : fits ? QB_OK : QB_EUNSUPPORTED);
                 EXPECT(qb_stable_embedding(A, QB_F32, rows, dim, B, QB_I32, n, 1.0, A, nullptr, QB_F32, 1e-5, A, QB_F32,
                                            nullptr), fits ? QB_OK : QB_EUNSUPPORTED);
                 // at most 2^31 - 1 blocks in a quantized table
@@ -148,8 +151,8 @@ int main()
                                             nullptr), n > 0 && (rows * dim + 63) / 64 > top ? QB_EINVAL : QB_OK);
             }
     for (int64_t n : {int64_t(0), int64_t(1), int64_t(511), int64_t(1) << 20, top})
-        for (int64_t dim : {int64_t(1), int64_t(4096), int64_t(16385), top}) {
-            const bool fits = n == 0 || dim <= INT64_MAX / 8 / (n > 0 ? n : 1);
+        for (int64_t dim : {int64_t(1), int64_t(4096), int64_t(16385), (int64_t(1) << 24) - 1, int64_t(1) << 24}) {
+            const bool fits = dim < int64_t(1) << 24;
             ws_bytes = qb_layer_norm_workspace_bytes(n, dim);
             EXPECT(qb_layer_norm_backward(A, B, QB_F32, n, dim, A, QB_F32, F, F, A, A, A, 0, ws_begin, ws_bytes, nullptr),
                    fits ? QB_OK : QB_EINVAL);
