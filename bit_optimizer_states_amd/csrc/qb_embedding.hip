@@ -12,6 +12,8 @@
 // zero rows of the table are written, which keeps HBM busy meanwhile
 // (k_prepare_grad).  The last launch sums and writes the rows of the ids that
 // have tokens, and only those (k_table_grad).
+#include <type_traits>
+
 #include "qb_token_sums.h"
 
 namespace qb {
@@ -23,7 +25,7 @@ namespace {
 // ---------------------------------------------------------------------------
 
 // `lanes` (a power of two) threads share a token, 256 / lanes tokens a workgroup.
-template <int TDT, int YDT, bool TAIL>
+template <int TDT, int YDT, int TAIL>
 __global__ __launch_bounds__(256) void k_embedding(IdArgs a, const void* __restrict__ table, float scale,
                                                    void* __restrict__ y, int log2lanes)
 {
@@ -67,8 +69,11 @@ hipError_t embedding_as(const IdArgs& a, const void* table, float scale, void* y
     return launch_rows(a.n, 256 >> k, [&](int64_t t0, int64_t m, int grid) {
         const IdArgs b = ids_from(a, t0, m);
         void* const out = static_cast<char*>(y) + t0 * a.dim * elem_bytes(YDT);
-        return a.dim % 8 ? launch_kernel(k_embedding<TDT, YDT, true>, grid, s, b, table, scale, out, k)
-                         : launch_kernel(k_embedding<TDT, YDT, false>, grid, s, b, table, scale, out, k);
+        auto go = [&](auto kernel) { return launch_kernel(kernel, grid, s, b, table, scale, out, k); };
+        const int tail = tail_of(a.dim);
+        return tail == kWhole     ? go(k_embedding<TDT, YDT, kWhole>)
+               : tail == kPartial ? go(k_embedding<TDT, YDT, kPartial>)
+                                  : go(k_embedding<TDT, YDT, kShort>);
     });
 }
 
@@ -89,7 +94,7 @@ hipError_t embedding_y(const IdArgs& a, const void* table, float scale, void* y,
 // block, and every element finds its own code and block; otherwise a unit of 8
 // elements is 4 or 8 aligned bytes of codes with one scale (blocks hold 64
 // elements or more).
-template <int BITS, int YDT, bool DQ, bool TAIL>
+template <int BITS, int YDT, bool DQ, int TAIL>
 __global__ __launch_bounds__(256) void k_dequant_embedding(IdArgs a, DequantDesc d, int log2B, int log2B2, int code4,
                                                            const QbTables* __restrict__ tab, float scale,
                                                            void* __restrict__ y, int log2lanes)
@@ -257,9 +262,12 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
 #pragma unroll
     for (int w = 0; w < kOrderWaves; ++w) base += s_below[w];
     const int j = threadIdx.x;
-    int32_t total = 0;
-    if (j < per)
-        for (int w = 0; w < kOrderWaves; ++w) total += s_cnt[w * per + j];
+    int32_t total = 0, of_wave[kOrderWaves];
+#pragma unroll
+    for (int w = 0; w < kOrderWaves; ++w) {
+        of_wave[w] = j < per ? s_cnt[w * per + j] : 0;
+        total += of_wave[w];
+    }
     int32_t incl = total;
     for (int step = 1; step < 64; step *= 2) {
         const int32_t up = __shfl_up(incl, step);
@@ -277,10 +285,10 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
     if (j < per) {
         int32_t run = base + before + incl - total;
         o.start[(int64_t)cls * per + j] = run;
+#pragma unroll
         for (int w = 0; w < kOrderWaves; ++w) {
-            const int32_t c = s_cnt[w * per + j];
             s_cnt[w * per + j] = run;
-            run += c;
+            run += of_wave[w];
         }
         if (cls == mask && j == per - 1) o.start[((int64_t)cls + 1) * per] = run;
     }
@@ -360,7 +368,7 @@ __device__ __forceinline__ void list_used(const OrderArgs& o, int64_t cls)
 
 // One wave: a chunk's tokens, 64 units.  Only the first and the last id of a chunk
 // can have more tokens than a chunk.
-template <int GDT, bool TAIL>
+template <int GDT, int TAIL>
 __device__ __forceinline__ void chunk_sums(const IdArgs& a, const OrderArgs& o, const void* dy, float* part,
                                            int64_t c, int unit)
 {
@@ -392,7 +400,7 @@ __device__ __forceinline__ void chunk_sums(const IdArgs& a, const OrderArgs& o, 
 
 // One workgroup of 256 threads: zeros into the empty ones of kZeroRows rows at a
 // time, workgroup wg of wgs.
-template <bool TAIL>
+template <int TAIL>
 __device__ __forceinline__ void zero_rows(const IdArgs& a, const OrderArgs& o, int64_t wg, int64_t wgs, int64_t pad,
                                           void* dtable, int ddt)
 {
@@ -413,7 +421,7 @@ __device__ __forceinline__ void zero_rows(const IdArgs& a, const OrderArgs& o, i
     }
 }
 
-template <int GDT, bool TAIL>
+template <int GDT, int TAIL>
 __global__ __launch_bounds__(256) void k_prepare_grad(IdArgs a, OrderArgs o, const void* __restrict__ dy,
                                                       float* __restrict__ part, int32_t slices, int32_t list_wgs,
                                                       int32_t chunk_wgs, int64_t pad,
@@ -467,7 +475,7 @@ struct TableGradArgs {
 // Lane l holds token c * chunk + l (two chunks are at most the 64 lanes) with the
 // range of its id; UN tokens' units are in flight while UN are added, whatever
 // ids they belong to.
-template <int GDT, bool TAIL>
+template <int GDT, int TAIL>
 __device__ __forceinline__ void sum_chunk_rows(const IdArgs& a, const OrderArgs& o, const TableGradArgs& p, int64_t c,
                                                int slice)
 {
@@ -506,37 +514,40 @@ __device__ __forceinline__ void sum_chunk_rows(const IdArgs& a, const OrderArgs&
     load(i);
     float sum[8] = {};
     for (; i < i1; i += UN) {
-        float v[UN][8];
+        Unit<GDT> v[UN];
 #pragma unroll
-        for (int q = 0; q < UN; ++q)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[q][j] = unit_at<GDT>(u[q], j);
+        for (int q = 0; q < UN; ++q) v[q] = u[q];
         if (i + UN < i1) load(i + UN);
+        // the pieces of ids among these UN tokens, one after the other: the code that
+        // ends an id is there once
+        const int held = i1 - i < UN ? i1 - i : UN;
+        for (int q0 = 0; q0 < held;) {
+            const unsigned long long rest = ends >> (i + q0);
+            const int e = rest ? q0 + __builtin_ctzll(rest) + 1 : held + 1;      // one past the id's last token
 #pragma unroll
-        for (int q = 0; q < UN; ++q) {
-            if (i + q >= i1) break;
+            for (int q = 0; q < UN; ++q)
+                if (q >= q0 && q < e && q < held) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += v[q][j];
-            if (!((ends >> (i + q)) & 1)) continue;
-            if ((longs >> (i + q)) & 1) {
+                    for (int j = 0; j < 8; ++j) sum[j] += unit_at<GDT>(v[q], j);
+                }
+            q0 = e;
+            if (e > held) break;
+            const int l = i + e - 1;
+            if ((longs >> l) & 1) {
                 const int64_t padded = (int64_t)units * 8;
-                float* const out = p.part + chunk_slot((int32_t)c, __builtin_amdgcn_readlane(lo, i + q), o.chunk) * padded +
+                float* const out = p.part + chunk_slot((int32_t)c, __builtin_amdgcn_readlane(lo, l), o.chunk) * padded +
                                    (int64_t)unit * 8;
                 if (unit < units) {
                     gst<f32x4>(out, f32x4{sum[0], sum[1], sum[2], sum[3]});
                     gst<f32x4>(out + 4, f32x4{sum[4], sum[5], sum[6], sum[7]});
                 }
             } else {
-                const int64_t v0 = __builtin_amdgcn_readlane(id, i + q);
+                const int64_t v0 = __builtin_amdgcn_readlane(id, l);
                 if (v0 != p.pad) {
                     char* const row = static_cast<char*>(p.dtable) + v0 * dim * (p.ddt == DT_F32 ? 4 : 2);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum[j] *= p.scale;
-                    if (p.accumulate) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (j < unit_count(unit, dim)) sum[j] += load1_rt(p.ddt, row, (int64_t)unit * 8 + j);
-                    }
+                    if (p.accumulate) add_row_unit_rt<TAIL>(p.ddt, row, unit, units, dim, sum);
                     store_row_unit_rt<TAIL, true>(p.ddt, row, unit, units, dim, sum);
                 }
             }
@@ -550,7 +561,7 @@ __device__ __forceinline__ void sum_chunk_rows(const IdArgs& a, const OrderArgs&
 // rows: the summing waves, which wait for chains of reads, start first and the
 // writes fill the time around them (16384 tokens of natural frequencies into [32000,
 // 4096] bf16: 80 us; taking turns 86, in two launches 54 + 33).
-template <int GDT, bool TAIL>
+template <int GDT, int TAIL>
 __global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, TableGradArgs p)
 {
     const int64_t b = blockIdx.x;
@@ -594,12 +605,15 @@ hipError_t prepare_grad_as(const IdArgs& a, const OrderArgs& o, const void* dy, 
         return launch_kernel(kernel, (int)(list + chunks + zeros), s, a, o, dy, part, slices, (int32_t)list,
                              (int32_t)chunks, pad, dtable, ddt);
     };
-    return a.dim % 8 ? go(k_prepare_grad<GDT, true>) : go(k_prepare_grad<GDT, false>);
+    const int tail = tail_of(a.dim);
+    return tail == kWhole     ? go(k_prepare_grad<GDT, kWhole>)
+           : tail == kPartial ? go(k_prepare_grad<GDT, kPartial>)
+                              : go(k_prepare_grad<GDT, kShort>);
 }
 
 // Few tokens: workgroup (t, slice) of 256 units works if token t is the first of
 // its id; workgroups beyond the tokens' write zero rows.
-template <int GDT, bool TAIL>
+template <int GDT, int TAIL>
 __global__ __launch_bounds__(256) void k_table_grad_direct(IdArgs a, const void* __restrict__ dy, float scale, int64_t pad,
                                                            int accumulate, void* __restrict__ dtable, int ddt,
                                                            int32_t slices)
@@ -621,11 +635,7 @@ __global__ __launch_bounds__(256) void k_table_grad_direct(IdArgs a, const void*
     char* const row = static_cast<char*>(dtable) + (int64_t)v * dim * (ddt == DT_F32 ? 4 : 2);
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[0][j] *= scale;
-    if (accumulate) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < unit_count(unit, dim)) sum[0][j] += load1_rt(ddt, row, (int64_t)unit * 8 + j);
-    }
+    if (accumulate) add_row_unit_rt<TAIL>(ddt, row, unit, units, dim, sum[0]);
     store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, sum[0]);
 }
 
@@ -648,8 +658,11 @@ hipError_t table_grad_as(const IdArgs& a, const OrderArgs& o, TableGradArgs p, h
     p.work = (int32_t)work;
     p.zeros = (int32_t)zeros;
     if (work + zeros == 0) return hipSuccess;
-    const hipError_t e = a.dim % 8 ? launch_kernel(k_table_grad<GDT, true>, (int)(work + zeros), s, a, o, p)
-                                   : launch_kernel(k_table_grad<GDT, false>, (int)(work + zeros), s, a, o, p);
+    auto go = [&](auto kernel) { return launch_kernel(kernel, (int)(work + zeros), s, a, o, p); };
+    const int tail = tail_of(a.dim);
+    const hipError_t e = tail == kWhole     ? go(k_table_grad<GDT, kWhole>)
+                         : tail == kPartial ? go(k_table_grad<GDT, kPartial>)
+                                            : go(k_table_grad<GDT, kShort>);
     if (e != hipSuccess || a.n <= o.chunk) return e;       // no id can be long
     return launch_kernel(k_long_rows, long_wgs(a, o), s, o, a.dim, p);
 }
@@ -697,10 +710,16 @@ hipError_t launch_table_grad_direct(const IdArgs& a, const void* dy, int gdt, fl
     auto go = [&](auto kernel) {
         return launch_kernel(kernel, (int)grid, s, a, dy, scale, pad, accumulate ? 1 : 0, dtable, ddt, (int32_t)slices);
     };
-    const bool tail = a.dim % 8 != 0;
-    if (gdt == DT_F32) return tail ? go(k_table_grad_direct<DT_F32, true>) : go(k_table_grad_direct<DT_F32, false>);
-    if (gdt == DT_F16) return tail ? go(k_table_grad_direct<DT_F16, true>) : go(k_table_grad_direct<DT_F16, false>);
-    return tail ? go(k_table_grad_direct<DT_BF16, true>) : go(k_table_grad_direct<DT_BF16, false>);
+    auto with = [&](auto gdt_c) {
+        constexpr int GDT = decltype(gdt_c)::value;
+        const int tail = tail_of(a.dim);
+        return tail == kWhole     ? go(k_table_grad_direct<GDT, kWhole>)
+               : tail == kPartial ? go(k_table_grad_direct<GDT, kPartial>)
+                                  : go(k_table_grad_direct<GDT, kShort>);
+    };
+    if (gdt == DT_F32) return with(std::integral_constant<int, DT_F32>{});
+    if (gdt == DT_F16) return with(std::integral_constant<int, DT_F16>{});
+    return with(std::integral_constant<int, DT_BF16>{});
 }
 
 hipError_t launch_join_chunks(const IdArgs& a, const OrderArgs& o, float* part, hipStream_t s)

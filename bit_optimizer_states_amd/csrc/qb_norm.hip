@@ -108,7 +108,7 @@ hipError_t layer_norm_as(const void* x, int64_t n, int64_t dim, const NormArgs& 
 
 // Backward pass.  NT threads: NT / TPR rows at a time.  LDS (dynamic): gamma in
 // binary32 while the rows are walked, then the joined sums, padded_dim floats.
-template <int XDT, int WDT, int TPR, int VPT, bool TAIL, int NT>
+template <int XDT, int WDT, int TPR, int VPT, int TAIL, int NT>
 __global__ __launch_bounds__(NT) void k_norm_grad(const void* __restrict__ dy, const void* __restrict__ x, int64_t n,
                                                   int dim, const void* __restrict__ gamma,
                                                   const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(256) void k_norm_cols(const void* __restrict__ dy, 
 
 constexpr int kLongParts = 64;
 
-template <int XDT, int WDT, bool TAIL>
+template <int XDT, int WDT, int TAIL>
 hipError_t grad_as(const void* dy, const void* x, int64_t n, int dim, const void* gamma, const float* mean,
                    const float* rstd, void* dx, float* part, hipStream_t s)
 {
@@ -311,12 +311,15 @@ hipError_t grad_as(const void* dy, const void* x, int64_t n, int dim, const void
         return launch_kernel_lds(kernel, grid, threads, lds, s, dy, x, n, dim, gamma, mean, rstd, dx, part);
     };
     if (units <= 16) return go(k_norm_grad<XDT, WDT, 16, 1, TAIL, 512>, 512);
-    if (units <= 64) return go(k_norm_grad<XDT, WDT, 64, 1, TAIL, 512>, 512);
-    if (units <= 128) return go(k_norm_grad<XDT, WDT, 64, 2, TAIL, 512>, 512);
-    if (units <= 256) return go(k_norm_grad<XDT, WDT, 64, 4, TAIL, 512>, 512);
-    if (units <= 512) return go(k_norm_grad<XDT, WDT, 256, 2, TAIL, 1024>, 1024);
-    if (units <= 1024) return go(k_norm_grad<XDT, WDT, 256, 4, TAIL, 512>, 512);
-    return go(k_norm_grad<XDT, WDT, 512, 4, TAIL, 512>, 512);
+    if constexpr (TAIL != kShort) {
+        if (units <= 64) return go(k_norm_grad<XDT, WDT, 64, 1, TAIL, 512>, 512);
+        if (units <= 128) return go(k_norm_grad<XDT, WDT, 64, 2, TAIL, 512>, 512);
+        if (units <= 256) return go(k_norm_grad<XDT, WDT, 64, 4, TAIL, 512>, 512);
+        if (units <= 512) return go(k_norm_grad<XDT, WDT, 256, 2, TAIL, 1024>, 1024);
+        if (units <= 1024) return go(k_norm_grad<XDT, WDT, 256, 4, TAIL, 512>, 512);
+        return go(k_norm_grad<XDT, WDT, 512, 4, TAIL, 512>, 512);
+    }
+    return hipErrorInvalidValue;
 }
 
 template <int XDT, int WDT>
@@ -339,8 +342,10 @@ hipError_t layer_norm_grad_as(const void* dy, const void* x, int64_t n, int64_t 
         if (grid >= (int64_t(1) << 24)) return hipErrorInvalidValue;
         return launch_kernel(k_norm_cols<XDT>, (int)grid, s, dy, x, n, dim, mean, rstd, part, parts);
     }
-    return dim % 8 ? grad_as<XDT, WDT, true>(dy, x, n, (int)dim, gamma, mean, rstd, dx, part, s)
-                   : grad_as<XDT, WDT, false>(dy, x, n, (int)dim, gamma, mean, rstd, dx, part, s);
+    const int tail = tail_of(dim);
+    return tail == kWhole     ? grad_as<XDT, WDT, kWhole>(dy, x, n, (int)dim, gamma, mean, rstd, dx, part, s)
+           : tail == kPartial ? grad_as<XDT, WDT, kPartial>(dy, x, n, (int)dim, gamma, mean, rstd, dx, part, s)
+                              : grad_as<XDT, WDT, kShort>(dy, x, n, (int)dim, gamma, mean, rstd, dx, part, s);
 }
 
 // dgamma, dbeta = the sum of the partial rows.  A workgroup takes 64 of the 2 *

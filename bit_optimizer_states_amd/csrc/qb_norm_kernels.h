@@ -213,7 +213,7 @@ constexpr int norm_threads(int tpr) { return tpr > 64 ? tpr : 256; }
 // stay in registers (EARLY) and the next row is read before the current one is
 // reduced.  GATHER: row t is scale * table[ids[t]] (zeros out where the id is
 // outside the table); the id is read one row further ahead.
-template <int XDT, int YDT, int WDT, int TPR, int VPT, bool TAIL, bool GATHER>
+template <int XDT, int YDT, int WDT, int TPR, int VPT, int TAIL, bool GATHER>
 __global__ __launch_bounds__(norm_threads(TPR)) void k_norm(const void* __restrict__ x, IdArgs a, float scale,
                                                             const void* __restrict__ gamma,
                                                             const void* __restrict__ beta, float eps,
@@ -314,7 +314,7 @@ using threads_c = std::integral_constant<int, N>;
 
 // Threads and units per row.  Up to 128 elements 16 lanes share a row, up to
 // 2048 one wave (no barrier), beyond that a workgroup.
-template <int XDT, int YDT, int WDT, bool TAIL, bool GATHER>
+template <int XDT, int YDT, int WDT, int TAIL, bool GATHER>
 hipError_t norm_as(const void* x, const IdArgs& a, float scale, const NormArgs& w, void* y, float* mean, float* rstd,
                    hipStream_t s)
 {
@@ -326,12 +326,14 @@ hipError_t norm_as(const void* x, const IdArgs& a, float scale, const NormArgs& 
         return launch_kernel_nt(kernel, grid, T, s, x, a, scale, w.gamma, w.beta, w.eps, y, mean, rstd);
     };
     if (units <= 16) return go(k_norm<XDT, YDT, WDT, 16, 1, TAIL, GATHER>, threads_c<16>{});
-    if (units <= 64) return go(k_norm<XDT, YDT, WDT, 64, 1, TAIL, GATHER>, threads_c<64>{});
-    if (units <= 128) return go(k_norm<XDT, YDT, WDT, 64, 2, TAIL, GATHER>, threads_c<64>{});
-    if (units <= 256) return go(k_norm<XDT, YDT, WDT, 64, 4, TAIL, GATHER>, threads_c<64>{});
-    if (units <= 512) return go(k_norm<XDT, YDT, WDT, 256, 2, TAIL, GATHER>, threads_c<256>{});
-    if (units <= 1024) return go(k_norm<XDT, YDT, WDT, 512, 2, TAIL, GATHER>, threads_c<512>{});
-    if (units <= 2048) return go(k_norm<XDT, YDT, WDT, 1024, 2, TAIL, GATHER>, threads_c<1024>{});
+    if constexpr (TAIL != kShort) {
+        if (units <= 64) return go(k_norm<XDT, YDT, WDT, 64, 1, TAIL, GATHER>, threads_c<64>{});
+        if (units <= 128) return go(k_norm<XDT, YDT, WDT, 64, 2, TAIL, GATHER>, threads_c<64>{});
+        if (units <= 256) return go(k_norm<XDT, YDT, WDT, 64, 4, TAIL, GATHER>, threads_c<64>{});
+        if (units <= 512) return go(k_norm<XDT, YDT, WDT, 256, 2, TAIL, GATHER>, threads_c<256>{});
+        if (units <= 1024) return go(k_norm<XDT, YDT, WDT, 512, 2, TAIL, GATHER>, threads_c<512>{});
+        if (units <= 2048) return go(k_norm<XDT, YDT, WDT, 1024, 2, TAIL, GATHER>, threads_c<1024>{});
+    }
     return hipErrorInvalidValue;
 }
 
@@ -339,8 +341,10 @@ template <int XDT, int YDT, int WDT, bool GATHER>
 hipError_t norm_dim(const void* x, const IdArgs& a, float scale, const NormArgs& w, void* y, float* mean, float* rstd,
                     hipStream_t s)
 {
-    return a.dim % 8 ? norm_as<XDT, YDT, WDT, true, GATHER>(x, a, scale, w, y, mean, rstd, s)
-                     : norm_as<XDT, YDT, WDT, false, GATHER>(x, a, scale, w, y, mean, rstd, s);
+    const int tail = tail_of(a.dim);
+    return tail == kWhole     ? norm_as<XDT, YDT, WDT, kWhole, GATHER>(x, a, scale, w, y, mean, rstd, s)
+           : tail == kPartial ? norm_as<XDT, YDT, WDT, kPartial, GATHER>(x, a, scale, w, y, mean, rstd, s)
+                              : norm_as<XDT, YDT, WDT, kShort, GATHER>(x, a, scale, w, y, mean, rstd, s);
 }
 
 }  // namespace qb

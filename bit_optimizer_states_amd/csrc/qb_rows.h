@@ -82,24 +82,31 @@ __device__ __forceinline__ void shift_unit(Unit<DT>& u, int by)
     }
 }
 
+// What the last unit of a row is: whole, partial, or the row's only one of fewer
+// than 8 elements.
+constexpr int kWhole = 0, kPartial = 1, kShort = 2;
+constexpr int tail_of(int64_t dim) { return dim < 8 ? kShort : dim % 8 ? kPartial : kWhole; }
+
 // Unit number `unit` of a row of `dim` elements.  A unit beyond the row (unit >=
-// ceil(dim / 8)) reads unit 0 instead (its caller masks it), so that no load
-// is under a branch.  TAIL: dim is no multiple of 8; the partial last unit is read as
-// the row's last 8 elements and shifted, for the same reason (element by element
-// the one lane that holds it took a chain of up to 7 loads while its wave
-// waited).  Only rows of fewer than 8 elements are read one by one.
-template <int DT, bool TAIL, bool NT>
+// ceil(dim / 8)) reads unit 0 instead (its caller masks it), and a partial last
+// unit is read as the row's last 8 elements and shifted, so that no load is under a
+// branch and a wave's loads are in flight together.  (Read element by element, the
+// one lane that holds the partial unit took a chain of up to 7 loads while its wave
+// waited; with a branch for rows of fewer than 8 elements every load was waited for
+// before the next.)
+template <int DT, int TAIL, bool NT>
 __device__ __forceinline__ Unit<DT> load_row_unit(const void* row, int unit, int units, int dim)
 {
     const int e = (unit < units ? unit : 0) * 8;
-    if constexpr (!TAIL) {
+    if constexpr (TAIL == kWhole) {
         return load_unit8<DT, NT>(row, e);
-    } else {
-        if (dim < 8) return load_part8<DT>(row, 0, dim);
+    } else if constexpr (TAIL == kPartial) {
         const int at = e < dim - 8 ? e : dim - 8;
         Unit<DT> u = load_unit8<DT, NT>(row, at);
         shift_unit<DT>(u, e - at);
         return u;
+    } else {
+        return load_part8<DT>(row, 0, dim);
     }
 }
 
@@ -138,7 +145,7 @@ __device__ __forceinline__ void store_unit8(void* row, int64_t elem, const float
 }
 
 // Stores unit `unit` of a row (nothing beyond the row, a partial last unit element by element).
-template <int DT, bool TAIL, bool NT>
+template <int DT, int TAIL, bool NT>
 __device__ __forceinline__ void store_row_unit(void* row, int unit, int units, int dim, const float* v)
 {
     if (unit >= units) return;
@@ -154,13 +161,54 @@ __device__ __forceinline__ void store_row_unit(void* row, int unit, int units, i
     store_unit8<DT, NT>(row, (int64_t)unit * 8, v);
 }
 
-// The same with the type known at run time only (uniform).
-template <bool TAIL, bool NT>
+// The same with the type known at run time only (uniform).  Both 16-bit types
+// share the stores: these calls sit in loops whose code a few waves run once, bound by
+// the fetch of its instructions.
+template <int TAIL, bool NT>
 __device__ __forceinline__ void store_row_unit_rt(int dt, void* row, int unit, int units, int dim, const float* v)
 {
-    if (dt == DT_F32) store_row_unit<DT_F32, TAIL, NT>(row, unit, units, dim, v);
-    else if (dt == DT_F16) store_row_unit<DT_F16, TAIL, NT>(row, unit, units, dim, v);
-    else store_row_unit<DT_BF16, TAIL, NT>(row, unit, units, dim, v);
+    if (dt == DT_F32) {
+        store_row_unit<DT_F32, TAIL, NT>(row, unit, units, dim, v);
+        return;
+    }
+    u32x4 a;
+    if (dt == DT_BF16)
+        a = u32x4{pack_pair<DT_BF16>(v[0], v[1]), pack_pair<DT_BF16>(v[2], v[3]), pack_pair<DT_BF16>(v[4], v[5]),
+                  pack_pair<DT_BF16>(v[6], v[7])};
+    else
+        a = u32x4{pack_pair<DT_F16>(v[0], v[1]), pack_pair<DT_F16>(v[2], v[3]), pack_pair<DT_F16>(v[4], v[5]),
+                  pack_pair<DT_F16>(v[6], v[7])};
+    if (unit >= units) return;
+    char* const p = static_cast<char*>(row) + (int64_t)unit * 16;
+    if (TAIL && dim - unit * 8 < 8) {
+        const int left = dim - unit * 8;
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < left) gst<uint16_t>(p + 2 * j, (uint16_t)(a[j >> 1] >> (16 * (j & 1))));
+        return;
+    }
+    QB_G u32x4_a2* const q = (QB_G u32x4_a2*)p;
+    if constexpr (NT) __builtin_nontemporal_store(a, q);
+    else *q = a;
+}
+
+// v += unit `unit` of a row whose type is known at run time only.
+template <int TAIL>
+__device__ __forceinline__ void add_row_unit_rt(int dt, const void* row, int unit, int units, int dim, float* v)
+{
+    if (dt == DT_F32) {
+        const Unit<DT_F32> u = load_row_unit<DT_F32, TAIL, false>(row, unit, units, dim);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += unit_at<DT_F32>(u, j);
+    } else {
+        // (the 16-bit loads do not depend on which of the two types it is)
+        const Unit<DT_BF16> u = load_row_unit<DT_BF16, TAIL, false>(row, unit, units, dim);
+        Unit<DT_F16> h;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h.w[j] = u.w[j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += dt == DT_BF16 ? unit_at<DT_BF16>(u, j) : unit_at<DT_F16>(h, j);
+    }
 }
 
 __device__ __forceinline__ float load1_rt(int dt, const void* p, int64_t i)

@@ -34,7 +34,7 @@ struct StableGradArgs {
 
 // Work on single ids by a whole workgroup: TPR threads, unit k * TPR + tid in
 // register k, the sums of dgamma and dbeta over the workgroup's ids.
-template <int GDT, int TDT, int TPR, int VPT, bool TAIL>
+template <int GDT, int TDT, int TPR, int VPT, int TAIL>
 struct StableRows {
     const IdArgs& a;
     const StableGradArgs& p;
@@ -116,11 +116,7 @@ struct StableRows {
             float out[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) out[j] = f * (sum[k][j] - __builtin_fmaf(x[k][j], c2, c1));
-            if (p.accumulate) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < unit_count(unit, dim)) out[j] += load1_rt(p.ddt, row, (int64_t)unit * 8 + j);
-            }
+            if (p.accumulate) add_row_unit_rt<TAIL>(p.ddt, row, unit, units, dim, out);
             store_row_unit_rt<TAIL, true>(p.ddt, row, unit, units, dim, out);
         }
     }
@@ -162,7 +158,7 @@ struct StableRows {
 // next id's row and first token before it works on the current one.  (Two ids at a
 // time, sharing the barriers, spilled or halved the resident workgroups: 60 to 65 us
 // against 55 for 4300 ids of 4096 elements.)
-template <int GDT, int TDT, int TPR, int VPT, bool TAIL>
+template <int GDT, int TDT, int TPR, int VPT, int TAIL>
 __global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, StableGradArgs p)
 {
     __shared__ float s_slot[2 * row_slot_words(TPR)];
@@ -221,7 +217,7 @@ __global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, Stab
 
 // Few tokens: workgroup t works if token t is the first of its id, and writes
 // partial sums in any case; workgroups beyond the tokens' write zero rows.
-template <int GDT, int TDT, int TPR, int VPT, bool TAIL>
+template <int GDT, int TDT, int TPR, int VPT, int TAIL>
 __global__ __launch_bounds__(TPR) void k_stable_grad_direct(IdArgs a, StableGradArgs p)
 {
     __shared__ float s_slot[2 * row_slot_words(TPR)];
@@ -245,7 +241,7 @@ __global__ __launch_bounds__(TPR) void k_stable_grad_direct(IdArgs a, StableGrad
     r.put_parts(t);
 }
 
-template <int GDT, int TDT, int TPR, int VPT, bool TAIL>
+template <int GDT, int TDT, int TPR, int VPT, int TAIL>
 hipError_t stable_grad_tpr(const IdArgs& a, const OrderArgs* o, const StableGradArgs& p, int parts, hipStream_t s)
 {
     if (!o)
@@ -256,15 +252,17 @@ hipError_t stable_grad_tpr(const IdArgs& a, const OrderArgs* o, const StableGrad
 
 // One unit per thread up to 8192 elements: a workgroup of many waves hides the
 // latency of its reads with the few registers of each.  o nullptr: few tokens.
-template <int GDT, int TDT, bool TAIL>
+template <int GDT, int TDT, int TAIL>
 hipError_t stable_grad_as(const IdArgs& a, const OrderArgs* o, const StableGradArgs& p, int parts, hipStream_t s)
 {
     const int units = (a.dim + 7) / 8;
     if (units <= 64) return stable_grad_tpr<GDT, TDT, 64, 1, TAIL>(a, o, p, parts, s);
-    if (units <= 256) return stable_grad_tpr<GDT, TDT, 256, 1, TAIL>(a, o, p, parts, s);
-    if (units <= 512) return stable_grad_tpr<GDT, TDT, 512, 1, TAIL>(a, o, p, parts, s);
-    if (units <= 1024) return stable_grad_tpr<GDT, TDT, 1024, 1, TAIL>(a, o, p, parts, s);
-    if (units <= 2048) return stable_grad_tpr<GDT, TDT, 1024, 2, TAIL>(a, o, p, parts, s);
+    if constexpr (TAIL != kShort) {
+        if (units <= 256) return stable_grad_tpr<GDT, TDT, 256, 1, TAIL>(a, o, p, parts, s);
+        if (units <= 512) return stable_grad_tpr<GDT, TDT, 512, 1, TAIL>(a, o, p, parts, s);
+        if (units <= 1024) return stable_grad_tpr<GDT, TDT, 1024, 1, TAIL>(a, o, p, parts, s);
+        if (units <= 2048) return stable_grad_tpr<GDT, TDT, 1024, 2, TAIL>(a, o, p, parts, s);
+    }
     return hipErrorInvalidValue;
 }
 
@@ -272,14 +270,16 @@ template <int GDT>
 hipError_t stable_grad_t(const IdArgs& a, const OrderArgs* o, const StableGradArgs& p, int parts, int tdt,
                          hipStream_t s)
 {
-    if (a.dim % 8) {
-        if (tdt == DT_F32) return stable_grad_as<GDT, DT_F32, true>(a, o, p, parts, s);
-        if (tdt == DT_F16) return stable_grad_as<GDT, DT_F16, true>(a, o, p, parts, s);
-        return stable_grad_as<GDT, DT_BF16, true>(a, o, p, parts, s);
-    }
-    if (tdt == DT_F32) return stable_grad_as<GDT, DT_F32, false>(a, o, p, parts, s);
-    if (tdt == DT_F16) return stable_grad_as<GDT, DT_F16, false>(a, o, p, parts, s);
-    return stable_grad_as<GDT, DT_BF16, false>(a, o, p, parts, s);
+    auto with = [&](auto tdt_c) {
+        constexpr int TDT = decltype(tdt_c)::value;
+        const int tail = tail_of(a.dim);
+        return tail == kWhole     ? stable_grad_as<GDT, TDT, kWhole>(a, o, p, parts, s)
+               : tail == kPartial ? stable_grad_as<GDT, TDT, kPartial>(a, o, p, parts, s)
+                                  : stable_grad_as<GDT, TDT, kShort>(a, o, p, parts, s);
+    };
+    if (tdt == DT_F32) return with(std::integral_constant<int, DT_F32>{});
+    if (tdt == DT_F16) return with(std::integral_constant<int, DT_F16>{});
+    return with(std::integral_constant<int, DT_BF16>{});
 }
 
 }  // namespace

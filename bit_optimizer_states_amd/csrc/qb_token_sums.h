@@ -10,7 +10,7 @@ constexpr int kZeroRows = 16;           // table rows of a zero-filling workgrou
 
 // sum[k] += dy of the units k * TPR + tid over the R tokens whose positions lanes
 // i .. i + R - 1 hold, in order; the loads of all R rows are in flight together.
-template <int GDT, bool TAIL, int TPR, int VPT, int R>
+template <int GDT, int TAIL, int TPR, int VPT, int R>
 __device__ __forceinline__ void add_tokens(int32_t pos, int32_t i, const void* dy, int tid, int units, int dim,
                                            float (&sum)[VPT][8])
 {
@@ -35,7 +35,7 @@ __device__ __forceinline__ void add_tokens(int32_t pos, int32_t i, const void* d
 // per lane, and handed out by readlane.  Most ids have one to three tokens:
 // each remainder has its own straight code, since a wave that reads a row it
 // does not need waits as long as for one that it does.
-template <int GDT, bool TAIL, int TPR, int VPT, int UN>
+template <int GDT, int TAIL, int TPR, int VPT, int UN>
 __device__ __forceinline__ void sum_tokens(const int32_t* order, int32_t first, int32_t last, const void* dy, int tid,
                                            int units, int dim, float (&sum)[VPT][8])
 {
@@ -124,7 +124,7 @@ struct DirectIds {
 
 // sum[k] += dy of the units k * TPR + tid over the tokens of `mask` (bit l: token
 // 64 h + l), in order, UN tokens in flight.
-template <int GDT, bool TAIL, int TPR, int VPT, int UN>
+template <int GDT, int TAIL, int TPR, int VPT, int UN>
 __device__ __forceinline__ void sum_masked(unsigned long long mask, int h, const void* dy, int tid, int units, int dim,
                                            float (&sum)[VPT][8])
 {
@@ -156,7 +156,7 @@ __device__ __forceinline__ void sum_masked(unsigned long long mask, int h, const
 
 // One workgroup of THREADS threads: zeros into the rows of kZeroRows that no
 // token names, and into pad's.
-template <bool TAIL, int THREADS>
+template <int TAIL, int THREADS>
 __device__ __forceinline__ void zero_unnamed(const IdArgs& a, const DirectIds& ids, int64_t v0, int64_t pad, void* dtable,
                                              int ddt)
 {
