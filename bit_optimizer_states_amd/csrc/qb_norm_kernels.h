@@ -222,7 +222,10 @@ __global__ __launch_bounds__(norm_threads(TPR)) void k_norm(const void* __restri
 {
     constexpr int RPB = norm_threads(TPR) / TPR;
     constexpr bool EARLY = VPT <= 2;
-    __shared__ float s_slot[RPB][row_slot_words(TPR)];
+    // two slots in turn: a wave may leave its share of the next row while another still
+    // reads this row's (one barrier a row)
+    __shared__ float s_slot[2][RPB][row_slot_words(TPR)];
+    int buf = 0;
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int dim = a.dim, units = (dim + 7) >> 3;
     const int64_t step = (int64_t)gridDim.x * RPB;
@@ -287,7 +290,10 @@ __global__ __launch_bounds__(norm_threads(TPR)) void k_norm(const void* __restri
         }
         load_row(id);
         float mean = 0.0f, rstd = 0.0f;
-        if (TPR < 64 || found) row_stats<TPR, VPT, XDT == DT_F32>(v, shape, lane, dim, eps, s_slot[grp], &mean, &rstd);
+        if (TPR < 64 || found) {
+            row_stats<TPR, VPT, XDT == DT_F32>(v, shape, lane, dim, eps, s_slot[buf][grp], &mean, &rstd);
+            buf ^= 1;                    // (only behind a barrier)
+        }
         if (t >= a.n) continue;
         if (lane == 0) {
             if (mean_out) mean_out[t] = mean;
