@@ -6,12 +6,14 @@
 //
 // Gradient: dW[v] = scale * (sum of dy_t over the tokens t with id_t = v), in
 // three launches.  The tokens are ordered by id (k_order), so that every sum is
-// taken by one wave in ascending order of the tokens: no atomics on
-// floating-point values, the same bits on every run.  An id with more tokens than a
-// chunk holds is summed chunk by chunk by many waves, and in the same launch the
-// zero rows of the table are written, which keeps HBM busy meanwhile
-// (k_prepare_grad).  The last launch sums and writes the rows of the ids that
-// have tokens, and only those (k_table_grad).
+// taken in ascending order of the tokens: no atomics on floating-point values,
+// the same bits on every run.  Then every wave streams one chunk of the ordered
+// tokens: it writes the rows of the ids that begin there, and a partial row for an
+// id that has more tokens than a chunk; the same launch writes the zero rows of the
+// table (k_table_grad).  The last launch adds the partial rows (k_long_rows).
+// Up to 128 tokens take one launch without ordering (k_table_grad_direct).  The
+// stable embedding's gradient shares the ordering and prepares its sums of long ids
+// and its zero rows with k_prepare_grad and k_join_chunks.
 #include <type_traits>
 
 #include "qb_token_sums.h"
@@ -24,7 +26,10 @@ namespace {
 // lookup
 // ---------------------------------------------------------------------------
 
-// `lanes` (a power of two) threads share a token, 256 / lanes tokens a workgroup.
+// `lanes` (a power of two) threads share a token, 256 / lanes tokens a workgroup;
+// the id is the only read that others wait for.  Bound by HBM: 16384 tokens of
+// natural frequencies, [32000, 4096] bf16, 45 us (134 MB of output and the 90 MB of
+// rows that are used: 5.0 TB/s); 16 tokens 2.6 us, the latency of two dependent reads.
 template <int TDT, int YDT, int TAIL>
 __global__ __launch_bounds__(256) void k_embedding(IdArgs a, const void* __restrict__ table, float scale,
                                                    void* __restrict__ y, int log2lanes)
@@ -93,7 +98,8 @@ hipError_t embedding_y(const IdArgs& a, const void* table, float scale, void* y,
 // rows.  TAIL: dim is no multiple of 8, rows may begin inside a byte or a
 // block, and every element finds its own code and block; otherwise a unit of 8
 // elements is 4 or 8 aligned bytes of codes with one scale (blocks hold 64
-// elements or more).
+// elements or more).  Bound by the writes of y: 16384 tokens of 4096, NF4 with nested
+// constants to bf16, 24 us (5.6 TB/s of 134 MB); 32 tokens 3.3 us.
 template <int BITS, int YDT, bool DQ, int TAIL>
 __global__ __launch_bounds__(256) void k_dequant_embedding(IdArgs a, DequantDesc d, int log2B, int log2B2, int code4,
                                                            const QbTables* __restrict__ tab, float scale,
@@ -207,7 +213,11 @@ hipError_t dequant_embedding_y(const IdArgs& a, const DequantDesc& d, int code4,
 // consecutive places by their lane, so the order is stable and no workgroup waits
 // for another.  The ids are read from L2 by every workgroup, n * classes reads in
 // exchange for one launch and no atomics in memory; up to 16384 tokens a wave
-// keeps its stretch in registers for the second time.
+// keeps its stretch in registers for the second time.  Bound by the chain load -
+// count - scan - place of one workgroup per CU, not by bytes: 16384 ids of 32000 in 11
+// us, 5003 in 8 us.  (Writing the zero rows beside it does not pay: their place is
+// known only after it, and zeros under rows that are written again later took it from
+// 11 to 17 us and the whole call with it.)
 template <bool ID64>
 __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs o)
 {
@@ -246,6 +256,7 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
         if (!once) load_ids(t0);
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
+            if (t0 + k * 64 >= last) break;            // (uniform; few tokens run little of this code)
             if (id[k] >= 0) {
                 const int32_t c = id[k] & mask;
                 below += c < cls ? 1 : 0;
@@ -304,6 +315,7 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
         if (!once) load_ids(t0);
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
+            if (t0 + k * 64 >= last) break;
             const bool mine = id[k] >= 0 && (id[k] & mask) == cls;
             unsigned long long todo = __ballot(mine);
             while (todo) {
@@ -421,6 +433,8 @@ __device__ __forceinline__ void zero_rows(const IdArgs& a, const OrderArgs& o, i
     }
 }
 
+// The work with the longest chains of reads first.  Bound by HBM: 54 us for the case of
+// k_table_grad, where 227 MB of zeros are written beside the long ids' tokens.
 template <int GDT, int TAIL>
 __global__ __launch_bounds__(256) void k_prepare_grad(IdArgs a, OrderArgs o, const void* __restrict__ dy,
                                                       float* __restrict__ part, int32_t slices, int32_t list_wgs,
@@ -444,7 +458,7 @@ __global__ __launch_bounds__(256) void k_prepare_grad(IdArgs a, OrderArgs o, con
 }
 
 // Joined sums of the long ids, 64 columns a wave, into the slot of the first
-// chunk (which no other wave reads in these columns).
+// chunk (which no other wave reads in these columns); 4.8 us as k_long_rows.
 __global__ __launch_bounds__(256) void k_join_chunks(OrderArgs o, float* __restrict__ part, int64_t padded)
 {
     const int lane = threadIdx.x % 64;
@@ -474,7 +488,9 @@ struct TableGradArgs {
 //  - the chunk's tokens of long ids, into the chunk's partial rows.
 // Lane l holds token c * chunk + l (two chunks are at most the 64 lanes) with the
 // range of its id; UN tokens' units are in flight while UN are added, whatever
-// ids they belong to.
+// ids they belong to (4 instead of 8 of 16 bits: 97 us against 93 for 16384 tokens of
+// 4096).  The code that ends an id is there UN times: once, in a loop over the
+// pieces of ids among the UN tokens, made calls of 300 to 4000 tokens 2 to 3 us slower.
 template <int GDT, int TAIL>
 __device__ __forceinline__ void sum_chunk_rows(const IdArgs& a, const OrderArgs& o, const TableGradArgs& p, int64_t c,
                                                int slice)
@@ -512,47 +528,41 @@ __device__ __forceinline__ void sum_chunk_rows(const IdArgs& a, const OrderArgs&
         }
     };
     load(i);
+    // an id's last token was added: its row, or the chunk's partial row
     float sum[8] = {};
+    auto end_id = [&](int l) {
+        if ((longs >> l) & 1) {
+            const int64_t padded = (int64_t)units * 8;
+            float* const out = p.part + chunk_slot((int32_t)c, __builtin_amdgcn_readlane(lo, l), o.chunk) * padded +
+                               (int64_t)unit * 8;
+            if (unit < units) {
+                gst<f32x4>(out, f32x4{sum[0], sum[1], sum[2], sum[3]});
+                gst<f32x4>(out + 4, f32x4{sum[4], sum[5], sum[6], sum[7]});
+            }
+        } else {
+            const int64_t v0 = __builtin_amdgcn_readlane(id, l);
+            if (v0 != p.pad) {
+                char* const row = static_cast<char*>(p.dtable) + v0 * dim * (p.ddt == DT_F32 ? 4 : 2);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] *= p.scale;
+                if (p.accumulate) add_row_unit_rt<TAIL>(p.ddt, row, unit, units, dim, sum);
+                store_row_unit_rt<TAIL, true>(p.ddt, row, unit, units, dim, sum);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    };
     for (; i < i1; i += UN) {
         Unit<GDT> v[UN];
 #pragma unroll
         for (int q = 0; q < UN; ++q) v[q] = u[q];
         if (i + UN < i1) load(i + UN);
-        // the pieces of ids among these UN tokens, one after the other: the code that
-        // ends an id is there once
-        const int held = i1 - i < UN ? i1 - i : UN;
-        for (int q0 = 0; q0 < held;) {
-            const unsigned long long rest = ends >> (i + q0);
-            const int e = rest ? q0 + __builtin_ctzll(rest) + 1 : held + 1;      // one past the id's last token
 #pragma unroll
-            for (int q = 0; q < UN; ++q)
-                if (q >= q0 && q < e && q < held) {
+        for (int q = 0; q < UN; ++q) {
+            if (i + q >= i1) break;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] += unit_at<GDT>(v[q], j);
-                }
-            q0 = e;
-            if (e > held) break;
-            const int l = i + e - 1;
-            if ((longs >> l) & 1) {
-                const int64_t padded = (int64_t)units * 8;
-                float* const out = p.part + chunk_slot((int32_t)c, __builtin_amdgcn_readlane(lo, l), o.chunk) * padded +
-                                   (int64_t)unit * 8;
-                if (unit < units) {
-                    gst<f32x4>(out, f32x4{sum[0], sum[1], sum[2], sum[3]});
-                    gst<f32x4>(out + 4, f32x4{sum[4], sum[5], sum[6], sum[7]});
-                }
-            } else {
-                const int64_t v0 = __builtin_amdgcn_readlane(id, l);
-                if (v0 != p.pad) {
-                    char* const row = static_cast<char*>(p.dtable) + v0 * dim * (p.ddt == DT_F32 ? 4 : 2);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] *= p.scale;
-                    if (p.accumulate) add_row_unit_rt<TAIL>(p.ddt, row, unit, units, dim, sum);
-                    store_row_unit_rt<TAIL, true>(p.ddt, row, unit, units, dim, sum);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+            for (int j = 0; j < 8; ++j) sum[j] += unit_at<GDT>(v[q], j);
+            if ((ends >> (i + q)) & 1) end_id(i + q);
         }
     }
 }
@@ -560,7 +570,8 @@ __device__ __forceinline__ void sum_chunk_rows(const IdArgs& a, const OrderArgs&
 // p.work workgroups that sum (four waves each), then p.zeros that write zero
 // rows: the summing waves, which wait for chains of reads, start first and the
 // writes fill the time around them (16384 tokens of natural frequencies into [32000,
-// 4096] bf16: 80 us; taking turns 86, in two launches 54 + 33).
+// 4096] bf16: 75 to 80 us; taking turns 86, in two launches 54 + 33).  Bound by HBM
+// with rows in scattered order: 383 MB to move, 5 TB/s.
 template <int GDT, int TAIL>
 __global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, TableGradArgs p)
 {
@@ -574,7 +585,8 @@ __global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, Table
     }
 }
 
-// The rows of the long ids, one wave per 64 columns.
+// The rows of the long ids, one wave per 64 columns: 4.8 us, mostly the launch and
+// the chain count - range - partial rows.
 __global__ __launch_bounds__(256) void k_long_rows(OrderArgs o, int dim, TableGradArgs p)
 {
     const int lane = threadIdx.x % 64;
@@ -612,7 +624,8 @@ hipError_t prepare_grad_as(const IdArgs& a, const OrderArgs& o, const void* dy, 
 }
 
 // Few tokens: workgroup (t, slice) of 256 units works if token t is the first of
-// its id; workgroups beyond the tokens' write zero rows.
+// its id; workgroups beyond the tokens' write zero rows.  A call is bound by its launch
+// on the host: 8.2 us, against 12 to 15 with the ordering.
 template <int GDT, int TAIL>
 __global__ __launch_bounds__(256) void k_table_grad_direct(IdArgs a, const void* __restrict__ dy, float scale, int64_t pad,
                                                            int accumulate, void* __restrict__ dtable, int ddt,
