@@ -260,22 +260,43 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_grad_long(const void* __r
     const char* const grow = static_cast<const char*>(dy) + row;
     char* const orow = static_cast<char*>(dx) + row;
     const float m = mean_in[t], r = rstd_in[t];
+    const int64_t whole = dim / 8, i = whole * 8 + threadIdx.x;        // i: one of the last dim % 8 elements
+    const bool last = i < dim;
     float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t i = threadIdx.x; i < dim; i += kLongThreads) {
-        const float g = load1<XDT>(grow, i) * (gamma ? load1<WDT>(gamma, i) : 1.0f);
-        s1 += g;
-        s2 = __builtin_fmaf(g, (load1<XDT>(xrow, i) - m) * r, s2);
+    for (int64_t u = threadIdx.x; u < whole; u += kLongThreads) {
+        const Unit<XDT> xu = load_unit8<XDT, false>(xrow, u * 8), du = load_unit8<XDT, false>(grow, u * 8);
+        Unit<WDT> gu;
+        if (gamma) gu = load_unit8<WDT, false>(gamma, u * 8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float g = unit_at<XDT>(du, j) * (gamma ? unit_at<WDT>(gu, j) : 1.0f);
+            s1 += g;
+            s2 = __builtin_fmaf(g, (unit_at<XDT>(xu, j) - m) * r, s2);
+        }
     }
+    const float gl = last ? load1<XDT>(grow, i) * (gamma ? load1<WDT>(gamma, i) : 1.0f) : 0.0f;
+    const float hl = last ? (load1<XDT>(xrow, i) - m) * r : 0.0f;
+    s1 += gl;
+    s2 = __builtin_fmaf(gl, hl, s2);
     row_sum2<kLongThreads>(s1, s2, s_slot);
     const float c1 = s1 / (float)dim, c2 = s2 / (float)dim;
-    for (int64_t i = threadIdx.x; i < dim; i += kLongThreads) {
-        const float g = load1<XDT>(grow, i) * (gamma ? load1<WDT>(gamma, i) : 1.0f);
-        store1<XDT>(orow, i, r * (g - __builtin_fmaf((load1<XDT>(xrow, i) - m) * r, c2, c1)));
+    for (int64_t u = threadIdx.x; u < whole; u += kLongThreads) {
+        const Unit<XDT> xu = load_unit8<XDT, false>(xrow, u * 8), du = load_unit8<XDT, false>(grow, u * 8);
+        Unit<WDT> gu;
+        if (gamma) gu = load_unit8<WDT, false>(gamma, u * 8);
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float g = unit_at<XDT>(du, j) * (gamma ? unit_at<WDT>(gu, j) : 1.0f);
+            o[j] = r * (g - __builtin_fmaf((unit_at<XDT>(xu, j) - m) * r, c2, c1));
+        }
+        store_unit8<XDT, true>(orow, u * 8, o);
     }
+    if (last) store1<XDT>(orow, i, r * (gl - __builtin_fmaf(hl, c2, c1)));
 }
 
 // ... and the column sums apart: workgroup (b % parts) takes the rows t = part,
-// part + parts, ... of 256 columns.
+// part + parts, ... of 256 columns, four rows in flight.
 template <int XDT>
 __global__ __launch_bounds__(256) void k_norm_cols(const void* __restrict__ dy, const void* __restrict__ x, int64_t n,
                                                    int64_t dim, const float* __restrict__ mean_in,
@@ -287,6 +308,7 @@ __global__ __launch_bounds__(256) void k_norm_cols(const void* __restrict__ dy, 
     if (c >= padded) return;
     float sg = 0.0f, sb = 0.0f;
     if (c < dim) {
+#pragma unroll 4
         for (int64_t t = p; t < n; t += parts) {
             const float d = load1<XDT>(dy, t * dim + c);
             sg = __builtin_fmaf(d, (load1<XDT>(x, t * dim + c) - mean_in[t]) * rstd_in[t], sg);
