@@ -459,18 +459,11 @@ __global__ __launch_bounds__(256) void k_prepare_grad(IdArgs a, OrderArgs o, con
 
 // Joined sums of the long ids, 64 columns a wave, into the slot of the first
 // chunk (which no other wave reads in these columns); 4.8 us as k_long_rows.
-__global__ __launch_bounds__(256) void k_join_chunks(OrderArgs o, float* __restrict__ part, int64_t padded)
+__global__ __launch_bounds__(kJoinWaves * 64) void k_join_chunks(OrderArgs o, float* __restrict__ part, int64_t padded)
 {
-    const int lane = threadIdx.x % 64;
-    const int64_t groups = (padded + 63) / 64, tasks = (int64_t)o.count[1] * groups;
-    for (int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64); w < tasks;
-         w += (int64_t)gridDim.x * 4) {
-        const int64_t s = slot_of(o.longs[w / groups], o), col = w % groups * 64 + lane;
-        const int32_t first = o.start[s], last = o.start[s + 1];
-        if (col < padded)
-            part[chunk_slot(first / o.chunk, first, o.chunk) * padded + col] =
-                join_column(part, o.chunk, first, last, padded, col);
-    }
+    join_long_ids(o, part, padded, [&](int64_t, int32_t first, int64_t col, float sum) {
+        part[chunk_slot(first / o.chunk, first, o.chunk) * padded + col] = sum;
+    });
 }
 
 struct TableGradArgs {
@@ -587,19 +580,15 @@ __global__ __launch_bounds__(256) void k_table_grad(IdArgs a, OrderArgs o, Table
 
 // The rows of the long ids, one wave per 64 columns: 4.8 us, mostly the launch and
 // the chain count - range - partial rows.
-__global__ __launch_bounds__(256) void k_long_rows(OrderArgs o, int dim, TableGradArgs p)
+__global__ __launch_bounds__(kJoinWaves * 64) void k_long_rows(OrderArgs o, int dim, TableGradArgs p)
 {
-    const int lane = threadIdx.x % 64;
-    const int64_t padded = (dim + 7) / 8 * 8, groups = (dim + 63) / 64, tasks = (int64_t)o.count[1] * groups;
-    for (int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64); w < tasks;
-         w += (int64_t)gridDim.x * 4) {
-        const int64_t v = o.longs[w / groups], s = slot_of(v, o), col = w % groups * 64 + lane;
-        if (v == p.pad || col >= dim) continue;
-        float sum = join_column(p.part, o.chunk, o.start[s], o.start[s + 1], padded, col) * p.scale;
+    join_long_ids(o, p.part, (dim + 7) / 8 * 8, [&](int64_t v, int32_t, int64_t col, float sum) {
+        if (v == p.pad || col >= dim) return;
+        sum *= p.scale;
         char* const row = static_cast<char*>(p.dtable) + v * dim * (p.ddt == DT_F32 ? 4 : 2);
         if (p.accumulate) sum += load1_rt(p.ddt, row, col);
         store1_rt(p.ddt, row, col, sum);
-    }
+    });
 }
 
 template <int GDT>
@@ -652,10 +641,10 @@ __global__ __launch_bounds__(256) void k_table_grad_direct(IdArgs a, const void*
     store_row_unit_rt<TAIL, true>(ddt, row, unit, units, dim, sum[0]);
 }
 
-// Workgroups for the columns of the long ids, 8 per CU at most.
+// Workgroups for the columns of the long ids, 4 per CU at most.
 int long_wgs(const IdArgs& a, const OrderArgs& o)
 {
-    const int64_t wgs = (a.n / o.chunk * ((a.dim + 63) / 64) + 3) / 4;
+    const int64_t wgs = (a.n / o.chunk * ((a.dim + 63) / 64) + kJoinWaves - 1) / kJoinWaves;
     return (int)(wgs < 2048 ? wgs : 2048);
 }
 
@@ -677,7 +666,7 @@ hipError_t table_grad_as(const IdArgs& a, const OrderArgs& o, TableGradArgs p, h
                          : tail == kPartial ? go(k_table_grad<GDT, kPartial>)
                                             : go(k_table_grad<GDT, kShort>);
     if (e != hipSuccess || a.n <= o.chunk) return e;       // no id can be long
-    return launch_kernel(k_long_rows, long_wgs(a, o), s, o, a.dim, p);
+    return launch_kernel_nt(k_long_rows, long_wgs(a, o), kJoinWaves * 64, s, o, a.dim, p);
 }
 
 }  // namespace
@@ -738,7 +727,7 @@ hipError_t launch_table_grad_direct(const IdArgs& a, const void* dy, int gdt, fl
 hipError_t launch_join_chunks(const IdArgs& a, const OrderArgs& o, float* part, hipStream_t s)
 {
     if (a.n <= o.chunk) return hipSuccess;             // no id can be long
-    return launch_kernel(k_join_chunks, long_wgs(a, o), s, o, part, padded_dim(a.dim));
+    return launch_kernel_nt(k_join_chunks, long_wgs(a, o), kJoinWaves * 64, s, o, part, padded_dim(a.dim));
 }
 
 hipError_t launch_table_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part, float scale,
