@@ -28,8 +28,9 @@ namespace {
 
 // `lanes` (a power of two) threads share a token, 256 / lanes tokens a workgroup;
 // the id is the only read that others wait for.  Bound by HBM: 16384 tokens of
-// natural frequencies, [32000, 4096] bf16, 45 us (134 MB of output and the 90 MB of
-// rows that are used: 5.0 TB/s); 16 tokens 2.6 us, the latency of two dependent reads.
+// natural frequencies from [32000, 4096] binary32 to bf16 in 44 us (134 MB of output and
+// the 90 MB of rows that are used: 5.0 TB/s); 16 tokens 2.6 us, the latency of two
+// dependent reads.
 template <int TDT, int YDT, int TAIL>
 __global__ __launch_bounds__(256) void k_embedding(IdArgs a, const void* __restrict__ table, float scale,
                                                    void* __restrict__ y, int log2lanes)
@@ -214,7 +215,7 @@ hipError_t dequant_embedding_y(const IdArgs& a, const DequantDesc& d, int code4,
 // for another.  The ids are read from L2 by every workgroup, n * classes reads in
 // exchange for one launch and no atomics in memory; up to 16384 tokens a wave
 // keeps its stretch in registers for the second time.  Bound by the chain load -
-// count - scan - place of one workgroup per CU, not by bytes: 16384 ids of 32000 in 11
+// count - scan - place of one workgroup per CU, not by bytes: 16384 ids of 32000 in 12
 // us, 5003 in 8 us.  (Writing the zero rows beside it does not pay: their place is
 // known only after it, and zeros under rows that are written again later took it from
 // 11 to 17 us and the whole call with it.)
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
         if (!once) load_ids(t0);
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
-            if (t0 + k * 64 >= last) break;            // (uniform; few tokens run little of this code)
+            if (k % 4 == 0 && t0 + k * 64 >= last) break;      // uniform: few tokens run little of this code
             if (id[k] >= 0) {
                 const int32_t c = id[k] & mask;
                 below += c < cls ? 1 : 0;
@@ -315,7 +316,7 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
         if (!once) load_ids(t0);
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
-            if (t0 + k * 64 >= last) break;
+            if (k % 4 == 0 && t0 + k * 64 >= last) break;
             const bool mine = id[k] >= 0 && (id[k] & mask) == cls;
             unsigned long long todo = __ballot(mine);
             while (todo) {
@@ -434,7 +435,7 @@ __device__ __forceinline__ void zero_rows(const IdArgs& a, const OrderArgs& o, i
 }
 
 // The work with the longest chains of reads first.  Bound by HBM: 54 us for the case of
-// k_table_grad, where 227 MB of zeros are written beside the long ids' tokens.
+// k_table_grad, where 217 MB of zeros are written beside the long ids' tokens.
 template <int GDT, int TAIL>
 __global__ __launch_bounds__(256) void k_prepare_grad(IdArgs a, OrderArgs o, const void* __restrict__ dy,
                                                       float* __restrict__ part, int32_t slices, int32_t list_wgs,
