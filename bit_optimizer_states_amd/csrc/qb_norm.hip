@@ -10,7 +10,7 @@
 // row, and a second kernel adds the partial rows.  Every sum has a fixed order:
 // the same bits on every run.  Bound by HBM: 16384 rows of 4096 bf16 in 69 us and 4.5
 // us for the partial rows (403 MB: 5.5 TB/s together).  Few long rows are bound by the
-// latency of a row or two per workgroup: 1023 rows of 5001 binary32 in 20 and 4 us (61 MB).
+// latency of a row or two per workgroup: 1023 rows of 5001 binary32 in 17 and 4 us (61 MB).
 #include "qb_norm_kernels.h"
 
 namespace qb {
@@ -326,6 +326,12 @@ __global__ __launch_bounds__(256) void k_norm_cols(const void* __restrict__ dy, 
 
 constexpr int kLongParts = 64;
 
+// Threads and units per row: two units a thread where a row allows it, so that h and g
+// stay in registers and 16 waves fit a CU (8192 rows: 5001 binary32 elements 127 -> 104
+// us against four units a thread, 8192 bf16 83 -> 78).  Up to 2048 elements a wave
+// with four units needs no barrier, which pays for whole units (16384 rows of 2048 bf16:
+// 39.8 against 41.2 us), but not where shifting the last unit needs registers too
+// (1500: 45.4 against 37.8).
 template <int XDT, int WDT, int TAIL>
 hipError_t grad_as(const void* dy, const void* x, int64_t n, int dim, const void* gamma, const float* mean,
                    const float* rstd, void* dx, float* part, hipStream_t s)
@@ -340,10 +346,14 @@ hipError_t grad_as(const void* dy, const void* x, int64_t n, int dim, const void
     if constexpr (TAIL != kShort) {
         if (units <= 64) return go(k_norm_grad<XDT, WDT, 64, 1, TAIL, 512>, 512);
         if (units <= 128) return go(k_norm_grad<XDT, WDT, 64, 2, TAIL, 512>, 512);
-        if (units <= 256) return go(k_norm_grad<XDT, WDT, 64, 4, TAIL, 512>, 512);
+        if constexpr (TAIL == kWhole) {
+            if (units <= 256) return go(k_norm_grad<XDT, WDT, 64, 4, TAIL, 512>, 512);
+        } else {
+            if (units <= 256) return go(k_norm_grad<XDT, WDT, 128, 2, TAIL, 1024>, 1024);
+        }
         if (units <= 512) return go(k_norm_grad<XDT, WDT, 256, 2, TAIL, 1024>, 1024);
-        if (units <= 1024) return go(k_norm_grad<XDT, WDT, 256, 4, TAIL, 512>, 512);
-        return go(k_norm_grad<XDT, WDT, 512, 4, TAIL, 512>, 512);
+        if (units <= 1024) return go(k_norm_grad<XDT, WDT, 512, 2, TAIL, 1024>, 1024);
+        return go(k_norm_grad<XDT, WDT, 1024, 2, TAIL, 1024>, 1024);
     }
     return hipErrorInvalidValue;
 }
