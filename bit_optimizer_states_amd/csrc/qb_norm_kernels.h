@@ -110,14 +110,15 @@ __device__ __forceinline__ bool whole_step(int k, int dim)
 // deviation of its own elements (wave_stats), which are then joined over the row's
 // waves (join_stats, behind one barrier) as those of parts of a sample:
 //   mean = sum n_w mean_w / dim,  M2 = sum (M2_w + n_w (mean_w - mean)^2).
-// EXACT (binary32 rows): a wave's mean is corrected by the mean of the rounded
-// differences, so that a row whose mean is large against its spread keeps its
-// digits; 16-bit elements have no such digits.
+// A wave's mean is corrected by the mean of the differences, so that a row whose mean
+// is large against its spread keeps its digits: the mean's first rounding would come
+// out multiplied by up to 1/sqrt(eps), also in a row of equal 16-bit values (159
+// values of 60000 were normalized to 0.78 instead of 0 without it).
 struct WaveStats {
     float m0, c, m2;          // mean m0 + c (not rounded to one binary32), squared deviation
 };
 
-template <int TPR, int VPT, bool EXACT>
+template <int TPR, int VPT>
 __device__ __forceinline__ WaveStats wave_stats(const float (&x)[VPT][8], const RowShape<TPR, VPT>& shape, int lane,
                                                 int dim)
 {
@@ -138,7 +139,7 @@ __device__ __forceinline__ WaveStats wave_stats(const float (&x)[VPT][8], const 
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float d = x[k][j] - m0;
-                if constexpr (EXACT) ud += d;
+                ud += d;
                 uq = __builtin_fmaf(d, d, uq);
             }
         } else {
@@ -146,50 +147,45 @@ __device__ __forceinline__ WaveStats wave_stats(const float (&x)[VPT][8], const 
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float d = j < cnt ? x[k][j] - m0 : 0.0f;
-                if constexpr (EXACT) ud += d;
+                ud += d;
                 uq = __builtin_fmaf(d, d, uq);
             }
         }
-        if constexpr (EXACT) sd += ud;
+        sd += ud;
         sq += uq;
     }
-    WaveStats w{m0, 0.0f, lanes_sum<L>(sq)};
-    if constexpr (EXACT) {
-        sd = lanes_sum<L>(sd);
-        w.c = sd * shape.inv_mine;
-        w.m2 -= sd * w.c;
-    }
-    return w;
+    sq = lanes_sum<L>(sq);
+    sd = lanes_sum<L>(sd);
+    const float c = sd * shape.inv_mine;
+    return WaveStats{m0, c, sq - sd * c};
 }
 
 // Leaves a wave's share in the row's slot (row_slot_words(TPR) words).
-template <int TPR, int VPT, bool EXACT>
+template <int TPR, int VPT>
 __device__ __forceinline__ void put_stats(const WaveStats& w, const RowShape<TPR, VPT>& shape, float* slot)
 {
-    constexpr int S = EXACT ? 3 : 2;
     if (RowShape<TPR, VPT>::W > 1 && threadIdx.x % 64 == 0) {
-        slot[S * shape.wave] = w.m0;
-        slot[S * shape.wave + 1] = w.m2;
-        if constexpr (EXACT) slot[S * shape.wave + 2] = w.c;
+        slot[3 * shape.wave] = w.m0;
+        slot[3 * shape.wave + 1] = w.m2;
+        slot[3 * shape.wave + 2] = w.c;
     }
 }
 
-template <int TPR, int VPT, bool EXACT>
+template <int TPR, int VPT>
 __device__ __forceinline__ void join_stats(const WaveStats& w, const RowShape<TPR, VPT>& shape, float eps,
                                            const float* slot, float* mean, float* rstd)
 {
-    constexpr int W = RowShape<TPR, VPT>::W, S = EXACT ? 3 : 2;
+    constexpr int W = RowShape<TPR, VPT>::W;
     float m = w.m0 + w.c, m2 = w.m2;
     if constexpr (W > 1) {
         // differences from wave 0's mean (it holds elements in every row): the join keeps
         // the digits that the waves' means share.  A wave without elements has mean 0, weight 0.
         // Lane l takes wave l % W.
         const int l = threadIdx.x % W;
-        const float m00 = slot[0], c00 = EXACT ? slot[2] : 0.0f;
-        float d = slot[S * l] - m00;
-        if constexpr (EXACT) d += slot[S * l + 2] - c00;
+        const float m00 = slot[0], c00 = slot[2];
+        const float d = (slot[3 * l] - m00) + (slot[3 * l + 2] - c00);
         const float nd = shape.held * d;
-        const float dm = group_sum<W>(nd), dq = group_sum<W>(nd * d), q = group_sum<W>(slot[S * l + 1]);
+        const float dm = group_sum<W>(nd), dq = group_sum<W>(nd * d), q = group_sum<W>(slot[3 * l + 1]);
         const float shift = dm * shape.inv_dim;
         m = m00 + (c00 + shift);
         m2 = q + (dq - dm * shift);
@@ -198,14 +194,14 @@ __device__ __forceinline__ void join_stats(const WaveStats& w, const RowShape<TP
     *rstd = inv_deviation(m2 * shape.inv_dim, eps);
 }
 
-template <int TPR, int VPT, bool EXACT>
+template <int TPR, int VPT>
 __device__ __forceinline__ void row_stats(const float (&x)[VPT][8], const RowShape<TPR, VPT>& shape, int lane, int dim,
                                           float eps, float* slot, float* mean, float* rstd)
 {
-    const WaveStats w = wave_stats<TPR, VPT, EXACT>(x, shape, lane, dim);
-    put_stats<TPR, VPT, EXACT>(w, shape, slot);
+    const WaveStats w = wave_stats<TPR, VPT>(x, shape, lane, dim);
+    put_stats<TPR, VPT>(w, shape, slot);
     if constexpr (TPR > 64) lds_barrier();
-    join_stats<TPR, VPT, EXACT>(w, shape, eps, slot, mean, rstd);
+    join_stats<TPR, VPT>(w, shape, eps, slot, mean, rstd);
 }
 
 // Threads of a workgroup: a row that waves share has one to itself.
@@ -289,7 +285,7 @@ __global__ __launch_bounds__(norm_threads(TPR)) void k_norm(const void* __restri
         load_row(id);
         float mean = 0.0f, rstd = 0.0f;
         if (TPR < 64 || found) {
-            row_stats<TPR, VPT, XDT == DT_F32>(v, shape, lane, dim, eps, s_slot[buf][grp], &mean, &rstd);
+            row_stats<TPR, VPT>(v, shape, lane, dim, eps, s_slot[buf][grp], &mean, &rstd);
             buf ^= 1;                    // (only behind a barrier)
         }
         if (t >= a.n) continue;

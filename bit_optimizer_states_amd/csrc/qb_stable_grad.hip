@@ -94,7 +94,7 @@ struct StableRows {
             }
         }
         float mean, rstd;
-        row_stats<TPR, VPT, TDT == DT_F32>(x, shape, tid, dim, p.eps, slot, &mean, &rstd);
+        row_stats<TPR, VPT>(x, shape, tid, dim, p.eps, slot, &mean, &rstd);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int k = 0; k < VPT; ++k)

@@ -1,0 +1,87 @@
+"""GPU: statistics of rows whose spread is small against their mean, for every
+type and every way that a row is spread over threads.
+
+Rows of equal values x.  The first mean m0 is off by delta, at most (L + 2) u |x|; the
+differences x - m0 are exact (x and m0 within a factor of two), multiples of the
+last place of x by a small whole number, so their sum is exact and its mean c is
+off by 2 u delta at most: m0 + c rounds to x.  So the mean is x, every normalized
+value is zero, and with them the weight's gradient."""
+import numpy as np
+import pytest
+import torch
+
+import layers_reference as ref
+from gpu_helpers import DEV, qb
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+TYPES = [F32, F16, BF16]
+EPS = 1e-5
+# numbers of elements that are no powers of two, whole and ragged, for every way of spreading a row over
+# threads (an ordinary width of 896 among them), and two beyond the registers
+DIMS = [3, 65, 127, 159, 500, 896, 1126, 1500, 2050, 3600, 4099, 5199, 9000, 16000, 16387, 20000]
+VALUES = [3.0, -1000.0, 60000.0, 0.0, 1.0 / 3.0, -4096.0]
+
+
+def constant_rows(values, dim, dt):
+    return torch.tensor(values, device=DEV).to(dt)[:, None].expand(len(values), dim).contiguous()
+
+
+def norm(L, x):
+    y = torch.full_like(x, 7.0)
+    mean, rstd = (torch.full((x.shape[0],), 7.0, device=DEV) for _ in range(2))
+    L.qb_layer_norm(x, None, None, EPS, y, mean=mean, rstd=rstd)
+    return y, mean, rstd
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+def test_rows_of_equal_values(dim, dt):
+    L = qb()
+    x = constant_rows(VALUES, dim, dt)
+    y, mean, rstd = norm(L, x)
+    assert torch.equal(mean, x[:, 0].float())
+    assert (y == 0).all()
+    # The squared differences n delta^2 are taken off again up to (L + 6) u of them; rstd is off by half of
+    # what is left against eps, and by 3 u of its own.
+    delta = (ref.L + 2) * ref.U * np.abs(ref.f64(x[:, 0]))
+    left = delta ** 2 * (ref.L + 6) * ref.U / EPS
+    want = 1 / np.sqrt(np.full(len(VALUES), float(np.float32(EPS))))
+    ref.assert_close(rstd, want, want * (left / 2 + 3 * ref.U), "rstd")
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("dim", DIMS)
+def test_means_far_from_zero(dim, dt):
+    """The bounds of binary32 rows (mean: its own rounding and 50 u of the spread) hold for 16-bit rows too."""
+    L = qb()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(dim)
+    x = (1000 + 8 * torch.randint(-3, 4, (40, dim), device=DEV, generator=g).float()).to(dt)
+    x[20:] = (30000 + 256 * torch.randint(0, 2, (20, dim), device=DEV, generator=g).float()).to(dt)
+    y, mean, rstd = norm(L, x)
+    want, err, m, r, e_m, e_r = ref.layer_norm(ref.f64(x), None, None, float(np.float32(EPS)), True)
+    ref.assert_close(y, want, err, "y")
+    ref.assert_close(mean, m, e_m, "mean")
+    ref.assert_close(rstd, r, e_r, "rstd")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("n", [50, 300])
+def test_stable_embedding_of_equal_values(n, dt):
+    """A lookup scaled by 0.7 has binary32 values whatever the table's type; both forms of the gradient."""
+    L = qb()
+    rows = len(VALUES)
+    for dim in [d for d in DIMS if d <= 16384]:
+        table = constant_rows(VALUES, dim, dt)
+        ids = torch.arange(n, device=DEV) % rows
+        y = torch.full((n, dim), 7.0, device=DEV)
+        L.qb_stable_embedding(table, ids, None, None, EPS, y, scale=0.7)
+        assert (y == 0).all(), dim
+        dy = torch.empty(n, dim, device=DEV).normal_(0, 1)
+        ws = torch.empty(L.qb_stable_embedding_workspace_bytes(n, rows, dim), dtype=torch.uint8, device=DEV)
+        dtable = torch.empty(rows, dim, device=DEV)
+        dgamma = torch.full((dim,), 7.0, device=DEV)
+        L.qb_stable_embedding_backward(dy, table, ids, None, EPS, dtable, dgamma, None, ws, scale=0.7)
+        assert (dgamma == 0).all(), dim
