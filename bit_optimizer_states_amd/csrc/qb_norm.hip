@@ -29,7 +29,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(const void* __restri
                                                             void* __restrict__ y, float* __restrict__ mean_out,
                                                             float* __restrict__ rstd_out)
 {
-    __shared__ float s_slot[4 * (kLongThreads / 64)];
+    __shared__ float s_slot[6 * (kLongThreads / 64)];
     const int64_t t = blockIdx.x;
     const char* const xrow = static_cast<const char*>(x) + t * dim * elem_bytes(XDT);
     char* const yrow = static_cast<char*>(y) + t * dim * elem_bytes(XDT);
@@ -47,29 +47,39 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(const void* __restri
     if ((int)threadIdx.x < left) sum += load1<XDT>(xrow, whole * 8 + threadIdx.x);
     float none = 0.0f;
     row_sum2<kLongThreads>(sum, none, s_slot);
-    const float m0 = sum / (float)dim;
-    float sd = 0.0f, sq = 0.0f;
-    for (int64_t u = threadIdx.x; u < whole; u += kLongThreads) {
-        const Unit<XDT> w = load_unit8<XDT, false>(xrow, u * 8);
-        float a = 0.0f, b = 0.0f;
+    // differences from m and their squares, as deviations()
+    float sd, sq;
+    auto around = [&](float m, float* slot) {
+        sd = sq = 0.0f;
+        for (int64_t u = threadIdx.x; u < whole; u += kLongThreads) {
+            const Unit<XDT> w = load_unit8<XDT, false>(xrow, u * 8);
+            float a = 0.0f, b = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float d = unit_at<XDT>(w, j) - m0;
-            a += d;
-            b = __builtin_fmaf(d, d, b);
+            for (int j = 0; j < 8; ++j) {
+                const float d = unit_at<XDT>(w, j) - m;
+                a += d;
+                b = __builtin_fmaf(d, d, b);
+            }
+            sd += a;
+            sq += b;
         }
-        sd += a;
-        sq += b;
+        if ((int)threadIdx.x < left) {
+            const float d = load1<XDT>(xrow, whole * 8 + threadIdx.x) - m;
+            sd += d;
+            sq = __builtin_fmaf(d, d, sq);
+        }
+        row_sum2<kLongThreads>(sd, sq, slot);
+    };
+    float m0 = sum / (float)dim;
+    around(m0, s_slot + 2 * (kLongThreads / 64));
+    float c = sd / (float)dim;
+    if (mostly_rounding(sd, c, sq)) {                  // (the same for all threads)
+        m0 += c;
+        around(m0, s_slot + 4 * (kLongThreads / 64));
+        c = sd / (float)dim;
     }
-    if ((int)threadIdx.x < left) {
-        const float d = load1<XDT>(xrow, whole * 8 + threadIdx.x) - m0;
-        sd += d;
-        sq = __builtin_fmaf(d, d, sq);
-    }
-    row_sum2<kLongThreads>(sd, sq, s_slot + 2 * (kLongThreads / 64));
-    const float c = sd / (float)dim;
     const float mean = m0 + c;
-    const float rstd = inv_deviation(sq / (float)dim - c * c, eps);
+    const float rstd = inv_deviation(without_mean(sq, sd * c) / (float)dim, eps);
     if (threadIdx.x == 0) {
         if (mean_out) mean_out[t] = mean;
         if (rstd_out) rstd_out[t] = rstd;

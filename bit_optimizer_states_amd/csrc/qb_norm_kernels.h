@@ -16,6 +16,7 @@
 // of a binary32 table ([32000, 4096], natural frequencies) 52 us: the 90 MB of used rows
 // come to 167 MB, since each of the 8 L2s fetches the frequent ones.
 #pragma once
+#include <cfloat>
 #include <type_traits>
 
 #include "qb_rows.h"
@@ -118,6 +119,51 @@ struct WaveStats {
     float m0, c, m2;          // mean m0 + c (not rounded to one binary32), squared deviation
 };
 
+// Sums over a row's lanes of the differences from m and of their squares.
+template <int TPR, int VPT>
+__device__ __forceinline__ void deviations(const float (&x)[VPT][8], float m, int lane, int dim, float& sd, float& sq)
+{
+    constexpr int L = RowShape<TPR, VPT>::L;
+    sd = sq = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        float ud = 0.0f, uq = 0.0f;
+        if (whole_step<TPR>(k, dim)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = x[k][j] - m;
+                ud += d;
+                uq = __builtin_fmaf(d, d, uq);
+            }
+        } else {
+            const int cnt = unit_count(k * TPR + lane, dim);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = j < cnt ? x[k][j] - m : 0.0f;
+                ud += d;
+                uq = __builtin_fmaf(d, d, uq);
+            }
+        }
+        sd += ud;
+        sq += uq;
+    }
+    sq = lanes_sum<L>(sq);
+    sd = lanes_sum<L>(sd);
+}
+
+// Whether the squares sq around a mean are more than half that mean's own error (sd * c):
+// what would be left of them has lost digits, or they overflowed.
+__device__ __forceinline__ bool mostly_rounding(float sd, float c, float sq)
+{
+    return !(sd * c <= 0.5f * fminf(sq, FLT_MAX));
+}
+
+// The squares less the mean's share; infinite squares stay so.
+__device__ __forceinline__ float without_mean(float sq, float share) { return sq <= FLT_MAX ? sq - share : sq; }
+
+// A row (nearly) of equal values takes its squares a second time, around the corrected
+// mean: its elements and that mean, rounded, are whole multiples of one last place, so
+// that these differences are exact and at most half of their squares is the mean's.
 template <int TPR, int VPT>
 __device__ __forceinline__ WaveStats wave_stats(const float (&x)[VPT][8], const RowShape<TPR, VPT>& shape, int lane,
                                                 int dim)
@@ -130,34 +176,17 @@ __device__ __forceinline__ WaveStats wave_stats(const float (&x)[VPT][8], const 
         const float b = (x[k][4] + x[k][5]) + (x[k][6] + x[k][7]);
         s += a + b;
     }
-    const float m0 = lanes_sum<L>(s) * shape.inv_mine;
-    float sd = 0.0f, sq = 0.0f;
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        float ud = 0.0f, uq = 0.0f;
-        if (whole_step<TPR>(k, dim)) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float d = x[k][j] - m0;
-                ud += d;
-                uq = __builtin_fmaf(d, d, uq);
-            }
-        } else {
-            const int cnt = unit_count(k * TPR + lane, dim);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float d = j < cnt ? x[k][j] - m0 : 0.0f;
-                ud += d;
-                uq = __builtin_fmaf(d, d, uq);
-            }
-        }
-        sd += ud;
-        sq += uq;
+    float m0 = lanes_sum<L>(s) * shape.inv_mine, sd, sq;
+    deviations<TPR, VPT>(x, m0, lane, dim, sd, sq);
+    float c = sd * shape.inv_mine;
+    const bool again = mostly_rounding(sd, c, sq);
+    if (__any(again)) {                                // (several rows may share the wave)
+        const float m1 = again ? m0 + c : m0;
+        deviations<TPR, VPT>(x, m1, lane, dim, sd, sq);
+        m0 = m1;
+        c = sd * shape.inv_mine;
     }
-    sq = lanes_sum<L>(sq);
-    sd = lanes_sum<L>(sd);
-    const float c = sd * shape.inv_mine;
-    return WaveStats{m0, c, sq - sd * c};
+    return WaveStats{m0, c, without_mean(sq, sd * c)};
 }
 
 // Leaves a wave's share in the row's slot (row_slot_words(TPR) words).
@@ -188,7 +217,7 @@ __device__ __forceinline__ void join_stats(const WaveStats& w, const RowShape<TP
         const float dm = group_sum<W>(nd), dq = group_sum<W>(nd * d), q = group_sum<W>(slot[3 * l + 1]);
         const float shift = dm * shape.inv_dim;
         m = m00 + (c00 + shift);
-        m2 = q + (dq - dm * shift);
+        m2 = q + without_mean(dq, dm * shift);
     }
     *mean = m;
     *rstd = inv_deviation(m2 * shape.inv_dim, eps);

@@ -85,3 +85,73 @@ def test_stable_embedding_of_equal_values(n, dt):
         dgamma = torch.full((dim,), 7.0, device=DEV)
         L.qb_stable_embedding_backward(dy, table, ids, None, EPS, dtable, dgamma, None, ws, scale=0.7)
         assert (dgamma == 0).all(), dim
+
+
+# Rows whose squared differences from a rounded mean are almost all the mean's own rounding, or overflow binary32.
+LARGE = [1e8 / 3, -1e12, 1e19 / 7, 3e25, -1e30, 1e33 / 3]
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("dim", DIMS)
+def test_large_rows_of_equal_values(dim, dt):
+    """The variance is zero whatever the value is: the differences from m0 + c, rounded to one binary32, are
+    exactly zero."""
+    L = qb()
+    x = constant_rows(LARGE, dim, dt)
+    y, mean, rstd = norm(L, x)
+    assert torch.equal(mean, x[:, 0].float())
+    assert (y == 0).all()
+    want = 1 / np.sqrt(np.full(len(LARGE), float(np.float32(EPS))))
+    ref.assert_close(rstd, want, want * 3 * ref.U, "rstd")
+    if dim > 16384:
+        return
+    # the same statistics inside the stable embedding and its gradient: h = 0, dtable = rstd (dy - mean dy)
+    ids = torch.arange(len(LARGE), device=DEV)
+    z = torch.full_like(x, 7.0)
+    L.qb_stable_embedding(x, ids, None, None, EPS, z)
+    assert (z == 0).all()
+    dy = torch.empty(len(LARGE), dim, device=DEV).normal_(0, 1)
+    ws = torch.empty(L.qb_stable_embedding_workspace_bytes(len(LARGE), len(LARGE), dim), dtype=torch.uint8, device=DEV)
+    dtable, dgamma = torch.empty_like(dy), torch.full((dim,), 7.0, device=DEV)
+    L.qb_stable_embedding_backward(dy, x, ids, None, EPS, dtable, dgamma, None, ws)
+    assert (dgamma == 0).all()
+    d = ref.f64(dy)
+    err_r = want * 3 * ref.U
+    g, err = ref.norm_grad(d, np.zeros_like(d), np.zeros_like(d), np.zeros_like(d), want, err_r, np.ones(dim))
+    ref.assert_close(dtable, g, err, "dtable")
+
+
+@pytest.mark.parametrize("dim", DIMS)
+def test_spreads_of_the_last_place(dim):
+    """x = a + k s with whole k and s the last place of a: differences from any mean that is a multiple of s
+    are exact, so the variance keeps its digits."""
+    L = qb()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(dim)
+    k = torch.randint(-3, 4, (40, dim), device=DEV, generator=g).float()
+    k[::4] = (k[::4] == 3).float()
+    a = torch.tensor([1e6, 1e4, -3e8, 5e10], device=DEV).repeat(10)[:, None]
+    s = 2.0 ** torch.floor(torch.log2(a.abs()) - 23)
+    x = (a + k * s).contiguous()
+    assert torch.equal((x - a) / s, k)
+    y, mean, rstd = norm(L, x)
+    xd = ref.f64(x)
+    m, _, r = ref.statistics(xd, float(np.float32(EPS)))
+    # the mean: its own rounding and the correction's.  rstd: at most half of the squared differences are the
+    # mean's, so what is left of them is off by 2 (L + 6) u.
+    ref.assert_close(mean, m, ref.U * np.abs(m) + (ref.L + 2) * ref.U / r, "mean")
+    ref.assert_close(rstd, r, r * ((2 * (ref.L + 6)) / 2 + 3) * ref.U, "rstd")
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("dim", [d for d in DIMS if d > 3])
+def test_variance_beyond_binary32(dim, dt):
+    """Differences whose squares overflow: var is infinite, 1 / sqrt(var + eps) zero, and y is beta."""
+    L = qb()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(dim)
+    x = (1e25 * (torch.randn(8, dim, device=DEV, generator=g) + 3 * torch.randn(8, 1, device=DEV, generator=g))).to(dt)
+    y, mean, rstd = norm(L, x)
+    assert (y == 0).all() and (rstd == 0).all()
+    xd = ref.f64(x)
+    ref.assert_close(mean, xd.mean(1), ref.U * np.abs(xd.mean(1)) + (ref.L + 2) * ref.U * xd.std(1), "mean")
