@@ -71,12 +71,13 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(const void* __restri
         row_sum2<kLongThreads>(sd, sq, slot);
     };
     float m0 = sum / (float)dim;
+    const float inv = 1.0f / (float)dim;
     around(m0, s_slot + 2 * (kLongThreads / 64));
-    float c = sd / (float)dim;
+    float c = correction(sd, inv);
     if (mostly_rounding(sd, c, sq)) {                  // (the same for all threads)
         m0 += c;
         around(m0, s_slot + 4 * (kLongThreads / 64));
-        c = sd / (float)dim;
+        c = correction(sd, inv);
     }
     const float mean = m0 + c;
     const float rstd = inv_deviation(without_mean(sq, sd * c) / (float)dim, eps);

@@ -158,6 +158,14 @@ __device__ __forceinline__ bool mostly_rounding(float sd, float c, float sq)
     return !(sd * c <= 0.5f * fminf(sq, FLT_MAX));
 }
 
+// The correction of a mean: none where the row holds infinities or NaN, whose mean the
+// first sum already is (inf - inf is no correction).
+__device__ __forceinline__ float correction(float sd, float inv)
+{
+    const float c = sd * inv;
+    return __builtin_fabsf(c) <= FLT_MAX ? c : 0.0f;
+}
+
 // The squares less the mean's share; infinite squares stay so.
 __device__ __forceinline__ float without_mean(float sq, float share) { return sq <= FLT_MAX ? sq - share : sq; }
 
@@ -178,13 +186,13 @@ __device__ __forceinline__ WaveStats wave_stats(const float (&x)[VPT][8], const 
     }
     float m0 = lanes_sum<L>(s) * shape.inv_mine, sd, sq;
     deviations<TPR, VPT>(x, m0, lane, dim, sd, sq);
-    float c = sd * shape.inv_mine;
+    float c = correction(sd, shape.inv_mine);
     const bool again = mostly_rounding(sd, c, sq);
     if (__any(again)) {                                // (several rows may share the wave)
         const float m1 = again ? m0 + c : m0;
         deviations<TPR, VPT>(x, m1, lane, dim, sd, sq);
         m0 = m1;
-        c = sd * shape.inv_mine;
+        c = correction(sd, shape.inv_mine);
     }
     return WaveStats{m0, c, without_mean(sq, sd * c)};
 }
@@ -217,6 +225,8 @@ __device__ __forceinline__ void join_stats(const WaveStats& w, const RowShape<TP
         const float dm = group_sum<W>(nd), dq = group_sum<W>(nd * d), q = group_sum<W>(slot[3 * l + 1]);
         const float shift = dm * shape.inv_dim;
         m = m00 + (c00 + shift);
+        if (!(__builtin_fabsf(shift) <= FLT_MAX))      // infinities, NaN: the mean of the waves' means
+            m = group_sum<W>(slot[3 * l] * (shape.held * shape.inv_dim));
         m2 = q + without_mean(dq, dm * shift);
     }
     *mean = m;

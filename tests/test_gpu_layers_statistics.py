@@ -155,3 +155,30 @@ def test_variance_beyond_binary32(dim, dt):
     assert (y == 0).all() and (rstd == 0).all()
     xd = ref.f64(x)
     ref.assert_close(mean, xd.mean(1), ref.U * np.abs(xd.mean(1)) + (ref.L + 2) * ref.U * xd.std(1), "mean")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("dim", DIMS + [64, 1024, 2048, 8192])
+def test_means_of_rows_that_hold_infinities(dim, dt):
+    """The mean is the infinity (NaN for both of them), as sum x / dim; var, rstd and y are NaN, inf - inf."""
+    L = qb()
+    inf, nan = float("inf"), float("nan")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(dim)
+    x = torch.randn(9, dim, device=DEV, generator=g)
+    x[1, 0] = inf
+    x[2, dim - 1] = -inf
+    x[3, dim // 2] = inf
+    x[3, dim // 3] = inf
+    x[4, 0], x[4, dim - 1] = inf, -inf
+    x[5, dim // 2] = nan
+    x[6] = inf
+    x[7, 0], x[7, dim // 2] = inf, nan
+    want = torch.tensor([inf, -inf, inf, nan, nan, inf, nan], device=DEV)
+    x = x.to(dt)
+    clean = norm(L, x[::8].clone())
+    y, mean, rstd = norm(L, x)
+    assert torch.equal(mean[1:8].nan_to_num(nan=5.0), want.nan_to_num(nan=5.0))
+    assert rstd[1:8].isnan().all() and y[1:8].isnan().all()
+    for got, alone in zip((y, mean, rstd), clean):
+        assert torch.equal(got[::8], alone)
