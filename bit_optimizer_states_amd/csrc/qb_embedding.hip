@@ -596,10 +596,10 @@ template <int GDT>
 hipError_t prepare_grad_as(const IdArgs& a, const OrderArgs& o, const void* dy, float* part, int64_t pad,
                            bool accumulate, void* dtable, int ddt, hipStream_t s)
 {
-    const int32_t slices = (a.dim + 511) / 512;
+    const int32_t slices = (int32_t)chunk_slices(a.dim);
     const int64_t most = int64_t(1) << 22;
     const int64_t list = ((int64_t(1) << o.log2g) + 3) / 4;
-    int64_t chunks = (chunk_count(a.n) * slices + 3) / 4;
+    int64_t chunks = (chunk_count(a.n, o.chunk) * slices + 3) / 4;
     int64_t zeros = accumulate ? 0 : (a.rows + kZeroRows - 1) / kZeroRows;
     if (chunks > most) chunks = most;
     if (zeros > most) zeros = most;
@@ -653,11 +653,11 @@ template <int GDT>
 hipError_t table_grad_as(const IdArgs& a, const OrderArgs& o, TableGradArgs p, hipStream_t s)
 {
     const int64_t most = int64_t(1) << 22;
-    int64_t work = (chunk_count(a.n) * ((a.dim + 511) / 512) + 3) / 4;
+    p.slices = (int32_t)chunk_slices(a.dim);
+    int64_t work = (chunk_count(a.n, o.chunk) * p.slices + 3) / 4;
     int64_t zeros = p.accumulate ? 0 : (a.rows + kZeroRows - 1) / kZeroRows;
     if (work > most) work = most;
     if (zeros > most) zeros = most;
-    p.slices = (a.dim + 511) / 512;
     p.work = (int32_t)work;
     p.zeros = (int32_t)zeros;
     if (work + zeros == 0) return hipSuccess;

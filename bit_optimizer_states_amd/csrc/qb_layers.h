@@ -57,13 +57,24 @@ constexpr int32_t order_log2g(int64_t rows)
 constexpr int64_t order_per(int64_t rows) { return (rows + (int64_t(1) << order_log2g(rows)) - 1) >> order_log2g(rows); }
 
 // Tokens per chunk of the ordered list: an id with more tokens than this is
-// summed chunk by chunk, then joined.  Two chunks fit the lanes of a wave.  Few
-// tokens need the more waves of short chunks (16 against 32 tokens a chunk: 300
-// tokens of 704 elements 14.6 against 18.2 us, 5003 of 1001 binary32 25.1 against
-// 30.6), many tokens the fewer partial rows of long ones (16384 of 4096: 96 against
-// 93 us; all of one id: 160 against 127).
-constexpr int32_t chunk_tokens(int64_t n) { return n < 16384 ? 16 : 32; }
-constexpr int64_t chunk_count(int64_t n) { return (n + chunk_tokens(n) - 1) / chunk_tokens(n); }
+// summed chunk by chunk, then joined.  Two chunks fit the lanes of a wave.  A wave
+// takes a chunk's share of 512 columns.  Short chunks give few tokens the more waves
+// (16 against 32 tokens a chunk: 300 tokens of 704 elements 14.6 against 18.2 us, 5003 of
+// 1001 binary32 25.1 against 30.6); beyond about 12 waves a CU the chip is full and they
+// only leave more partial rows.  Both, in us for natural frequencies over 8191 and 32000
+// rows of bf16: 16384 x 64 24.9/28.2 and 26.0/29.6, 65536 x 64 55.4/57.0 and 57.8/57.3,
+// 131072 x 64 93.4/89.6 and 92.5/91.3; 16384 x 1024 30.0/30.9 and 35.8/38.4, 32768 x 1024
+// 51.6/47.4 and 53.2/53.5; 5003 x 4096 37.5/38.2 and 71.1/72.3, 12000 x 4096 52.3/50.3 and
+// 86.3/84.5.  Ids even over the table cross at twice the tokens; a batch of a single id
+// is 10 to 15% faster with 32 throughout.
+constexpr int32_t kChunkShort = 16, kChunkLong = 32;
+constexpr int64_t kChunkWaves = 12 * 256;
+constexpr int64_t chunk_count(int64_t n, int64_t chunk = kChunkLong) { return (n + chunk - 1) / chunk; }
+constexpr int64_t chunk_slices(int64_t dim) { return (dim + 511) / 512; }
+constexpr int32_t chunk_tokens(int64_t n, int64_t dim)
+{
+    return chunk_count(n, kChunkShort) * chunk_slices(dim) <= kChunkWaves ? kChunkShort : kChunkLong;
+}
 constexpr int64_t padded_dim(int64_t dim) { return (dim + 7) / 8 * 8; }
 
 // Workgroups whose partial sums of the norm's weight gradients are joined.

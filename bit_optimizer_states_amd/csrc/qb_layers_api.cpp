@@ -61,13 +61,14 @@ GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim, int parts)
     l.used = l.key + round_up((size_t)n * sizeof(int32_t), 256);
     l.list = l.used + round_up((size_t)(2 * classes + 2) * sizeof(int32_t), 256);
     l.longs = l.list + round_up((size_t)(n < rows ? n : rows) * 4 * sizeof(int32_t), 256);
-    l.chunks = l.longs + round_up((size_t)(n / chunk_tokens(n) + 1) * sizeof(int32_t), 256);
-    l.parts = l.chunks + (size_t)(2 * chunk_count(n) * padded_dim(dim)) * sizeof(float);
+    const int32_t chunk = chunk_tokens(n, dim);
+    l.chunks = l.longs + round_up((size_t)(n / chunk + 1) * sizeof(int32_t), 256);
+    l.parts = l.chunks + (size_t)(2 * chunk_count(n, chunk) * padded_dim(dim)) * sizeof(float);
     l.bytes = l.parts + (size_t)parts * 2 * (size_t)padded_dim(dim) * sizeof(float);
     return l;
 }
 
-OrderArgs order_args(void* ws, const GradLayout& l, int64_t n, int64_t rows)
+OrderArgs order_args(void* ws, const GradLayout& l, int64_t n, int64_t rows, int64_t dim)
 {
     char* const w = static_cast<char*>(ws);
     int32_t* const used = reinterpret_cast<int32_t*>(w + l.used);
@@ -75,7 +76,7 @@ OrderArgs order_args(void* ws, const GradLayout& l, int64_t n, int64_t rows)
                      reinterpret_cast<int32_t*>(w + l.key), used,
                      used + (int64_t(2) << order_log2g(rows)), reinterpret_cast<int32_t*>(w + l.list),
                      reinterpret_cast<int32_t*>(w + l.longs), order_log2g(rows), (int32_t)order_per(rows),
-                     chunk_tokens(n)};
+                     chunk_tokens(n, dim)};
 }
 
 bool valid_grad_sizes(int64_t n, int64_t rows, int64_t dim)
@@ -168,7 +169,7 @@ qb_status qb_embedding_backward(const void* dy, qb_dtype gdt, const void* ids, q
     if (takes_direct(n, rows))
         return hip_status(launch_table_grad_direct(a, dy, (int)gdt, (float)scale, padding_id, accumulate != 0, dtable,
                                                    (int)ddt, s));
-    const OrderArgs o = order_args(ws, l, n, rows);
+    const OrderArgs o = order_args(ws, l, n, rows, dim);
     float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + l.chunks);
     hipError_t e = launch_order(a, o, s);
     if (e == hipSuccess)
@@ -273,7 +274,7 @@ qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void*
     if (ws_bytes < l.bytes) return QB_EWORKSPACE;
     char* const w = static_cast<char*>(ws);
     const IdArgs a = id_args(ids, idt, n, rows, dim);
-    const OrderArgs o = order_args(ws, l, n, rows);
+    const OrderArgs o = order_args(ws, l, n, rows, dim);
     float* const chunks = reinterpret_cast<float*>(w + l.chunks);
     float* const part = reinterpret_cast<float*>(w + l.parts);
     hipStream_t s = static_cast<hipStream_t>(stream);
