@@ -52,7 +52,28 @@ struct GradLayout {
     size_t order, key, used, list, longs, chunks, parts, bytes;
 };
 
-GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim, int parts)
+size_t longs_bytes(int64_t n, int32_t chunk) { return round_up((size_t)(n / chunk + 1) * sizeof(int32_t), 256); }
+
+// The list of long ids and the chunks' sums.
+size_t chunk_bytes(int64_t n, int64_t dim, int32_t chunk)
+{
+    return longs_bytes(n, chunk) + (size_t)(2 * chunk_count(n, chunk) * padded_dim(dim)) * sizeof(float);
+}
+
+// As much for whichever chunks a call takes: the size never shrinks when tokens or
+// elements are added, so a workspace for the largest batch serves every smaller one.
+// Short chunks are at most kChunkWaves waves of 512 columns.
+constexpr size_t kShortBytesMax = (size_t)2 * kChunkWaves * 512 * sizeof(float) +
+                                  ((size_t)(kChunkWaves + 1) * sizeof(int32_t) + 255) / 256 * 256;
+
+size_t chunk_bytes_reserved(int64_t n, int64_t dim)
+{
+    const size_t s = chunk_bytes(n, dim, kChunkShort), l = chunk_bytes(n, dim, kChunkLong);
+    const size_t at_most = s < kShortBytesMax ? s : kShortBytesMax;
+    return l > at_most ? l : at_most;
+}
+
+GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim, int64_t parts)
 {
     GradLayout l;
     const int64_t classes = int64_t(1) << order_log2g(rows), entries = classes * order_per(rows) + 1;
@@ -61,11 +82,18 @@ GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim, int parts)
     l.used = l.key + round_up((size_t)n * sizeof(int32_t), 256);
     l.list = l.used + round_up((size_t)(2 * classes + 2) * sizeof(int32_t), 256);
     l.longs = l.list + round_up((size_t)(n < rows ? n : rows) * 4 * sizeof(int32_t), 256);
-    const int32_t chunk = chunk_tokens(n, dim);
-    l.chunks = l.longs + round_up((size_t)(n / chunk + 1) * sizeof(int32_t), 256);
-    l.parts = l.chunks + (size_t)(2 * chunk_count(n, chunk) * padded_dim(dim)) * sizeof(float);
+    l.chunks = l.longs + longs_bytes(n, chunk_tokens(n, dim));
+    l.parts = l.longs + chunk_bytes_reserved(n, dim);
     l.bytes = l.parts + (size_t)parts * 2 * (size_t)padded_dim(dim) * sizeof(float);
     return l;
+}
+
+// Partial rows that the stable embedding's workspace holds: those of up to
+// kDirectTokens tokens, one each, are more than those of more tokens of few ids.
+int64_t stable_parts_reserved(int64_t n, int64_t rows)
+{
+    const int64_t parts = stable_parts(n, rows), direct = n < kDirectTokens ? n : kDirectTokens;
+    return rows > 0 && direct > parts ? direct : parts;
 }
 
 OrderArgs order_args(void* ws, const GradLayout& l, int64_t n, int64_t rows, int64_t dim)
@@ -250,7 +278,7 @@ qb_status qb_stable_embedding(const void* table, qb_dtype tdt, int64_t rows, int
 size_t qb_stable_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim)
 {
     if (!valid_grad_sizes(n, rows, dim) || dim > kRowRegMax) return 0;
-    return grad_layout(n, rows, dim, stable_parts(n, rows)).bytes;
+    return grad_layout(n, rows, dim, stable_parts_reserved(n, rows)).bytes;
 }
 
 qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void* table, qb_dtype tdt, int64_t rows,
@@ -270,7 +298,7 @@ qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void*
     if (!ws) return QB_EINVAL;
     if (!aligned16(ws)) return QB_EALIGN;
     const int parts = stable_parts(n, rows);
-    const GradLayout l = grad_layout(n, rows, dim, parts);
+    const GradLayout l = grad_layout(n, rows, dim, stable_parts_reserved(n, rows));
     if (ws_bytes < l.bytes) return QB_EWORKSPACE;
     char* const w = static_cast<char*>(ws);
     const IdArgs a = id_args(ids, idt, n, rows, dim);

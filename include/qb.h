@@ -599,6 +599,8 @@ size_t qb_optimizer_workspace_bytes(const qb_optim_hparams* hp, const qb_tensor*
  *   - Outputs must not overlap inputs or each other.
  *   - accumulate (0 or 1): add the gradient to what the outputs hold (read in
  *     their dtype, added in binary32, rounded once) instead of overwriting them.
+ *   - Workspaces: a *_workspace_bytes result never shrinks when n, rows or dim
+ *     grows, so a workspace for the largest call serves every smaller one.
  *   - Limits: n, rows < 2^31; dim < 2^24; a table's gradient takes at most 2^30
  *     tokens and 2^26 rows.
  */
