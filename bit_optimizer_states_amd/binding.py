@@ -21,6 +21,7 @@ QB_DYN8, QB_NF4, QB_FP4, QB_UDYN8 = 0, 1, 2, 3
 QB_I32, QB_I64 = 0, 1
 QB_ADAMW, QB_ADAM, QB_LION, QB_SGD, QB_RMSPROP, QB_LAMB, QB_LARS = range(7)
 
+_UINT8, _FLOAT32 = torch.uint8, torch.float32
 _INDEX = {torch.int32: QB_I32, torch.int64: QB_I64}
 _DTYPE = {torch.float32: QB_F32, torch.float16: QB_F16, torch.bfloat16: QB_BF16}
 
@@ -34,6 +35,7 @@ class QbError(RuntimeError):
 class qb_dq(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("absmax2", ctypes.c_void_p), ("offset", ctypes.c_void_p),
                 ("blocksize2", ctypes.c_int32), ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+    made_of = None      # make_dq: the tensors (codes, absmax2, offset)
 
 
 class qb_adamw_hparams(ctypes.Structure):
@@ -222,8 +224,10 @@ def qb_multi_tensor_workspace_bytes(count):
 
 def make_dq(codes, absmax2, offset, blocksize2, ws=None):
     """qb_dq from device tensors (ws may be None for dequantize)."""
-    return qb_dq(_ptr(codes), _ptr(absmax2), _ptr(offset), int(blocksize2), _ptr(ws),
-                 0 if ws is None else ws.numel() * ws.element_size())
+    dq = qb_dq(_ptr(codes), _ptr(absmax2), _ptr(offset), int(blocksize2), _ptr(ws),
+               0 if ws is None else ws.numel() * ws.element_size())
+    dq.made_of = codes, absmax2, offset          # kept as long as dq is, and for the calls that check them
+    return dq
 
 
 def qb_quantize(x, n, code, blocksize, codes, absmax=None, dq=None, stream=None):
@@ -480,18 +484,38 @@ def qb_embedding(table, ids, y, scale=1.0, stream=None):
               _at(y, d), _dtype(y))
 
 
+def _check_dq(dq, blocks, device):
+    """The nested constants of `blocks` blocks, where make_dq noted them."""
+    codes, absmax2, offset = dq.made_of or (None, None, None)
+    if codes is not None and (codes.dtype is not _UINT8 or codes.numel() < blocks or codes.get_device() != device):
+        raise ValueError("dq codes: uint8 codes of every block expected, on the same device")
+    if absmax2 is not None and (absmax2.dtype is not _FLOAT32 or absmax2.numel() * dq.blocksize2 < blocks or
+                                absmax2.get_device() != device):
+        raise ValueError("dq absmax2: fp32 absmax of every block expected, on the same device")
+    if offset is not None and (offset.dtype is not _FLOAT32 or offset.numel() < 1 or offset.get_device() != device):
+        raise ValueError("dq offset: one fp32 value expected, on the same device")
+
+
 def qb_dequant_embedding(codes, absmax, dq, code, blocksize, rows, ids, y, scale=1.0, stream=None):
     """qb_embedding from a quantized table of `rows` rows of y.shape[-1]
     elements (codes and absmax or dq as for qb_dequantize)."""
     lib()
     dim = y.shape[-1]
-    n = _tokens(y, dim, "y", ids)
+    n = ids.numel()
+    if dim == 0 or y.numel() != n * dim:
+        raise ValueError(f"y of {n} rows of at least one element expected")
     total = rows * dim
     if codes.numel() < (total if code == QB_DYN8 else (total + 1) // 2):
         raise ValueError("codes of the whole table expected")
     if absmax is not None and absmax.numel() * blocksize < total:
         raise ValueError("absmax of every block expected")
+    if codes.dtype != _UINT8:
+        raise ValueError("uint8 codes expected")
+    if absmax is not None and absmax.dtype != _FLOAT32:
+        raise ValueError("fp32 absmax expected")
     d = y.get_device()
+    if dq is not None and blocksize > 0:
+        _check_dq(dq, -(-total // blocksize), d)
     _row_call("qb_dequant_embedding", d, stream, _at(codes, d), _at(absmax, d),
               ctypes.byref(dq) if dq is not None else None, code, blocksize, rows, dim, _at(ids, d), _index(ids), n,
               scale, _at(y, d), _dtype(y))
