@@ -219,18 +219,30 @@ hipError_t dequant_embedding_y(const IdArgs& a, const DequantDesc& d, int code4,
 // us, 5003 in 8 us.  (Writing the zero rows beside it does not pay: their place is
 // known only after it, and zeros under rows that are written again later took it from
 // 11 to 17 us and the whole call with it.)
-template <bool ID64>
+//
+// With parts (order_in_parts) the same steps run twice: over all tokens with ranges of
+// classes in the place of classes (kDeal), then per class over its part's tokens
+// (kInPart).
+enum OrderStep { kAll, kDeal, kInPart };
+
+template <bool ID64, OrderStep STEP>
 __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs o)
 {
     extern __shared__ int32_t s_cnt[];                 // [kOrderWaves][per]
     __shared__ int32_t s_below[kOrderWaves], s_wave[kOrderWaves], s_used[2][kOrderWaves];
     constexpr int UN = 16;                             // loads in flight per lane
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    const int32_t cls = (int32_t)blockIdx.x, mask = (1 << o.log2g) - 1, per = o.per;
+    const int32_t cls = (int32_t)blockIdx.x, mask = (1 << o.log2g) - 1, per = STEP == kDeal ? 1 : o.per;
+    const int32_t shift = o.log2g - kOrderPartBits;
+    auto class_of = [&](int32_t id) { return STEP == kDeal ? (id & mask) >> shift : id & mask; };
+    auto entry_of = [&](int32_t id) { return STEP == kDeal ? 0 : id >> o.log2g; };
 
-    const int64_t stretch = ((a.n + kOrderWaves - 1) / kOrderWaves + 63) / 64 * 64;
-    const int64_t first = wave * stretch;
-    const int64_t last = first + stretch < a.n ? first + stretch : a.n;
+    // the tokens gone through: all, or the part's
+    const int64_t begin = STEP == kInPart ? o.part_start[cls >> shift] : 0;
+    const int64_t end = STEP == kInPart ? o.part_start[(cls >> shift) + 1] : a.n;
+    const int64_t stretch = ((end - begin + kOrderWaves - 1) / kOrderWaves + 63) / 64 * 64;
+    const int64_t first = begin + wave * stretch;
+    const int64_t last = first + stretch < end ? first + stretch : end;
     int32_t* const cnt = s_cnt + wave * per;
     // ids of the tokens t0 + k * 64 + lane; -1 beyond the stretch or outside the table
     int32_t id[UN];
@@ -240,7 +252,8 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
         for (int k = 0; k < UN; ++k) {
             const int64_t t = t0 + k * 64 + lane;
             const int64_t at = t < last ? t : last - 1;
-            if constexpr (ID64) raw[k] = gld<int64_t>(static_cast<const int64_t*>(a.ids) + at);
+            if constexpr (STEP == kInPart) raw[k] = gld<int32_t>(o.part_id + at);
+            else if constexpr (ID64) raw[k] = gld<int64_t>(static_cast<const int64_t*>(a.ids) + at);
             else raw[k] = gld<int32_t>(static_cast<const int32_t*>(a.ids) + at);
         }
 #pragma unroll
@@ -259,9 +272,9 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
         for (int k = 0; k < UN; ++k) {
             if (k % 4 == 0 && t0 + k * 64 >= last) break;      // uniform: few tokens run little of this code
             if (id[k] >= 0) {
-                const int32_t c = id[k] & mask;
+                const int32_t c = class_of(id[k]);
                 below += c < cls ? 1 : 0;
-                if (c == cls) atomicAdd(&cnt[id[k] >> o.log2g], 1);
+                if (c == cls) atomicAdd(&cnt[entry_of(id[k])], 1);
             }
         }
     }
@@ -270,7 +283,7 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
     __syncthreads();
 
     // exclusive scan over the entries: thread j owns entry j (per <= kOrderPerMax)
-    int32_t base = 0;
+    int32_t base = (int32_t)begin;
 #pragma unroll
     for (int w = 0; w < kOrderWaves; ++w) base += s_below[w];
     const int j = threadIdx.x;
@@ -296,16 +309,17 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
     for (int w = 0; w < wave; ++w) before += s_wave[w];
     if (j < per) {
         int32_t run = base + before + incl - total;
-        o.start[(int64_t)cls * per + j] = run;
+        int32_t* const start = (STEP == kDeal ? o.part_start : o.start) + (int64_t)cls * per;
+        start[j] = run;
 #pragma unroll
         for (int w = 0; w < kOrderWaves; ++w) {
             s_cnt[w * per + j] = run;
             run += of_wave[w];
         }
-        if (cls == mask && j == per - 1) o.start[((int64_t)cls + 1) * per] = run;
+        if (cls == (int32_t)gridDim.x - 1 && j == per - 1) start[per] = run;
     }
-    if (cls == 0 && j == 0) o.count[1] = 0;            // k_table_grad counts long ids in it
-    if (j < 2) {
+    if (STEP != kDeal && cls == 0 && j == 0) o.count[1] = 0;       // k_table_grad counts long ids in it
+    if (STEP != kDeal && j < 2) {
         int32_t used = 0;
         for (int w = 0; w < kOrderWaves; ++w) used += s_used[j][w];
         o.used[2 * (int64_t)cls + j] = used;
@@ -317,19 +331,21 @@ __global__ __launch_bounds__(kOrderWaves * 64) void k_order(IdArgs a, OrderArgs 
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
             if (k % 4 == 0 && t0 + k * 64 >= last) break;
-            const bool mine = id[k] >= 0 && (id[k] & mask) == cls;
+            const bool mine = id[k] >= 0 && class_of(id[k]) == cls;
             unsigned long long todo = __ballot(mine);
             while (todo) {
                 const int lead = __builtin_ctzll(todo);
                 const int32_t e = __builtin_amdgcn_readlane(id[k], lead);
-                const unsigned long long same = __ballot(mine && id[k] == e);
+                const bool equal = mine && (STEP == kDeal || id[k] == e);
+                const unsigned long long same = __ballot(equal);
                 int32_t at = 0;
-                if (lane == lead) at = atomicAdd(&cnt[e >> o.log2g], (int32_t)__popcll(same));
+                if (lane == lead) at = atomicAdd(&cnt[entry_of(e)], (int32_t)__popcll(same));
                 at = __builtin_amdgcn_readlane(at, lead);
-                if (mine && id[k] == e) {
+                if (equal) {
                     const int32_t p = at + (int32_t)__popcll(same & ((1ull << lane) - 1));
-                    o.order[p] = (int32_t)(t0 + k * 64 + lane);
-                    o.key[p] = e;
+                    const int64_t t = t0 + k * 64 + lane;
+                    (STEP == kDeal ? o.part_pos : o.order)[p] = STEP == kInPart ? gld<int32_t>(o.part_pos + t) : (int32_t)t;
+                    (STEP == kDeal ? o.part_id : o.key)[p] = id[k];
                 }
                 todo &= ~same;
             }
@@ -695,7 +711,12 @@ hipError_t launch_dequant_embedding(const IdArgs& a, const DequantDesc& t, int b
 hipError_t launch_order(const IdArgs& a, const OrderArgs& o, hipStream_t s)
 {
     const size_t lds = (size_t)kOrderWaves * o.per * sizeof(int32_t);
-    return launch_kernel_lds(a.id64 ? k_order<true> : k_order<false>, 1 << o.log2g, kOrderWaves * 64, lds, s, a, o);
+    const int threads = kOrderWaves * 64;
+    if (!o.part_start)
+        return launch_kernel_lds(a.id64 ? k_order<true, kAll> : k_order<false, kAll>, 1 << o.log2g, threads, lds, s, a, o);
+    const hipError_t e = launch_kernel_lds(a.id64 ? k_order<true, kDeal> : k_order<false, kDeal>, kOrderParts, threads,
+                                           kOrderWaves * sizeof(int32_t), s, a, o);
+    return e != hipSuccess ? e : launch_kernel_lds(k_order<false, kInPart>, 1 << o.log2g, threads, lds, s, a, o);
 }
 
 hipError_t launch_prepare_grad(const IdArgs& a, const OrderArgs& o, const void* dy, int gdt, float* part, int64_t pad,

@@ -27,6 +27,10 @@ struct IdArgs {
 // different classes.  start[class * per + entry] .. start[... + 1] is the range of
 // the id's tokens in `order`, which lists their positions in ascending order;
 // `key` lists their ids.
+// Where there are many classes (order_in_parts), the tokens are dealt into
+// kOrderParts ranges of classes first: part p is part_pos / part_id[part_start[p] ..
+// part_start[p + 1]), in ascending order of the positions, and a class goes through
+// its part only.
 // `list` holds the count[0] ids that have tokens, each as {id, begin, end, first
 // position}, `longs` the count[1] ids that have more than `chunk` tokens.
 struct OrderArgs {
@@ -40,6 +44,9 @@ struct OrderArgs {
     int32_t log2g;
     int32_t per;
     int32_t chunk;
+    int32_t* part_start; // [kOrderParts + 1], nullptr: without parts
+    int32_t* part_pos;   // [n]
+    int32_t* part_id;    // [n]
 };
 
 constexpr int kOrderWaves = 16;            // waves of the ordering kernel
@@ -55,6 +62,21 @@ constexpr int32_t order_log2g(int64_t rows)
     return g;
 }
 constexpr int64_t order_per(int64_t rows) { return (rows + (int64_t(1) << order_log2g(rows)) - 1) >> order_log2g(rows); }
+
+// Whether the ordering deals the tokens into parts first.  Every class's workgroup
+// reads all tokens' ids otherwise, n * 2^log2g reads: minutes for 2^30 tokens and the
+// 2^17 classes of 2^26 rows.  In parts it is n * (256 + 2^(log2g - 8)) and a launch more.
+// Up to 512 classes are resident at once, and the launch pays for many tokens only;
+// beyond that nearly always (whole gradient of rows of 8 elements in us, without / with
+// parts: 300000 rows, 16384 tokens 37.1 / 42.7, 49152 68.5 / 67.5, 2^20 886 / 666; 600000
+// rows, 300 tokens 31.0 / 34.1, 1024 39.9 / 38.7, 49152 102.6 / 72.8; 2^20 rows, 300 tokens
+// 47.0 / 46.9, 2^20 2617 / 745; 2^24 rows, 2^20 tokens 36400 / 1500).
+constexpr int kOrderPartBits = 8, kOrderParts = 1 << kOrderPartBits;
+constexpr bool order_in_parts(int64_t n, int64_t rows)
+{
+    const int32_t log2g = order_log2g(rows);
+    return log2g > 10 || (log2g == 10 && n >= 1024) || (log2g == 9 && n >= 49152);
+}
 
 // Tokens per chunk of the ordered list: an id with more tokens than this is
 // summed chunk by chunk, then joined.  Two chunks fit the lanes of a wave.  A wave

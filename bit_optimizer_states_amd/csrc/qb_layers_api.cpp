@@ -47,9 +47,10 @@ IdArgs id_args(const void* ids, qb_index idt, int64_t n, int64_t rows, int64_t d
 bool valid_eps(double eps) { return std::isfinite(eps) && (float)eps >= 0x1p-126f && std::isfinite((float)eps); }
 
 // Workspace of a table's gradient: the arrays of OrderArgs, the chunks' sums; then
-// (stable) the partial sums of dgamma and dbeta.
+// (stable) the partial sums of dgamma and dbeta; then the ordering's parts, where it
+// takes them.
 struct GradLayout {
-    size_t order, key, used, list, longs, chunks, parts, bytes;
+    size_t order, key, used, list, longs, chunks, parts, split, bytes;
 };
 
 size_t longs_bytes(int64_t n, int32_t chunk) { return round_up((size_t)(n / chunk + 1) * sizeof(int32_t), 256); }
@@ -73,6 +74,9 @@ size_t chunk_bytes_reserved(int64_t n, int64_t dim)
     return l > at_most ? l : at_most;
 }
 
+constexpr size_t split_start_bytes = ((kOrderParts + 1) * sizeof(int32_t) + 255) / 256 * 256;
+size_t split_bytes(int64_t n) { return round_up((size_t)n * sizeof(int32_t), 256); }
+
 GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim, int64_t parts)
 {
     GradLayout l;
@@ -84,7 +88,8 @@ GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim, int64_t parts)
     l.longs = l.list + round_up((size_t)(n < rows ? n : rows) * 4 * sizeof(int32_t), 256);
     l.chunks = l.longs + longs_bytes(n, chunk_tokens(n, dim));
     l.parts = l.longs + chunk_bytes_reserved(n, dim);
-    l.bytes = l.parts + (size_t)parts * 2 * (size_t)padded_dim(dim) * sizeof(float);
+    l.split = l.parts + (size_t)parts * 2 * (size_t)padded_dim(dim) * sizeof(float);
+    l.bytes = l.split + (order_in_parts(n, rows) ? split_start_bytes + 2 * split_bytes(n) : 0);
     return l;
 }
 
@@ -99,12 +104,13 @@ int64_t stable_parts_reserved(int64_t n, int64_t rows)
 OrderArgs order_args(void* ws, const GradLayout& l, int64_t n, int64_t rows, int64_t dim)
 {
     char* const w = static_cast<char*>(ws);
-    int32_t* const used = reinterpret_cast<int32_t*>(w + l.used);
-    return OrderArgs{reinterpret_cast<int32_t*>(w), reinterpret_cast<int32_t*>(w + l.order),
-                     reinterpret_cast<int32_t*>(w + l.key), used,
-                     used + (int64_t(2) << order_log2g(rows)), reinterpret_cast<int32_t*>(w + l.list),
-                     reinterpret_cast<int32_t*>(w + l.longs), order_log2g(rows), (int32_t)order_per(rows),
-                     chunk_tokens(n, dim)};
+    auto at = [w](size_t offset) { return reinterpret_cast<int32_t*>(w + offset); };
+    const bool parts = order_in_parts(n, rows);
+    int32_t* const used = at(l.used);
+    return OrderArgs{at(0), at(l.order), at(l.key), used, used + (int64_t(2) << order_log2g(rows)), at(l.list),
+                     at(l.longs), order_log2g(rows), (int32_t)order_per(rows), chunk_tokens(n, dim),
+                     parts ? at(l.split) : nullptr, parts ? at(l.split + split_start_bytes) : nullptr,
+                     parts ? at(l.split + split_start_bytes + split_bytes(n)) : nullptr};
 }
 
 bool valid_grad_sizes(int64_t n, int64_t rows, int64_t dim)

@@ -644,8 +644,10 @@ qb_status qb_dequant_embedding(const uint8_t* codes, const float* absmax, const 
  *   ws          device workspace of qb_embedding_workspace_bytes(n, rows, dim)
  *               bytes, 16-byte aligned; holds nothing between calls, and must not
  *               be shared by calls that may overlap in time.
- * Up to three kernels on `stream` (one for up to 128 tokens); no memory
- * operations, so it may be captured.
+ * Up to three kernels on `stream` (one for up to 128 tokens, four for many
+ * tokens of a table of over 256000 rows); no memory operations, so it may be
+ * captured.  Every id is read by 256 workgroups or more: 2^20 tokens of rows of 8
+ * elements take 0.6 ms, of which the time grows with the tokens.
  */
 qb_status qb_embedding_backward(const void* dy, qb_dtype gdt, const void* ids, qb_index idt, int64_t n, int64_t rows,
                                 int64_t dim, double scale, int64_t padding_id, int32_t accumulate, void* dtable,
@@ -710,7 +712,7 @@ qb_status qb_stable_embedding(const void* table, qb_dtype tdt, int64_t rows, int
  *   ws           device workspace of qb_stable_embedding_workspace_bytes(n, rows,
  *                dim) bytes, as for qb_embedding_backward.
  * Other arguments as qb_embedding_backward and qb_stable_embedding.  Up to five
- * kernels (two for up to 128 tokens).
+ * kernels (two for up to 128 tokens, six where qb_embedding_backward takes four).
  */
 qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void* table, qb_dtype tdt, int64_t rows,
                                        int64_t dim, const void* ids, qb_index idt, int64_t n, double scale,
