@@ -150,8 +150,8 @@ __global__ __launch_bounds__(NT) void k_norm_grad(const void* __restrict__ dy, c
             du[k] = load_row_unit<XDT, TAIL, true>(grow, k * TPR + lane, units, dim);
             xu[k] = load_row_unit<XDT, TAIL, true>(xrow, k * TPR + lane, units, dim);
         }
-        m = mean_in[at];
-        r = rstd_in[at];
+        m = t < n ? mean_in[at] : 0.0f;
+        r = t < n ? rstd_in[at] : 0.0f;
     };
     int64_t t0 = (int64_t)blockIdx.x * GROUPS;
     load_next(t0 + grp);
@@ -166,8 +166,8 @@ __global__ __launch_bounds__(NT) void k_norm_grad(const void* __restrict__ dy, c
         const int64_t t = t0 + grp;
         const bool live = t < n;
         const int64_t row = t * dim * elem_bytes(XDT);
-        // Units beyond the row, and rows beyond the last, take a dy of zero (and an x that is read: finite
-        // wherever the row is).
+        // Elements beyond the row, and rows beyond the last, take a dy and an h of zero ((0 - m) * r may
+        // overflow).
         float s1 = 0.0f, s2 = 0.0f;
         float hk[KEEP ? VPT : 1][8], gk[KEEP ? VPT : 1][8];
 #pragma unroll
@@ -178,10 +178,14 @@ __global__ __launch_bounds__(NT) void k_norm_grad(const void* __restrict__ dy, c
                 for (int j = 0; j < (XDT == DT_F32 ? 8 : 4); ++j) du[k].w[j] = xu[k].w[j] = 0u;
             }
             const float* const gam = s_cols + (unit < units ? unit : 0) * 8;
+            const bool whole = whole_step<TPR>(k, dim);
+            const float rk = TAIL != kWhole || whole || unit < units ? r : 0.0f;
+            const int cnt = unit_count(unit, dim);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float d = unit_at<XDT>(du[k], j);
-                const float h = (unit_at<XDT>(xu[k], j) - m) * r;
+                float h = (unit_at<XDT>(xu[k], j) - m) * rk;
+                if (TAIL != kWhole && !whole) h = j < cnt ? h : 0.0f;
                 const float g = d * gam[j];
                 s1 += g;
                 s2 = __builtin_fmaf(g, h, s2);

@@ -97,10 +97,16 @@ struct StableRows {
         row_stats<TPR, VPT>(x, shape, tid, dim, p.eps, slot, &mean, &rstd);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int k = 0; k < VPT; ++k)
+        for (int k = 0; k < VPT; ++k) {
+            // h is zero beyond the row, where (0 - mean) * rstd may overflow
+            const bool whole = whole_step<TPR>(k, dim);
+            const float rk = TAIL != kWhole || whole || k * TPR + tid < units ? rstd : 0.0f;
+            const int cnt = unit_count(k * TPR + tid, dim);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float d = sum[k][j], h = (x[k][j] - mean) * rstd, g = d * gam[k][j];
+                const float d = sum[k][j], g = d * gam[k][j];
+                float h = (x[k][j] - mean) * rk;
+                if (TAIL != kWhole && !whole) h = j < cnt ? h : 0.0f;
                 sum[k][j] = g;
                 x[k][j] = h;
                 accg[k][j] = __builtin_fmaf(d, h, accg[k][j]);
@@ -108,6 +114,7 @@ struct StableRows {
                 s1 += g;
                 s2 = __builtin_fmaf(g, h, s2);
             }
+        }
         row_sum2<TPR>(s1, s2, slot + row_slot_words(TPR));
         if (v == p.pad) return;                        // its row takes no gradient
         const float c1 = s1 * shape.inv_dim, c2 = s2 * shape.inv_dim, f = p.scale * rstd;

@@ -182,3 +182,40 @@ def test_means_of_rows_that_hold_infinities(dim, dt):
     assert rstd[1:8].isnan().all() and y[1:8].isnan().all()
     for got, alone in zip((y, mean, rstd), clean):
         assert torch.equal(got[::8], alone)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("dim", DIMS + [64, 4096])
+def test_gradients_of_very_large_rows_of_equal_values(dim, dt):
+    """|mean| * rstd overflows, which only an element outside the row would meet: h = 0 in the row, so
+    dx = rstd (g - mean g), dgamma = 0."""
+    L = qb()
+    x = constant_rows([1e34, -3e33, 2.0, 1e33] * 10, dim, dt)[:37 if dim < 5000 else 5]
+    n, eps = x.shape[0], 1e-12
+    y = torch.full_like(x, 7.0)
+    mean, rstd = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    L.qb_layer_norm(x, None, None, eps, y, mean=mean, rstd=rstd)
+    assert (y == 0).all() and torch.equal(mean, x[:, 0].float())
+    r = ref.f64(rstd)
+    dy = torch.empty(n, dim, device=DEV).normal_(0, 1).to(dt)
+    dx = torch.full_like(x, 7.0)
+    dgamma = torch.full((dim,), 7.0, device=DEV)
+    ws = torch.empty(L.qb_layer_norm_workspace_bytes(n, dim), dtype=torch.uint8, device=DEV)
+    L.qb_layer_norm_backward(dy, x, None, mean, rstd, dx, dgamma, None, ws)
+    d = ref.f64(dy)
+    zero = np.zeros_like(d)
+    want, err = ref.norm_grad(d, zero, zero, zero, r, np.zeros_like(r), np.ones(dim))
+    ref.assert_close(dx, want, err, "dx")
+    assert (dgamma == 0).all()
+    if dim > 16384:
+        return
+    for m in (n, 200):                                  # both forms of the table's gradient
+        ids = torch.arange(m, device=DEV) % n
+        dy = torch.empty(m, dim, device=DEV).normal_(0, 1)
+        dtable = torch.full((n, dim), 7.0, device=DEV)
+        ws = torch.empty(L.qb_stable_embedding_workspace_bytes(m, n, dim), dtype=torch.uint8, device=DEV)
+        L.qb_stable_embedding_backward(dy, x, ids, None, eps, dtable, dgamma, None, ws)
+        s, e_s, _ = ref.token_sums(ref.f64(dy), ids.tolist(), n)
+        want, err = ref.norm_grad(s, e_s, np.zeros_like(s), np.zeros_like(s), r, 3 * ref.U * r, np.ones(dim))
+        ref.assert_close(dtable, want, err, f"dtable of {m} tokens")
+        assert (dgamma == 0).all()
