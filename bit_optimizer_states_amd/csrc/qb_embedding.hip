@@ -5,7 +5,7 @@
 // by HBM: the rows that are used are read, y is written.
 //
 // Gradient: dW[v] = scale * (sum of dy_t over the tokens t with id_t = v), in
-// three launches.  The tokens are ordered by id (k_order), so that every sum is
+// three launches (four for large tables).  The tokens are ordered by id (k_order), so that every sum is
 // taken in ascending order of the tokens: no atomics on floating-point values,
 // the same bits on every run.  Then every wave streams one chunk of the ordered
 // tokens: it writes the rows of the ids that begin there, and a partial row for an

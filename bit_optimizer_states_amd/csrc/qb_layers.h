@@ -7,7 +7,7 @@
 
 namespace qb {
 
-// Longest row of the kernels that hold a row in registers (256 threads x 8
+// Longest row of the kernels that hold a row in registers (1024 threads x 2
 // units x 8 elements).
 constexpr int64_t kRowRegMax = 16384;
 

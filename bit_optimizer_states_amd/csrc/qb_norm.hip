@@ -10,16 +10,17 @@
 // row, and a second kernel adds the partial rows.  Every sum has a fixed order:
 // the same bits on every run.  Bound by HBM: 16384 rows of 4096 bf16 in 69 us and 4.5
 // us for the partial rows (403 MB: 5.5 TB/s together).  Few long rows are bound by the
-// latency of a row or two per workgroup: 1023 rows of 5001 binary32 in 17 and 4 us (61 MB).
+// latency of a row or two per workgroup: 1023 rows of 5001 binary32 in 19 and 4 us (61 MB).
 #include "qb_norm_kernels.h"
 
 namespace qb {
 
 namespace {
 
-// Rows too long for registers (dim > kRowRegMax): one workgroup of 1024
-// threads per row reads it three times (the second and third time from L2): 2048 rows
-// of 32768 bf16 in 62 us, 4.4 TB/s.
+// Rows beyond the kernels of two units a thread (dim > kRowRegMax): one workgroup of
+// 1024 threads per row reads it three times (the second and third time from L2): 2048 rows
+// of 32768 bf16 in 64 us, 4.2 TB/s.  (16-bit rows of that length would fit registers as
+// four raw units a thread; no such kernel was built.)
 constexpr int kLongThreads = 1024;
 
 template <int XDT, int WDT>

@@ -10,9 +10,10 @@
 //
 // One read and one write of every row: the kernel is bound by HBM (16384 rows of
 // 4096 bf16 in 47 us, 5.8 TB/s; a copy of the same 268 MB takes 45), with the vector
-// ALU close behind: about 210 instructions per wave and row there; a first version of
-// 550 was bound by them (50 us), so uniform conditions are kept out of the lanes and
-// everything that depends on the row's length alone is computed once.  Gathering rows
+// ALU close behind: about 280 instructions per wave and row there, active 0.72 of the
+// time (55 of them for the correction of 16-bit rows' means and its checks, 46.8 -> 47.5
+// us); a first version of 550 was bound by them (50 us), so uniform conditions are kept out
+// of the lanes and everything that depends on the row's length alone is computed once.  Gathering rows
 // of a binary32 table ([32000, 4096], natural frequencies) 52 us: the 90 MB of used rows
 // come to 167 MB, since each of the 8 L2s fetches the frequent ones.
 #pragma once

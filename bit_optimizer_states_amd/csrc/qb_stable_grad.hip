@@ -9,8 +9,8 @@
 // the norm's backward pass runs once per used id instead of once per token, and
 // no [tokens, dim] intermediate is written: the bytes are those of the plain
 // embedding's gradient plus the used rows of W.  16384 tokens, [32000, 4096] binary32
-// with bf16 gradients: 128 us for 473 MB in five launches (ordering 11, k_prepare_grad
-// 54, joined chunks 4.8, k_stable_grad 55, partial rows 4.8).
+// with bf16 gradients: 127 us for 473 MB in five launches (ordering 12, k_prepare_grad
+// 54, joined chunks 5, k_stable_grad 55, partial rows 5).
 #include <type_traits>
 
 #include "qb_norm_kernels.h"
@@ -20,7 +20,7 @@ namespace qb {
 
 namespace {
 
-constexpr int kStableParts = 512;        // workgroups of the gradient, two per CU
+constexpr int kStableParts = 512;        // workgroups of the gradient: two of 512 threads are all a CU holds
 
 struct StableGradArgs {
     const void* dy;
@@ -165,9 +165,13 @@ struct StableRows {
 // TPR threads (one workgroup) to a listed id; a workgroup walks the list by
 // the grid, looks its next 64 ids up at once (lane l the l-th), and reads the
 // next id's row and first token before it works on the current one.  Bound by the
-// latency of an id's chain (row and token, two barriers, further tokens), at 44% of the
-// vector ALU: 512 workgroups measured best (133 us for the whole gradient; 768 and 1024
-// 136 to 140, since each leaves a partial row).  (Two ids at a time, sharing the barriers, spilled or halved the resident workgroups: 60 to 65 us
+// latency of an id's chain (row and token, two barriers, further tokens), at 56% of the
+// vector ALU, and hidden no further because of the registers: 115 to 127 VGPRs let two
+// workgroups of 512 threads reside on a CU, 512 in all; 768 or 1024 of them queue, and each
+// leaves a partial row (136 to 140 us for the whole gradient against 133 then).  Ragged rows
+// with binary32 dy take 129 to 143 VGPRs (rows of 2049 to 4096 elements: one workgroup a
+// CU), with a binary32 table too 36 bytes a lane of scratch beyond 4096 elements; rows of
+// 8193 to 16384 spill 152 to 348 bytes.  None of these is tuned.  (Two ids at a time, sharing the barriers, spilled or halved the resident workgroups: 60 to 65 us
 // against 55 for 4300 ids of 4096 elements.)
 template <int GDT, int TDT, int TPR, int VPT, int TAIL>
 __global__ __launch_bounds__(TPR) void k_stable_grad(IdArgs a, OrderArgs o, StableGradArgs p)
