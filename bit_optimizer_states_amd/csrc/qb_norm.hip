@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(const void* __restri
     const float inv = 1.0f / (float)dim;
     around(m0, s_slot + 2 * (kLongThreads / 64));
     float c = correction(sd, inv);
-    if (mostly_rounding(sd, c, sq)) {                  // (the same for all threads)
+    if (mostly_rounding(sd * c, sq)) {                 // (the same for all threads)
         m0 += c;
         around(m0, s_slot + 4 * (kLongThreads / 64));
         c = correction(sd, inv);

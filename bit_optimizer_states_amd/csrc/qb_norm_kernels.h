@@ -10,8 +10,8 @@
 //
 // One read and one write of every row: the kernel is bound by HBM (16384 rows of
 // 4096 bf16 in 47 us, 5.8 TB/s; a copy of the same 268 MB takes 45), with the vector
-// ALU close behind: about 280 instructions per wave and row there, active 0.72 of the
-// time (55 of them for the correction of 16-bit rows' means and its checks, 46.8 -> 47.5
+// ALU close behind: about 265 instructions per wave and row there, active 0.68 of the
+// time (42 of them for the correction of 16-bit rows' means and its check, 46.7 -> 47.1
 // us); a first version of 550 was bound by them (50 us), so uniform conditions are kept out
 // of the lanes and everything that depends on the row's length alone is computed once.  Gathering rows
 // of a binary32 table ([32000, 4096], natural frequencies) 52 us: the 90 MB of used rows
@@ -152,11 +152,12 @@ __device__ __forceinline__ void deviations(const float (&x)[VPT][8], float m, in
     sd = lanes_sum<L>(sd);
 }
 
-// Whether the squares sq around a mean are more than half that mean's own error (sd * c):
-// what would be left of them has lost digits, or they overflowed.
-__device__ __forceinline__ bool mostly_rounding(float sd, float c, float sq)
+// Whether the squares sq around a mean are more than half that mean's own error, share =
+// sd * c: what would be left of them has lost digits, or both overflowed (inf - inf), or
+// the row holds an infinity or NaN.
+__device__ __forceinline__ bool mostly_rounding(float share, float sq)
 {
-    return !(sd * c <= 0.5f * fminf(sq, FLT_MAX));
+    return !(__builtin_fmaf(-2.0f, share, sq) >= 0.0f);
 }
 
 // The correction of a mean: none where the row holds infinities or NaN, whose mean the
@@ -187,15 +188,15 @@ __device__ __forceinline__ WaveStats wave_stats(const float (&x)[VPT][8], const 
     }
     float m0 = lanes_sum<L>(s) * shape.inv_mine, sd, sq;
     deviations<TPR, VPT>(x, m0, lane, dim, sd, sq);
-    float c = correction(sd, shape.inv_mine);
-    const bool again = mostly_rounding(sd, c, sq);
+    float c = sd * shape.inv_mine, m2 = sq - sd * c;
+    const bool again = mostly_rounding(sd * c, sq);
     if (__any(again)) {                                // (several rows may share the wave)
-        const float m1 = again ? m0 + c : m0;
-        deviations<TPR, VPT>(x, m1, lane, dim, sd, sq);
-        m0 = m1;
+        m0 = again ? m0 + correction(sd, shape.inv_mine) : m0;
+        deviations<TPR, VPT>(x, m0, lane, dim, sd, sq);
         c = correction(sd, shape.inv_mine);
+        m2 = without_mean(sq, sd * c);
     }
-    return WaveStats{m0, c, without_mean(sq, sd * c)};
+    return WaveStats{m0, c, m2};
 }
 
 // Leaves a wave's share in the row's slot (row_slot_words(TPR) words).
@@ -225,10 +226,14 @@ __device__ __forceinline__ void join_stats(const WaveStats& w, const RowShape<TP
         const float nd = shape.held * d;
         const float dm = group_sum<W>(nd), dq = group_sum<W>(nd * d), q = group_sum<W>(slot[3 * l + 1]);
         const float shift = dm * shape.inv_dim;
+        float between = dq - dm * shift;
         m = m00 + (c00 + shift);
-        if (!(__builtin_fabsf(shift) <= FLT_MAX))      // infinities, NaN: the mean of the waves' means
-            m = group_sum<W>(slot[3 * l] * (shape.held * shape.inv_dim));
-        m2 = q + without_mean(dq, dm * shift);
+        if (between != between) {                      // squares beyond binary32, infinities, NaN
+            between = without_mean(dq, dm * shift);
+            if (!(__builtin_fabsf(shift) <= FLT_MAX))  // the mean of the waves' means
+                m = group_sum<W>(slot[3 * l] * (shape.held * shape.inv_dim));
+        }
+        m2 = q + between;
     }
     *mean = m;
     *rstd = inv_deviation(m2 * shape.inv_dim, eps);

@@ -165,7 +165,7 @@ struct StableRows {
 // TPR threads (one workgroup) to a listed id; a workgroup walks the list by
 // the grid, looks its next 64 ids up at once (lane l the l-th), and reads the
 // next id's row and first token before it works on the current one.  Bound by the
-// latency of an id's chain (row and token, two barriers, further tokens), at 56% of the
+// latency of an id's chain (row and token, two barriers, further tokens), at 54% of the
 // vector ALU, and hidden no further because of the registers: 115 to 127 VGPRs let two
 // workgroups of 512 threads reside on a CU, 512 in all; 768 or 1024 of them queue, and each
 // leaves a partial row (136 to 140 us for the whole gradient against 133 then).  Ragged rows
