@@ -1,5 +1,5 @@
 """GPU: the table's gradient on either side of the sizes where its chunks of
-ordered tokens go from 16 to 32 (3072 waves of 512 columns), with ids of one
+ordered tokens go from 16 to 32 (12 waves of 512 columns a CU), with ids of one
 token, of about a chunk and of many chunks; whole-numbered dy, so that every sum is
 exact, and a workspace of exactly the size asked for."""
 import pytest

@@ -13,7 +13,7 @@ def L():
 
 
 # around every size where a kernel's form changes: the direct gradients (128 tokens), chunks of 16 or 32
-# tokens (3072 waves), partial rows (256 and 512 workgroups), and powers of two
+# tokens (12 waves a CU), partial rows (256 and 512 workgroups), and powers of two
 TOKENS = [0, 1, 2, 15, 16, 17, 31, 32, 33, 127, 128, 129, 130, 255, 256, 257, 511, 512, 513, 1535, 1536, 1537, 1552, 1553,
           4095, 6143, 6144, 6145, 8191, 8192, 8193, 12287, 12288, 12289, 16383, 16384, 16385, 24575, 24576, 24577, 30000,
           32767, 32768, 49151, 49152, 49153, 65536, 100000, 1 << 20, (1 << 20) + 1, (1 << 24) - 1, 1 << 24, 1 << 30]
