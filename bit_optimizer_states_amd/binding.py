@@ -19,6 +19,7 @@ QB_OK, QB_EINVAL, QB_EALIGN, QB_EUNSUPPORTED, QB_EHIP, QB_EWORKSPACE, QB_EINIT =
 QB_F32, QB_F16, QB_BF16 = 0, 1, 2
 QB_DYN8, QB_NF4, QB_FP4, QB_UDYN8 = 0, 1, 2, 3
 QB_I32, QB_I64 = 0, 1
+QB_ACT_NONE, QB_ACT_RELU, QB_ACT_GELU, QB_ACT_GELU_TANH, QB_ACT_SILU = range(5)
 QB_ADAMW, QB_ADAM, QB_LION, QB_SGD, QB_RMSPROP, QB_LAMB, QB_LARS = range(7)
 
 _UINT8, _FLOAT32 = torch.uint8, torch.float32
@@ -71,6 +72,15 @@ class qb_matmul_weight(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p), ("c2", ctypes.c_void_p),
                 ("absmax2", ctypes.c_void_p), ("offset", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("N", ctypes.c_int64)]
+
+
+class qb_weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p), ("c2", ctypes.c_void_p),
+                ("absmax2", ctypes.c_void_p), ("offset", ctypes.c_void_p)]
+
+
+class qb_grad(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int)]
 
 
 QB_MATMUL_GROUP_MAX = 8
@@ -148,6 +158,25 @@ def lib():
                         (L.qb_stable_embedding_workspace_bytes, [i64, i64, i64])):
             f.argtypes = args
             f.restype = sz
+        dqp, wp, gp = ctypes.POINTER(qb_dq), ctypes.POINTER(qb_weight), ctypes.POINTER(qb_grad)
+        L.qb_dequant_linear.argtypes = [vp, i32, i64, i64, vp, vp, dqp, i32, i32, i64, vp, i32, i32, vp, vp, vp, vp, sz,
+                                        vp]
+        L.qb_dequant_linear_backward.argtypes = [vp, vp, i32, i64, i64, vp, vp, dqp, i32, i32, i64, i32, vp, vp, vp,
+                                                 i32, i32, vp, sz, vp]
+        L.qb_dequant_gated.argtypes = [vp, i32, i64, i64, wp, wp, i32, i32, i32, i64, i32, vp, vp, vp, vp, sz, vp]
+        L.qb_dequant_gated_backward.argtypes = [vp, vp, vp, i32, i64, i64, wp, wp, i32, i32, i32, i64, i32, vp, vp, vp,
+                                                vp, sz, vp]
+        L.qb_multi_tensor_grad_norm.argtypes = [gp, i32, vp, vp, sz, vp]
+        L.qb_multi_tensor_clip_grads.argtypes = [gp, i32, f64, vp, vp]
+        for f in (L.qb_dequant_linear, L.qb_dequant_linear_backward, L.qb_dequant_gated, L.qb_dequant_gated_backward,
+                  L.qb_multi_tensor_grad_norm, L.qb_multi_tensor_clip_grads):
+            f.restype = ctypes.c_int
+        for f in (L.qb_dequant_linear_workspace_bytes, L.qb_dequant_linear_backward_workspace_bytes,
+                  L.qb_dequant_gated_workspace_bytes, L.qb_dequant_gated_backward_workspace_bytes):
+            f.argtypes = [i32, i64, i64, i64]
+            f.restype = sz
+        L.qb_multi_tensor_grad_norm_workspace_bytes.argtypes = [i32]
+        L.qb_multi_tensor_grad_norm_workspace_bytes.restype = sz
         for f in (L.qb_quantize, L.qb_dequantize, L.qb_adamw8bit_step, L.qb_multi_tensor_step,
                   L.qb_multi_tensor_step_noalloc,
                   L.qb_multi_tensor_dequantize, L.qb_multi_tensor_quantize, L.qb_optimizer8bit_step,
@@ -612,6 +641,182 @@ def qb_stable_embedding_backward(dy, table, ids, gamma, eps, dtable, dgamma, dbe
     _row_call("qb_stable_embedding_backward", d, stream, _at(dy, d), _dtype(dy), _at(table, d), tdt, rows, dim,
               _at(ids, d), _index(ids), n, scale, _at(gamma, d), wdt, eps, padding_id, accumulate, _at(dtable, d),
               _dtype(dtable), _at(dgamma, d), _at(dbeta, d), _at(ws, d), ws.numel() * ws.element_size())
+
+
+# ---------------------------------------------------------------------------
+# 4-bit layers with an epilogue and their gradients; the gradient norm.  As above: the
+# sizes come from the tensors, which share a device, and shapes and dtypes are checked
+# here.  The leading dimensions of the row arrays may have any shape, as long as the
+# numbers of rows agree.
+# ---------------------------------------------------------------------------
+
+def _rows_like(t, m, n, dtype, name):
+    """Checks an [m, n] array (leading dimensions of any shape) of `dtype`; None passes."""
+    if t is not None and (t.dtype != dtype or t.shape[-1] != n or t.numel() != m * n):
+        raise ValueError(f"{name} of {m} rows of {n} elements of the compute dtype expected")
+
+
+def _weight_parts(codes, absmax, dq, code, blocksize, n, k, device):
+    """Checks a 4-bit weight [n, k]."""
+    total = n * k
+    if codes.dtype is not _UINT8 or codes.numel() * 2 < total:
+        raise ValueError("uint8 codes of the whole weight expected")
+    if absmax is not None and (absmax.dtype is not _FLOAT32 or absmax.numel() * blocksize < total):
+        raise ValueError("fp32 absmax of every block expected")
+    if dq is not None and blocksize > 0:
+        _check_dq(dq, -(-total // blocksize), device)
+
+
+def _layer_bias(t, n, xdt, name="bias"):
+    if t is None:
+        return xdt
+    if t.numel() != n:
+        raise ValueError(f"{name} of {n} elements expected")
+    return _dtype(t)
+
+
+def _ws_args(ws, device):
+    return (None, 0) if ws is None else (_at(ws, device), ws.numel() * ws.element_size())
+
+
+def qb_dequant_linear_workspace_bytes(xdt, M, K, N):
+    """xdt: QB_F32/QB_F16/QB_BF16."""
+    return lib().qb_dequant_linear_workspace_bytes(int(xdt), int(M), int(K), int(N))
+
+
+def qb_dequant_linear(x, codes, absmax, code, blocksize, N, y, ws=None, bias=None, act=QB_ACT_NONE, residual=None,
+                      z=None, dq=None, stream=None):
+    """y = act(z) + residual, z = x W^T + bias with W [N, K] as 4-bit codes (absmax, or the nested constants in dq);
+    bias, residual and the output z may be None, residual may be y."""
+    lib()
+    k, dt = x.shape[-1], x.dtype
+    m = x.numel() // k if k else 0
+    d, xdt = x.get_device(), _dtype(x)
+    _rows_like(y, m, N, dt, "y")
+    _rows_like(residual, m, N, dt, "residual")
+    _rows_like(z, m, N, dt, "z")
+    _weight_parts(codes, absmax, dq, code, blocksize, N, k, d)
+    _row_call("qb_dequant_linear", d, stream, _at(x, d), xdt, m, k, _at(codes, d), _at(absmax, d),
+              ctypes.byref(dq) if dq is not None else None, code, blocksize, N, _at(bias, d), _layer_bias(bias, N, xdt),
+              act, _at(residual, d), _at(z, d), _at(y, d), *_ws_args(ws, d))
+
+
+def qb_dequant_linear_backward_workspace_bytes(xdt, M, K, N):
+    return lib().qb_dequant_linear_backward_workspace_bytes(int(xdt), int(M), int(K), int(N))
+
+
+def qb_dequant_linear_backward(dy, codes, absmax, code, blocksize, K, dx, ws=None, act=QB_ACT_NONE, z=None, dz=None,
+                               dbias=None, accumulate=False, dq=None, stream=None):
+    """dx = dz W, dbias = sum of dz over rows, dz = dy act'(z); the outputs dx, dz and dbias may be None."""
+    lib()
+    n, dt = dy.shape[-1], dy.dtype
+    m = dy.numel() // n if n else 0
+    d, xdt = dy.get_device(), _dtype(dy)
+    _rows_like(z, m, n, dt, "z")
+    _rows_like(dz, m, n, dt, "dz")
+    _rows_like(dx, m, K, dt, "dx")
+    if dx is not None:
+        _weight_parts(codes, absmax, dq, code, blocksize, n, K, d)
+    _row_call("qb_dequant_linear_backward", d, stream, _at(dy, d), _at(z, d), xdt, m, K, _at(codes, d), _at(absmax, d),
+              ctypes.byref(dq) if dq is not None else None, code, blocksize, n, act, _at(dx, d), _at(dz, d),
+              _at(dbias, d), _layer_bias(dbias, n, xdt, "dbias"), accumulate, *_ws_args(ws, d))
+
+
+def _gated_weights(gate, up, code, blocksize, n, k, device):
+    """Two (codes, absmax, dq) tuples as qb_weight structures, and blocksize2."""
+    out, sizes = [], set()
+    for codes, absmax, dq in (gate, up):
+        _weight_parts(codes, absmax, dq, code, blocksize, n, k, device)
+        if dq is None:
+            out.append(qb_weight(_at(codes, device), _at(absmax, device), None, None, None))
+        else:
+            sizes.add(dq.blocksize2)
+            out.append(qb_weight(_at(codes, device), _at(absmax, device), dq.codes, dq.absmax2, dq.offset))
+    if len(sizes) > 1:
+        raise ValueError("gate and up must share the nested block size")
+    return out[0], out[1], sizes.pop() if sizes else 0
+
+
+def qb_dequant_gated_workspace_bytes(xdt, M, K, N):
+    return lib().qb_dequant_gated_workspace_bytes(int(xdt), int(M), int(K), int(N))
+
+
+def qb_dequant_gated(x, gate, up, code, blocksize, N, y, ws=None, act=QB_ACT_SILU, gate_out=None, up_out=None,
+                     stream=None):
+    """y = act(x Wg^T) (x Wu^T); gate and up: (codes, absmax, dq) of Wg, Wu [N, K] (absmax None with a qb_dq, dq None
+    without).  gate_out and up_out (may be None) take the two products."""
+    lib()
+    k, dt = x.shape[-1], x.dtype
+    m = x.numel() // k if k else 0
+    d = x.get_device()
+    for t, name in ((y, "y"), (gate_out, "gate_out"), (up_out, "up_out")):
+        _rows_like(t, m, N, dt, name)
+    g, u, b2 = _gated_weights(gate, up, code, blocksize, N, k, d)
+    _row_call("qb_dequant_gated", d, stream, _at(x, d), _dtype(x), m, k, ctypes.byref(g), ctypes.byref(u), code,
+              blocksize, b2, N, act, _at(gate_out, d), _at(up_out, d), _at(y, d), *_ws_args(ws, d))
+
+
+def qb_dequant_gated_backward_workspace_bytes(xdt, M, K, N):
+    return lib().qb_dequant_gated_backward_workspace_bytes(int(xdt), int(M), int(K), int(N))
+
+
+def qb_dequant_gated_backward(dy, gate_out, up_out, gate, up, code, blocksize, K, dx, ws=None, act=QB_ACT_SILU,
+                              dgate=None, dup=None, stream=None):
+    """dx = dg Wg + du Wu, dg = dy u act'(g), du = dy act(g); the outputs dx, dgate and dup may be None."""
+    lib()
+    n, dt = dy.shape[-1], dy.dtype
+    m = dy.numel() // n if n else 0
+    d = dy.get_device()
+    for t, name in ((gate_out, "gate_out"), (up_out, "up_out"), (dgate, "dgate"), (dup, "dup")):
+        _rows_like(t, m, n, dt, name)
+    _rows_like(dx, m, K, dt, "dx")
+    g, u, b2 = _gated_weights(gate, up, code, blocksize, n, K, d)
+    _row_call("qb_dequant_gated_backward", d, stream, _at(dy, d), _at(gate_out, d), _at(up_out, d), _dtype(dy), m, K,
+              ctypes.byref(g), ctypes.byref(u), code, blocksize, b2, n, act, _at(dx, d), _at(dgate, d), _at(dup, d),
+              *_ws_args(ws, d))
+
+
+def grad_table(grads):
+    """ctypes array of qb_grad from tensors, or from (g, out) pairs for clipping out of place (a tensor alone is clipped
+    in place).  A program whose gradients stay where they are builds it once."""
+    arr = (qb_grad * max(len(grads), 1))()
+    device = None
+    for i, entry in enumerate(grads):
+        g, out = entry if isinstance(entry, (tuple, list)) else (entry, entry)
+        if device is None:
+            device = g.get_device()
+        if out.dtype != g.dtype or out.numel() != g.numel():
+            raise ValueError("out like its gradient expected")
+        arr[i] = qb_grad(_at(g, device), _at(out, device), g.numel(), _dtype(g))
+    return arr
+
+
+def qb_multi_tensor_grad_norm_workspace_bytes(count):
+    return lib().qb_multi_tensor_grad_norm_workspace_bytes(int(count))
+
+
+def _norm_of_one(norm):
+    if norm.dtype is not _FLOAT32 or norm.numel() != 1:
+        raise ValueError("norm: one fp32 value expected")
+    return norm.get_device()
+
+
+def qb_multi_tensor_grad_norm(table, count, norm, ws, stream=None):
+    """norm[0] = the norm of all gradients of `table` (grad_table)."""
+    lib()
+    d = _norm_of_one(norm)
+    if count > len(table):
+        raise ValueError("a table of count gradients expected")
+    _row_call("qb_multi_tensor_grad_norm", d, stream, table, count, _at(norm, d), *_ws_args(ws, d))
+
+
+def qb_multi_tensor_clip_grads(table, count, max_norm, norm, stream=None):
+    """out = g * min(1, max_norm / (norm[0] + 1e-6)) for every gradient of `table` (grad_table)."""
+    lib()
+    d = _norm_of_one(norm)
+    if count > len(table):
+        raise ValueError("a table of count gradients expected")
+    _row_call("qb_multi_tensor_clip_grads", d, stream, table, count, max_norm, _at(norm, d))
 
 
 def qb_code_table_bytes():

@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libqb.so")
 # the two optimizer sources first: they take longest, and compile in parallel
 SOURCES = ["qb_optim.hip", "qb_optim_uv.hip", "qb_tables.cpp", "qb_api.cpp", "qb_runtime.hip", "qb_quant.hip",
            "qb_dequant.hip", "qb_codes.hip", "qb_matmul.hip", "qb_layers_api.cpp", "qb_embedding.hip", "qb_norm.hip",
-           "qb_stable.hip", "qb_stable_grad.hip"]
+           "qb_stable.hip", "qb_stable_grad.hip", "qb_linear_api.cpp", "qb_linear.hip", "qb_gemm.hip", "qb_linear_grad.hip",
+           "qb_clip.hip"]
 ARCH = os.environ.get("QB_OFFLOAD_ARCH", "gfx950")
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", "-Wno-unused-function",

@@ -1,0 +1,388 @@
+// qb_gemm.hip -- the tiled matrix product behind the 4-bit layers of many rows, and the
+// kernels that lay its weights out.
+//
+// From a few hundred rows on the products bound the layer, not the weights: each
+// weight is dequantized once into a workspace in the compute dtype (N K elements written
+// and read back, mostly through the last-level cache), and C = A B^T runs at the matrix
+// instructions' rate, with the layer's epilogue on the binary32 sums in registers.
+#include "qb_linear.h"
+#include "qb_mm_device.h"
+#include "qb_epilogue.h"
+
+namespace qb {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// weights into the compute dtype
+// ---------------------------------------------------------------------------
+
+template <bool DQ>
+__device__ __forceinline__ void stage_code_tables(float* s_val, float* s_dyn, int code4, const QbTables* tab)
+{
+    if (threadIdx.x < 16) s_val[threadIdx.x] = (code4 == 0 ? tab->nf4 : tab->fp4)[threadIdx.x];
+    if constexpr (DQ) {
+        if (threadIdx.x < 256) s_dyn[threadIdx.x] = tab->dyn8[threadIdx.x];
+    }
+}
+
+// The constant of block blk.
+template <bool DQ>
+__device__ __forceinline__ float block_constant(const Weight4& w, int64_t blk, int log2B2, const float* s_dyn, float mu)
+{
+    if constexpr (DQ) return s_dyn[gld<uint8_t>(w.c2 + blk)] * gld<float>(w.absmax2 + (blk >> log2B2)) + mu;
+    else return gld<float>(w.absmax + blk);
+}
+
+struct Weights2 {
+    Weight4 w[2];
+};
+
+template <int XDT>
+__device__ __forceinline__ void store_frag(void* p, const Frag<XDT>& f)
+{
+    if constexpr (XDT == DT_F32) {
+        gst<f32x4>(p, f32x4{f.w[0], f.w[1], f.w[2], f.w[3]});
+        gst<f32x4>(static_cast<char*>(p) + 16, f32x4{f.w[4], f.w[5], f.w[6], f.w[7]});
+    } else {
+        gst<u32x4>(p, u32x4{f.w[0], f.w[1], f.w[2], f.w[3]});
+    }
+}
+
+// A thread takes 8 weights at a time: 4 bytes of codes, 16 bytes out (consecutive lanes next
+// to each other).  A unit of work is 256 threads' worth of a row.
+template <int XDT, bool DQ>
+__global__ __launch_bounds__(256) void k_unpack(const Weights2 ws, int count, int64_t N, int64_t K, int64_t pitch,
+                                                const Weight4Format f, void* __restrict__ out,
+                                                const QbTables* __restrict__ tab)
+{
+    constexpr int ES = XDT == DT_F32 ? 4 : 2;
+    __shared__ float s_val[16];
+    __shared__ float s_dyn[DQ ? 256 : 1];
+    stage_code_tables<DQ>(s_val, s_dyn, f.code4, tab);
+    __syncthreads();
+    const int64_t per_row = (K + 2047) / 2048, units = per_row * N * count;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t row = u / per_row;
+        const int64_t k = (u - row * per_row) * 2048 + threadIdx.x * 8;
+        if (k >= K) continue;
+        const int which = count == 2 && row >= N ? 1 : 0;
+        const Weight4 w = ws.w[which];
+        const int64_t n = row - which * N, e = n * K + k;
+        const int64_t to = count == 2 ? n / 16 * 32 + which * 16 + n % 16 : n;
+        const float mu = DQ ? gld<float>(w.offset) : 0.0f;
+        Frag<XDT> v;
+        dequant_frag<XDT>(gld<uint32_t>(w.codes + e / 2), block_constant<DQ>(w, e >> f.log2B, f.log2B2, s_dyn, mu),
+                          s_val, v);
+        store_frag<XDT>(static_cast<char*>(out) + (to * pitch + k) * ES, v);
+    }
+}
+
+// Transposed: a workgroup takes 64 rows n and 128 columns k, 8 weights a thread at a time
+// into LDS, and writes rows k of 64 n.
+template <int XDT, bool DQ>
+__global__ __launch_bounds__(256) void k_unpack_transposed(const Weights2 ws, int count, int64_t N, int64_t K,
+                                                           int64_t pitch, const Weight4Format f, void* __restrict__ out,
+                                                           const QbTables* __restrict__ tab)
+{
+    constexpr int ES = XDT == DT_F32 ? 4 : 2;
+    constexpr int LP = 64 * ES + (XDT == DT_F32 ? 16 : 16);       // bytes of an LDS row of 64 n
+    __shared__ __attribute__((aligned(16))) char s_t[128 * LP];
+    __shared__ float s_val[16];
+    __shared__ float s_dyn[DQ ? 256 : 1];
+    stage_code_tables<DQ>(s_val, s_dyn, f.code4, tab);
+    __syncthreads();
+    const int64_t np = pitch / count, tn = np / 64 + (np % 64 ? 1 : 0), tk = (K + 127) / 128, tiles = tn * tk * count;
+    const int tid = threadIdx.x;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t tw = t / tk, k0 = (t - tw * tk) * 128;
+        const int which = (int)(tw / tn);
+        const int64_t n0 = (tw - which * tn) * 64;
+        const Weight4 w = ws.w[which];
+        const float mu = DQ ? gld<float>(w.offset) : 0.0f;
+        // lane: 8 columns k, rows 2 q and 2 q + 1 of the tile, 16 row pairs at a time
+        const int kl = (tid & 15) * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int pr = (tid >> 4) + 16 * i;
+            Frag<DT_F32> v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = n0 + 2 * pr + h, e = n * K + k0 + kl;
+                if (n < N && k0 + kl < K) {
+                    dequant_frag<DT_F32>(gld<uint32_t>(w.codes + e / 2),
+                                         block_constant<DQ>(w, e >> f.log2B, f.log2B2, s_dyn, mu), s_val, v[h]);
+                } else {
+                    frag_zero<DT_F32>(v[h]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                char* const p = s_t + (kl + j) * LP + 2 * pr * ES;
+                if constexpr (XDT == DT_F32) {
+                    reinterpret_cast<float*>(p)[0] = v[0].w[j];
+                    reinterpret_cast<float*>(p)[1] = v[1].w[j];
+                } else {
+                    *reinterpret_cast<uint32_t*>(p) = pack_pair<XDT>(v[0].w[j], v[1].w[j]);
+                }
+            }
+        }
+        __syncthreads();
+        constexpr int CPR = 64 * ES / 16;                    // 16-byte chunks of a row
+#pragma unroll
+        for (int i = 0; i < 128 * CPR / 256; ++i) {
+            const int o = tid + 256 * i, row = o / CPR, c = o % CPR;
+            if (k0 + row < K && n0 + c * (16 / ES) < np)
+                gst<u32x4>(static_cast<char*>(out) + ((k0 + row) * pitch + which * np + n0) * ES + 16 * c,
+                           *reinterpret_cast<const u32x4*>(s_t + row * LP + 16 * c));
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// C = A B^T
+// ---------------------------------------------------------------------------
+//
+// A workgroup of WM x WN waves computes BM rows (of A) by BN columns (rows of B), each
+// wave BM / WM by BN / WN of them in 16x16 tiles.  A step is 128 bytes of every row (64
+// 16-bit elements, 32 binary32 ones), staged in LDS by direct global-to-LDS loads of 16
+// bytes a lane, two buffers in turn: the next step loads while one is multiplied.  16-byte
+// chunk p of an LDS row holds chunk p ^ (row % 8) of the operand's row, so that the rows
+// of one fragment lie in different banks.  A fragment is one chunk a lane: row lane % 16,
+// chunk 4 kk + lane / 16; with binary32 its four elements go to four instructions, the same
+// k order in both operands.  B's fragment is the first operand, so that a lane's four sums
+// are four neighbouring columns of C: one access of 8 (16) bytes.
+
+struct GemmParams {
+    GemmArgs g;
+    Epilogue e;
+    int32_t steps, steps0, half, tiles_m, tiles_n;
+};
+
+template <int XDT>
+__device__ __forceinline__ void mma_chunk(const u32x4& a, const u32x4& b, f32x4& acc)
+{
+    if constexpr (XDT == DT_BF16) {
+        bf16x8 av, bv;
+        __builtin_memcpy(&av, &a, 16);
+        __builtin_memcpy(&bv, &b, 16);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, acc, 0, 0, 0);
+    } else if constexpr (XDT == DT_F16) {
+        f16x8 av, bv;
+        __builtin_memcpy(&av, &a, 16);
+        __builtin_memcpy(&bv, &b, 16);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bv, acc, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(ffrom(a[i]), ffrom(b[i]), acc, 0, 0, 0);
+    }
+}
+
+template <int XDT, int BM, int BN, int WM, int WN, bool GATED>
+__global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
+{
+    constexpr int NW = WM * WN;                        // waves
+    constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16x16 tiles of a wave
+    constexpr int A_PER = BM / 8 / NW, B_PER = BN / 8 / NW;   // loads (8 rows each) of a wave and step
+    static_assert(A_PER * NW * 8 == BM && B_PER * NW * 8 == BN && (!GATED || TN % 2 == 0), "whole loads");
+    constexpr int BUF = (BM + BN) * 128;
+    __shared__ __attribute__((aligned(16))) char s_ab[2 * BUF];   // two buffers, A's rows then B's
+    constexpr int ES = XDT == DT_F32 ? 4 : 2;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int r = lane & 15, g = lane >> 4;
+
+    // each XCD takes a contiguous range of tiles, numbered so that 8 rows of tiles are
+    // walked column by column: the tiles that run together share A and B in its L2
+    const int64_t tile = tile_of<true>(blockIdx.x, gridDim.x);
+    const int64_t band = tile / (8 * p.tiles_n), in_band = tile - band * 8 * p.tiles_n;
+    const int rows_here = p.tiles_m - band * 8 < 8 ? (int)(p.tiles_m - band * 8) : 8;
+    const int64_t m0 = (band * 8 + in_band % rows_here) * BM, n0 = in_band / rows_here * BN;
+
+    // rows past the end read the last row (their sums are never stored)
+    uint32_t a_off[A_PER], b_off[B_PER], chunk_hi;
+    {
+        const int row8 = lane >> 3, c = (lane & 7) ^ row8;
+        chunk_hi = c >= 4 ? 64u : 0u;
+#pragma unroll
+        for (int i = 0; i < A_PER; ++i) {
+            int64_t row = (i * NW + wave) * 8 + row8;
+            row = m0 + row < p.g.M ? row : p.g.M - 1 - m0;
+            a_off[i] = (uint32_t)(row * p.g.lda * ES + c * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < B_PER; ++i) {
+            int64_t row = (i * NW + wave) * 8 + row8;
+            row = n0 + row < p.g.R ? row : p.g.R - 1 - n0;
+            b_off[i] = (uint32_t)(row * p.g.ldb * ES + c * 16);
+        }
+    }
+    const char* const a0 = static_cast<const char*>(p.g.a0) + m0 * p.g.lda * ES;
+    const char* const a1 = static_cast<const char*>(p.g.a1) + m0 * p.g.lda * ES;
+    const char* const b0 = static_cast<const char*>(p.g.b) + n0 * p.g.ldb * ES;
+
+    auto load_step = [&](int s) {
+        char* const dst = s_ab + (s & 1) * BUF;
+        const char* const as = s < p.steps0 ? a0 + (int64_t)s * 128 : a1 + (int64_t)(s - p.steps0) * 128;
+        const char* const bs = b0 + (int64_t)s * 128;
+        // a last step of half the length: its upper chunks are read again from the lower half
+        const uint32_t back = p.half && s + 1 == p.steps ? chunk_hi : 0u;
+#pragma unroll
+        for (int i = 0; i < A_PER; ++i)
+            __builtin_amdgcn_global_load_lds((gptr_t)(as + (a_off[i] - back)), (lptr_t)(dst + (i * NW + wave) * 1024),
+                                             16, 0, 0);
+#pragma unroll
+        for (int i = 0; i < B_PER; ++i)
+            __builtin_amdgcn_global_load_lds((gptr_t)(bs + (b_off[i] - back)),
+                                             (lptr_t)(dst + BM * 128 + (i * NW + wave) * 1024), 16, 0, 0);
+    };
+
+    f32x4 acc[TN][TM];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int t = 0; t < TM; ++t) acc[j][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int a_row = (wm * (BM / WM) + r) * 128, b_row = BM * 128 + (wn * (BN / WN) + r) * 128;
+    load_step(0);
+    for (int s = 0; s < p.steps; ++s) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();                               // step s has landed; the other buffer is free
+        if (s + 1 < p.steps) load_step(s + 1);
+        const char* const buf = s_ab + (s & 1) * BUF;
+        const int halves = p.half && s + 1 == p.steps ? 1 : 2;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            if (kk >= halves) break;
+            const int c = ((4 * kk + g) ^ (r & 7)) * 16;
+            u32x4 bf[TN], af[TM];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) bf[j] = *reinterpret_cast<const u32x4*>(buf + b_row + j * 16 * 128 + c);
+#pragma unroll
+            for (int t = 0; t < TM; ++t) af[t] = *reinterpret_cast<const u32x4*>(buf + a_row + t * 16 * 128 + c);
+#pragma unroll
+            for (int t = 0; t < TM; ++t)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) mma_chunk<XDT>(bf[j], af[t], acc[j][t]);
+        }
+    }
+
+    // lane: column r of the 16x16 tile is C's row, its elements 4 g + i are C's columns
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+        const int64_t m = m0 + wm * (BM / WM) + 16 * t + r;
+        if (m >= p.g.M) continue;
+        if constexpr (GATED) {
+            const int64_t nb = (n0 + wn * (BN / WN)) / 2 + 4 * g;
+#pragma unroll
+            for (int j = 0; j < TN; j += 2) finish_gated4<XDT>(p.e, m, nb + 8 * j, acc[j][t], acc[j + 1][t]);
+        } else {
+            const int64_t nb = n0 + wn * (BN / WN) + 4 * g;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) finish_linear4<XDT>(p.e, m, nb + 16 * j, acc[j][t]);
+        }
+    }
+}
+
+// `rows` rows of an array of `width` elements further on.
+const void* further(const void* p, int64_t rows, int64_t width, int es)
+{
+    return p ? static_cast<const char*>(p) + rows * width * es : nullptr;
+}
+void* further(void* p, int64_t rows, int64_t width, int es)
+{
+    return p ? static_cast<char*>(p) + rows * width * es : nullptr;
+}
+
+// One launch, or several of whole tiles where a grid would not hold them.
+template <int XDT, int BM, int BN, int WM, int WN, bool GATED>
+hipError_t gemm_as(GemmParams p, hipStream_t s)
+{
+    constexpr int ES = XDT == DT_F32 ? 4 : 2;
+    p.tiles_n = (int)((p.g.R + BN - 1) / BN);
+    const int64_t M = p.g.M, most = ((int64_t(1) << 21) / p.tiles_n) * BM;
+    const GemmParams all = p;
+    for (int64_t m = 0; m < M; m += most) {
+        p.g.M = M - m < most ? M - m : most;
+        p.tiles_m = (int)((p.g.M + BM - 1) / BM);
+        p.g.a0 = further(all.g.a0, m, p.g.lda, ES);
+        p.g.a1 = further(all.g.a1, m, p.g.lda, ES);
+        p.e.residual = further(all.e.residual, m, p.e.N, ES);
+        p.e.z = further(all.e.z, m, p.e.N, ES);
+        p.e.u = further(all.e.u, m, p.e.N, ES);
+        p.e.y = further(all.e.y, m, p.e.N, ES);
+        const hipError_t e = launch_kernel_nt(k_gemm<XDT, BM, BN, WM, WN, GATED>, p.tiles_m * p.tiles_n, 64 * WM * WN, s, p);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <int XDT, bool GATED>
+hipError_t gemm_tiles(const GemmParams& p, hipStream_t s)
+{
+    if ((p.g.M + 255) / 256 * ((p.g.R + 255) / 256) >= 200) return gemm_as<XDT, 256, 256, 2, 4, GATED>(p, s);
+    return gemm_as<XDT, 128, 128, 2, 4, GATED>(p, s);
+}
+
+template <int XDT, bool DQ>
+hipError_t unpack_as(const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
+                     bool transposed, hipStream_t s)
+{
+    const QbTables* tab = device_tables();
+    if (!tab) return hipErrorNotInitialized;
+    Weights2 ws{{w[0], w[count - 1]}};
+    if (transposed) {
+        const int64_t np = gemm_pitch(XDT, N), tiles = (np + 63) / 64 * ((K + 127) / 128) * count;
+        const int grid = persistent_grid(k_unpack_transposed<XDT, DQ>, tiles);
+        return launch_kernel(k_unpack_transposed<XDT, DQ>, grid, s, ws, count, N, K, np * count, f, out, tab);
+    }
+    const int64_t units = (K + 2047) / 2048 * N * count;
+    const int grid = persistent_grid(k_unpack<XDT, DQ>, units);
+    return launch_kernel(k_unpack<XDT, DQ>, grid, s, ws, count, N, K, gemm_pitch(XDT, K), f, out, tab);
+}
+
+hipError_t unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
+                  bool transposed, hipStream_t s)
+{
+    switch (xdt) {
+    case DT_F32:
+        return f.nested ? unpack_as<DT_F32, true>(w, count, N, K, f, out, transposed, s)
+                        : unpack_as<DT_F32, false>(w, count, N, K, f, out, transposed, s);
+    case DT_F16:
+        return f.nested ? unpack_as<DT_F16, true>(w, count, N, K, f, out, transposed, s)
+                        : unpack_as<DT_F16, false>(w, count, N, K, f, out, transposed, s);
+    default:
+        return f.nested ? unpack_as<DT_BF16, true>(w, count, N, K, f, out, transposed, s)
+                        : unpack_as<DT_BF16, false>(w, count, N, K, f, out, transposed, s);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
+                         hipStream_t s)
+{
+    return unpack(xdt, w, count, N, K, f, out, false, s);
+}
+
+hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f,
+                                    void* out, hipStream_t s)
+{
+    return unpack(xdt, w, count, N, K, f, out, true, s);
+}
+
+hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, hipStream_t s)
+{
+    const int64_t step = gemm_step(xdt);
+    GemmParams p{g, e, (int32_t)((g.len + step - 1) / step), (int32_t)((g.len0 + step - 1) / step),
+                 g.len % step ? 1 : 0, 0, 0};
+    switch (xdt) {
+    case DT_F32: return gated ? gemm_tiles<DT_F32, true>(p, s) : gemm_tiles<DT_F32, false>(p, s);
+    case DT_F16: return gated ? gemm_tiles<DT_F16, true>(p, s) : gemm_tiles<DT_F16, false>(p, s);
+    default: return gated ? gemm_tiles<DT_BF16, true>(p, s) : gemm_tiles<DT_BF16, false>(p, s);
+    }
+}
+
+}  // namespace qb

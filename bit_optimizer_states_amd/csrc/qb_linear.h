@@ -1,0 +1,88 @@
+// qb_linear.h -- internal launchers of the 4-bit layers with a fused epilogue: the linear
+// layer (bias, activation, residual), the gated block (two projections, activation,
+// product) and their gradients.  Argument checks are done by the callers in
+// qb_linear_api.cpp.
+#pragma once
+#include "qb_launch.h"
+
+namespace qb {
+
+// A weight [N, K] in 4 bits: codes and block constants, plain (absmax) or nested (c2,
+// absmax2, offset).
+struct Weight4 {
+    const uint8_t* codes;
+    const float* absmax;
+    const uint8_t* c2;
+    const float* absmax2;
+    const float* offset;
+};
+
+// The code and block sizes that the weights of a call share.
+struct Weight4Format {
+    int32_t log2B, log2B2, code4, nested;
+};
+
+// What becomes of a sum z of products, in binary32 and rounded once per output.
+//   linear: z += bias (each optional); z out; y = act(z) + residual.
+//   gated:  the sums g and u of one column: g, u out (z, u); y = act(g) * u.
+// y [M, N], as are z, u and residual (which may be y itself).
+struct Epilogue {
+    const void* bias;        // [N] of dtype bias_dt
+    const void* residual;
+    void* z;
+    void* u;
+    void* y;
+    int64_t N;
+    int32_t bias_dt, act;
+};
+
+// Rows of x up to which a wave per 16 weight rows multiplies straight from the codes.
+constexpr int64_t kRowsMax = 64;
+
+// y = epilogue(x W^T) for up to kRowsMax rows of x (count 1: linear, 2: gated).
+hipError_t launch_linear_rows(int xdt, const void* x, int64_t M, int64_t K, const Weight4* w, int count,
+                              const Weight4Format& f, const Epilogue& e, hipStream_t s);
+
+// Elements of a step of the tiled product, and of the multiples that its operands' rows
+// are padded to: 128 bytes.
+constexpr int64_t gemm_step(int dt) { return dt == 0 ? 32 : 64; }
+constexpr int64_t gemm_pitch(int dt, int64_t k) { return (k + gemm_step(dt) - 1) / gemm_step(dt) * gemm_step(dt); }
+// Rows of the two weights of a gated block, dealt in groups of 16: rows 16 g .. 16 g + 15
+// of the first, then of the second.
+constexpr int64_t gated_rows(int64_t n) { return (n + 15) / 16 * 32; }
+
+// Weights in the compute dtype: out[row of n][k] of pitch gemm_pitch(K), for a gated block
+// the rows of both dealt as above.
+hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
+                         hipStream_t s);
+// The same transposed: out[k][n], for two weights next to each other (columns n of the
+// second at gemm_pitch(N) + n); the pitch is count * gemm_pitch(N), its padding zero.
+hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f,
+                                    void* out, hipStream_t s);
+
+// C = epilogue(A B^T).  A [M, len] in one or two pieces of columns (a0: the first len0, a1
+// the others; both of `lda` elements a row, 16-byte aligned rows), B [R, len] of ldb
+// elements a row.  len0 is a multiple of the step unless it is len, len of half the step.
+struct GemmArgs {
+    const void* a0;
+    const void* a1;
+    const void* b;
+    int64_t M, R, len0, len, lda, ldb;
+};
+hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, hipStream_t s);
+
+// dz = dy act'(z) [M, N] into `dz` of pitch `pitch` (its padding zero; nullptr: not
+// wanted) and into `dz_out` [M, N] (nullptr: not wanted), and per slice of rows the sums of
+// dz over its rows, part[slice][N] (nullptr: not wanted).  z == nullptr: dz = dy.
+hipError_t launch_linear_dz(int xdt, const void* dy, const void* z, int act, int64_t M, int64_t N, void* dz,
+                            int64_t pitch, void* dz_out, float* part, int slices, hipStream_t s);
+int linear_dz_slices(int64_t M, int64_t N);
+// db[n] = the sum of part[.][n] in order (plus what it holds).
+hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool accumulate, void* db, int bias_dt,
+                           hipStream_t s);
+// dg = dh u act'(g) and du = dh act(g) into `dz` ([M, pitch] each, du behind dg; nullptr:
+// not wanted) and into dg_out, du_out [M, N] (nullptr: not wanted).
+hipError_t launch_gated_dz(int xdt, const void* dh, const void* g, const void* u, int act, int64_t M, int64_t N,
+                           void* dz, int64_t pitch, void* dg_out, void* du_out, hipStream_t s);
+
+}  // namespace qb

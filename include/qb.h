@@ -1,9 +1,10 @@
 /*
  * qb.h -- C ABI of libqb: block-wise dynamic quantization, nested quantization
  * of the block constants, the fused 8-bit AdamW step and its sibling 8-bit
- * optimizers (with paged states), user codes, the product of a 4-bit layer, and
- * the stable embedding layer (embedding lookup, layer norm, their gradients),
- * for AMD Instinct MI355X (gfx950).
+ * optimizers (with paged states), user codes, the product of a 4-bit layer, the
+ * stable embedding layer (embedding lookup, layer norm, their gradients), and the
+ * training step around a 4-bit layer (linear and gated layers with their
+ * gradients, the global gradient norm), for AMD Instinct MI355X (gfx950).
  *
  * The method: a tensor is cut into blocks of `blocksize` consecutive elements;
  * every block is scaled by its own absolute maximum and each scaled value is
@@ -720,6 +721,149 @@ qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void*
                                        int32_t accumulate, void* dtable, qb_dtype ddt, void* dgamma, void* dbeta,
                                        void* ws, size_t ws_bytes, void* stream);
 size_t qb_stable_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim);
+
+/*
+ * The 4-bit layers: the product of qb_dequant_matmul with what a layer does to it, in one
+ * kernel (the layers whose weights the pages hold in 4 bits: page "Quantize 🤗 Transformers
+ * models", section Using NF4), and the gradients that fine-tuning through
+ * frozen 4-bit weights takes (page "bitsandbytes - Quantização de LLM", section on QLoRA;
+ * page "Bitsandbytes", section QLoRA: Hesaplama veri türü).  Common to these calls:
+ *   - W is the weight [N, K] as qb_dequantize gives it in the compute dtype xdt; codes,
+ *     absmax, dq, code, blocksize as for qb_dequant_matmul.  x, y and every other [M, .]
+ *     array is row-major and dense, of dtype xdt, 16-byte aligned.
+ *   - K is a positive multiple of 32; K, N < 2^21; M < 2^31.  M == 0 is a no-op (but see the
+ *     bias's gradient).
+ *   - Products of two xdt values are summed in binary32, in an order of the kernel's own that
+ *     depends on the sizes alone (the same bits on every run); bias, activation, product and
+ *     residual are binary32 too, and each output is rounded once.  NaN and infinities
+ *     propagate as in the formulas, into the rows that they enter.
+ *   - Outputs must not overlap inputs or each other, unless said otherwise.
+ *   - ws: device workspace, 16-byte aligned, of the *_workspace_bytes size (0: none, ws may be
+ *     NULL), which never shrinks when M, K or N grows.  It holds nothing between calls and
+ *     must not be shared by calls that may overlap in time (two captured graphs that run at
+ *     once among them).
+ *   - No memory operations, so the calls may be captured; the first call on a device that
+ *     needs the library's constant tables uploads them: make one before.
+ */
+typedef enum {
+    QB_ACT_NONE = 0,
+    QB_ACT_RELU = 1,          /* max(z, 0), derivative 0 at 0 */
+    QB_ACT_GELU = 2,          /* z P(z), P the normal distribution */
+    QB_ACT_GELU_TANH = 3,     /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    QB_ACT_SILU = 4           /* z / (1 + e^-z) */
+} qb_act;
+
+/* A 4-bit weight of a gated block: a plain one gives absmax and leaves c2, absmax2, offset
+ * NULL; a nested one gives these (the qb_dq fields) and absmax NULL. */
+typedef struct {
+    const uint8_t* codes;
+    const float*   absmax;
+    const uint8_t* c2;
+    const float*   absmax2;
+    const float*   offset;
+} qb_weight;
+
+/*
+ * qb_dequant_linear -- z = x W^T + bias,  y = act(z) + residual.
+ *   x         [M, K].
+ *   bias      [N] of dtype bdt (QB_F32 or xdt, else QB_EUNSUPPORTED), or NULL.
+ *   residual  [M, N], or NULL; may be y itself.
+ *   z         [M, N] out, or NULL: the pre-activation, which the gradient takes.
+ *   y         [M, N] out.
+ * Up to 64 rows one kernel reads the codes and no workspace is needed; from 65 rows on the
+ * weights are dequantized into ws first (two kernels).  N == 0 is a no-op.
+ */
+qb_status qb_dequant_linear(const void* x, qb_dtype xdt, int64_t M, int64_t K, const uint8_t* codes,
+                            const float* absmax, const qb_dq* dq, qb_code code, int32_t blocksize, int64_t N,
+                            const void* bias, qb_dtype bdt, qb_act act, const void* residual, void* z, void* y,
+                            void* ws, size_t ws_bytes, void* stream);
+size_t qb_dequant_linear_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int64_t N);
+
+/*
+ * qb_dequant_linear_backward -- dz = dy act'(z),  dx = dz W,  dbias = sum over rows of dz.
+ *   dy      [M, N] (the residual's gradient is dy itself).
+ *   z       [M, N] as qb_dequant_linear wrote it; not looked at for QB_ACT_NONE.
+ *   dx      [M, K] out, dz [M, N] out (the gradient that an adapter beside W takes), dbias [N]
+ *           of dtype bdt (QB_F32 or xdt) out: each may be NULL (not wanted).
+ *   accumulate   dbias is added to what it holds (in binary32, rounded once); with M == 0 it
+ *           is left as it is, and zero otherwise.
+ * dz is rounded to xdt before it is multiplied by W (the matrix instructions take
+ * that type; for binary32 nothing is rounded); dbias sums the unrounded dz.  N >= 1.
+ * The workspace is needed for dx and dbias.  Up to four kernels.
+ */
+qb_status qb_dequant_linear_backward(const void* dy, const void* z, qb_dtype xdt, int64_t M, int64_t K,
+                                     const uint8_t* codes, const float* absmax, const qb_dq* dq, qb_code code,
+                                     int32_t blocksize, int64_t N, qb_act act, void* dx, void* dz, void* dbias,
+                                     qb_dtype bdt, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+size_t qb_dequant_linear_backward_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int64_t N);
+
+/*
+ * qb_dequant_gated -- the gated feed-forward block's two projections, activation and product:
+ *   g = x Wg^T,  u = x Wu^T,  y = act(g) u.
+ *   gate, up           host: the weights Wg, Wu [N, K]; both plain or both nested (else
+ *                      QB_EUNSUPPORTED); code, blocksize and blocksize2 (nested only) are shared.
+ *   gate_out, up_out   [M, N] out, each may be NULL: g and u, which the gradient takes.
+ *   y                  [M, N] out.
+ * One kernel up to 64 rows, two from there on.  N == 0 is a no-op.
+ */
+qb_status qb_dequant_gated(const void* x, qb_dtype xdt, int64_t M, int64_t K, const qb_weight* gate,
+                           const qb_weight* up, qb_code code, int32_t blocksize, int32_t blocksize2, int64_t N,
+                           qb_act act, void* gate_out, void* up_out, void* y, void* ws, size_t ws_bytes, void* stream);
+size_t qb_dequant_gated_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int64_t N);
+
+/*
+ * qb_dequant_gated_backward -- dg = dy u act'(g),  du = dy act(g),  dx = dg Wg + du Wu.
+ *   dy, gate_out, up_out   [M, N]: the gradient of y; g and u as qb_dequant_gated wrote them.
+ *   dx          [M, K] out, dgate, dup [M, N] out: each may be NULL (not wanted).
+ * dg and du are rounded to xdt before they are multiplied.  N >= 1.  The workspace is needed
+ * for dx.  Up to three kernels.
+ */
+qb_status qb_dequant_gated_backward(const void* dy, const void* gate_out, const void* up_out, qb_dtype xdt, int64_t M,
+                                    int64_t K, const qb_weight* gate, const qb_weight* up, qb_code code,
+                                    int32_t blocksize, int32_t blocksize2, int64_t N, qb_act act, void* dx,
+                                    void* dgate, void* dup, void* ws, size_t ws_bytes, void* stream);
+size_t qb_dequant_gated_backward_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int64_t N);
+
+/*
+ * The global gradient norm, and clipping by it, before an optimizer step (the 8-bit
+ * optimizers are drop-in replacements in a training loop: page "bitsandbytes - Quantização de
+ * LLM", section Workflow 3).
+ * One gradient: n values of its own dtype at g and (clipping) out; out may be g.  Both may
+ * begin at any element, as views of a bucket do.  n < 2^33; n == 0 is skipped.
+ */
+typedef struct {
+    const void* g;
+    void*       out;
+    int64_t     n;
+    qb_dtype    dtype;
+} qb_grad;
+
+/*
+ * qb_multi_tensor_grad_norm -- norm[0] = sqrt(sum over gradients and elements of g^2): squares
+ * and sums in binary64, rounded once to binary32.
+ *   grads   host array of `count` descriptors (read during the call only).
+ *   norm    [1] fp32 out, 16-byte aligned; 0 without gradients.
+ *   ws      device workspace of qb_multi_tensor_grad_norm_workspace_bytes(count) bytes, 16-byte
+ *           aligned; holds nothing between calls.
+ * The same bits on every run.  One launch per 120 gradients and one more (a few small
+ * gradients: one in all); no memory operations, so the call may be captured.  Several
+ * ranks' norms of their own gradients make the global one as sqrt(sum of norm^2).
+ */
+qb_status qb_multi_tensor_grad_norm(const qb_grad* grads, int32_t count, float* norm, void* ws, size_t ws_bytes,
+                                    void* stream);
+size_t qb_multi_tensor_grad_norm_workspace_bytes(int32_t count);
+
+/*
+ * qb_multi_tensor_clip_grads -- out = g * s with s = min(1, max_norm / (norm[0] + 1e-6)), in
+ * binary64 and rounded to binary32; one binary32 product, rounded once.
+ *   max_norm   finite, >= 0.
+ *   norm       device [1] fp32, 16-byte aligned: what qb_multi_tensor_grad_norm wrote, or a
+ *              norm over several ranks.  An infinite norm makes s 0, a NaN s NaN.
+ * With s = 1 and out = g a gradient is left as it is (not read).  Gradients must not overlap
+ * each other.  One launch per 120 gradients; may be captured.
+ */
+qb_status qb_multi_tensor_clip_grads(const qb_grad* grads, int32_t count, double max_norm, const float* norm,
+                                     void* stream);
 
 /*
  * qb_codebook -- host: copy the decode table of `code` (indexed by stored code)
