@@ -42,6 +42,31 @@ __device__ __forceinline__ float act_value(int act, float x)
     }
 }
 
+// act of each of N values, the kind told apart once.
+template <int N>
+__device__ __forceinline__ void act_values(int act, float* v)
+{
+    switch (act) {
+    case ACT_RELU:
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_value(ACT_RELU, v[j]);
+        return;
+    case ACT_GELU:
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_value(ACT_GELU, v[j]);
+        return;
+    case ACT_GELU_TANH:
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_value(ACT_GELU_TANH, v[j]);
+        return;
+    case ACT_SILU:
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_value(ACT_SILU, v[j]);
+        return;
+    default: return;
+    }
+}
+
 // a s(q) s(-q), zero where that product is (a may be infinite there).
 __device__ __forceinline__ float times_slope(float a, float s, float s_neg)
 {

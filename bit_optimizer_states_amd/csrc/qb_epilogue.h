@@ -11,6 +11,7 @@ namespace qb {
 // Rows of C begin at any element (N may be odd): accesses of four elements through types
 // of element alignment, which the GLOBAL instructions take as they are.
 typedef u32x2 __attribute__((aligned(2))) u32x2_e2;
+typedef u32x4 __attribute__((aligned(2))) u32x4_e2;
 typedef f32x4 __attribute__((aligned(4))) f32x4_e4;
 
 // Up to four elements from element i on (cnt of them).
@@ -67,13 +68,96 @@ __device__ __forceinline__ void finish_linear4(const Epilogue& e, int64_t m, int
     const int64_t at = m * e.N + n;
     if (e.bias) z += load_bias4(e, n, cnt);
     if (e.z) store_up_to4<XDT>(e.z, at, cnt, z);
-    f32x4 y = z;
-    if (e.act != ACT_NONE) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = act_value(e.act, z[j]);
-    }
+    float a[4] = {z.x, z.y, z.z, z.w};
+    act_values<4>(e.act, a);
+    f32x4 y = {a[0], a[1], a[2], a[3]};
     if (e.residual) y += load_up_to4<XDT>(e.residual, at, cnt);
     store_up_to4<XDT>(e.y, at, cnt, y);
+}
+
+// Eight neighbouring columns (cnt of them below N), the bias and the residual read before.
+template <int DT>
+__device__ __forceinline__ void load_up_to8(const void* p, int64_t i, int cnt, float* v)
+{
+    if (cnt >= 8) {
+        if constexpr (DT == DT_F32) {
+            *reinterpret_cast<f32x4*>(v) = load_up_to4<DT>(p, i, 4);
+            *reinterpret_cast<f32x4*>(v + 4) = load_up_to4<DT>(p, i + 4, 4);
+        } else {
+            const u32x4 w = *(const QB_G u32x4_e2*)(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = half_lo<DT>(w[j]);
+                v[2 * j + 1] = half_hi<DT>(w[j]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < cnt) v[j] = load1<DT>(p, i + j);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_up_to8(void* p, int64_t i, int cnt, const float* v)
+{
+    if (cnt >= 8) {
+        if constexpr (DT == DT_F32) {
+            store_up_to4<DT>(p, i, 4, f32x4{v[0], v[1], v[2], v[3]});
+            store_up_to4<DT>(p, i + 4, 4, f32x4{v[4], v[5], v[6], v[7]});
+        } else {
+            *(QB_G u32x4_e2*)(static_cast<uint16_t*>(p) + i) =
+                u32x4{pack_pair<DT>(v[0], v[1]), pack_pair<DT>(v[2], v[3]), pack_pair<DT>(v[4], v[5]),
+                      pack_pair<DT>(v[6], v[7])};
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < cnt) store1<DT>(p, i + j, v[j]);
+    }
+}
+
+__device__ __forceinline__ int columns_left8(int64_t n, int64_t N) { return N - n >= 8 ? 8 : N > n ? (int)(N - n) : 0; }
+
+__device__ __forceinline__ void load_bias8(const Epilogue& e, int64_t n, int cnt, float* v)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    if (!e.bias) return;
+    if (e.bias_dt == DT_F32) load_up_to8<DT_F32>(e.bias, n, cnt, v);
+    else if (e.bias_dt == DT_F16) load_up_to8<DT_F16>(e.bias, n, cnt, v);
+    else load_up_to8<DT_BF16>(e.bias, n, cnt, v);
+}
+
+template <int XDT>
+__device__ __forceinline__ void finish_linear8(const Epilogue& e, int64_t m, int64_t n, int cnt, float* z,
+                                               const float* bias, const float* residual)
+{
+    const int64_t at = m * e.N + n;
+    if (e.bias) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] += bias[j];
+    }
+    if (e.z) store_up_to8<XDT>(e.z, at, cnt, z);
+    act_values<8>(e.act, z);
+    if (e.residual) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] += residual[j];
+    }
+    store_up_to8<XDT>(e.y, at, cnt, z);
+}
+
+template <int XDT>
+__device__ __forceinline__ void finish_gated8(const Epilogue& e, int64_t m, int64_t n, int cnt, float* g,
+                                              const float* u)
+{
+    const int64_t at = m * e.N + n;
+    if (e.z) store_up_to8<XDT>(e.z, at, cnt, g);
+    if (e.u) store_up_to8<XDT>(e.u, at, cnt, u);
+    act_values<8>(e.act, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] *= u[j];
+    store_up_to8<XDT>(e.y, at, cnt, g);
 }
 
 template <int XDT>
@@ -84,10 +168,9 @@ __device__ __forceinline__ void finish_gated4(const Epilogue& e, int64_t m, int6
     const int64_t at = m * e.N + n;
     if (e.z) store_up_to4<XDT>(e.z, at, cnt, g);
     if (e.u) store_up_to4<XDT>(e.u, at, cnt, u);
-    f32x4 y;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = act_value(e.act, g[j]) * u[j];
-    store_up_to4<XDT>(e.y, at, cnt, y);
+    float a[4] = {g.x, g.y, g.z, g.w};
+    act_values<4>(e.act, a);
+    store_up_to4<XDT>(e.y, at, cnt, f32x4{a[0] * u.x, a[1] * u.y, a[2] * u.z, a[3] * u.w});
 }
 
 }  // namespace qb

@@ -151,13 +151,21 @@ __global__ __launch_bounds__(256) void k_unpack_transposed(const Weights2 ws, in
 // chunk p of an LDS row holds chunk p ^ (row % 8) of the operand's row, so that the rows
 // of one fragment lie in different banks.  A fragment is one chunk a lane: row lane % 16,
 // chunk 4 kk + lane / 16; with binary32 its four elements go to four instructions, the same
-// k order in both operands.  B's fragment is the first operand, so that a lane's four sums
-// are four neighbouring columns of C: one access of 8 (16) bytes.
+// k order in both operands.  All fragments of a step are read before its products begin,
+// and the next step's loads are issued behind the first half of them: the other wave of
+// the SIMD multiplies meanwhile.  4096 x 4096 x 11008 bf16 of 8-bit random values: 268 us;
+// with the loads first and each half read before its products 286; steps of half the
+// length in four buffers 300; four waves of 128 x 128 each 315; two groups of waves kept
+// half a step apart by barriers 355.
+// B's fragment is the first operand, so that a lane's four sums are four neighbouring
+// columns of C.
 
 struct GemmParams {
     GemmArgs g;
     Epilogue e;
-    int32_t steps, steps0, half, tiles_m, tiles_n;
+    float* part;                 // partial sums [split][M][R] of a product split over its length
+    int32_t steps, steps0, half, tiles_m, tiles_n, split, per_split;
+    int64_t n_first;             // first row of B
 };
 
 template <int XDT>
@@ -179,14 +187,78 @@ __device__ __forceinline__ void mma_chunk(const u32x4& a, const u32x4& b, f32x4&
     }
 }
 
+// Binary32 word of column group n4 (four columns) of row m of a staged tile of BN columns:
+// groups are exchanged within eight by the row, so that neither the lanes that write a
+// column group of 16 rows nor those that read a row meet in a bank.
+template <int BN>
+__device__ __forceinline__ int staged_word(int m, int n4)
+{
+    return m * BN + 4 * (n4 ^ (m & 7));
+}
+
+// The epilogue of `rows` staged rows (m0 onwards) of BN columns (of B: n0 onwards), 8
+// outputs a thread at a time; a thread stays in its columns, and the residual is read
+// two turns ahead.
+template <int XDT, int BN, int NT, bool GATED>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, const float* tile, int rows, int64_t m0, int64_t n0,
+                                            int64_t M)
+{
+    constexpr int TPR = BN / (GATED ? 16 : 8), STEP = NT / TPR;     // threads of a row, rows at a time
+    const int tid = threadIdx.x, q = tid % TPR;
+    const int64_t n = GATED ? n0 / 2 + q * 8 : n0 + q * 8;
+    const int cnt = columns_left8(n, e.N);
+    if (cnt == 0) return;
+    const int last = M - m0 < rows ? (int)(M - m0) : rows;
+    if constexpr (GATED) {
+        const int g4 = (q >> 1) * 8 + (q & 1) * 2;         // the gate's column group; the up's is 4 further
+#pragma unroll 1
+        for (int row = tid / TPR; row < last; row += STEP) {
+            float g[8], u[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                *reinterpret_cast<f32x4*>(g + 4 * h) = *reinterpret_cast<const f32x4*>(tile + staged_word<BN>(row, g4 + h));
+                *reinterpret_cast<f32x4*>(u + 4 * h) =
+                    *reinterpret_cast<const f32x4*>(tile + staged_word<BN>(row, g4 + 4 + h));
+            }
+            finish_gated8<XDT>(e, m0 + row, n, cnt, g, u);
+        }
+    } else {
+        float bias[8];
+        load_bias8(e, n, cnt, bias);
+        float r0[8], r1[8];
+        auto residual = [&](int row, float* r) {
+            if (e.residual && row < last) load_up_to8<XDT>(e.residual, (m0 + row) * e.N + n, cnt, r);
+        };
+        residual(tid / TPR, r0);
+        residual(tid / TPR + STEP, r1);
+#pragma unroll 1
+        for (int row = tid / TPR; row < last; row += STEP) {
+            float z[8], r[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                r[j] = r0[j];
+                r0[j] = r1[j];
+            }
+            residual(row + 2 * STEP, r1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<f32x4*>(z + 4 * h) = *reinterpret_cast<const f32x4*>(tile + staged_word<BN>(row, 2 * q + h));
+            finish_linear8<XDT>(e, m0 + row, n, cnt, z, bias, r);
+        }
+    }
+}
+
 template <int XDT, int BM, int BN, int WM, int WN, bool GATED>
 __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
 {
-    constexpr int NW = WM * WN;                        // waves
+    constexpr int NW = WM * WN, NT = 64 * NW;          // waves, threads
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16x16 tiles of a wave
     constexpr int A_PER = BM / 8 / NW, B_PER = BN / 8 / NW;   // loads (8 rows each) of a wave and step
-    static_assert(A_PER * NW * 8 == BM && B_PER * NW * 8 == BN && (!GATED || TN % 2 == 0), "whole loads");
+    static_assert(A_PER * NW * 8 == BM && B_PER * NW * 8 == BN, "whole loads");
     constexpr int BUF = (BM + BN) * 128;
+    // the epilogue stages the tile in the same memory, the rows of WM / PASSES waves at once
+    constexpr int PASSES = (BM * BN * 4 + 2 * BUF - 1) / (2 * BUF);
+    static_assert(WM % PASSES == 0, "whole waves' rows per pass");
     __shared__ __attribute__((aligned(16))) char s_ab[2 * BUF];   // two buffers, A's rows then B's
     constexpr int ES = XDT == DT_F32 ? 4 : 2;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -196,10 +268,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
 
     // each XCD takes a contiguous range of tiles, numbered so that 8 rows of tiles are
     // walked column by column: the tiles that run together share A and B in its L2
-    const int64_t tile = tile_of<true>(blockIdx.x, gridDim.x);
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int64_t item = tile_of<true>(blockIdx.x, gridDim.x);
+    const int piece = (int)(item / tiles);
+    const int64_t tile = item - (int64_t)piece * tiles;
     const int64_t band = tile / (8 * p.tiles_n), in_band = tile - band * 8 * p.tiles_n;
     const int rows_here = p.tiles_m - band * 8 < 8 ? (int)(p.tiles_m - band * 8) : 8;
-    const int64_t m0 = (band * 8 + in_band % rows_here) * BM, n0 = in_band / rows_here * BN;
+    const int64_t m0 = (band * 8 + in_band % rows_here) * BM, n0 = p.n_first + in_band / rows_here * BN;
+    const int begin = piece * p.per_split, end = p.steps - begin < p.per_split ? p.steps : begin + p.per_split;
 
     // rows past the end read the last row (their sums are never stored)
     uint32_t a_off[A_PER], b_off[B_PER], chunk_hi;
@@ -246,43 +322,88 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
         for (int t = 0; t < TM; ++t) acc[j][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     const int a_row = (wm * (BM / WM) + r) * 128, b_row = BM * 128 + (wn * (BN / WN) + r) * 128;
-    load_step(0);
-    for (int s = 0; s < p.steps; ++s) {
+    u32x4 bf[2][TN], af[2][TM];
+    auto read_half = [&](const char* buf, int kk) {
+        const int c = ((4 * kk + g) ^ (r & 7)) * 16;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) bf[kk][j] = *reinterpret_cast<const u32x4*>(buf + b_row + j * 16 * 128 + c);
+#pragma unroll
+        for (int t = 0; t < TM; ++t) af[kk][t] = *reinterpret_cast<const u32x4*>(buf + a_row + t * 16 * 128 + c);
+    };
+    auto multiply_half = [&](int kk) {
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) mma_chunk<XDT>(bf[kk][j], af[kk][t], acc[j][t]);
+    };
+    load_step(begin);
+    for (int s = begin; s < end; ++s) {
         __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();                               // step s has landed; the other buffer is free
-        if (s + 1 < p.steps) load_step(s + 1);
+        lds_barrier();                                 // step s has landed; the other buffer is free
         const char* const buf = s_ab + (s & 1) * BUF;
-        const int halves = p.half && s + 1 == p.steps ? 1 : 2;
+        read_half(buf, 0);
+        if (s + 1 < end) load_step(s + 1);
+        const bool whole = !(p.half && s + 1 == p.steps);
+        if (whole) read_half(buf, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply_half(0);
+        if (whole) multiply_half(1);
+    }
+
+    // lane: its column r of a 16x16 tile is C's row, its elements 4 g + i are C's columns
+    if (p.split > 1) {
+        float* const out = p.part + (int64_t)piece * p.g.M * p.g.R;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            if (kk >= halves) break;
-            const int c = ((4 * kk + g) ^ (r & 7)) * 16;
-            u32x4 bf[TN], af[TM];
+        for (int t = 0; t < TM; ++t) {
+            const int64_t m = m0 + wm * (BM / WM) + 16 * t + r;
+            if (m >= p.g.M) continue;
 #pragma unroll
-            for (int j = 0; j < TN; ++j) bf[j] = *reinterpret_cast<const u32x4*>(buf + b_row + j * 16 * 128 + c);
+            for (int j = 0; j < TN; ++j) {
+                const int64_t n = n0 + wn * (BN / WN) + 16 * j + 4 * g;
+                const int cnt = columns_left(n, p.g.R);
+                if (cnt > 0) store_up_to4<DT_F32>(out, m * p.g.R + n, cnt, acc[j][t]);
+            }
+        }
+        return;
+    }
+    float* const staged = reinterpret_cast<float*>(s_ab);
 #pragma unroll
-            for (int t = 0; t < TM; ++t) af[t] = *reinterpret_cast<const u32x4*>(buf + a_row + t * 16 * 128 + c);
+    for (int pass = 0; pass < PASSES; ++pass) {
+        __syncthreads();
+        if (wm / (WM / PASSES) == pass) {
 #pragma unroll
             for (int t = 0; t < TM; ++t)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) mma_chunk<XDT>(bf[j], af[t], acc[j][t]);
+                for (int j = 0; j < TN; ++j) {
+                    const int m = (wm % (WM / PASSES)) * (BM / WM) + 16 * t + r, n4 = (wn * (BN / WN) + 16 * j) / 4 + g;
+                    *reinterpret_cast<f32x4*>(staged + staged_word<BN>(m, n4)) = acc[j][t];
+                }
         }
+        __syncthreads();
+        finish_rows<XDT, BN, NT, GATED>(p.e, staged, BM / PASSES, m0 + pass * (BM / PASSES), n0, p.g.M);
     }
+}
 
-    // lane: column r of the 16x16 tile is C's row, its elements 4 g + i are C's columns
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-        const int64_t m = m0 + wm * (BM / WM) + 16 * t + r;
-        if (m >= p.g.M) continue;
-        if constexpr (GATED) {
-            const int64_t nb = (n0 + wn * (BN / WN)) / 2 + 4 * g;
-#pragma unroll
-            for (int j = 0; j < TN; j += 2) finish_gated4<XDT>(p.e, m, nb + 8 * j, acc[j][t], acc[j + 1][t]);
-        } else {
-            const int64_t nb = n0 + wn * (BN / WN) + 4 * g;
-#pragma unroll
-            for (int j = 0; j < TN; ++j) finish_linear4<XDT>(p.e, m, nb + 16 * j, acc[j][t]);
-        }
+// The pieces of a split product added in order, then the epilogue: four columns a thread.
+template <int XDT, bool GATED>
+__global__ __launch_bounds__(256) void k_join_split(const GemmParams p, int64_t groups)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = i / groups, n = (i - m * groups) * 4;
+    if (m >= p.g.M) return;
+    auto sum = [&](int64_t column) {
+        const int cnt = columns_left(column, p.g.R);
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int s = 0; s < p.split; ++s) v += load_up_to4<DT_F32>(p.part, ((int64_t)s * p.g.M + m) * p.g.R + column, cnt);
+        return v;
+    };
+    if constexpr (GATED) {
+        const int64_t column = n / 16 * 32 + n % 16;
+        const f32x4 g = sum(column), u = sum(column + 16);
+        finish_gated4<XDT>(p.e, m, n, g, u);
+    } else {
+        finish_linear4<XDT>(p.e, m, n, sum(n));
     }
 }
 
@@ -296,34 +417,69 @@ void* further(void* p, int64_t rows, int64_t width, int es)
     return p ? static_cast<char*>(p) + rows * width * es : nullptr;
 }
 
-// One launch, or several of whole tiles where a grid would not hold them.
-template <int XDT, int BM, int BN, int WM, int WN, bool GATED>
-hipError_t gemm_as(GemmParams p, hipStream_t s)
+// Rows m .. m + rows - 1 of the product.
+template <int XDT>
+GemmParams rows_of(const GemmParams& all, int64_t m, int64_t rows)
 {
     constexpr int ES = XDT == DT_F32 ? 4 : 2;
-    p.tiles_n = (int)((p.g.R + BN - 1) / BN);
-    const int64_t M = p.g.M, most = ((int64_t(1) << 21) / p.tiles_n) * BM;
-    const GemmParams all = p;
+    GemmParams p = all;
+    p.g.M = rows;
+    p.g.a0 = further(all.g.a0, m, p.g.lda, ES);
+    p.g.a1 = further(all.g.a1, m, p.g.lda, ES);
+    p.e.residual = further(all.e.residual, m, p.e.N, ES);
+    p.e.z = further(all.e.z, m, p.e.N, ES);
+    p.e.u = further(all.e.u, m, p.e.N, ES);
+    p.e.y = further(all.e.y, m, p.e.N, ES);
+    return p;
+}
+
+int64_t tiles_over(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+
+// Columns n_first .. R - 1 of B in BN-wide tiles (`columns` tiles of them at most).
+template <int XDT, int BM, int BN, int WM, int WN, bool GATED>
+hipError_t gemm_as(GemmParams p, int64_t n_first, int64_t columns, hipStream_t s)
+{
+    p.n_first = n_first;
+    const int64_t all = tiles_over(p.g.R - n_first, BN);
+    p.tiles_n = (int)(all < columns ? all : columns);
+    p.tiles_m = (int)tiles_over(p.g.M, BM);
+    return launch_kernel_nt(k_gemm<XDT, BM, BN, WM, WN, GATED>, p.tiles_m * p.tiles_n * p.split, 64 * WM * WN, s, p);
+}
+
+constexpr int64_t kEveryColumn = int64_t(1) << 40;
+
+// Tiles of 256 x 256 where they fill the CUs (one workgroup a CU), else of 128 x 128 (two a
+// CU), else of 64 x 64, the length split where that leaves CUs idle.
+template <int XDT, bool GATED>
+hipError_t gemm_tiles(GemmParams p, hipStream_t s)
+{
+    const int64_t M = p.g.M, R = p.g.R;
+    p.split = 1;
+    p.per_split = p.steps;
+    if (tiles_over(M, 256) * tiles_over(R, 256) >= 192)
+        return gemm_as<XDT, 256, 256, 2, 4, GATED>(p, 0, kEveryColumn, s);
+    if (tiles_over(M, 128) * tiles_over(R, 128) >= 192)
+        return gemm_as<XDT, 128, 128, 2, 4, GATED>(p, 0, kEveryColumn, s);
+    p.split = gemm_split(M, R, p.steps);
+    if (!p.part) p.split = 1;
+    p.per_split = (int)tiles_over(p.steps, p.split);
+    p.split = (int)tiles_over(p.steps, p.per_split);
+    hipError_t e = gemm_as<XDT, 64, 64, 2, 2, GATED>(p, 0, kEveryColumn, s);
+    if (e != hipSuccess || p.split == 1) return e;
+    const int64_t groups = (p.e.N + 3) / 4;
+    return launch_kernel(k_join_split<XDT, GATED>, (int)tiles_over(M * groups, 256), s, p, groups);
+}
+
+// One product, or several of fewer rows where a grid would not hold them.
+template <int XDT, bool GATED>
+hipError_t gemm_rows(const GemmParams& p, hipStream_t s)
+{
+    const int64_t M = p.g.M, most = (int64_t(1) << 21) / tiles_over(p.g.R, 128) * 128;
     for (int64_t m = 0; m < M; m += most) {
-        p.g.M = M - m < most ? M - m : most;
-        p.tiles_m = (int)((p.g.M + BM - 1) / BM);
-        p.g.a0 = further(all.g.a0, m, p.g.lda, ES);
-        p.g.a1 = further(all.g.a1, m, p.g.lda, ES);
-        p.e.residual = further(all.e.residual, m, p.e.N, ES);
-        p.e.z = further(all.e.z, m, p.e.N, ES);
-        p.e.u = further(all.e.u, m, p.e.N, ES);
-        p.e.y = further(all.e.y, m, p.e.N, ES);
-        const hipError_t e = launch_kernel_nt(k_gemm<XDT, BM, BN, WM, WN, GATED>, p.tiles_m * p.tiles_n, 64 * WM * WN, s, p);
+        const hipError_t e = gemm_tiles<XDT, GATED>(rows_of<XDT>(p, m, M - m < most ? M - m : most), s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
-}
-
-template <int XDT, bool GATED>
-hipError_t gemm_tiles(const GemmParams& p, hipStream_t s)
-{
-    if ((p.g.M + 255) / 256 * ((p.g.R + 255) / 256) >= 200) return gemm_as<XDT, 256, 256, 2, 4, GATED>(p, s);
-    return gemm_as<XDT, 128, 128, 2, 4, GATED>(p, s);
 }
 
 template <int XDT, bool DQ>
@@ -373,15 +529,30 @@ hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_
     return unpack(xdt, w, count, N, K, f, out, true, s);
 }
 
-hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, hipStream_t s)
+// Pieces of the length of a product of few tiles: about three workgroups of 64 x 64 a CU,
+// four steps each at least.
+int gemm_split(int64_t M, int64_t R, int64_t steps)
+{
+    const int64_t tiles = tiles_over(M, 64) * tiles_over(R, 64);
+    int64_t split = kSplitTiles / tiles;
+    if (split > steps / 4) split = steps / 4;
+    return (int)(split < 1 ? 1 : split > kSplitMax ? kSplitMax : split);
+}
+
+hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t s)
 {
     const int64_t step = gemm_step(xdt);
-    GemmParams p{g, e, (int32_t)((g.len + step - 1) / step), (int32_t)((g.len0 + step - 1) / step),
-                 g.len % step ? 1 : 0, 0, 0};
+    GemmParams p{};
+    p.g = g;
+    p.e = e;
+    p.part = part;
+    p.steps = (int32_t)((g.len + step - 1) / step);
+    p.steps0 = (int32_t)((g.len0 + step - 1) / step);
+    p.half = g.len % step ? 1 : 0;
     switch (xdt) {
-    case DT_F32: return gated ? gemm_tiles<DT_F32, true>(p, s) : gemm_tiles<DT_F32, false>(p, s);
-    case DT_F16: return gated ? gemm_tiles<DT_F16, true>(p, s) : gemm_tiles<DT_F16, false>(p, s);
-    default: return gated ? gemm_tiles<DT_BF16, true>(p, s) : gemm_tiles<DT_BF16, false>(p, s);
+    case DT_F32: return gated ? gemm_rows<DT_F32, true>(p, s) : gemm_rows<DT_F32, false>(p, s);
+    case DT_F16: return gated ? gemm_rows<DT_F16, true>(p, s) : gemm_rows<DT_F16, false>(p, s);
+    default: return gated ? gemm_rows<DT_BF16, true>(p, s) : gemm_rows<DT_BF16, false>(p, s);
     }
 }
 

@@ -69,7 +69,20 @@ struct GemmArgs {
     const void* b;
     int64_t M, R, len0, len, lda, ldb;
 };
-hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, hipStream_t s);
+// part: room for the partial sums of a product split over its length, gemm_part_floats()
+// (a product of few tiles is not split without it).
+hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t s);
+int gemm_split(int64_t M, int64_t R, int64_t steps);
+
+// A product is split into kSplitTiles workgroups of 64 x 64 at most, kSplitMax pieces.
+constexpr int64_t kSplitTiles = 768, kSplitMax = 16;
+// At most split * tiles <= kSplitTiles tiles of 64 x 64, and kSplitMax pieces of M x R: never
+// less for more rows or columns.
+constexpr int64_t gemm_part_floats(int64_t M, int64_t R)
+{
+    const int64_t most = kSplitMax * M * R, cap = kSplitTiles * 64 * 64;
+    return most < cap ? most : cap;
+}
 
 // dz = dy act'(z) [M, N] into `dz` of pitch `pitch` (its padding zero; nullptr: not
 // wanted) and into `dz_out` [M, N] (nullptr: not wanted), and per slice of rows the sums of

@@ -90,15 +90,27 @@ qb_status check_ws(size_t need, const void* ws, size_t ws_bytes)
     return ws_bytes < need ? QB_EWORKSPACE : QB_OK;
 }
 
+// Workspace of a forward call from kRowsMax rows on: the weights' `rows` rows, then the
+// partial sums of a split product.
+size_t unpacked_bytes(int xdt, int64_t K, int64_t rows)
+{
+    return round_up((size_t)rows * (size_t)gemm_pitch(xdt, K) * dtype_bytes(xdt), 256);
+}
+
 size_t forward_bytes(int xdt, int64_t M, int64_t K, int64_t rows)
 {
-    return M <= kRowsMax ? 0 : (size_t)rows * (size_t)gemm_pitch(xdt, K) * dtype_bytes(xdt);
+    return M <= kRowsMax ? 0 : unpacked_bytes(xdt, K, rows) + (size_t)gemm_part_floats(M, rows) * sizeof(float);
+}
+
+float* forward_part(int xdt, int64_t K, int64_t rows, void* ws)
+{
+    return reinterpret_cast<float*>(static_cast<char*>(ws) + unpacked_bytes(xdt, K, rows));
 }
 
 // Workspace of a gradient: the weights transposed, dz (dg and du) padded, the partial
-// sums of the bias's gradient.
+// sums of a split product and of the bias's gradient.
 struct BackwardLayout {
-    size_t dz, part, bytes;
+    size_t dz, split, part, bytes;
 };
 
 BackwardLayout backward_layout(int xdt, int64_t M, int64_t K, int64_t N, int count)
@@ -108,7 +120,8 @@ BackwardLayout backward_layout(int xdt, int64_t M, int64_t K, int64_t N, int cou
     const size_t most = (size_t)((M + 15) / 16) * (size_t)N, cap = (size_t)2048 * 512 + (size_t)N;
     BackwardLayout l;
     l.dz = round_up((size_t)K * pitch, 256);
-    l.part = l.dz + round_up((size_t)M * pitch, 256);
+    l.split = l.dz + round_up((size_t)M * pitch, 256);
+    l.part = l.split + round_up((size_t)gemm_part_floats(M, K) * sizeof(float), 256);
     l.bytes = l.part + (count == 1 ? (most < cap ? most : cap) * sizeof(float) : 0);
     return l;
 }
@@ -117,7 +130,8 @@ bool whole_steps(int xdt, int64_t n) { return n % gemm_step(xdt) == 0; }
 
 // dx = [dz_0 dz_1] [W_0; W_1] for dz of rows of `lda` elements.
 hipError_t input_gradient(int xdt, const void* dz0, const void* dz1, int64_t lda, const Weight4* w, int count,
-                          const Weight4Format& f, int64_t M, int64_t K, int64_t N, void* dx, void* ws, hipStream_t s)
+                          const Weight4Format& f, int64_t M, int64_t K, int64_t N, void* dx, void* ws, float* part,
+                          hipStream_t s)
 {
     const int64_t pitch = gemm_pitch(xdt, N);
     hipError_t e = launch_unpack_transposed(xdt, w, count, N, K, f, ws, s);
@@ -126,7 +140,7 @@ hipError_t input_gradient(int xdt, const void* dz0, const void* dz1, int64_t lda
     Epilogue out{};
     out.y = dx;
     out.N = K;
-    return launch_gemm(xdt, false, g, out, s);
+    return launch_gemm(xdt, false, g, out, part, s);
 }
 
 }  // namespace
@@ -162,7 +176,8 @@ qb_status qb_dequant_linear(const void* x, qb_dtype xdt, int64_t M, int64_t K, c
     if (M <= kRowsMax) return hip_status(launch_linear_rows(xdt, x, M, K, &w, 1, f, e, s));
     hipError_t err = launch_unpack(xdt, &w, 1, N, K, f, ws, s);
     if (err == hipSuccess)
-        err = launch_gemm(xdt, false, GemmArgs{x, nullptr, ws, M, N, K, K, K, gemm_pitch(xdt, K)}, e, s);
+        err = launch_gemm(xdt, false, GemmArgs{x, nullptr, ws, M, N, K, K, K, gemm_pitch(xdt, K)}, e,
+                          forward_part(xdt, K, N, ws), s);
     return hip_status(err);
 }
 
@@ -218,7 +233,8 @@ qb_status qb_dequant_linear_backward(const void* dy, const void* z, qb_dtype xdt
     if (e == hipSuccess && dbias)
         e = launch_bias_sum(reinterpret_cast<float*>(wp + l.part), M > 0 ? linear_dz_slices(M, N) : 0, N,
                             accumulate != 0, dbias, bdt, s);
-    if (e == hipSuccess && dx && M > 0) e = input_gradient(xdt, a, nullptr, lda, &w, 1, f, M, K, N, dx, wp, s);
+    if (e == hipSuccess && dx && M > 0) e = input_gradient(xdt, a, nullptr, lda, &w, 1, f, M, K, N, dx, wp,
+                                                              reinterpret_cast<float*>(wp + l.split), s);
     return hip_status(e);
 }
 
@@ -251,7 +267,8 @@ qb_status qb_dequant_gated(const void* x, qb_dtype xdt, int64_t M, int64_t K, co
     if (M <= kRowsMax) return hip_status(launch_linear_rows(xdt, x, M, K, w, 2, f, e, s));
     hipError_t err = launch_unpack(xdt, w, 2, N, K, f, ws, s);
     if (err == hipSuccess)
-        err = launch_gemm(xdt, true, GemmArgs{x, nullptr, ws, M, gated_rows(N), K, K, K, gemm_pitch(xdt, K)}, e, s);
+        err = launch_gemm(xdt, true, GemmArgs{x, nullptr, ws, M, gated_rows(N), K, K, K, gemm_pitch(xdt, K)}, e,
+                          forward_part(xdt, K, gated_rows(N), ws), s);
     return hip_status(err);
 }
 
@@ -292,7 +309,7 @@ qb_status qb_dequant_gated_backward(const void* dy, const void* gate_out, const 
     if (e == hipSuccess && dx) {
         const void* const dg = given ? dgate : wp + l.dz;
         const void* const du = given ? dup : wp + l.dz + (size_t)M * pitch * dtype_bytes(xdt);
-        e = input_gradient(xdt, dg, du, pitch, w, 2, f, M, K, N, dx, wp, s);
+        e = input_gradient(xdt, dg, du, pitch, w, 2, f, M, K, N, dx, wp, reinterpret_cast<float*>(wp + l.split), s);
     }
     return hip_status(e);
 }

@@ -141,6 +141,14 @@ __device__ __forceinline__ void dequant_chunk(const u32x4& cw, float a, const fl
     dequant_frag<XDT>(cw.w, a, s_val, f[3]);
 }
 
+// Workgroup barrier that orders LDS accesses only: global loads and stores stay in flight across it.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Pointers of a direct global-to-LDS load.
 typedef const void __attribute__((address_space(1)))* gptr_t;
 typedef void __attribute__((address_space(3)))* lptr_t;

@@ -226,3 +226,16 @@ def test_no_rows_and_refusals():
         with pytest.raises(L.QbError) as e:
             call(**bad)
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("M,K,N", [(3600, 160, 1751), (3601, 3520, 67), (1500, 224, 1055), (1499, 2112, 49)])
+@pytest.mark.parametrize("xdt", [BF16, F32])
+def test_large_tiles(M, K, N, xdt):
+    L = qb()
+    w = pair(N, K, NF4, 64, True, xdt, seed=M)
+    x = ref.normal((M, K), M, 10 / np.sqrt(K), dtype=xdt)
+    y, g, u = forward(L, x, w, keep=True)
+    check_forward(L, x, w, "SILU", y, g, u)
+    dy = ref.normal((M, N), 5, 0.1, xdt)
+    dx, dg, du = backward(L, dy, g, u, w, keep=(True, True))
+    check_backward(L, dy, g, u, w, "SILU", dx, dg, du)

@@ -362,3 +362,22 @@ def test_binding_refuses_wrong_shapes_and_types():
         L.qb_dequant_linear(ref.normal((65, 128), 1, dtype=BF16), w.codes, None, NF4, 64, 64,
                             torch.empty(65, 64, dtype=BF16, device=DEV), dq=w.dq(L))
     assert e.value.status == L.QB_EINVAL
+
+
+# products of enough tiles for the larger tile shapes, ragged at both ends: 256 x 256 (15 x 14 forward, 15 x 14
+# backward), 128 x 128 (12 x 17)
+LARGE = [(3600, 160, 3501), (3601, 3520, 130), (1500, 224, 2111), (1499, 2112, 97)]
+
+
+@pytest.mark.parametrize("M,K,N", LARGE)
+@pytest.mark.parametrize("xdt", [BF16, F32])
+def test_large_tiles(M, K, N, xdt):
+    L = qb()
+    w = ref.Weight(N, K, NF4, 64, True, xdt, seed=M)
+    x, bias, residual = (ref.normal(s, M + i, dtype=xdt) for i, s in enumerate([(M, K), (N,), (M, N)]))
+    y, z = forward(L, x, w, bias, "GELU", residual, keep=True)
+    check_forward(L, x, w, bias, "GELU", residual, y, z)
+    assert torch.equal(forward(L, x, w, bias, "GELU", residual, in_place=True), y)
+    dy = ref.normal((M, N), 5, 0.1, xdt)
+    dx, dz, db = backward(L, dy, w, z, "GELU", dz=True, bias_dt=F32)
+    check_backward(L, dy, w, z, "GELU", dx, dz, db)
