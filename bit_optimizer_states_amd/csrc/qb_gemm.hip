@@ -151,12 +151,13 @@ __global__ __launch_bounds__(256) void k_unpack_transposed(const Weights2 ws, in
 // chunk p of an LDS row holds chunk p ^ (row % 8) of the operand's row, so that the rows
 // of one fragment lie in different banks.  A fragment is one chunk a lane: row lane % 16,
 // chunk 4 kk + lane / 16; with binary32 its four elements go to four instructions, the same
-// k order in both operands.  All fragments of a step are read before its products begin,
-// and the next step's loads are issued behind the first half of them: the other wave of
-// the SIMD multiplies meanwhile.  4096 x 4096 x 11008 bf16 of 8-bit random values: 268 us;
-// with the loads first and each half read before its products 286; steps of half the
-// length in four buffers 300; four waves of 128 x 128 each 315; two groups of waves kept
-// half a step apart by barriers 355.
+// k order in both operands.  The first half of a step's fragments are read, then the next
+// step's loads are issued, then the second half's reads are dealt among the first half's
+// products.  4096 x 4096 x 11008 bf16 (the loop alone, binary32 out): 258 us, 1431 TFLOP/s, the
+// matrix pipes busy 72% of the time at the 1.9 GHz that the chip holds then; all fragments
+// read before the products 266; the loads first and each half read before its products
+// 286; steps of half the length in four buffers 291; four waves of 128 x 128 each 315; two
+// groups of waves kept half a step apart by barriers 355.
 // B's fragment is the first operand, so that a lane's four sums are four neighbouring
 // columns of C.
 
@@ -278,10 +279,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
     const int begin = piece * p.per_split, end = p.steps - begin < p.per_split ? p.steps : begin + p.per_split;
 
     // rows past the end read the last row (their sums are never stored)
-    uint32_t a_off[A_PER], b_off[B_PER], chunk_hi;
+    uint32_t a_off[A_PER], b_off[B_PER];
     {
         const int row8 = lane >> 3, c = (lane & 7) ^ row8;
-        chunk_hi = c >= 4 ? 64u : 0u;
 #pragma unroll
         for (int i = 0; i < A_PER; ++i) {
             int64_t row = (i * NW + wave) * 8 + row8;
@@ -296,23 +296,23 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
         }
     }
     const char* const a0 = static_cast<const char*>(p.g.a0) + m0 * p.g.lda * ES;
-    const char* const a1 = static_cast<const char*>(p.g.a1) + m0 * p.g.lda * ES;
+    const char* const a1 = static_cast<const char*>(p.g.a1) + m0 * p.g.lda * ES - (int64_t)p.steps0 * 128;
     const char* const b0 = static_cast<const char*>(p.g.b) + n0 * p.g.ldb * ES;
 
+    // a length of half a step too many: its last step begins half a step early, and only its
+    // upper half is multiplied
     auto load_step = [&](int s) {
         char* const dst = s_ab + (s & 1) * BUF;
-        const char* const as = s < p.steps0 ? a0 + (int64_t)s * 128 : a1 + (int64_t)(s - p.steps0) * 128;
-        const char* const bs = b0 + (int64_t)s * 128;
-        // a last step of half the length: its upper chunks are read again from the lower half
-        const uint32_t back = p.half && s + 1 == p.steps ? chunk_hi : 0u;
+        const int64_t at = (int64_t)s * 128 - (p.half && s + 1 == p.steps ? 64 : 0);
+        const char* const as = (s < p.steps0 ? a0 : a1) + at;
+        const char* const bs = b0 + at;
 #pragma unroll
         for (int i = 0; i < A_PER; ++i)
-            __builtin_amdgcn_global_load_lds((gptr_t)(as + (a_off[i] - back)), (lptr_t)(dst + (i * NW + wave) * 1024),
-                                             16, 0, 0);
+            __builtin_amdgcn_global_load_lds((gptr_t)(as + a_off[i]), (lptr_t)(dst + (i * NW + wave) * 1024), 16, 0, 0);
 #pragma unroll
         for (int i = 0; i < B_PER; ++i)
-            __builtin_amdgcn_global_load_lds((gptr_t)(bs + (b_off[i] - back)),
-                                             (lptr_t)(dst + BM * 128 + (i * NW + wave) * 1024), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((gptr_t)(bs + b_off[i]), (lptr_t)(dst + BM * 128 + (i * NW + wave) * 1024),
+                                             16, 0, 0);
     };
 
     f32x4 acc[TN][TM];
@@ -336,18 +336,31 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
 #pragma unroll
             for (int j = 0; j < TN; ++j) mma_chunk<XDT>(bf[kk][j], af[kk][t], acc[j][t]);
     };
+    const int full = end - (p.half && end == p.steps ? 1 : 0);      // steps of the whole length
     load_step(begin);
-    for (int s = begin; s < end; ++s) {
+    for (int s = begin; s < full; ++s) {
         __builtin_amdgcn_s_waitcnt(0);
         lds_barrier();                                 // step s has landed; the other buffer is free
         const char* const buf = s_ab + (s & 1) * BUF;
         read_half(buf, 0);
-        if (s + 1 < end) load_step(s + 1);
-        const bool whole = !(p.half && s + 1 == p.steps);
-        if (whole) read_half(buf, 1);
         __builtin_amdgcn_sched_barrier(0);
+        if (s + 1 < end) load_step(s + 1);
+        read_half(buf, 1);
         multiply_half(0);
-        if (whole) multiply_half(1);
+        multiply_half(1);
+        // the second half's reads are dealt among the first half's products
+#pragma unroll
+        for (int i = 0; i < TM + TN; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, XDT == DT_F32 ? 8 : 2, 0);      // matrix instructions
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                          // an LDS read
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 2 * TM * TN * (XDT == DT_F32 ? 4 : 1), 0);
+    }
+    if (full < end) {
+        __builtin_amdgcn_s_waitcnt(0);
+        lds_barrier();
+        read_half(s_ab + (full & 1) * BUF, 1);
+        multiply_half(1);
     }
 
     // lane: its column r of a 16x16 tile is C's row, its elements 4 g + i are C's columns
@@ -412,10 +425,6 @@ const void* further(const void* p, int64_t rows, int64_t width, int es)
 {
     return p ? static_cast<const char*>(p) + rows * width * es : nullptr;
 }
-void* further(void* p, int64_t rows, int64_t width, int es)
-{
-    return p ? static_cast<char*>(p) + rows * width * es : nullptr;
-}
 
 // Rows m .. m + rows - 1 of the product.
 template <int XDT>
@@ -426,10 +435,7 @@ GemmParams rows_of(const GemmParams& all, int64_t m, int64_t rows)
     p.g.M = rows;
     p.g.a0 = further(all.g.a0, m, p.g.lda, ES);
     p.g.a1 = further(all.g.a1, m, p.g.lda, ES);
-    p.e.residual = further(all.e.residual, m, p.e.N, ES);
-    p.e.z = further(all.e.z, m, p.e.N, ES);
-    p.e.u = further(all.e.u, m, p.e.N, ES);
-    p.e.y = further(all.e.y, m, p.e.N, ES);
+    p.e = epilogue_rows(all.e, m, ES);
     return p;
 }
 
@@ -456,8 +462,16 @@ hipError_t gemm_tiles(GemmParams p, hipStream_t s)
     const int64_t M = p.g.M, R = p.g.R;
     p.split = 1;
     p.per_split = p.steps;
-    if (tiles_over(M, 256) * tiles_over(R, 256) >= 192)
-        return gemm_as<XDT, 256, 256, 2, 4, GATED>(p, 0, kEveryColumn, s);
+    const int64_t rows256 = tiles_over(M, 256), columns256 = tiles_over(R, 256), tiles256 = rows256 * columns256;
+    if (tiles256 >= 192) {
+        // the columns that whole rounds of 256 workgroups cover in 256 x 256 tiles, and the rest, where it is less
+        // than half a round, in 128 x 128 ones, which every CU takes part in
+        const int64_t whole = tiles256 / 256 * 256 / rows256, left = tiles256 - whole * rows256;
+        const bool apart = whole > 0 && left > 0 && left <= 128;
+        const hipError_t e = gemm_as<XDT, 256, 256, 2, 4, GATED>(p, 0, apart ? whole : kEveryColumn, s);
+        if (e != hipSuccess || !apart) return e;
+        return gemm_as<XDT, 128, 128, 2, 4, GATED>(p, whole * 256, kEveryColumn, s);
+    }
     if (tiles_over(M, 128) * tiles_over(R, 128) >= 192)
         return gemm_as<XDT, 128, 128, 2, 4, GATED>(p, 0, kEveryColumn, s);
     p.split = gemm_split(M, R, p.steps);

@@ -36,10 +36,23 @@ struct Epilogue {
     int32_t bias_dt, act;
 };
 
-// Rows of x up to which a wave per 16 weight rows multiplies straight from the codes.
-constexpr int64_t kRowsMax = 64;
+// The epilogue of the rows m onwards (of types of `es` bytes).
+inline Epilogue epilogue_rows(Epilogue e, int64_t m, int es)
+{
+    const int64_t at = m * e.N * es;
+    if (e.residual) e.residual = static_cast<const char*>(e.residual) + at;
+    if (e.z) e.z = static_cast<char*>(e.z) + at;
+    if (e.u) e.u = static_cast<char*>(e.u) + at;
+    e.y = static_cast<char*>(e.y) + at;
+    return e;
+}
 
-// y = epilogue(x W^T) for up to kRowsMax rows of x (count 1: linear, 2: gated).
+// Rows of x up to which the products are taken straight from the codes; beyond, the weights
+// are dequantized first (unless the length is shorter than a step of the tiled product).
+constexpr int64_t kRowsMax = 64;
+constexpr bool takes_rows(int64_t M, int64_t K) { return M <= kRowsMax || K < 64; }
+
+// y = epilogue(x W^T) straight from the codes (count 1: linear, 2: gated).
 hipError_t launch_linear_rows(int xdt, const void* x, int64_t M, int64_t K, const Weight4* w, int count,
                               const Weight4Format& f, const Epilogue& e, hipStream_t s);
 
@@ -62,7 +75,8 @@ hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_
 
 // C = epilogue(A B^T).  A [M, len] in one or two pieces of columns (a0: the first len0, a1
 // the others; both of `lda` elements a row, 16-byte aligned rows), B [R, len] of ldb
-// elements a row.  len0 is a multiple of the step unless it is len, len of half the step.
+// elements a row.  len is at least a step and a multiple of half a step, len0 of a step
+// unless it is len.
 struct GemmArgs {
     const void* a0;
     const void* a1;

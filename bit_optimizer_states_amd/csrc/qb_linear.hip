@@ -65,7 +65,7 @@ __global__ __launch_bounds__(kThreadsRows) void k_linear_rows(const RowsArgs a, 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16, M = a.M, K = a.K, N = a.e.N;
+    const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * MT), M = a.M, K = a.K, N = a.e.N;
     // weight rows past N read row N - 1 (their sums are never stored)
     const int64_t rn = n0 + r < N ? n0 + r : N - 1;
     const int64_t e_lane = rn * K + 32 * g;             // the lane's first weight of step 0
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kThreadsRows) void k_linear_rows(const RowsArgs a, 
         Frag<XDT> xf[MT][4];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const int64_t m = 16 * t + r;
+            const int64_t m = m0 + 16 * t + r;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if constexpr (STAGED) {
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kThreadsRows) void k_linear_rows(const RowsArgs a, 
     for (int o = tid; o < MT * 256; o += kThreadsRows) {
         const int ml = o >> 4, nl = o & 15, t = ml >> 4, mm = ml & 15;
         const int l = (mm >> 2) * 16 + nl, j = mm & 3;      // C[m][n] of the tile: lane, element
-        if (ml >= M || n0 + nl >= N) continue;
+        if (m0 + ml >= M || n0 + nl >= N) continue;
         float sum[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
@@ -175,18 +175,29 @@ __global__ __launch_bounds__(kThreadsRows) void k_linear_rows(const RowsArgs a, 
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) sum[i] += s_red[w][i * MT + t][j][l];
         }
-        if constexpr (G == 1) finish_linear1<XDT>(a.e, ml, n0 + nl, sum[0]);
-        else finish_gated1<XDT>(a.e, ml, n0 + nl, sum[0], sum[1]);
+        if constexpr (G == 1) finish_linear1<XDT>(a.e, m0 + ml, n0 + nl, sum[0]);
+        else finish_gated1<XDT>(a.e, m0 + ml, n0 + nl, sum[0], sum[1]);
     }
+}
+
+template <typename... KArgs, typename... Args>
+hipError_t launch_2d(void (*kernel)(KArgs...), dim3 grid, size_t lds, hipStream_t s, Args&&... args)
+{
+    std::tuple<KArgs...> vals(std::forward<Args>(args)...);
+    return std::apply(
+        [&](auto&... v) {
+            void* ptrs[] = {static_cast<void*>(&v)...};
+            return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kThreadsRows), ptrs, lds, s);
+        },
+        vals);
 }
 
 template <int XDT, bool DQ, int G>
 hipError_t rows_as(const RowsArgs& a, const QbTables* tab, hipStream_t s)
 {
-    const int64_t grid = (a.e.N + 15) / 16, steps = (a.K + kStepK - 1) / kStepK;
-    if (grid >= (int64_t(1) << 22) || a.M > kRowsMax) return hipErrorInvalidValue;
+    const int64_t gx = (a.e.N + 15) / 16, steps = (a.K + kStepK - 1) / kStepK;
     auto go = [&](auto kernel, size_t lds) {
-        return launch_kernel_lds(kernel, (int)grid, kThreadsRows, lds, s, a, tab);
+        return launch_2d(kernel, dim3((unsigned)gx), lds, s, a, tab);
     };
     if constexpr (XDT != DT_F32) {
         if (a.M <= kXsRows && a.M * steps * kStepK * 2 <= kXsBytes)
@@ -194,7 +205,19 @@ hipError_t rows_as(const RowsArgs& a, const QbTables* tab, hipStream_t s)
     }
     if (a.M <= 16) return go(k_linear_rows<XDT, DQ, G, 1, false>, 0);
     if (a.M <= 32) return go(k_linear_rows<XDT, DQ, G, 2, false>, 0);
-    return go(k_linear_rows<XDT, DQ, G, 4, false>, 0);
+    // 64 rows a workgroup; rows beyond a grid's in launches of their own
+    constexpr int64_t kMost = 32768 * 64;
+    constexpr int ES = XDT == DT_F32 ? 4 : 2;
+    for (int64_t m = 0; m < a.M; m += kMost) {
+        RowsArgs b = a;
+        b.M = a.M - m < kMost ? a.M - m : kMost;
+        b.x = static_cast<const char*>(a.x) + m * a.K * ES;
+        b.e = epilogue_rows(a.e, m, ES);
+        const dim3 grid((unsigned)gx, (unsigned)((b.M + 63) / 64));
+        const hipError_t e = launch_2d(k_linear_rows<XDT, DQ, G, 4, false>, grid, 0, s, b, tab);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <int XDT>

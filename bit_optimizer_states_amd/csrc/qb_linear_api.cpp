@@ -90,7 +90,7 @@ qb_status check_ws(size_t need, const void* ws, size_t ws_bytes)
     return ws_bytes < need ? QB_EWORKSPACE : QB_OK;
 }
 
-// Workspace of a forward call from kRowsMax rows on: the weights' `rows` rows, then the
+// Workspace of a forward call that dequantizes the weights first: the weights' `rows` rows, then the
 // partial sums of a split product.
 size_t unpacked_bytes(int xdt, int64_t K, int64_t rows)
 {
@@ -99,7 +99,7 @@ size_t unpacked_bytes(int xdt, int64_t K, int64_t rows)
 
 size_t forward_bytes(int xdt, int64_t M, int64_t K, int64_t rows)
 {
-    return M <= kRowsMax ? 0 : unpacked_bytes(xdt, K, rows) + (size_t)gemm_part_floats(M, rows) * sizeof(float);
+    return takes_rows(M, K) ? 0 : unpacked_bytes(xdt, K, rows) + (size_t)gemm_part_floats(M, rows) * sizeof(float);
 }
 
 float* forward_part(int xdt, int64_t K, int64_t rows, void* ws)
@@ -173,7 +173,7 @@ qb_status qb_dequant_linear(const void* x, qb_dtype xdt, int64_t M, int64_t K, c
     if (st != QB_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Epilogue e{bias, residual, z, nullptr, y, N, (int32_t)bdt, (int32_t)act};
-    if (M <= kRowsMax) return hip_status(launch_linear_rows(xdt, x, M, K, &w, 1, f, e, s));
+    if (takes_rows(M, K)) return hip_status(launch_linear_rows(xdt, x, M, K, &w, 1, f, e, s));
     hipError_t err = launch_unpack(xdt, &w, 1, N, K, f, ws, s);
     if (err == hipSuccess)
         err = launch_gemm(xdt, false, GemmArgs{x, nullptr, ws, M, N, K, K, K, gemm_pitch(xdt, K)}, e,
@@ -264,7 +264,7 @@ qb_status qb_dequant_gated(const void* x, qb_dtype xdt, int64_t M, int64_t K, co
     if (st != QB_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Epilogue e{nullptr, nullptr, gate_out, up_out, y, N, 0, (int32_t)act};
-    if (M <= kRowsMax) return hip_status(launch_linear_rows(xdt, x, M, K, w, 2, f, e, s));
+    if (takes_rows(M, K)) return hip_status(launch_linear_rows(xdt, x, M, K, w, 2, f, e, s));
     hipError_t err = launch_unpack(xdt, w, 2, N, K, f, ws, s);
     if (err == hipSuccess)
         err = launch_gemm(xdt, true, GemmArgs{x, nullptr, ws, M, gated_rows(N), K, K, K, gemm_pitch(xdt, K)}, e,
