@@ -108,4 +108,35 @@ __device__ __forceinline__ void act_both(int act, float x, float& value, float& 
     }
 }
 
+// a[j] *= act'(z[j]), b[j] *= act(z[j]) (act known at compile time).
+template <int ACT, int N>
+__device__ __forceinline__ void times_act_of(const float* z, float* a, float* b)
+{
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        float value, slope;
+        act_both(ACT, z[j], value, slope);
+        a[j] *= slope;
+        if (b) b[j] *= value;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void times_act_both(int act, const float* z, float* a, float* b)
+{
+    switch (act) {
+    case ACT_RELU: return times_act_of<ACT_RELU, N>(z, a, b);
+    case ACT_GELU: return times_act_of<ACT_GELU, N>(z, a, b);
+    case ACT_GELU_TANH: return times_act_of<ACT_GELU_TANH, N>(z, a, b);
+    case ACT_SILU: return times_act_of<ACT_SILU, N>(z, a, b);
+    default: return times_act_of<ACT_NONE, N>(z, a, b);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void times_act_slopes(int act, const float* z, float* d)
+{
+    times_act_both<N>(act, z, d, nullptr);
+}
+
 }  // namespace qb

@@ -5,19 +5,22 @@
 namespace qb {
 
 // Gradients of one launch, passed by value: no table is copied to the device, so that the
-// calls may be captured into a graph and need no host memory afterwards (3.5 KB of
-// kernel arguments).
-constexpr int kGradsPerLaunch = 120;
+// calls may be captured into a graph and need no host memory afterwards (3.6 KB of
+// kernel arguments).  size[i]: elements << 2 | dtype; tiles: of all of them.
+constexpr int kNormGrads = 224, kScaleGrads = 150;
 
-struct GradTable {
-    const void* g[kGradsPerLaunch];
-    void* out[kGradsPerLaunch];
-    int64_t n[kGradsPerLaunch];
-    int32_t tile_begin[kGradsPerLaunch + 1];     // first tile of every gradient; the last is the total
-    uint8_t dt[kGradsPerLaunch];
-    int32_t count;
+struct NormTable {
+    const void* g[kNormGrads];
+    uint64_t size[kNormGrads];
+    int32_t count, tiles;
 };
-static_assert(sizeof(GradTable) <= 3600, "kernel arguments are at most 4 KB");
+struct ScaleTable {
+    const void* g[kScaleGrads];
+    void* out[kScaleGrads];
+    uint64_t size[kScaleGrads];
+    int32_t count, tiles;
+};
+static_assert(sizeof(NormTable) <= 3700 && sizeof(ScaleTable) <= 3700, "kernel arguments are at most 4 KB");
 
 // A tile is a wave's 8 accesses of 16 bytes a lane.
 constexpr int64_t grad_tile_elems(int dt) { return 64 * 8 * (dt == 0 ? 4 : 8); }
@@ -29,11 +32,11 @@ constexpr int kNormFewTiles = 64;
 
 // part[0 .. groups) = the sums of squares of the workgroups of one launch; returns their
 // number.  norm != nullptr: one workgroup, which writes sqrt of its sum there.
-hipError_t launch_grad_squares(const GradTable& t, double* part, int* groups, float* norm, hipStream_t s);
+hipError_t launch_grad_squares(const NormTable& t, double* part, int* groups, float* norm, hipStream_t s);
 // norm[0] = sqrt(sum of part), in order.
 hipError_t launch_grad_norm(const double* part, int count, float* norm, hipStream_t s);
 // out = g * min(1, max_norm / (norm[0] + 1e-6)), every gradient from its end (the table
 // lists the gradients from the last on).
-hipError_t launch_grad_scale(const GradTable& t, double max_norm, const float* norm, hipStream_t s);
+hipError_t launch_grad_scale(const ScaleTable& t, double max_norm, const float* norm, hipStream_t s);
 
 }  // namespace qb

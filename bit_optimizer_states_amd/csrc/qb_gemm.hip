@@ -3,8 +3,8 @@
 //
 // From a few hundred rows on the products bound the layer, not the weights: each
 // weight is dequantized once into a workspace in the compute dtype (N K elements written
-// and read back, mostly through the last-level cache), and C = A B^T runs at the matrix
-// instructions' rate, with the layer's epilogue on the binary32 sums in registers.
+// and read back), and C = A B^T runs at the matrix instructions' rate, with the layer's
+// epilogue on the binary32 sums.
 #include "qb_linear.h"
 #include "qb_mm_device.h"
 #include "qb_epilogue.h"
@@ -13,130 +13,88 @@ namespace qb {
 
 namespace {
 
+int64_t tiles_over(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+
 // ---------------------------------------------------------------------------
 // weights into the compute dtype
 // ---------------------------------------------------------------------------
-
-template <bool DQ>
-__device__ __forceinline__ void stage_code_tables(float* s_val, float* s_dyn, int code4, const QbTables* tab)
-{
-    if (threadIdx.x < 16) s_val[threadIdx.x] = (code4 == 0 ? tab->nf4 : tab->fp4)[threadIdx.x];
-    if constexpr (DQ) {
-        if (threadIdx.x < 256) s_dyn[threadIdx.x] = tab->dyn8[threadIdx.x];
-    }
-}
-
-// The constant of block blk.
-template <bool DQ>
-__device__ __forceinline__ float block_constant(const Weight4& w, int64_t blk, int log2B2, const float* s_dyn, float mu)
-{
-    if constexpr (DQ) return s_dyn[gld<uint8_t>(w.c2 + blk)] * gld<float>(w.absmax2 + (blk >> log2B2)) + mu;
-    else return gld<float>(w.absmax + blk);
-}
 
 struct Weights2 {
     Weight4 w[2];
 };
 
-template <int XDT>
-__device__ __forceinline__ void store_frag(void* p, const Frag<XDT>& f)
-{
-    if constexpr (XDT == DT_F32) {
-        gst<f32x4>(p, f32x4{f.w[0], f.w[1], f.w[2], f.w[3]});
-        gst<f32x4>(static_cast<char*>(p) + 16, f32x4{f.w[4], f.w[5], f.w[6], f.w[7]});
-    } else {
-        gst<u32x4>(p, u32x4{f.w[0], f.w[1], f.w[2], f.w[3]});
-    }
-}
-
-// A thread takes 8 weights at a time: 4 bytes of codes, 16 bytes out (consecutive lanes next
-// to each other).  A unit of work is 256 threads' worth of a row.
+// Transposed, into out[k][n]: a workgroup takes 64 rows n and 128 columns k, 8 weights of two
+// neighbouring rows a thread at a time into LDS, and writes rows k of 64 n (128 bytes, 256 in
+// binary32).  16-byte chunk c of LDS row k lies at chunk c ^ spread(k): the threads of a
+// wave, which hold 16 k eight apart and 4 row pairs, write to different banks but for two
+// each.  (Rows padded by 16 bytes instead fell into one bank: 4096 x 4096 15.1 us.)
 template <int XDT, bool DQ>
-__global__ __launch_bounds__(256) void k_unpack(const Weights2 ws, int count, int64_t N, int64_t K, int64_t pitch,
-                                                const Weight4Format f, void* __restrict__ out,
-                                                const QbTables* __restrict__ tab)
-{
-    constexpr int ES = XDT == DT_F32 ? 4 : 2;
-    __shared__ float s_val[16];
-    __shared__ float s_dyn[DQ ? 256 : 1];
-    stage_code_tables<DQ>(s_val, s_dyn, f.code4, tab);
-    __syncthreads();
-    const int64_t per_row = (K + 2047) / 2048, units = per_row * N * count;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t row = u / per_row;
-        const int64_t k = (u - row * per_row) * 2048 + threadIdx.x * 8;
-        if (k >= K) continue;
-        const int which = count == 2 && row >= N ? 1 : 0;
-        const Weight4 w = ws.w[which];
-        const int64_t n = row - which * N, e = n * K + k;
-        const int64_t to = count == 2 ? n / 16 * 32 + which * 16 + n % 16 : n;
-        const float mu = DQ ? gld<float>(w.offset) : 0.0f;
-        Frag<XDT> v;
-        dequant_frag<XDT>(gld<uint32_t>(w.codes + e / 2), block_constant<DQ>(w, e >> f.log2B, f.log2B2, s_dyn, mu),
-                          s_val, v);
-        store_frag<XDT>(static_cast<char*>(out) + (to * pitch + k) * ES, v);
-    }
-}
-
-// Transposed: a workgroup takes 64 rows n and 128 columns k, 8 weights a thread at a time
-// into LDS, and writes rows k of 64 n.
-template <int XDT, bool DQ>
-__global__ __launch_bounds__(256) void k_unpack_transposed(const Weights2 ws, int count, int64_t N, int64_t K,
-                                                           int64_t pitch, const Weight4Format f, void* __restrict__ out,
+__global__ __launch_bounds__(256) void k_unpack_transposed(const Weights2 ws, int64_t N, int64_t K, int64_t pitch,
+                                                           int64_t np, const Weight4Format f, void* __restrict__ out,
                                                            const QbTables* __restrict__ tab)
 {
     constexpr int ES = XDT == DT_F32 ? 4 : 2;
-    constexpr int LP = 64 * ES + (XDT == DT_F32 ? 16 : 16);       // bytes of an LDS row of 64 n
+    constexpr int LP = 64 * ES, CPR = LP / 16;                // bytes and chunks of an LDS row of 64 n
     __shared__ __attribute__((aligned(16))) char s_t[128 * LP];
     __shared__ float s_val[16];
     __shared__ float s_dyn[DQ ? 256 : 1];
-    stage_code_tables<DQ>(s_val, s_dyn, f.code4, tab);
+    const int tid = threadIdx.x, kl = (tid & 15) * 8;
+    const int64_t k0 = (int64_t)blockIdx.x * 128, n0 = (int64_t)blockIdx.y * 64;
+    const Weight4 w = ws.w[blockIdx.z];
+    // row pairs tid / 16 and tid / 16 + 16 of the tile: codes and constants of 8 weights of each row
+    uint32_t code[2][2], c2[2][2];
+    float a[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t n = n0 + 2 * ((tid >> 4) + 16 * i) + h, e = n * K + k0 + kl, blk = e >> f.log2B;
+            code[i][h] = c2[i][h] = 0u;
+            a[i][h] = 0.0f;
+            if (n < N && k0 + kl < K) {
+                code[i][h] = gld<uint32_t>(w.codes + e / 2);
+                if constexpr (DQ) {
+                    c2[i][h] = gld<uint8_t>(w.c2 + blk);
+                    a[i][h] = gld<float>(w.absmax2 + (blk >> f.log2B2));
+                } else {
+                    a[i][h] = gld<float>(w.absmax + blk);
+                }
+            }
+        }
+    const float mu = DQ ? gld<float>(w.offset) : 0.0f;
+    if (tid < 16) s_val[tid] = (f.code4 == 0 ? tab->nf4 : tab->fp4)[tid];
+    if constexpr (DQ) s_dyn[tid] = tab->dyn8[tid];
     __syncthreads();
-    const int64_t np = pitch / count, tn = np / 64 + (np % 64 ? 1 : 0), tk = (K + 127) / 128, tiles = tn * tk * count;
-    const int tid = threadIdx.x;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t tw = t / tk, k0 = (t - tw * tk) * 128;
-        const int which = (int)(tw / tn);
-        const int64_t n0 = (tw - which * tn) * 64;
-        const Weight4 w = ws.w[which];
-        const float mu = DQ ? gld<float>(w.offset) : 0.0f;
-        // lane: 8 columns k, rows 2 q and 2 q + 1 of the tile, 16 row pairs at a time
-        const int kl = (tid & 15) * 8;
+    auto spread = [](int k) { return XDT == DT_F32 ? ((k >> 3) & 7) * 2 : (k >> 3) & 7; };
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int pr = (tid >> 4) + 16 * i;
-            Frag<DT_F32> v[2];
+    for (int i = 0; i < 2; ++i) {
+        const int pr = (tid >> 4) + 16 * i;
+        Frag<DT_F32> v[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t n = n0 + 2 * pr + h, e = n * K + k0 + kl;
-                if (n < N && k0 + kl < K) {
-                    dequant_frag<DT_F32>(gld<uint32_t>(w.codes + e / 2),
-                                         block_constant<DQ>(w, e >> f.log2B, f.log2B2, s_dyn, mu), s_val, v[h]);
-                } else {
-                    frag_zero<DT_F32>(v[h]);
-                }
-            }
+        for (int h = 0; h < 2; ++h) {
+            const int64_t n = n0 + 2 * pr + h;
+            const float c = DQ ? s_dyn[c2[i][h]] * a[i][h] + mu : a[i][h];       // two rounded operations
+            dequant_frag<DT_F32>(code[i][h], n < N ? c : 0.0f, s_val, v[h]);     // zeros beyond the last row
+        }
+        const int at = 2 * pr * ES;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                char* const p = s_t + (kl + j) * LP + 2 * pr * ES;
-                if constexpr (XDT == DT_F32) {
-                    reinterpret_cast<float*>(p)[0] = v[0].w[j];
-                    reinterpret_cast<float*>(p)[1] = v[1].w[j];
-                } else {
-                    *reinterpret_cast<uint32_t*>(p) = pack_pair<XDT>(v[0].w[j], v[1].w[j]);
-                }
+        for (int j = 0; j < 8; ++j) {
+            char* const p = s_t + (kl + j) * LP + ((at / 16) ^ spread(kl)) * 16 + at % 16;
+            if constexpr (XDT == DT_F32) {
+                typedef float f32x2_t __attribute__((ext_vector_type(2)));
+                *reinterpret_cast<f32x2_t*>(p) = f32x2_t{v[0].w[j], v[1].w[j]};
+            } else {
+                *reinterpret_cast<uint32_t*>(p) = pack_pair<XDT>(v[0].w[j], v[1].w[j]);
             }
         }
-        __syncthreads();
-        constexpr int CPR = 64 * ES / 16;                    // 16-byte chunks of a row
+    }
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 128 * CPR / 256; ++i) {
-            const int o = tid + 256 * i, row = o / CPR, c = o % CPR;
-            if (k0 + row < K && n0 + c * (16 / ES) < np)
-                gst<u32x4>(static_cast<char*>(out) + ((k0 + row) * pitch + which * np + n0) * ES + 16 * c,
-                           *reinterpret_cast<const u32x4*>(s_t + row * LP + 16 * c));
-        }
-        __syncthreads();
+    for (int i = 0; i < 128 * CPR / 256; ++i) {
+        const int o = tid + 256 * i, row = o / CPR, c = o % CPR;
+        if (k0 + row < K && n0 + c * (16 / ES) < np)
+            gst<u32x4>(static_cast<char*>(out) + ((k0 + row) * pitch + blockIdx.z * np + n0) * ES + 16 * c,
+                       *reinterpret_cast<const u32x4*>(s_t + row * LP + (c ^ spread(row)) * 16));
     }
 }
 
@@ -291,13 +249,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
 #pragma unroll
         for (int i = 0; i < B_PER; ++i) {
             int64_t row = (i * NW + wave) * 8 + row8;
-            row = n0 + row < p.g.R ? row : p.g.R - 1 - n0;
+            if constexpr (GATED) {                     // rows 16 g .. of one weight, then of the other
+                row = row / 32 * 16 + row % 16;
+                row = n0 / 2 + row < p.e.N ? row : p.e.N - 1 - n0 / 2;
+            } else {
+                row = n0 + row < p.g.R ? row : p.g.R - 1 - n0;
+            }
             b_off[i] = (uint32_t)(row * p.g.ldb * ES + c * 16);
         }
     }
     const char* const a0 = static_cast<const char*>(p.g.a0) + m0 * p.g.lda * ES;
     const char* const a1 = static_cast<const char*>(p.g.a1) + m0 * p.g.lda * ES - (int64_t)p.steps0 * 128;
-    const char* const b0 = static_cast<const char*>(p.g.b) + n0 * p.g.ldb * ES;
+    // a gated block's waves load 8 rows of 16 alternately from the two weights, each always from the same one
+    static_assert(!GATED || NW % 4 == 0, "a wave's loads are of one weight");
+    const char* const b0 = GATED ? static_cast<const char*>((wave >> 1) & 1 ? p.g.b1 : p.g.b) + n0 / 2 * p.g.ldb * ES
+                                 : static_cast<const char*>(p.g.b) + n0 * p.g.ldb * ES;
 
     // a length of half a step too many: its last step begins half a step early, and only its
     // upper half is multiplied
@@ -439,7 +405,7 @@ GemmParams rows_of(const GemmParams& all, int64_t m, int64_t rows)
     return p;
 }
 
-int64_t tiles_over(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+
 
 // Columns n_first .. R - 1 of B in BN-wide tiles (`columns` tiles of them at most).
 template <int XDT, int BM, int BN, int WM, int WN, bool GATED>
@@ -497,50 +463,42 @@ hipError_t gemm_rows(const GemmParams& p, hipStream_t s)
 }
 
 template <int XDT, bool DQ>
-hipError_t unpack_as(const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
-                     bool transposed, hipStream_t s)
+hipError_t transposed_as(const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
+                         hipStream_t s)
 {
     const QbTables* tab = device_tables();
     if (!tab) return hipErrorNotInitialized;
-    Weights2 ws{{w[0], w[count - 1]}};
-    if (transposed) {
-        const int64_t np = gemm_pitch(XDT, N), tiles = (np + 63) / 64 * ((K + 127) / 128) * count;
-        const int grid = persistent_grid(k_unpack_transposed<XDT, DQ>, tiles);
-        return launch_kernel(k_unpack_transposed<XDT, DQ>, grid, s, ws, count, N, K, np * count, f, out, tab);
-    }
-    const int64_t units = (K + 2047) / 2048 * N * count;
-    const int grid = persistent_grid(k_unpack<XDT, DQ>, units);
-    return launch_kernel(k_unpack<XDT, DQ>, grid, s, ws, count, N, K, gemm_pitch(XDT, K), f, out, tab);
+    const Weights2 ws{{w[0], w[count - 1]}};
+    const int64_t np = gemm_pitch(XDT, N), pitch = np * count;
+    const dim3 grid((unsigned)tiles_over(K, 128), (unsigned)tiles_over(np, 64), (unsigned)count);
+    return launch_grid(k_unpack_transposed<XDT, DQ>, grid, 256, 0, s, ws, N, K, pitch, np, f, out, tab);
 }
 
-hipError_t unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
-                  bool transposed, hipStream_t s)
+template <int XDT>
+hipError_t transposed_dq(const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
+                         hipStream_t s)
 {
-    switch (xdt) {
-    case DT_F32:
-        return f.nested ? unpack_as<DT_F32, true>(w, count, N, K, f, out, transposed, s)
-                        : unpack_as<DT_F32, false>(w, count, N, K, f, out, transposed, s);
-    case DT_F16:
-        return f.nested ? unpack_as<DT_F16, true>(w, count, N, K, f, out, transposed, s)
-                        : unpack_as<DT_F16, false>(w, count, N, K, f, out, transposed, s);
-    default:
-        return f.nested ? unpack_as<DT_BF16, true>(w, count, N, K, f, out, transposed, s)
-                        : unpack_as<DT_BF16, false>(w, count, N, K, f, out, transposed, s);
-    }
+    return f.nested ? transposed_as<XDT, true>(w, count, N, K, f, out, s)
+                    : transposed_as<XDT, false>(w, count, N, K, f, out, s);
 }
 
 }  // namespace
 
-hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
+hipError_t launch_unpack(int xdt, const Weight4& w, int64_t N, int64_t K, const Weight4Format& f, void* out,
                          hipStream_t s)
 {
-    return unpack(xdt, w, count, N, K, f, out, false, s);
+    const DequantDesc d{w.codes, w.absmax, w.c2, w.absmax2, w.offset, out, N * K, 0};
+    return launch_dequant4_kept(d, f.code4, 1 << f.log2B, 1 << f.log2B2, f.nested != 0, xdt, s);
 }
 
 hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f,
                                     void* out, hipStream_t s)
 {
-    return unpack(xdt, w, count, N, K, f, out, true, s);
+    switch (xdt) {
+    case DT_F32: return transposed_dq<DT_F32>(w, count, N, K, f, out, s);
+    case DT_F16: return transposed_dq<DT_F16>(w, count, N, K, f, out, s);
+    default: return transposed_dq<DT_BF16>(w, count, N, K, f, out, s);
+    }
 }
 
 // Pieces of the length of a product of few tiles: about three workgroups of 64 x 64 a CU,

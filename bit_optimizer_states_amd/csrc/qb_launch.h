@@ -182,6 +182,19 @@ hipError_t launch_kernel_lds(void (*kernel)(KArgs...), int grid, int threads, si
         vals);
 }
 
+// The same on a grid of up to three dimensions.
+template <typename... KArgs, typename... Args>
+hipError_t launch_grid(void (*kernel)(KArgs...), dim3 grid, int threads, size_t lds, hipStream_t s, Args&&... args)
+{
+    std::tuple<KArgs...> vals(std::forward<Args>(args)...);
+    return std::apply(
+        [&](auto&... v) {
+            void* ptrs[] = {static_cast<void*>(&v)...};
+            return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), ptrs, lds, s);
+        },
+        vals);
+}
+
 template <typename... KArgs, typename... Args>
 hipError_t launch_kernel(void (*kernel)(KArgs...), int grid, hipStream_t s, Args&&... args)
 {
@@ -266,6 +279,9 @@ hipError_t launch_dq_mean(const QuantDesc& single, const TileMap<QuantDesc>* map
 // all); bits 8 (dynamic code) or 4 (code4: 0 NF4, 1 FP4); dq: nested absmax.
 hipError_t launch_dequant(const DequantDesc& single, const TileMap<DequantDesc>* map, int64_t ntiles, int bits,
                           int code4, int B, int B2, bool dq, int ydt, hipStream_t s);
+
+// One tensor of 4-bit codes, its values left in the caches for the kernel behind.
+hipError_t launch_dequant4_kept(const DequantDesc& d, int code4, int B, int B2, bool dq, int ydt, hipStream_t s);
 
 // Elements per tile of the dequantization kernel: 4-bit codes for one tensor
 // and for a grouped launch, and 8-bit codes into binary32 and into 16-bit

@@ -56,31 +56,30 @@ constexpr bool takes_rows(int64_t M, int64_t K) { return M <= kRowsMax || K < 64
 hipError_t launch_linear_rows(int xdt, const void* x, int64_t M, int64_t K, const Weight4* w, int count,
                               const Weight4Format& f, const Epilogue& e, hipStream_t s);
 
-// Elements of a step of the tiled product, and of the multiples that its operands' rows
-// are padded to: 128 bytes.
+// Elements of a step of the tiled product, and of the multiples that the reduced dimension
+// of a gradient is padded to: 128 bytes.
 constexpr int64_t gemm_step(int dt) { return dt == 0 ? 32 : 64; }
 constexpr int64_t gemm_pitch(int dt, int64_t k) { return (k + gemm_step(dt) - 1) / gemm_step(dt) * gemm_step(dt); }
-// Rows of the two weights of a gated block, dealt in groups of 16: rows 16 g .. 16 g + 15
-// of the first, then of the second.
+// Columns of a gated block's product: those of the two weights, dealt in groups of 16.
 constexpr int64_t gated_rows(int64_t n) { return (n + 15) / 16 * 32; }
 
-// Weights in the compute dtype: out[row of n][k] of pitch gemm_pitch(K), for a gated block
-// the rows of both dealt as above.
-hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
+// A weight in the compute dtype, out[n][k] (as qb_dequantize).
+hipError_t launch_unpack(int xdt, const Weight4& w, int64_t N, int64_t K, const Weight4Format& f, void* out,
                          hipStream_t s);
-// The same transposed: out[k][n], for two weights next to each other (columns n of the
-// second at gemm_pitch(N) + n); the pitch is count * gemm_pitch(N), its padding zero.
+// Transposed: out[k][n], for two weights next to each other (columns n of the second at
+// gemm_pitch(N) + n); the pitch is count * gemm_pitch(N), its padding zero.
 hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f,
                                     void* out, hipStream_t s);
 
 // C = epilogue(A B^T).  A [M, len] in one or two pieces of columns (a0: the first len0, a1
 // the others; both of `lda` elements a row, 16-byte aligned rows), B [R, len] of ldb
-// elements a row.  len is at least a step and a multiple of half a step, len0 of a step
+// elements a row; gated: B is dealt from b and b1, of N rows each, and R = gated_rows(N).  len is at least a step and a multiple of half a step, len0 of a step
 // unless it is len.
 struct GemmArgs {
     const void* a0;
     const void* a1;
     const void* b;
+    const void* b1;
     int64_t M, R, len0, len, lda, ldb;
 };
 // part: room for the partial sums of a product split over its length, gemm_part_floats()

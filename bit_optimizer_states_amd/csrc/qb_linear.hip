@@ -180,24 +180,12 @@ __global__ __launch_bounds__(kThreadsRows) void k_linear_rows(const RowsArgs a, 
     }
 }
 
-template <typename... KArgs, typename... Args>
-hipError_t launch_2d(void (*kernel)(KArgs...), dim3 grid, size_t lds, hipStream_t s, Args&&... args)
-{
-    std::tuple<KArgs...> vals(std::forward<Args>(args)...);
-    return std::apply(
-        [&](auto&... v) {
-            void* ptrs[] = {static_cast<void*>(&v)...};
-            return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kThreadsRows), ptrs, lds, s);
-        },
-        vals);
-}
-
 template <int XDT, bool DQ, int G>
 hipError_t rows_as(const RowsArgs& a, const QbTables* tab, hipStream_t s)
 {
     const int64_t gx = (a.e.N + 15) / 16, steps = (a.K + kStepK - 1) / kStepK;
     auto go = [&](auto kernel, size_t lds) {
-        return launch_2d(kernel, dim3((unsigned)gx), lds, s, a, tab);
+        return launch_grid(kernel, dim3((unsigned)gx), kThreadsRows, lds, s, a, tab);
     };
     if constexpr (XDT != DT_F32) {
         if (a.M <= kXsRows && a.M * steps * kStepK * 2 <= kXsBytes)
@@ -214,7 +202,7 @@ hipError_t rows_as(const RowsArgs& a, const QbTables* tab, hipStream_t s)
         b.x = static_cast<const char*>(a.x) + m * a.K * ES;
         b.e = epilogue_rows(a.e, m, ES);
         const dim3 grid((unsigned)gx, (unsigned)((b.M + 63) / 64));
-        const hipError_t e = launch_2d(k_linear_rows<XDT, DQ, G, 4, false>, grid, 0, s, b, tab);
+        const hipError_t e = launch_grid(k_linear_rows<XDT, DQ, G, 4, false>, grid, kThreadsRows, 0, s, b, tab);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

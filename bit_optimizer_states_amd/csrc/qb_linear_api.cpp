@@ -21,7 +21,7 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int dtype_bytes(int d) { return d == QB_F32 ? 4 : 2; }
 
 constexpr int64_t kRowMax = int64_t(1) << 31;        // rows of x
-constexpr int64_t kGradMax = int64_t(1) << 33;       // elements of a gradient
+constexpr int64_t kGradMax = int64_t(1) << 33;       // elements of a gradient: 2^22 tiles at most
 constexpr int64_t kWidthMax = int64_t(1) << 21;      // inputs, outputs of a layer
 
 qb_status hip_status(hipError_t e)
@@ -90,21 +90,32 @@ qb_status check_ws(size_t need, const void* ws, size_t ws_bytes)
     return ws_bytes < need ? QB_EWORKSPACE : QB_OK;
 }
 
-// Workspace of a forward call that dequantizes the weights first: the weights' `rows` rows, then the
-// partial sums of a split product.
-size_t unpacked_bytes(int xdt, int64_t K, int64_t rows)
+// Workspace of a forward call that dequantizes its weights first: these, then the partial
+// sums of a split product of R columns.
+size_t unpacked_bytes(int xdt, int64_t K, int64_t N)
 {
-    return round_up((size_t)rows * (size_t)gemm_pitch(xdt, K) * dtype_bytes(xdt), 256);
+    return round_up((size_t)N * (size_t)K * dtype_bytes(xdt), 256);
 }
 
-size_t forward_bytes(int xdt, int64_t M, int64_t K, int64_t rows)
+size_t forward_bytes(int xdt, int64_t M, int64_t K, int64_t N, int count)
 {
-    return takes_rows(M, K) ? 0 : unpacked_bytes(xdt, K, rows) + (size_t)gemm_part_floats(M, rows) * sizeof(float);
+    if (takes_rows(M, K)) return 0;
+    return count * unpacked_bytes(xdt, K, N) +
+           (size_t)gemm_part_floats(M, count == 2 ? gated_rows(N) : N) * sizeof(float);
 }
 
-float* forward_part(int xdt, int64_t K, int64_t rows, void* ws)
+// y = epilogue(x W^T) through the workspace.
+hipError_t unpack_and_multiply(int xdt, const void* x, int64_t M, int64_t K, const Weight4* w, int count, int64_t N,
+                               const Weight4Format& f, const Epilogue& e, void* ws, hipStream_t s)
 {
-    return reinterpret_cast<float*>(static_cast<char*>(ws) + unpacked_bytes(xdt, K, rows));
+    const size_t each = unpacked_bytes(xdt, K, N);
+    char* const b = static_cast<char*>(ws);
+    for (int i = 0; i < count; ++i) {
+        const hipError_t err = launch_unpack(xdt, w[i], N, K, f, b + i * each, s);
+        if (err != hipSuccess) return err;
+    }
+    const GemmArgs g{x, nullptr, b, b + (count - 1) * each, M, count == 2 ? gated_rows(N) : N, K, K, K, K};
+    return launch_gemm(xdt, count == 2, g, e, reinterpret_cast<float*>(b + count * each), s);
 }
 
 // Workspace of a gradient: the weights transposed, dz (dg and du) padded, the partial
@@ -136,7 +147,7 @@ hipError_t input_gradient(int xdt, const void* dz0, const void* dz1, int64_t lda
     const int64_t pitch = gemm_pitch(xdt, N);
     hipError_t e = launch_unpack_transposed(xdt, w, count, N, K, f, ws, s);
     if (e != hipSuccess) return e;
-    const GemmArgs g{dz0, dz1, ws, M, K, pitch, pitch * count, lda, pitch * count};
+    const GemmArgs g{dz0, dz1, ws, nullptr, M, K, pitch, pitch * count, lda, pitch * count};
     Epilogue out{};
     out.y = dx;
     out.N = K;
@@ -149,7 +160,7 @@ extern "C" {
 
 size_t qb_dequant_linear_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int64_t N)
 {
-    return valid_sizes(xdt, M, K, N) ? forward_bytes(xdt, M, K, N) : 0;
+    return valid_sizes(xdt, M, K, N) ? forward_bytes(xdt, M, K, N, 1) : 0;
 }
 
 qb_status qb_dequant_linear(const void* x, qb_dtype xdt, int64_t M, int64_t K, const uint8_t* codes,
@@ -169,16 +180,12 @@ qb_status qb_dequant_linear(const void* x, qb_dtype xdt, int64_t M, int64_t K, c
     st = check_weight(w, &nested);
     if (st != QB_OK) return st;
     if (!aligned16(x) || !aligned16(bias) || !aligned16(residual) || !aligned16(z) || !aligned16(y)) return QB_EALIGN;
-    st = check_ws(forward_bytes(xdt, M, K, N), ws, ws_bytes);
+    st = check_ws(forward_bytes(xdt, M, K, N, 1), ws, ws_bytes);
     if (st != QB_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Epilogue e{bias, residual, z, nullptr, y, N, (int32_t)bdt, (int32_t)act};
     if (takes_rows(M, K)) return hip_status(launch_linear_rows(xdt, x, M, K, &w, 1, f, e, s));
-    hipError_t err = launch_unpack(xdt, &w, 1, N, K, f, ws, s);
-    if (err == hipSuccess)
-        err = launch_gemm(xdt, false, GemmArgs{x, nullptr, ws, M, N, K, K, K, gemm_pitch(xdt, K)}, e,
-                          forward_part(xdt, K, N, ws), s);
-    return hip_status(err);
+    return hip_status(unpack_and_multiply(xdt, x, M, K, &w, 1, N, f, e, ws, s));
 }
 
 size_t qb_dequant_linear_backward_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int64_t N)
@@ -240,7 +247,7 @@ qb_status qb_dequant_linear_backward(const void* dy, const void* z, qb_dtype xdt
 
 size_t qb_dequant_gated_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int64_t N)
 {
-    return valid_sizes(xdt, M, K, N) ? forward_bytes(xdt, M, K, gated_rows(N)) : 0;
+    return valid_sizes(xdt, M, K, N) ? forward_bytes(xdt, M, K, N, 2) : 0;
 }
 
 qb_status qb_dequant_gated(const void* x, qb_dtype xdt, int64_t M, int64_t K, const qb_weight* gate,
@@ -260,16 +267,12 @@ qb_status qb_dequant_gated(const void* x, qb_dtype xdt, int64_t M, int64_t K, co
         if (st != QB_OK) return st;
     }
     if (!aligned16(x) || !aligned16(gate_out) || !aligned16(up_out) || !aligned16(y)) return QB_EALIGN;
-    st = check_ws(forward_bytes(xdt, M, K, gated_rows(N)), ws, ws_bytes);
+    st = check_ws(forward_bytes(xdt, M, K, N, 2), ws, ws_bytes);
     if (st != QB_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Epilogue e{nullptr, nullptr, gate_out, up_out, y, N, 0, (int32_t)act};
     if (takes_rows(M, K)) return hip_status(launch_linear_rows(xdt, x, M, K, w, 2, f, e, s));
-    hipError_t err = launch_unpack(xdt, w, 2, N, K, f, ws, s);
-    if (err == hipSuccess)
-        err = launch_gemm(xdt, true, GemmArgs{x, nullptr, ws, M, gated_rows(N), K, K, K, gemm_pitch(xdt, K)}, e,
-                          forward_part(xdt, K, gated_rows(N), ws), s);
-    return hip_status(err);
+    return hip_status(unpack_and_multiply(xdt, x, M, K, w, 2, N, f, e, ws, s));
 }
 
 size_t qb_dequant_gated_backward_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int64_t N)
@@ -317,7 +320,7 @@ qb_status qb_dequant_gated_backward(const void* dy, const void* gate_out, const 
 size_t qb_multi_tensor_grad_norm_workspace_bytes(int32_t count)
 {
     if (count <= 0) return 0;
-    return (size_t)((count + kGradsPerLaunch - 1) / kGradsPerLaunch) * kNormGroups * sizeof(double);
+    return (size_t)((count + kNormGrads - 1) / kNormGrads) * kNormGroups * sizeof(double);
 }
 
 }  // extern "C"
@@ -340,23 +343,38 @@ qb_status check_grads(const qb_grad* grads, int32_t count, bool out)
     return QB_OK;
 }
 
-// The next launch's gradients: up to kGradsPerLaunch of the non-empty ones from *at on, in
-// steps of 1 or -1.
-void next_table(const qb_grad* grads, int32_t count, int32_t* at, int step, GradTable* t)
+uint64_t size_of(const qb_grad& g) { return (uint64_t)g.n << 2 | (uint64_t)g.dtype; }
+
+int32_t tiles_of(const qb_grad& g)
 {
-    t->count = 0;
-    t->tile_begin[0] = 0;
-    while (t->count < kGradsPerLaunch && *at >= 0 && *at < count) {
+    const int64_t tile = grad_tile_elems(g.dtype);
+    return (int32_t)((g.n + tile - 1) / tile);
+}
+
+// The next launch's gradients, empty ones left out: from *at on ...
+void next_table(const qb_grad* grads, int32_t count, int32_t* at, NormTable* t)
+{
+    t->count = t->tiles = 0;
+    for (; t->count < kNormGrads && *at < count; ++*at) {
         const qb_grad& g = grads[*at];
-        *at += step;
         if (g.n == 0) continue;
-        const int i = t->count++;
-        t->g[i] = g.g;
-        t->out[i] = g.out;
-        t->n[i] = g.n;
-        t->dt[i] = (uint8_t)g.dtype;
-        const int64_t tile = grad_tile_elems(g.dtype);
-        t->tile_begin[i + 1] = t->tile_begin[i] + (int32_t)((g.n + tile - 1) / tile);
+        t->g[t->count] = g.g;
+        t->size[t->count++] = size_of(g);
+        t->tiles += tiles_of(g);
+    }
+}
+
+// ... or from *at back.
+void next_table(const qb_grad* grads, int32_t* at, ScaleTable* t)
+{
+    t->count = t->tiles = 0;
+    for (; t->count < kScaleGrads && *at >= 0; --*at) {
+        const qb_grad& g = grads[*at];
+        if (g.n == 0) continue;
+        t->g[t->count] = g.g;
+        t->out[t->count] = g.out;
+        t->size[t->count++] = size_of(g);
+        t->tiles += tiles_of(g);
     }
 }
 
@@ -378,12 +396,12 @@ qb_status qb_multi_tensor_grad_norm(const qb_grad* grads, int32_t count, float* 
     int32_t at = 0;
     int parts = 0;
     while (at < count) {
-        GradTable t{};
+        NormTable t;
         const bool first = at == 0;
-        next_table(grads, count, &at, 1, &t);
+        next_table(grads, count, &at, &t);
         if (t.count == 0) continue;
         int groups = 0;
-        const bool few = first && at >= count && t.tile_begin[t.count] <= kNormFewTiles;
+        const bool few = first && at >= count && t.tiles <= kNormFewTiles;
         const hipError_t e = launch_grad_squares(t, part + parts, &groups, few ? norm : nullptr, s);
         if (e != hipSuccess || few) return hip_status(e);
         parts += groups;
@@ -400,8 +418,8 @@ qb_status qb_multi_tensor_clip_grads(const qb_grad* grads, int32_t count, double
     if (!aligned16(norm)) return QB_EALIGN;
     int32_t at = count - 1;
     while (at >= 0) {
-        GradTable t{};
-        next_table(grads, count, &at, -1, &t);
+        ScaleTable t;
+        next_table(grads, &at, &t);
         if (t.count == 0) continue;
         const hipError_t e = launch_grad_scale(t, max_norm, norm, static_cast<hipStream_t>(stream));
         if (e != hipSuccess) return hip_status(e);

@@ -16,8 +16,7 @@ namespace {
 constexpr int kCols = 512;               // columns of a workgroup: a wave's 64 units of 8
 constexpr int kGradWaves = 4;
 
-// The unit's values in the compute dtype at row `row` of an array of `width` columns;
-// with pad, units of zeros up to `width`.
+// A unit at row `row` of an array padded to `pitch` columns (a multiple of 8).
 template <int XDT>
 __device__ __forceinline__ void store_padded(void* p, int64_t row, int64_t pitch, int unit, const float* v)
 {
@@ -39,17 +38,24 @@ __device__ __forceinline__ void store_plain(void* p, int64_t row, int64_t N, int
     }
 }
 
-// Unit `unit` of a row (zeros beyond it).
-template <int XDT, int TAIL>
-__device__ __forceinline__ void load_values(const void* p, int64_t row, int64_t N, int unit, int units, float* v)
+// Row `row` of an array of N columns.
+template <int XDT>
+__device__ __forceinline__ const char* row_of(const void* p, int64_t row, int64_t N)
 {
-    const Unit<XDT> u = load_row_unit<XDT, TAIL, false>(static_cast<const char*>(p) + row * N * elem_bytes(XDT), unit,
-                                                        units, (int)N);
-    const int cnt = unit_count(unit, (int)N);
+    return static_cast<const char*>(p) + row * N * elem_bytes(XDT);
+}
+
+// A unit's values, zeros beyond the row.
+template <int XDT, int TAIL>
+__device__ __forceinline__ void unit_values(const Unit<XDT>& u, int unit, int N, float* v)
+{
+    const int cnt = unit_count(unit, N);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = j < cnt ? unit_at<XDT>(u, j) : 0.0f;
 }
 
+// Workgroup (block of columns, slice of rows); its waves take the slice's rows in turn, the
+// next row in flight.
 template <int XDT, int TAIL>
 __global__ __launch_bounds__(64 * kGradWaves) void k_linear_dz(const void* __restrict__ dy, const void* __restrict__ z,
                                                                int act, int64_t M, int64_t N, void* __restrict__ dz,
@@ -61,19 +67,26 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_linear_dz(const void* __res
     const int slice = blockIdx.x % slices;
     const int64_t block = blockIdx.x / slices;
     const int units = (int)((N + 7) / 8), unit = (int)(block * 64 + lane);
+    const int64_t step = (int64_t)slices * kGradWaves;
     float sum[8] = {};
-    for (int64_t m = slice * kGradWaves + wave; m < M; m += (int64_t)slices * kGradWaves) {
+    Unit<XDT> du, zu;
+    auto load_row = [&](int64_t m) {
+        if (m >= M) return;
+        du = load_row_unit<XDT, TAIL, false>(row_of<XDT>(dy, m, N), unit, units, (int)N);
+        if (z) zu = load_row_unit<XDT, TAIL, false>(row_of<XDT>(z, m, N), unit, units, (int)N);
+    };
+    int64_t m = slice * kGradWaves + wave;
+    load_row(m);
+    for (; m < M; m += step) {
         float d[8];
-        load_values<XDT, TAIL>(dy, m, N, unit, units, d);
+        unit_values<XDT, TAIL>(du, unit, (int)N, d);
         if (z) {
             float zv[8];
-            load_values<XDT, TAIL>(z, m, N, unit, units, zv);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float value, slope;
-                act_both(act, zv[j], value, slope);
-                d[j] *= slope;
-            }
+            unit_values<XDT, TAIL>(zu, unit, (int)N, zv);
+            load_row(m + step);
+            times_act_slopes<8>(act, zv, d);
+        } else {
+            load_row(m + step);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] += d[j];
@@ -92,16 +105,29 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_linear_dz(const void* __res
     }
 }
 
-__global__ __launch_bounds__(256) void k_bias_sum(const float* __restrict__ part, int slices, int64_t N, int accumulate,
-                                                  void* __restrict__ db, int bias_dt)
+// 64 columns a workgroup; the slices dealt to 16 waves, joined in wave order (4096 columns
+// of 128 slices: one thread a column takes 7 us).
+constexpr int kSumWaves = 16;
+
+__global__ __launch_bounds__(64 * kSumWaves) void k_bias_sum(const float* __restrict__ part, int slices, int64_t N,
+                                                             int accumulate, void* __restrict__ db, int bias_dt)
 {
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= N) return;
+    __shared__ float s_sum[kSumWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = (int64_t)blockIdx.x * 64 + lane;
     float v = 0.0f;
+    if (n < N) {
 #pragma unroll 8
-    for (int s = 0; s < slices; ++s) v += part[(int64_t)s * N + n];
-    if (accumulate) v += load1_rt(bias_dt, db, n);
-    store1_rt(bias_dt, db, n, v);
+        for (int s = wave; s < slices; s += kSumWaves) v += part[(int64_t)s * N + n];
+    }
+    s_sum[wave][lane] = v;
+    __syncthreads();
+    if (wave != 0 || n >= N) return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSumWaves; ++w) sum += s_sum[w][lane];
+    if (accumulate) sum += load1_rt(bias_dt, db, n);
+    store1_rt(bias_dt, db, n, sum);
 }
 
 template <int XDT, int TAIL>
@@ -114,18 +140,28 @@ __global__ __launch_bounds__(256) void k_gated_dz(const void* __restrict__ dh, c
     const int64_t block = blockIdx.x % blocks;
     const int64_t rows = (int64_t)gridDim.x / blocks * 4;
     const int units = (int)((N + 7) / 8), unit = (int)(block * 64 + lane);
-    for (int64_t m = (int64_t)(blockIdx.x / blocks) * 4 + wave; m < M; m += rows) {
+    Unit<XDT> du, gu, uu;
+    auto load_row = [&](int64_t m) {
+        if (m >= M) return;
+        du = load_row_unit<XDT, TAIL, true>(row_of<XDT>(dh, m, N), unit, units, (int)N);
+        gu = load_row_unit<XDT, TAIL, true>(row_of<XDT>(g, m, N), unit, units, (int)N);
+        uu = load_row_unit<XDT, TAIL, true>(row_of<XDT>(u, m, N), unit, units, (int)N);
+    };
+    int64_t m = (int64_t)(blockIdx.x / blocks) * 4 + wave;
+    load_row(m);
+    for (; m < M; m += rows) {
         float d[8], gv[8], uv[8], a[8];
-        load_values<XDT, TAIL>(dh, m, N, unit, units, d);
-        load_values<XDT, TAIL>(g, m, N, unit, units, gv);
-        load_values<XDT, TAIL>(u, m, N, unit, units, uv);
+        unit_values<XDT, TAIL>(du, unit, (int)N, d);
+        unit_values<XDT, TAIL>(gu, unit, (int)N, gv);
+        unit_values<XDT, TAIL>(uu, unit, (int)N, uv);
+        load_row(m + rows);
+        // d u act'(g) and d act(g)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float value, slope;
-            act_both(act, gv[j], value, slope);
-            a[j] = d[j] * uv[j] * slope;
-            uv[j] = d[j] * value;
+            a[j] = d[j] * uv[j];
+            uv[j] = d[j];
         }
+        times_act_both<8>(act, gv, a, uv);
         if (dz) {
             store_padded<XDT>(dz, m, pitch, unit, a);
             store_padded<XDT>(static_cast<char*>(dz) + M * pitch * elem_bytes(XDT), m, pitch, unit, uv);
@@ -201,7 +237,7 @@ hipError_t launch_linear_dz(int xdt, const void* dy, const void* z, int act, int
 hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool accumulate, void* db, int bias_dt,
                            hipStream_t s)
 {
-    return launch_kernel(k_bias_sum, (int)((N + 255) / 256), s, part, slices, N, accumulate ? 1 : 0, db, bias_dt);
+    return launch_kernel_nt(k_bias_sum, (int)((N + 63) / 64), 64 * kSumWaves, s, part, slices, N, accumulate ? 1 : 0, db, bias_dt);
 }
 
 hipError_t launch_gated_dz(int xdt, const void* dh, const void* g, const void* u, int act, int64_t M, int64_t N,
