@@ -49,7 +49,10 @@ inline Epilogue epilogue_rows(Epilogue e, int64_t m, int es)
 
 // Rows of x up to which the products are taken straight from the codes; beyond, the weights
 // are dequantized first (unless the length is shorter than a step of the tiled product).
-constexpr int64_t kRowsMax = 64;
+#ifndef QB_ROWS_MAX
+#define QB_ROWS_MAX 64
+#endif
+constexpr int64_t kRowsMax = QB_ROWS_MAX;
 constexpr bool takes_rows(int64_t M, int64_t K) { return M <= kRowsMax || K < 64; }
 
 // y = epilogue(x W^T) straight from the codes (count 1: linear, 2: gated).
