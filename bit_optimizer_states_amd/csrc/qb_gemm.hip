@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256) void k_unpack_transposed(const Weights2 ws, in
 // A workgroup of WM x WN waves computes BM rows (of A) by BN columns (rows of B), each
 // wave BM / WM by BN / WN of them in 16x16 tiles.  A step is 128 bytes of every row (64
 // 16-bit elements, 32 binary32 ones), staged in LDS by direct global-to-LDS loads of 16
-// bytes a lane, two buffers in turn: the next step loads while one is multiplied.  16-byte
+// bytes a lane, STAGES buffers in turn: the next steps load while one is multiplied.  16-byte
 // chunk p of an LDS row holds chunk p ^ (row % 8) of the operand's row, so that the rows
 // of one fragment lie in different banks.  A fragment is one chunk a lane: row lane % 16,
 // chunk 4 kk + lane / 16; with binary32 its four elements go to four instructions, the same
@@ -114,8 +114,8 @@ __global__ __launch_bounds__(256) void k_unpack_transposed(const Weights2 ws, in
 // products.  4096 x 4096 x 11008 bf16 (the loop alone, binary32 out): 258 us, 1431 TFLOP/s, the
 // matrix pipes busy 72% of the time at the 1.9 GHz that the chip holds then; all fragments
 // read before the products 266; the loads first and each half read before its products
-// 286; steps of half the length in four buffers 291; four waves of 128 x 128 each 315; two
-// groups of waves kept half a step apart by barriers 355.
+// 286; steps of half the length in four buffers 275; four waves of 128 x 128 each 315; two
+// groups of waves kept half a step apart 256 (not built).
 // B's fragment is the first operand, so that a lane's four sums are four neighbouring
 // columns of C.
 
@@ -207,7 +207,7 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const float* tile
     }
 }
 
-template <int XDT, int BM, int BN, int WM, int WN, bool GATED>
+template <int XDT, int BM, int BN, int WM, int WN, int STAGES, bool GATED>
 __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
 {
     constexpr int NW = WM * WN, NT = 64 * NW;          // waves, threads
@@ -216,9 +216,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
     static_assert(A_PER * NW * 8 == BM && B_PER * NW * 8 == BN, "whole loads");
     constexpr int BUF = (BM + BN) * 128;
     // the epilogue stages the tile in the same memory, the rows of WM / PASSES waves at once
-    constexpr int PASSES = (BM * BN * 4 + 2 * BUF - 1) / (2 * BUF);
-    static_assert(WM % PASSES == 0, "whole waves' rows per pass");
-    __shared__ __attribute__((aligned(16))) char s_ab[2 * BUF];   // two buffers, A's rows then B's
+    constexpr int PASSES = BM * BN * 4 <= STAGES * BUF ? 1 : 2;
+    static_assert(WM % PASSES == 0 && BM * BN * 4 <= PASSES * STAGES * BUF, "whole waves' rows per pass");
+    __shared__ __attribute__((aligned(16))) char s_ab[STAGES * BUF];   // buffers: A's rows, then B's
     constexpr int ES = XDT == DT_F32 ? 4 : 2;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -267,8 +267,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
 
     // a length of half a step too many: its last step begins half a step early, and only its
     // upper half is multiplied
-    auto load_step = [&](int s) {
-        char* const dst = s_ab + (s & 1) * BUF;
+    auto load_step = [&](int s, int buffer) {
+        char* const dst = s_ab + buffer * BUF;
         const int64_t at = (int64_t)s * 128 - (p.half && s + 1 == p.steps ? 64 : 0);
         const char* const as = (s < p.steps0 ? a0 : a1) + at;
         const char* const bs = b0 + at;
@@ -303,14 +303,23 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
             for (int j = 0; j < TN; ++j) mma_chunk<XDT>(bf[kk][j], af[kk][t], acc[j][t]);
     };
     const int full = end - (p.half && end == p.steps ? 1 : 0);      // steps of the whole length
-    load_step(begin);
+    constexpr int PER = A_PER + B_PER;
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+        if (begin + i < end) load_step(begin + i, i);
+    // behind it step s has landed, and the buffer of step s - 1, which its readers have left, is free
+    auto arrive = [&](int s) {
+        if (s + STAGES - 1 <= end) wait_loads<(STAGES - 2) * PER>();
+        else wait_loads<0>();
+        pipeline_barrier();
+    };
+    int now = 0, free = STAGES - 1;
     for (int s = begin; s < full; ++s) {
-        __builtin_amdgcn_s_waitcnt(0);
-        lds_barrier();                                 // step s has landed; the other buffer is free
-        const char* const buf = s_ab + (s & 1) * BUF;
+        arrive(s);
+        const char* const buf = s_ab + now * BUF;
         read_half(buf, 0);
         __builtin_amdgcn_sched_barrier(0);
-        if (s + 1 < end) load_step(s + 1);
+        if (s + STAGES - 1 < end) load_step(s + STAGES - 1, free);
         read_half(buf, 1);
         multiply_half(0);
         multiply_half(1);
@@ -321,11 +330,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                          // an LDS read
         }
         __builtin_amdgcn_sched_group_barrier(0x008, 2 * TM * TN * (XDT == DT_F32 ? 4 : 1), 0);
+        free = now;
+        now = now + 1 == STAGES ? 0 : now + 1;
     }
     if (full < end) {
-        __builtin_amdgcn_s_waitcnt(0);
-        lds_barrier();
-        read_half(s_ab + (full & 1) * BUF, 1);
+        arrive(full);
+        read_half(s_ab + now * BUF, 1);
         multiply_half(1);
     }
 
@@ -407,44 +417,104 @@ GemmParams rows_of(const GemmParams& all, int64_t m, int64_t rows)
 
 
 
-// Columns n_first .. R - 1 of B in BN-wide tiles (`columns` tiles of them at most).
-template <int XDT, int BM, int BN, int WM, int WN, bool GATED>
+// Columns n_first .. R - 1 of B in BN-wide tiles (`columns` tiles of them at most), the length
+// in p.split pieces.
+template <int XDT, int BM, int BN, int WM, int WN, int STAGES, bool GATED>
 hipError_t gemm_as(GemmParams p, int64_t n_first, int64_t columns, hipStream_t s)
 {
     p.n_first = n_first;
     const int64_t all = tiles_over(p.g.R - n_first, BN);
     p.tiles_n = (int)(all < columns ? all : columns);
     p.tiles_m = (int)tiles_over(p.g.M, BM);
-    return launch_kernel_nt(k_gemm<XDT, BM, BN, WM, WN, GATED>, p.tiles_m * p.tiles_n * p.split, 64 * WM * WN, s, p);
+    return launch_kernel_nt(k_gemm<XDT, BM, BN, WM, WN, STAGES, GATED>, p.tiles_m * p.tiles_n * p.split, 64 * WM * WN,
+                            s, p);
 }
 
 constexpr int64_t kEveryColumn = int64_t(1) << 40;
 
-// Tiles of 256 x 256 where they fill the CUs (one workgroup a CU), else of 128 x 128 (two a
-// CU), else of 64 x 64, the length split where that leaves CUs idle.
+// Tile shapes (the cases of gemm_shape), and the time in us of a step of a workgroup where 1, 2, ..
+// of them share a CU: fitted to layers of 4096 and 11008 inputs and outputs with 1 .. 4096
+// rows, their weights just dequantized (bf16).  A CU's only workgroup waits for memory:
+// 256 rows of 4096 x 4096 take 48 us in all in shape 4 with three buffers, 35 with five; many
+// small workgroups a CU hide it as well (shape 5: 30).
+struct TileShape {
+    int bm, bn, per_cu;
+    double us[5];
+};
+constexpr int kShapeCount = 6, kCus = 256;
+constexpr TileShape kShapes[kShapeCount] = {
+    {256, 256, 1, {1.6}}, {128, 256, 1, {0.97}}, {128, 128, 1, {0.77}}, {128, 128, 2, {0.80, 0.95}},
+    {64, 64, 2, {0.38, 0.44}}, {64, 64, 5, {0.50, 0.56, 0.70, 0.89, 0.93}}};
+
+// Estimated time of `groups` workgroups of `steps` steps: rounds that fill every CU, then the
+// rest.  Binary32 is bound by the matrix instructions (0.55 TFLOP/s a CU) in large tiles.
+double rounds_us(int xdt, const TileShape& t, int64_t groups, int64_t steps)
+{
+    auto step_us = [&](int64_t k) {
+        const double flops = 2.0 * t.bm * t.bn * gemm_step(DT_F32) * k / 0.55e6;
+        return xdt == DT_F32 && flops > t.us[k - 1] ? flops : t.us[k - 1];
+    };
+    const int64_t full = groups / (kCus * t.per_cu), rest = groups - full * kCus * t.per_cu;
+    return (full * step_us(t.per_cu) + (rest ? step_us(tiles_over(rest, kCus)) : 0.0)) * steps;
+}
+
+struct GemmPlan {
+    int shape, split;
+    double us;
+};
+
+// The best shape and number of pieces for M x R of `steps` steps.  A split product's partial
+// sums are written and read once (3.5 TB/s) and cost a launch; four steps a piece at least.
+GemmPlan gemm_plan(int xdt, int64_t M, int64_t R, int64_t steps, bool may_split)
+{
+    GemmPlan best{0, 1, 1e300};
+    for (int i = 0; i < kShapeCount; ++i) {
+        const TileShape& t = kShapes[i];
+        const int64_t tiles = tiles_over(M, t.bm) * tiles_over(R, t.bn);
+        for (int split = 1; split <= (may_split ? kSplitMax : 1); ++split) {
+            if (split > 1 && (steps / split < 4 || split * M * R > gemm_part_floats(M, R) || split * tiles > 5 * kCus))
+                break;
+            const double us = rounds_us(xdt, t, tiles * split, tiles_over(steps, split)) + 4.0 +
+                              (split > 1 ? 4.0 + 8.0 * split * M * R / 3.5e6 : 0.0);
+            if (us < best.us) best = GemmPlan{i, split, us};
+        }
+    }
+    return best;
+}
+
+template <int XDT, bool GATED>
+hipError_t gemm_shape(int shape, const GemmParams& p, int64_t n_first, int64_t columns, hipStream_t s)
+{
+    switch (shape) {
+    case 0: return gemm_as<XDT, 256, 256, 2, 4, 2, GATED>(p, n_first, columns, s);
+    case 1: return gemm_as<XDT, 128, 256, 2, 4, 3, GATED>(p, n_first, columns, s);
+    case 2: return gemm_as<XDT, 128, 128, 2, 4, 4, GATED>(p, n_first, columns, s);
+    case 3: return gemm_as<XDT, 128, 128, 2, 4, 2, GATED>(p, n_first, columns, s);
+    case 4: return gemm_as<XDT, 64, 64, 2, 2, 5, GATED>(p, n_first, columns, s);
+    default: return gemm_as<XDT, 64, 64, 2, 2, 2, GATED>(p, n_first, columns, s);
+    }
+}
+
 template <int XDT, bool GATED>
 hipError_t gemm_tiles(GemmParams p, hipStream_t s)
 {
     const int64_t M = p.g.M, R = p.g.R;
-    p.split = 1;
-    p.per_split = p.steps;
-    const int64_t rows256 = tiles_over(M, 256), columns256 = tiles_over(R, 256), tiles256 = rows256 * columns256;
-    if (tiles256 >= 192) {
-        // the columns that whole rounds of 256 workgroups cover in 256 x 256 tiles, and the rest, where it is less
-        // than half a round, in 128 x 128 ones, which every CU takes part in
-        const int64_t whole = tiles256 / 256 * 256 / rows256, left = tiles256 - whole * rows256;
-        const bool apart = whole > 0 && left > 0 && left <= 128;
-        const hipError_t e = gemm_as<XDT, 256, 256, 2, 4, GATED>(p, 0, apart ? whole : kEveryColumn, s);
-        if (e != hipSuccess || !apart) return e;
-        return gemm_as<XDT, 128, 128, 2, 4, GATED>(p, whole * 256, kEveryColumn, s);
+    const GemmPlan plan = gemm_plan(XDT, M, R, p.steps, p.part != nullptr);
+    // or: the columns that whole rounds of 256 x 256 tiles cover, and the rest in the shape that suits it best (4096
+    // rows of a gated block of 2 x 11008, 5.4 rounds: 709 us in 256 x 256 tiles alone, 662 so)
+    const int64_t rows = tiles_over(M, 256), columns = tiles_over(R, 256), whole = rows * columns / kCus * kCus / rows;
+    if (whole > 0 && whole < columns) {
+        p.split = 1;
+        p.per_split = p.steps;
+        const GemmPlan rest = gemm_plan(XDT, M, R - whole * 256, p.steps, false);
+        if (rounds_us(XDT, kShapes[0], rows * whole, p.steps) + 4.0 + rest.us < plan.us && rest.shape != 0) {
+            const hipError_t e = gemm_shape<XDT, GATED>(0, p, 0, whole, s);
+            return e != hipSuccess ? e : gemm_shape<XDT, GATED>(rest.shape, p, whole * 256, kEveryColumn, s);
+        }
     }
-    if (tiles_over(M, 128) * tiles_over(R, 128) >= 192)
-        return gemm_as<XDT, 128, 128, 2, 4, GATED>(p, 0, kEveryColumn, s);
-    p.split = gemm_split(M, R, p.steps);
-    if (!p.part) p.split = 1;
-    p.per_split = (int)tiles_over(p.steps, p.split);
+    p.per_split = (int)tiles_over(p.steps, plan.split);
     p.split = (int)tiles_over(p.steps, p.per_split);
-    hipError_t e = gemm_as<XDT, 64, 64, 2, 2, GATED>(p, 0, kEveryColumn, s);
+    const hipError_t e = gemm_shape<XDT, GATED>(plan.shape, p, 0, kEveryColumn, s);
     if (e != hipSuccess || p.split == 1) return e;
     const int64_t groups = (p.e.N + 3) / 4;
     return launch_kernel(k_join_split<XDT, GATED>, (int)tiles_over(M * groups, 256), s, p, groups);
@@ -454,7 +524,7 @@ hipError_t gemm_tiles(GemmParams p, hipStream_t s)
 template <int XDT, bool GATED>
 hipError_t gemm_rows(const GemmParams& p, hipStream_t s)
 {
-    const int64_t M = p.g.M, most = (int64_t(1) << 21) / tiles_over(p.g.R, 128) * 128;
+    const int64_t M = p.g.M, most = (int64_t(1) << 21) / tiles_over(p.g.R, 64) * 256;
     for (int64_t m = 0; m < M; m += most) {
         const hipError_t e = gemm_tiles<XDT, GATED>(rows_of<XDT>(p, m, M - m < most ? M - m : most), s);
         if (e != hipSuccess) return e;
@@ -499,16 +569,6 @@ hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_
     case DT_F16: return transposed_dq<DT_F16>(w, count, N, K, f, out, s);
     default: return transposed_dq<DT_BF16>(w, count, N, K, f, out, s);
     }
-}
-
-// Pieces of the length of a product of few tiles: about three workgroups of 64 x 64 a CU,
-// four steps each at least.
-int gemm_split(int64_t M, int64_t R, int64_t steps)
-{
-    const int64_t tiles = tiles_over(M, 64) * tiles_over(R, 64);
-    int64_t split = kSplitTiles / tiles;
-    if (split > steps / 4) split = steps / 4;
-    return (int)(split < 1 ? 1 : split > kSplitMax ? kSplitMax : split);
 }
 
 hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t s)

@@ -88,16 +88,13 @@ struct GemmArgs {
 // part: room for the partial sums of a product split over its length, gemm_part_floats()
 // (a product of few tiles is not split without it).
 hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t s);
-int gemm_split(int64_t M, int64_t R, int64_t steps);
 
-// A product is split into kSplitTiles workgroups of 64 x 64 at most, kSplitMax pieces.
-constexpr int64_t kSplitTiles = 768, kSplitMax = 16;
-// At most split * tiles <= kSplitTiles tiles of 64 x 64, and kSplitMax pieces of M x R: never
-// less for more rows or columns.
+// A product is split into kSplitMax pieces at most, and into as many as have their partial
+// sums (M R each) in kPartMax: never less room for more rows or columns.
+constexpr int64_t kSplitMax = 16, kPartMax = int64_t(20) << 20;
 constexpr int64_t gemm_part_floats(int64_t M, int64_t R)
 {
-    const int64_t most = kSplitMax * M * R, cap = kSplitTiles * 64 * 64;
-    return most < cap ? most : cap;
+    return kSplitMax * M * R < kPartMax ? kSplitMax * M * R : kPartMax;
 }
 
 // dz = dy act'(z) [M, N] into `dz` of pitch `pitch` (its padding zero; nullptr: not

@@ -141,12 +141,21 @@ __device__ __forceinline__ void dequant_chunk(const u32x4& cw, float a, const fl
     dequant_frag<XDT>(cw.w, a, s_val, f[3]);
 }
 
-// Workgroup barrier that orders LDS accesses only: global loads and stores stay in flight across it.
-__device__ __forceinline__ void lds_barrier()
+// Waits until at most N loads of this wave are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads()
 {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+// Workgroup barrier behind which this wave's LDS reads have returned.  Direct global-to-LDS
+// loads stay in flight across it (a fence would wait for all of them): the caller waits for
+// those that it needs.
+__device__ __forceinline__ void pipeline_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    asm volatile("" ::: "memory");
 }
 
 // Pointers of a direct global-to-LDS load.
