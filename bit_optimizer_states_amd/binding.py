@@ -695,10 +695,11 @@ def qb_dequant_linear(x, codes, absmax, code, blocksize, N, y, ws=None, bias=Non
     _rows_like(y, m, N, dt, "y")
     _rows_like(residual, m, N, dt, "residual")
     _rows_like(z, m, N, dt, "z")
+    bdt = _layer_bias(bias, N, xdt)
     _weight_parts(codes, absmax, dq, code, blocksize, N, k, d)
     _row_call("qb_dequant_linear", d, stream, _at(x, d), xdt, m, k, _at(codes, d), _at(absmax, d),
-              ctypes.byref(dq) if dq is not None else None, code, blocksize, N, _at(bias, d), _layer_bias(bias, N, xdt),
-              act, _at(residual, d), _at(z, d), _at(y, d), *_ws_args(ws, d))
+              ctypes.byref(dq) if dq is not None else None, code, blocksize, N, _at(bias, d), bdt, act,
+              _at(residual, d), _at(z, d), _at(y, d), *_ws_args(ws, d))
 
 
 def qb_dequant_linear_backward_workspace_bytes(xdt, M, K, N):
@@ -715,11 +716,12 @@ def qb_dequant_linear_backward(dy, codes, absmax, code, blocksize, K, dx, ws=Non
     _rows_like(z, m, n, dt, "z")
     _rows_like(dz, m, n, dt, "dz")
     _rows_like(dx, m, K, dt, "dx")
+    bdt = _layer_bias(dbias, n, xdt, "dbias")
     if dx is not None:
         _weight_parts(codes, absmax, dq, code, blocksize, n, K, d)
     _row_call("qb_dequant_linear_backward", d, stream, _at(dy, d), _at(z, d), xdt, m, K, _at(codes, d), _at(absmax, d),
               ctypes.byref(dq) if dq is not None else None, code, blocksize, n, act, _at(dx, d), _at(dz, d),
-              _at(dbias, d), _layer_bias(dbias, n, xdt, "dbias"), accumulate, *_ws_args(ws, d))
+              _at(dbias, d), bdt, accumulate, *_ws_args(ws, d))
 
 
 def _gated_weights(gate, up, code, blocksize, n, k, device):
@@ -727,6 +729,7 @@ def _gated_weights(gate, up, code, blocksize, n, k, device):
     out, sizes = [], set()
     for codes, absmax, dq in (gate, up):
         _weight_parts(codes, absmax, dq, code, blocksize, n, k, device)
+    for codes, absmax, dq in (gate, up):
         if dq is None:
             out.append(qb_weight(_at(codes, device), _at(absmax, device), None, None, None))
         else:
@@ -788,6 +791,7 @@ def grad_table(grads):
         if out.dtype != g.dtype or out.numel() != g.numel():
             raise ValueError("out like its gradient expected")
         arr[i] = qb_grad(_at(g, device), _at(out, device), g.numel(), _dtype(g))
+    arr.device = device
     return arr
 
 
@@ -795,27 +799,29 @@ def qb_multi_tensor_grad_norm_workspace_bytes(count):
     return lib().qb_multi_tensor_grad_norm_workspace_bytes(int(count))
 
 
-def _norm_of_one(norm):
+def _norm_of_one(norm, table, count):
+    """The device of a call over `count` gradients of `table`, whose norm is norm[0]."""
     if norm.dtype is not _FLOAT32 or norm.numel() != 1:
         raise ValueError("norm: one fp32 value expected")
-    return norm.get_device()
+    if count > len(table):
+        raise ValueError("a table of count gradients expected")
+    device = norm.get_device()
+    if getattr(table, "device", None) not in (None, device):
+        raise ValueError(f"norm on the gradients' device {table.device} expected")
+    return device
 
 
 def qb_multi_tensor_grad_norm(table, count, norm, ws, stream=None):
     """norm[0] = the norm of all gradients of `table` (grad_table)."""
     lib()
-    d = _norm_of_one(norm)
-    if count > len(table):
-        raise ValueError("a table of count gradients expected")
+    d = _norm_of_one(norm, table, count)
     _row_call("qb_multi_tensor_grad_norm", d, stream, table, count, _at(norm, d), *_ws_args(ws, d))
 
 
 def qb_multi_tensor_clip_grads(table, count, max_norm, norm, stream=None):
     """out = g * min(1, max_norm / (norm[0] + 1e-6)) for every gradient of `table` (grad_table)."""
     lib()
-    d = _norm_of_one(norm)
-    if count > len(table):
-        raise ValueError("a table of count gradients expected")
+    d = _norm_of_one(norm, table, count)
     _row_call("qb_multi_tensor_clip_grads", d, stream, table, count, max_norm, _at(norm, d))
 
 

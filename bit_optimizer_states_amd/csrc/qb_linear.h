@@ -102,7 +102,15 @@ constexpr int64_t gemm_part_floats(int64_t M, int64_t R)
 // dz over its rows, part[slice][N] (nullptr: not wanted).  z == nullptr: dz = dy.
 hipError_t launch_linear_dz(int xdt, const void* dy, const void* z, int act, int64_t M, int64_t N, void* dz,
                             int64_t pitch, void* dz_out, float* part, int slices, hipStream_t s);
-int linear_dz_slices(int64_t M, int64_t N);
+constexpr int kDzCols = 512, kDzWaves = 4;
+// Slices of rows: enough workgroups for the chip (2048 over the blocks of columns), four rows a
+// wave at least where there are that many.
+inline int linear_dz_slices(int64_t M, int64_t N)
+{
+    const int64_t blocks = (N + kDzCols - 1) / kDzCols, want = (2048 + blocks - 1) / blocks,
+                  most = (M + 4 * kDzWaves - 1) / (4 * kDzWaves), n = want < most ? want : most;
+    return (int)(n < 1 ? 1 : n);
+}
 // db[n] = the sum of part[.][n] in order (plus what it holds).
 hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool accumulate, void* db, int bias_dt,
                            hipStream_t s);

@@ -13,8 +13,7 @@ namespace qb {
 
 namespace {
 
-constexpr int kCols = 512;               // columns of a workgroup: a wave's 64 units of 8
-constexpr int kGradWaves = 4;
+constexpr int kCols = kDzCols, kGradWaves = kDzWaves;     // a workgroup: a wave's 64 units of 8 columns, 4 waves
 
 // A unit at row `row` of an array padded to `pitch` columns (a multiple of 8).
 template <int XDT>
@@ -213,16 +212,6 @@ hipError_t gated_dz_dt(const void* dh, const void* g, const void* u, int act, in
 }
 
 }  // namespace
-
-// Slices of rows: enough workgroups for the chip (2048 over the column blocks), four rows a
-// wave at least where there are that many.
-int linear_dz_slices(int64_t M, int64_t N)
-{
-    const int64_t blocks = (N + kCols - 1) / kCols, want = (2048 + blocks - 1) / blocks,
-                  most = (M + 4 * kGradWaves - 1) / (4 * kGradWaves);
-    const int64_t n = want < most ? want : most;
-    return (int)(n < 1 ? 1 : n);
-}
 
 hipError_t launch_linear_dz(int xdt, const void* dy, const void* z, int act, int64_t M, int64_t N, void* dz,
                             int64_t pitch, void* dz_out, float* part, int slices, hipStream_t s)
