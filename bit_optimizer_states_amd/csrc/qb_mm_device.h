@@ -131,6 +131,33 @@ __device__ __forceinline__ void dequant_frag(uint32_t word, float a, const float
     }
 }
 
+// dequant_frag in two steps: the code values of eight weights, and their products.
+__device__ __forceinline__ void code_values(uint32_t word, const float* s_val, float* v)
+{
+    const char* const tv = reinterpret_cast<const char*>(s_val);
+    uint32_t th = (word >> 2) & 0x3C3C3C3Cu, tl = (word << 2) & 0x3C3C3C3Cu;
+    asm("" : "+v"(th), "+v"(tl));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = *reinterpret_cast<const float*>(tv + __builtin_amdgcn_ubfe(th, 8 * j, 8));
+        v[2 * j + 1] = *reinterpret_cast<const float*>(tv + __builtin_amdgcn_ubfe(tl, 8 * j, 8));
+    }
+}
+
+template <int XDT>
+__device__ __forceinline__ void scaled(const float* v, float a, Frag<XDT>& f)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (XDT == DT_F32) {
+            f.w[2 * j] = v[2 * j] * a;
+            f.w[2 * j + 1] = v[2 * j + 1] * a;
+        } else {
+            f.w[j] = pack_pair<XDT>(v[2 * j] * a, v[2 * j + 1] * a);
+        }
+    }
+}
+
 // The 32 weights of a lane's chunk.
 template <int XDT>
 __device__ __forceinline__ void dequant_chunk(const u32x4& cw, float a, const float* s_val, Frag<XDT>* f)

@@ -249,3 +249,25 @@ def test_product_plans(M, K, N, xdt):
     assert torch.equal(dz, dy)
     linear.check_backward(L, dy[at], w, None, "NONE", dx[at], None, None)
     assert dx.isfinite().all()
+
+
+# few rows through layers whose block constants pass LDS in several parts, blocks that begin inside a row, steps
+# filled in part, fewer steps than waves; both numbers of waves, every number of rows a workgroup takes
+LONG = [(1, 12320, 20), (4, 24704, 33), (5, 12288, 6200), (8, 36896, 40), (11, 12384, 6161), (16, 24608, 17),
+        (17, 49184, 19), (40, 12416, 33), (48, 24576, 16), (64, 12512, 35)]
+
+
+@pytest.mark.parametrize("M,K,N", LONG)
+@pytest.mark.parametrize("nested,blocksize", [(False, 64), (True, 64), (True, 4096)])
+@pytest.mark.parametrize("xdt", [BF16, F32])
+def test_few_rows_of_long_layers(M, K, N, nested, blocksize, xdt):
+    L = qb()
+    print(f"[long] {M} {K} {N} {nested} {blocksize} {xdt}", flush=True)
+    x = ref.normal((M, K), M, dtype=xdt)
+    if N < 6000:
+        w = gated.pair(N, K, oracle.NF4, blocksize, nested, xdt, K)
+        x = x * (10 / K ** 0.5)
+        y, g, u = gated.forward(L, x, w, "SILU", keep=True)
+        gated.check_forward(L, x, w, "SILU", y, g, u)
+    w = ref.Weight(N, K, oracle.FP4, blocksize, nested, xdt, seed=M)
+    linear.check_forward(L, x, w, None, "NONE", None, linear.forward(L, x, w))
