@@ -23,6 +23,8 @@
 //
 // Many tensors go in one launch: tiles of all tensors are numbered in one
 // range and a workgroup finds its tensor through the coarse bucket index.
+#include <type_traits>
+
 #include "qb_device.h"
 
 namespace qb {
@@ -93,9 +95,14 @@ __device__ __forceinline__ uint32_t elem_code(const uint8_t* codes, int64_t idx)
 // USER: 8-bit codes of a user code (`user`) instead of the dynamic code.
 // KEEP: ordinary stores, for an output that the next kernel reads: a product of 4096 rows
 // right behind the dequantization of its 4096 x 11008 weights takes 322 us in all with them
-// and 340 with the non-temporal ones, which leave nothing in the caches.
+// and 340 with the non-temporal ones, which leave nothing in the caches.  One or two weights
+// of one size in a launch (grid row i: the i-th).
+struct DequantPair {
+    DequantDesc w[2];
+};
+
 template <int BITS, int YDT, bool DQ, bool MULTI, bool USER = false, bool KEEP = false>
-__global__ __launch_bounds__(kDqThreads) void k_dequant(DequantDesc single, TileMap<DequantDesc> map, int log2B,
+__global__ __launch_bounds__(kDqThreads) void k_dequant(std::conditional_t<KEEP, DequantPair, DequantDesc> single, TileMap<DequantDesc> map, int log2B,
                                                         int log2B2, int code4, const QbTables* __restrict__ tab,
                                                         const UserCode* __restrict__ user)
 {
@@ -117,7 +124,8 @@ __global__ __launch_bounds__(kDqThreads) void k_dequant(DequantDesc single, Tile
         d = map.descs[find_tensor(map, tile)];
         lt = tile - d.tile_begin;
     } else {
-        d = single;
+        if constexpr (KEEP) d = single.w[blockIdx.y];
+        else d = single;
         lt = tile;
     }
     const int64_t n = d.n;
@@ -223,15 +231,14 @@ hipError_t dequant_as(const DequantDesc& single, const TileMap<DequantDesc>* map
 }
 
 template <int YDT>
-hipError_t kept_as(const DequantDesc& d, int64_t ntiles, int code4, int B, int B2, bool dq, const QbTables* tab,
-                   hipStream_t s)
+hipError_t kept_as(const DequantPair& d, dim3 grid, int code4, int B, int B2, bool dq, const QbTables* tab, hipStream_t s)
 {
     const TileMap<DequantDesc> none{};
     if (dq)
-        return launch_kernel_nt(k_dequant<4, YDT, true, false, false, true>, (int)ntiles, kDqThreads, s, d, none,
-                                ilog2(B), ilog2(B2), code4, tab, (const UserCode*)nullptr);
-    return launch_kernel_nt(k_dequant<4, YDT, false, false, false, true>, (int)ntiles, kDqThreads, s, d, none,
-                            ilog2(B), ilog2(B2), code4, tab, (const UserCode*)nullptr);
+        return launch_grid(k_dequant<4, YDT, true, false, false, true>, grid, kDqThreads, 0, s, d, none, ilog2(B),
+                           ilog2(B2), code4, tab, (const UserCode*)nullptr);
+    return launch_grid(k_dequant<4, YDT, false, false, false, true>, grid, kDqThreads, 0, s, d, none, ilog2(B), ilog2(B2),
+                       code4, tab, (const UserCode*)nullptr);
 }
 
 template <int BITS, bool DQ>
@@ -269,16 +276,20 @@ hipError_t launch_dequant_user(const DequantDesc& d, int64_t ntiles, int B, int 
     }
 }
 
-hipError_t launch_dequant4_kept(const DequantDesc& d, int code4, int B, int B2, bool dq, int ydt, hipStream_t s)
+hipError_t launch_dequant4_kept(const DequantDesc* d, int count, int code4, int B, int B2, bool dq, int ydt,
+                                hipStream_t s)
 {
     const QbTables* tab = device_tables();
     if (!tab) return hipErrorNotInitialized;
-    const int64_t tile = dequant_tile_elems(4, false, ydt), ntiles = (d.n + tile - 1) / tile;
+    const int64_t tile = dequant_tile_elems(4, false, ydt), ntiles = (d->n + tile - 1) / tile;
     if (ntiles >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    const DequantPair pair{{d[0], d[count - 1]}};
+    const dim3 grid((unsigned)ntiles, (unsigned)count);
     switch (ydt) {
-    case DT_F32: return kept_as<DT_F32>(d, ntiles, code4, B, B2, dq, tab, s);
-    case DT_F16: return kept_as<DT_F16>(d, ntiles, code4, B, B2, dq, tab, s);
-    default: return kept_as<DT_BF16>(d, ntiles, code4, B, B2, dq, tab, s);
+    case DT_F32: return kept_as<DT_F32>(pair, grid, code4, B, B2, dq, tab, s);
+    case DT_F16: return kept_as<DT_F16>(pair, grid, code4, B, B2, dq, tab, s);
+    case DT_BF16: return kept_as<DT_BF16>(pair, grid, code4, B, B2, dq, tab, s);
+    default: return hipErrorInvalidValue;
     }
 }
 

@@ -448,14 +448,15 @@ constexpr TileShape kShapes[kShapeCount] = {
 
 // Estimated time of `groups` workgroups of `steps` steps: rounds that fill every CU, then the
 // rest.  Binary32 is bound by the matrix instructions (0.55 TFLOP/s a CU) in large tiles.
-double rounds_us(int xdt, const TileShape& t, int64_t groups, int64_t steps)
+// (32-bit numbers, since the host takes this estimate at every call.)
+double rounds_us(int xdt, const TileShape& t, uint32_t groups, uint32_t steps)
 {
-    auto step_us = [&](int64_t k) {
+    auto step_us = [&](uint32_t k) {
         const double flops = 2.0 * t.bm * t.bn * gemm_step(DT_F32) * k / 0.55e6;
         return xdt == DT_F32 && flops > t.us[k - 1] ? flops : t.us[k - 1];
     };
-    const int64_t full = groups / (kCus * t.per_cu), rest = groups - full * kCus * t.per_cu;
-    return (full * step_us(t.per_cu) + (rest ? step_us(tiles_over(rest, kCus)) : 0.0)) * steps;
+    const uint32_t round = kCus * t.per_cu, full = groups / round, rest = groups - full * round;
+    return (full * step_us(t.per_cu) + (rest ? step_us((rest + kCus - 1) / kCus) : 0.0)) * steps;
 }
 
 struct GemmPlan {
@@ -465,18 +466,20 @@ struct GemmPlan {
 
 // The best shape and number of pieces for M x R of `steps` steps.  A split product's partial
 // sums are written and read once (3.5 TB/s) and cost a launch; four steps a piece at least.
-GemmPlan gemm_plan(int xdt, int64_t M, int64_t R, int64_t steps, bool may_split)
+// (gemm_rows keeps the number of tiles below 2^24.)
+GemmPlan gemm_plan(int xdt, int64_t M, int64_t R, uint32_t steps, bool may_split)
 {
     GemmPlan best{0, 1, 1e300};
+    const double sums = (double)M * (double)R;
+    const uint32_t fit = sums * kSplitMax <= (double)kPartMax ? (uint32_t)kSplitMax : (uint32_t)((double)kPartMax / sums);
+    const uint32_t most = may_split ? (steps / 4 < fit ? steps / 4 : fit) : 1;
     for (int i = 0; i < kShapeCount; ++i) {
         const TileShape& t = kShapes[i];
-        const int64_t tiles = tiles_over(M, t.bm) * tiles_over(R, t.bn);
-        for (int split = 1; split <= (may_split ? kSplitMax : 1); ++split) {
-            if (split > 1 && (steps / split < 4 || split * M * R > gemm_part_floats(M, R) || split * tiles > 5 * kCus))
-                break;
-            const double us = rounds_us(xdt, t, tiles * split, tiles_over(steps, split)) + 4.0 +
-                              (split > 1 ? 4.0 + 8.0 * split * M * R / 3.5e6 : 0.0);
-            if (us < best.us) best = GemmPlan{i, split, us};
+        const uint32_t tiles = (uint32_t)((M + t.bm - 1) / t.bm * ((R + t.bn - 1) / t.bn));
+        for (uint32_t split = 1; split == 1 || (split <= most && split * tiles <= 5u * kCus); ++split) {
+            const double us = rounds_us(xdt, t, tiles * split, (steps + split - 1) / split) + 4.0 +
+                              (split > 1 ? 4.0 + 8.0 * split * sums / 3.5e6 : 0.0);
+            if (us < best.us) best = GemmPlan{i, (int)split, us};
         }
     }
     return best;
@@ -507,7 +510,7 @@ hipError_t gemm_tiles(GemmParams p, hipStream_t s)
         p.split = 1;
         p.per_split = p.steps;
         const GemmPlan rest = gemm_plan(XDT, M, R - whole * 256, p.steps, false);
-        if (rounds_us(XDT, kShapes[0], rows * whole, p.steps) + 4.0 + rest.us < plan.us && rest.shape != 0) {
+        if (rounds_us(XDT, kShapes[0], (uint32_t)(rows * whole), p.steps) + 4.0 + rest.us < plan.us && rest.shape != 0) {
             const hipError_t e = gemm_shape<XDT, GATED>(0, p, 0, whole, s);
             return e != hipSuccess ? e : gemm_shape<XDT, GATED>(rest.shape, p, whole * 256, kEveryColumn, s);
         }
@@ -554,11 +557,14 @@ hipError_t transposed_dq(const Weight4* w, int count, int64_t N, int64_t K, cons
 
 }  // namespace
 
-hipError_t launch_unpack(int xdt, const Weight4& w, int64_t N, int64_t K, const Weight4Format& f, void* out,
-                         hipStream_t s)
+hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
+                         size_t each, hipStream_t s)
 {
-    const DequantDesc d{w.codes, w.absmax, w.c2, w.absmax2, w.offset, out, N * K, 0};
-    return launch_dequant4_kept(d, f.code4, 1 << f.log2B, 1 << f.log2B2, f.nested != 0, xdt, s);
+    DequantDesc d[2];
+    for (int i = 0; i < count; ++i)
+        d[i] = DequantDesc{w[i].codes,   w[i].absmax, w[i].c2, w[i].absmax2,
+                           w[i].offset, static_cast<char*>(out) + i * each, N * K, 0};
+    return launch_dequant4_kept(d, count, f.code4, 1 << f.log2B, 1 << f.log2B2, f.nested != 0, xdt, s);
 }
 
 hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f,
@@ -569,6 +575,11 @@ hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_
     case DT_F16: return transposed_dq<DT_F16>(w, count, N, K, f, out, s);
     default: return transposed_dq<DT_BF16>(w, count, N, K, f, out, s);
     }
+}
+
+double gemm_us(int xdt, int64_t M, int64_t R, int64_t len)
+{
+    return gemm_plan(xdt, M, R, (uint32_t)tiles_over(len, gemm_step(xdt)), true).us;
 }
 
 hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t s)

@@ -280,8 +280,10 @@ hipError_t launch_dq_mean(const QuantDesc& single, const TileMap<QuantDesc>* map
 hipError_t launch_dequant(const DequantDesc& single, const TileMap<DequantDesc>* map, int64_t ntiles, int bits,
                           int code4, int B, int B2, bool dq, int ydt, hipStream_t s);
 
-// One tensor of 4-bit codes, its values left in the caches for the kernel behind.
-hipError_t launch_dequant4_kept(const DequantDesc& d, int code4, int B, int B2, bool dq, int ydt, hipStream_t s);
+// One or two tensors of 4-bit codes, of one size, their values left in the caches for the
+// kernel behind.
+hipError_t launch_dequant4_kept(const DequantDesc* d, int count, int code4, int B, int B2, bool dq, int ydt,
+                                hipStream_t s);
 
 // Elements per tile of the dequantization kernel: 4-bit codes for one tensor
 // and for a grouped launch, and 8-bit codes into binary32 and into 16-bit

@@ -47,12 +47,10 @@ inline Epilogue epilogue_rows(Epilogue e, int64_t m, int es)
     return e;
 }
 
-// Rows of x up to which the products are taken straight from the codes; beyond, the weights
-// are dequantized first (unless the length is shorter than a step of the tiled product).
-#ifndef QB_ROWS_MAX
-#define QB_ROWS_MAX 64
-#endif
-constexpr int64_t kRowsMax = QB_ROWS_MAX;
+// Rows of x up to which the products are always taken straight from the codes, and without a
+// workspace; beyond, by an estimate, or after the weights are dequantized (which takes a length
+// of a step of the tiled product at least).
+constexpr int64_t kRowsMax = 64;
 constexpr bool takes_rows(int64_t M, int64_t K) { return M <= kRowsMax || K < 64; }
 
 // y = epilogue(x W^T) straight from the codes (count 1: linear, 2: gated).
@@ -66,9 +64,10 @@ constexpr int64_t gemm_pitch(int dt, int64_t k) { return (k + gemm_step(dt) - 1)
 // Columns of a gated block's product: those of the two weights, dealt in groups of 16.
 constexpr int64_t gated_rows(int64_t n) { return (n + 15) / 16 * 32; }
 
-// A weight in the compute dtype, out[n][k] (as qb_dequantize).
-hipError_t launch_unpack(int xdt, const Weight4& w, int64_t N, int64_t K, const Weight4Format& f, void* out,
-                         hipStream_t s);
+// One or two weights in the compute dtype, [n][k] (as qb_dequantize), the second `each` bytes
+// behind the first.
+hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
+                         size_t each, hipStream_t s);
 // Transposed: out[k][n], for two weights next to each other (columns n of the second at
 // gemm_pitch(N) + n); the pitch is count * gemm_pitch(N), its padding zero.
 hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f,
@@ -88,6 +87,10 @@ struct GemmArgs {
 // part: room for the partial sums of a product split over its length, gemm_part_floats()
 // (a product of few tiles is not split without it).
 hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t s);
+
+// Estimated times in us: of launch_linear_rows, and of launch_gemm of M x R x len.
+double rows_us(int xdt, int64_t M, int64_t K, int64_t N, int count);
+double gemm_us(int xdt, int64_t M, int64_t R, int64_t len);
 
 // A product is split into kSplitMax pieces at most, and into as many as have their partial
 // sums (M R each) in kPartMax: never less room for more rows or columns.

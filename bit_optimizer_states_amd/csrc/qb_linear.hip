@@ -317,6 +317,9 @@ hipError_t rows_launch(const RowsArgs& a, const QbTables* tab, hipStream_t s)
     return hipSuccess;
 }
 
+// Beyond 32 rows: blocks of 48 where those of 64 are not fewer.
+int rows_of_block(int64_t M) { return (M + 47) / 48 == (M + 63) / 64 ? 48 : 64; }
+
 template <int XDT, bool DQ, int G>
 hipError_t rows_as(const RowsArgs& a, const QbTables* tab, hipStream_t s)
 {
@@ -337,7 +340,7 @@ hipError_t rows_as(const RowsArgs& a, const QbTables* tab, hipStream_t s)
         if (a.M <= 8) return rows_launch<XDT, DQ, G, 8, 8>(a, tab, s);
         if (a.M <= 16) return rows_launch<XDT, DQ, G, 16, 8>(a, tab, s);
         if (a.M <= 32) return rows_launch<XDT, DQ, G, 32, 8>(a, tab, s);
-        if (a.M <= 48) return rows_launch<XDT, DQ, G, 48, 8>(a, tab, s);
+        if (rows_of_block(a.M) == 48) return rows_launch<XDT, DQ, G, 48, 8>(a, tab, s);
         return rows_launch<XDT, DQ, G, 64, 8>(a, tab, s);
     }
 }
@@ -350,6 +353,17 @@ hipError_t rows_dq(const RowsArgs& a, int count, const QbTables* tab, hipStream_
 }
 
 }  // namespace
+
+// A launch, and rounds of one workgroup a CU (fitted to 65 .. 384 rows of layers of 512 .. 11008
+// inputs and 1001 .. 11008 outputs).
+double rows_us(int xdt, int64_t M, int64_t K, int64_t N, int count)
+{
+    const int block = xdt == DT_F32 ? 32 : rows_of_block(M);
+    const double fixed = xdt == DT_F32 ? 2.4 : count == 2 ? 4.0 : 2.5,
+                 each = (xdt == DT_F32 ? 2.9 * count : count == 2 ? 2.05 : 1.8) * K / 1024;
+    const int64_t rounds = ((N + 15) / 16 * ((M + block - 1) / block) + 255) / 256;
+    return 3.0 + rounds * (fixed + each) * (block == 48 ? 0.87 : 1.0);
+}
 
 hipError_t launch_linear_rows(int xdt, const void* x, int64_t M, int64_t K, const Weight4* w, int count,
                               const Weight4Format& f, const Epilogue& e, hipStream_t s)

@@ -104,16 +104,29 @@ size_t forward_bytes(int xdt, int64_t M, int64_t K, int64_t N, int count)
            (size_t)gemm_part_floats(M, count == 2 ? gated_rows(N) : N) * sizeof(float);
 }
 
+// The rows kernel, where it is needed or the faster one by the estimates: each reads the
+// codes once a block of rows and needs one launch; two launches and the dequantized weights
+// (5.6 TB/s) in the other.  bf16, us: 77 rows of 992 x 1001 14.4 dequantized, 9.8 so; 128 rows
+// of 4096 x 4096 25 and 21, 256 rows 30 and 40; 128 rows of 4096 x 11008 50 and 57, of a gated block
+// of them 81 and 70.
+bool rows_win(int xdt, int64_t M, int64_t K, int64_t N, int count)
+{
+    if (takes_rows(M, K)) return true;
+    if (M > 1024) return false;
+    const double rows = rows_us(xdt, M, K, N, count);
+    if (rows < 13.0) return true;               // two launches take that much in any case
+    const double unpack = 3.0 + count * (double)N * (double)K * (0.5 + dtype_bytes(xdt)) / 5.6e6;
+    return rows < 0.9 * (unpack + gemm_us(xdt, M, count == 2 ? gated_rows(N) : N, K));
+}
+
 // y = epilogue(x W^T) through the workspace.
 hipError_t unpack_and_multiply(int xdt, const void* x, int64_t M, int64_t K, const Weight4* w, int count, int64_t N,
                                const Weight4Format& f, const Epilogue& e, void* ws, hipStream_t s)
 {
     const size_t each = unpacked_bytes(xdt, K, N);
     char* const b = static_cast<char*>(ws);
-    for (int i = 0; i < count; ++i) {
-        const hipError_t err = launch_unpack(xdt, w[i], N, K, f, b + i * each, s);
-        if (err != hipSuccess) return err;
-    }
+    const hipError_t err = launch_unpack(xdt, w, count, N, K, f, b, each, s);
+    if (err != hipSuccess) return err;
     const GemmArgs g{x, nullptr, b, b + (count - 1) * each, M, count == 2 ? gated_rows(N) : N, K, K, K, K};
     return launch_gemm(xdt, count == 2, g, e, reinterpret_cast<float*>(b + count * each), s);
 }
@@ -184,7 +197,7 @@ qb_status qb_dequant_linear(const void* x, qb_dtype xdt, int64_t M, int64_t K, c
     if (st != QB_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Epilogue e{bias, residual, z, nullptr, y, N, (int32_t)bdt, (int32_t)act};
-    if (takes_rows(M, K)) return hip_status(launch_linear_rows(xdt, x, M, K, &w, 1, f, e, s));
+    if (rows_win(xdt, M, K, N, 1)) return hip_status(launch_linear_rows(xdt, x, M, K, &w, 1, f, e, s));
     return hip_status(unpack_and_multiply(xdt, x, M, K, &w, 1, N, f, e, ws, s));
 }
 
@@ -271,7 +284,7 @@ qb_status qb_dequant_gated(const void* x, qb_dtype xdt, int64_t M, int64_t K, co
     if (st != QB_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Epilogue e{nullptr, nullptr, gate_out, up_out, y, N, 0, (int32_t)act};
-    if (takes_rows(M, K)) return hip_status(launch_linear_rows(xdt, x, M, K, w, 2, f, e, s));
+    if (rows_win(xdt, M, K, N, 2)) return hip_status(launch_linear_rows(xdt, x, M, K, w, 2, f, e, s));
     return hip_status(unpack_and_multiply(xdt, x, M, K, w, 2, N, f, e, ws, s));
 }
 

@@ -42,18 +42,23 @@ namespace qb {
 static hipError_t done() { ++launches; return hipSuccess; }
 static int es(int dt) { return dt == 0 ? 4 : 2; }
 static double dz_end = 0, weights_end = 0;
+static bool rows_cheap = false;           // which of the two forms the estimates favour
 
 hipError_t launch_linear_rows(int, const void*, int64_t M, int64_t K, const Weight4*, int, const Weight4Format&,
                               const Epilogue& e, hipStream_t)
 {
-    if (!takes_rows(M, K) || !e.y) ++failures;
+    if ((!takes_rows(M, K) && (M > 1024 || !rows_cheap)) || !e.y) ++failures;
     return done();
 }
-hipError_t launch_unpack(int xdt, const Weight4& w, int64_t N, int64_t K, const Weight4Format&, void* out, hipStream_t)
+double rows_us(int, int64_t, int64_t, int64_t, int) { return rows_cheap ? 1.0 : 1e30; }
+double gemm_us(int, int64_t, int64_t, int64_t) { return 100.0; }
+hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format&, void* out,
+                         size_t each, hipStream_t)
 {
-    if (!w.codes) ++failures;
-    inside(out, (double)N * (double)K * es(xdt));
-    weights_end = offset_of(out) + (double)N * (double)K * es(xdt);
+    const double bytes = (double)N * (double)K * es(xdt);
+    if (!w[0].codes || !w[count - 1].codes || bytes > (double)each) ++failures;
+    inside(out, (count - 1) * (double)each + bytes);
+    weights_end = offset_of(out) + (count - 1) * (double)each + bytes;
     return done();
 }
 hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format&,
@@ -130,10 +135,11 @@ int main()
     const qb_weight w{U, F, nullptr, nullptr, nullptr}, nested{U, nullptr, U, F, F};
     const int64_t widest = (int64_t(1) << 21) - 1, tall = (int64_t(1) << 31) - 1;
 
-    for (qb_dtype dt : {QB_F32, QB_F16, QB_BF16})
+    for (qb_dtype dt : {QB_F32, QB_F16, QB_BF16, QB_F16, QB_F32})
         for (int64_t M : {int64_t(0), int64_t(1), int64_t(64), int64_t(65), int64_t(301), int64_t(4096), tall})
             for (int64_t K : {int64_t(32), int64_t(96), int64_t(4096), widest / 32 * 32})
                 for (int64_t N : {int64_t(1), int64_t(64), int64_t(1001), int64_t(11008), widest}) {
+                    qb::rows_cheap = !qb::rows_cheap;
                     const bool blocks = (N * K + 63) / 64 < int64_t(1) << 31;
                     const int ok = blocks ? QB_OK : QB_EINVAL;
                     ws_bytes = qb_dequant_linear_workspace_bytes(dt, M, K, N);

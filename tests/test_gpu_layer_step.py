@@ -271,3 +271,21 @@ def test_few_rows_of_long_layers(M, K, N, nested, blocksize, xdt):
         gated.check_forward(L, x, w, "SILU", y, g, u)
     w = ref.Weight(N, K, oracle.FP4, blocksize, nested, xdt, seed=M)
     linear.check_forward(L, x, w, None, "NONE", None, linear.forward(L, x, w))
+
+
+@pytest.mark.parametrize("M,K,N", [(66, 8192, 700), (130, 4096, 3001), (200, 6144, 1100), (300, 2080, 2000),
+                                   (520, 1056, 3000), (1025, 96, 2500), (2050, 160, 1025), (4100, 64, 2200)])
+@pytest.mark.parametrize("xdt", [BF16, F32])
+def test_gated_plans(M, K, N, xdt):
+    L = qb()
+    print(f"[gated plan] {M} {K} {N} {xdt}", flush=True)
+    w = gated.pair(N, K, oracle.NF4, 64, True, xdt, seed=M)
+    x = ref.normal((M, K), M, 10 / K ** 0.5, dtype=xdt)
+    y, g, u = gated.forward(L, x, w, keep=True)
+    at = torch.tensor(sorted({0, 1, 16, 64, M - 1, *range(M - 1, 0, -(M // 40 + 1))}), device=DEV)
+    gated.check_forward(L, x[at], w, "SILU", y[at], g[at], u[at])
+    assert y.isfinite().all()
+    dy = ref.normal((M, N), 5, 0.1, xdt)
+    dx = gated.backward(L, dy, g, u, w)[0]
+    gated.check_backward(L, dy[at], g[at], u[at], w, "SILU", dx[at])
+    assert dx.isfinite().all()
