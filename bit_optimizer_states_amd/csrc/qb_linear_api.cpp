@@ -141,7 +141,7 @@ BackwardLayout backward_layout(int xdt, int64_t M, int64_t K, int64_t N, int cou
 {
     const size_t pitch = (size_t)gemm_pitch(xdt, N) * count * dtype_bytes(xdt);
     // the partial sums' slices shrink as columns are added: what is reserved never does
-    const size_t most = (size_t)((M + 15) / 16) * (size_t)N, cap = (size_t)2048 * 512 + (size_t)N;
+    const size_t most = (size_t)((M + 7) / 8) * (size_t)N, cap = (size_t)2048 * 512 + (size_t)N;
     BackwardLayout l;
     l.dz = round_up((size_t)K * pitch, 256);
     l.split = l.dz + round_up((size_t)M * pitch, 256);
