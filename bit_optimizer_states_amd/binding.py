@@ -783,7 +783,7 @@ def grad_table(grads):
     """ctypes array of qb_grad from tensors, or from (g, out) pairs for clipping out of place (a tensor alone is clipped
     in place).  A program whose gradients stay where they are builds it once."""
     arr = (qb_grad * max(len(grads), 1))()
-    device = None
+    device, spans = None, []
     for i, entry in enumerate(grads):
         g, out = entry if isinstance(entry, (tuple, list)) else (entry, entry)
         if device is None:
@@ -791,7 +791,21 @@ def grad_table(grads):
         if out.dtype != g.dtype or out.numel() != g.numel():
             raise ValueError("out like its gradient expected")
         arr[i] = qb_grad(_at(g, device), _at(out, device), g.numel(), _dtype(g))
+        size = g.numel() * g.element_size()
+        if size:
+            spans.append((arr[i].out, arr[i].out + size, True))
+            if arr[i].g != arr[i].out:
+                spans.append((arr[i].g, arr[i].g + size, False))
     arr.device = device
+    # an output that overlaps another gradient or output: no clipping
+    arr.overlap, written, read = False, 0, 0
+    for begin, end, out in sorted(spans):
+        if begin < written or (out and begin < read):
+            arr.overlap = True
+        if out:
+            written = max(written, end)
+        else:
+            read = max(read, end)
     return arr
 
 
@@ -822,6 +836,8 @@ def qb_multi_tensor_clip_grads(table, count, max_norm, norm, stream=None):
     """out = g * min(1, max_norm / (norm[0] + 1e-6)) for every gradient of `table` (grad_table)."""
     lib()
     d = _norm_of_one(norm, table, count)
+    if getattr(table, "overlap", False):
+        raise ValueError("gradients that overlap no other one, nor appear twice, expected")
     _row_call("qb_multi_tensor_clip_grads", d, stream, table, count, max_norm, _at(norm, d))
 
 

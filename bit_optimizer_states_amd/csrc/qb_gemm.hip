@@ -115,7 +115,8 @@ __global__ __launch_bounds__(256) void k_unpack_transposed(const Weights2 ws, in
 // matrix pipes busy 72% of the time at the 1.9 GHz that the chip holds then; all fragments
 // read before the products 266; the loads first and each half read before its products
 // 286; steps of half the length in four buffers 275; four waves of 128 x 128 each 315; two
-// groups of waves kept half a step apart 256 (not built).
+// groups of waves kept half a step apart 256 (not built).  32x32x16 instructions, free of bank
+// conflicts too, take the whole layer from 320 to 340.
 // B's fragment is the first operand, so that a lane's four sums are four neighbouring
 // columns of C.
 

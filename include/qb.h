@@ -723,8 +723,8 @@ qb_status qb_stable_embedding_backward(const void* dy, qb_dtype gdt, const void*
 size_t qb_stable_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim);
 
 /*
- * The 4-bit layers: the product of qb_dequant_matmul with what a layer does to it, in one
- * kernel (the layers whose weights the pages hold in 4 bits: page "Quantize 🤗 Transformers
+ * The 4-bit layers: the product of qb_dequant_matmul with what a layer does to it in its
+ * epilogue (the layers whose weights the pages hold in 4 bits: page "Quantize 🤗 Transformers
  * models", section Using NF4), and the gradients that fine-tuning through
  * frozen 4-bit weights takes (page "bitsandbytes - Quantização de LLM", section on QLoRA;
  * page "Bitsandbytes", section QLoRA: Hesaplama veri türü).  Common to these calls:
@@ -739,9 +739,10 @@ size_t qb_stable_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim)
  *     propagate as in the formulas, into the rows that they enter.
  *   - Outputs must not overlap inputs or each other, unless said otherwise.
  *   - ws: device workspace, 16-byte aligned, of the *_workspace_bytes size (0: none, ws may be
- *     NULL), which never shrinks when M, K or N grows.  It holds nothing between calls and
- *     must not be shared by calls that may overlap in time (two captured graphs that run at
- *     once among them).
+ *     NULL), which never shrinks when M, K or N grows: the weights in the compute dtype, and up
+ *     to 80 MiB for partial sums of products split over their length.  It holds nothing
+ *     between calls and must not be shared by calls that may overlap in time (two captured
+ *     graphs that run at once among them).
  *   - No memory operations, so the calls may be captured; the first call on a device that
  *     needs the library's constant tables uploads them: make one before.
  */
@@ -770,8 +771,10 @@ typedef struct {
  *   residual  [M, N], or NULL; may be y itself.
  *   z         [M, N] out, or NULL: the pre-activation, which the gradient takes.
  *   y         [M, N] out.
- * Up to 64 rows one kernel reads the codes and no workspace is needed; from 65 rows on the
- * weights are dequantized into ws first (two kernels).  N == 0 is a no-op.
+ * Up to 64 rows (any number with K = 32) one kernel reads the codes and no workspace is needed.
+ * Beyond, the workspace is needed, and one kernel does it all where an estimate from the sizes
+ * favours it; else the weights are dequantized into ws and multiplied from there (two to four
+ * kernels).  N == 0 is a no-op.
  */
 qb_status qb_dequant_linear(const void* x, qb_dtype xdt, int64_t M, int64_t K, const uint8_t* codes,
                             const float* absmax, const qb_dq* dq, qb_code code, int32_t blocksize, int64_t N,
@@ -789,7 +792,8 @@ size_t qb_dequant_linear_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int
  *           is left as it is, and zero otherwise.
  * dz is rounded to xdt before it is multiplied by W (the matrix instructions take
  * that type; for binary32 nothing is rounded); dbias sums the unrounded dz.  N >= 1.
- * The workspace is needed for dx and dbias.  Up to four kernels.
+ * The workspace is needed for dx and dbias.  Up to six kernels: dz, dbias, the weights
+ * transposed, the product in one or two launches, its pieces joined.
  */
 qb_status qb_dequant_linear_backward(const void* dy, const void* z, qb_dtype xdt, int64_t M, int64_t K,
                                      const uint8_t* codes, const float* absmax, const qb_dq* dq, qb_code code,
@@ -804,7 +808,7 @@ size_t qb_dequant_linear_backward_workspace_bytes(qb_dtype xdt, int64_t M, int64
  *                      QB_EUNSUPPORTED); code, blocksize and blocksize2 (nested only) are shared.
  *   gate_out, up_out   [M, N] out, each may be NULL: g and u, which the gradient takes.
  *   y                  [M, N] out.
- * One kernel up to 64 rows, two from there on.  N == 0 is a no-op.
+ * Kernels and workspace as for qb_dequant_linear.  N == 0 is a no-op.
  */
 qb_status qb_dequant_gated(const void* x, qb_dtype xdt, int64_t M, int64_t K, const qb_weight* gate,
                            const qb_weight* up, qb_code code, int32_t blocksize, int32_t blocksize2, int64_t N,
@@ -816,7 +820,8 @@ size_t qb_dequant_gated_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int6
  *   dy, gate_out, up_out   [M, N]: the gradient of y; g and u as qb_dequant_gated wrote them.
  *   dx          [M, K] out, dgate, dup [M, N] out: each may be NULL (not wanted).
  * dg and du are rounded to xdt before they are multiplied.  N >= 1.  The workspace is needed
- * for dx.  Up to three kernels.
+ * for dx.  Up to five kernels: dg and du, the weights transposed, the product in one or two
+ * launches, its pieces joined.
  */
 qb_status qb_dequant_gated_backward(const void* dy, const void* gate_out, const void* up_out, qb_dtype xdt, int64_t M,
                                     int64_t K, const qb_weight* gate, const qb_weight* up, qb_code code,
@@ -828,8 +833,9 @@ size_t qb_dequant_gated_backward_workspace_bytes(qb_dtype xdt, int64_t M, int64_
  * The global gradient norm, and clipping by it, before an optimizer step (the 8-bit
  * optimizers are drop-in replacements in a training loop: page "bitsandbytes - Quantização de
  * LLM", section Workflow 3).
- * One gradient: n values of its own dtype at g and (clipping) out; out may be g.  Both may
- * begin at any element, as views of a bucket do.  n < 2^33; n == 0 is skipped.
+ * One gradient: n values of its own dtype at g and (clipping) out, which is g or overlaps no
+ * gradient.  Both may begin at any element, as views of a bucket do.  n < 2^33; n == 0 is
+ * skipped.
  */
 typedef struct {
     const void* g;
@@ -860,7 +866,7 @@ size_t qb_multi_tensor_grad_norm_workspace_bytes(int32_t count);
  *   norm       device [1] fp32, 16-byte aligned: what qb_multi_tensor_grad_norm wrote, or a
  *              norm over several ranks.  An infinite norm makes s 0, a NaN s NaN.
  * With s = 1 and out = g a gradient is left as it is (not read).  Gradients must not overlap
- * each other.  One launch per 150 gradients; may be captured.
+ * each other, nor appear twice.  One launch per 150 gradients; may be captured.
  */
 qb_status qb_multi_tensor_clip_grads(const qb_grad* grads, int32_t count, double max_norm, const float* norm,
                                      void* stream);

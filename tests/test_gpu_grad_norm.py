@@ -218,3 +218,21 @@ def test_refusals():
         with pytest.raises(L.QbError) as e:
             call()
         assert e.value.status == status
+
+
+def test_overlapping_gradients_are_measured_and_not_clipped():
+    """The norm may count a gradient twice; clipping would scale it twice or once, by chance."""
+    L = qb()
+    a, b = torch.full((100,), 3.0, device=DEV), torch.full((100,), 4.0, device=DEV)
+    out = torch.empty(200, device=DEV)
+    for entries in ([a, a], [a, a[50:]], [(a, out[:100]), (b, out[99:199])], [(a, b), b], [(a[:50], a[25:75])], [a, (b, a)]):
+        table = L.grad_table(entries)
+        norm = norm_of(L, table, len(entries))
+        assert abs(norm.item() - exact_norm([e[0] if isinstance(e, tuple) else e for e in entries])) < 1e-4
+        with pytest.raises(ValueError, match="overlap"):
+            L.qb_multi_tensor_clip_grads(table, len(entries), 1.0, norm)
+    for entries in ([a[:50], a[50:]], [(a, out[:100]), (b, out[100:])], [(a, out[:100]), (a, out[100:])], [a, a[:0], b]):
+        L.qb_multi_tensor_clip_grads(L.grad_table(entries), len(entries), 1.0, torch.ones(1, device=DEV))
+    one = torch.ones(1, device=DEV)             # the scale is 1 / (1 + 1e-6): a was clipped twice in place, b once
+    assert torch.equal(a, expected(expected(torch.full_like(a, 3.0), 1.0, one), 1.0, one))
+    assert torch.equal(b, expected(torch.full_like(b, 4.0), 1.0, one))
