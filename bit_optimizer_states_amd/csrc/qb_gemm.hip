@@ -306,36 +306,49 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
     const int full = end - (p.half && end == p.steps ? 1 : 0);      // steps of the whole length
     constexpr int PER = A_PER + B_PER;
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i)
+    for (int i = 0; i < STAGES; ++i)
         if (begin + i < end) load_step(begin + i, i);
-    // behind it step s has landed, and the buffer of step s - 1, which its readers have left, is free
-    auto arrive = [&](int s) {
-        if (s + STAGES - 1 <= end) wait_loads<(STAGES - 2) * PER>();
-        else wait_loads<0>();
-        pipeline_barrier();
-    };
-    int now = 0, free = STAGES - 1;
-    for (int s = begin; s < full; ++s) {
-        arrive(s);
-        const char* const buf = s_ab + now * BUF;
-        read_half(buf, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (s + STAGES - 1 < end) load_step(s + STAGES - 1, free);
-        read_half(buf, 1);
+    int now = 0;
+    // Step s with its first half's fragments in registers.  Behind the barrier step s + 1 has landed
+    // and every wave has read what it takes of step s: its buffer goes to step s + STAGES.
+    auto step = [&](int s, bool more, bool next) {
+        read_half(s_ab + now * BUF, 1);
         multiply_half(0);
-        multiply_half(1);
-        // the second half's reads are dealt among the first half's products
+        // the reads are dealt among the products
 #pragma unroll
         for (int i = 0; i < TM + TN; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, XDT == DT_F32 ? 8 : 2, 0);      // matrix instructions
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                          // an LDS read
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, 2 * TM * TN * (XDT == DT_F32 ? 4 : 1), 0);
-        free = now;
+        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN * (XDT == DT_F32 ? 4 : 1), 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) wait_loads<(STAGES - 2) * PER>();
+        else wait_loads<0>();
+        pipeline_barrier();
+        if (more) load_step(s + STAGES, now);
         now = now + 1 == STAGES ? 0 : now + 1;
-    }
+        if (next) read_half(s_ab + now * BUF, 0);
+        multiply_half(1);
+        if (next) {
+#pragma unroll
+            for (int i = 0; i < TM + TN; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, XDT == DT_F32 ? 8 : 2, 1);
+                if (more && i < PER) __builtin_amdgcn_sched_group_barrier(0x020, 1, 1);     // a load
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, TM * TN * (XDT == DT_F32 ? 4 : 1), 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (begin + STAGES <= end) wait_loads<(STAGES - 1) * PER>();
+    else wait_loads<0>();
+    pipeline_barrier();
+    if (begin < full) read_half(s_ab, 0);
+    int s = begin;
+    for (; s + STAGES < end; ++s) step(s, true, true);
+    for (; s + 1 < full; ++s) step(s, false, true);
+    if (s < full) step(s, false, false);
     if (full < end) {
-        arrive(full);
         read_half(s_ab + now * BUF, 1);
         multiply_half(1);
     }
