@@ -268,18 +268,22 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
 
     // a length of half a step too many: its last step begins half a step early, and only its
     // upper half is multiplied
-    auto load_step = [&](int s, int buffer) {
+    constexpr int PER = A_PER + B_PER;
+    auto load_one = [&](int s, int buffer, int i) {
         char* const dst = s_ab + buffer * BUF;
         const int64_t at = (int64_t)s * 128 - (p.half && s + 1 == p.steps ? 64 : 0);
-        const char* const as = (s < p.steps0 ? a0 : a1) + at;
-        const char* const bs = b0 + at;
-#pragma unroll
-        for (int i = 0; i < A_PER; ++i)
+        if (i < A_PER) {
+            const char* const as = (s < p.steps0 ? a0 : a1) + at;
             __builtin_amdgcn_global_load_lds((gptr_t)(as + a_off[i]), (lptr_t)(dst + (i * NW + wave) * 1024), 16, 0, 0);
+        } else {
+            const char* const bs = b0 + at;
+            __builtin_amdgcn_global_load_lds((gptr_t)(bs + b_off[i - A_PER]),
+                                             (lptr_t)(dst + BM * 128 + ((i - A_PER) * NW + wave) * 1024), 16, 0, 0);
+        }
+    };
+    auto load_step = [&](int s, int buffer) {
 #pragma unroll
-        for (int i = 0; i < B_PER; ++i)
-            __builtin_amdgcn_global_load_lds((gptr_t)(bs + b_off[i]), (lptr_t)(dst + BM * 128 + (i * NW + wave) * 1024),
-                                             16, 0, 0);
+        for (int i = 0; i < PER; ++i) load_one(s, buffer, i);
     };
 
     f32x4 acc[TN][TM];
@@ -290,12 +294,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
 
     const int a_row = (wm * (BM / WM) + r) * 128, b_row = BM * 128 + (wn * (BN / WN) + r) * 128;
     u32x4 bf[2][TN], af[2][TM];
-    auto read_half = [&](const char* buf, int kk) {
+    auto read_one = [&](const char* buf, int kk, int i) {
         const int c = ((4 * kk + g) ^ (r & 7)) * 16;
+        if (i < TN) bf[kk][i] = *reinterpret_cast<const u32x4*>(buf + b_row + i * 16 * 128 + c);
+        else af[kk][i - TN] = *reinterpret_cast<const u32x4*>(buf + a_row + (i - TN) * 16 * 128 + c);
+    };
+    auto read_half = [&](const char* buf, int kk) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) bf[kk][j] = *reinterpret_cast<const u32x4*>(buf + b_row + j * 16 * 128 + c);
-#pragma unroll
-        for (int t = 0; t < TM; ++t) af[kk][t] = *reinterpret_cast<const u32x4*>(buf + a_row + t * 16 * 128 + c);
+        for (int i = 0; i < TN + TM; ++i) read_one(buf, kk, i);
     };
     auto multiply_half = [&](int kk) {
 #pragma unroll
@@ -304,7 +310,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
             for (int j = 0; j < TN; ++j) mma_chunk<XDT>(bf[kk][j], af[kk][t], acc[j][t]);
     };
     const int full = end - (p.half && end == p.steps ? 1 : 0);      // steps of the whole length
-    constexpr int PER = A_PER + B_PER;
 #pragma unroll
     for (int i = 0; i < STAGES; ++i)
         if (begin + i < end) load_step(begin + i, i);
@@ -325,20 +330,24 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
         if (more) wait_loads<(STAGES - 2) * PER>();
         else wait_loads<0>();
         pipeline_barrier();
-        if (more) load_step(s + STAGES, now);
+        // A load, some of the next step's reads and of the products in turn: the address unit takes a load of
+        // 64 lanes 16 cycles, and the eight waves' loads in a row would keep the products waiting
+        const int freed = now;
         now = now + 1 == STAGES ? 0 : now + 1;
-        if (next) read_half(s_ab + now * BUF, 0);
-        multiply_half(1);
-        if (next) {
+        const char* const ahead = s_ab + now * BUF;
 #pragma unroll
-            for (int i = 0; i < TM + TN; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, XDT == DT_F32 ? 8 : 2, 1);
-                if (more && i < PER) __builtin_amdgcn_sched_group_barrier(0x020, 1, 1);     // a load
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+        for (int i = 0; i < PER; ++i) {
+            if (more) load_one(s + STAGES, freed, i);
+            if (next) {
+#pragma unroll
+                for (int k = 0; k < TM + TN; ++k)
+                    if (k * PER / (TM + TN) == i) read_one(ahead, 0, k);
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, TM * TN * (XDT == DT_F32 ? 4 : 1), 1);
+#pragma unroll
+            for (int k = 0; k < TM * TN; ++k)
+                if (k * PER / (TM * TN) == i) mma_chunk<XDT>(bf[1][k % TN], af[1][k / TN], acc[k % TN][k / TN]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
     };
     if (begin + STAGES <= end) wait_loads<(STAGES - 1) * PER>();
     else wait_loads<0>();

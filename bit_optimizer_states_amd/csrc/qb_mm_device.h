@@ -180,7 +180,8 @@ __device__ __forceinline__ void wait_loads()
 // those that it needs.
 __device__ __forceinline__ void pipeline_barrier()
 {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));       // lgkmcnt(0), of which the compiler knows
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
