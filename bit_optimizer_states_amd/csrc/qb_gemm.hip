@@ -109,14 +109,16 @@ __global__ __launch_bounds__(256) void k_unpack_transposed(const Weights2 ws, in
 // chunk p of an LDS row holds chunk p ^ (row % 8) of the operand's row, so that the rows
 // of one fragment lie in different banks.  A fragment is one chunk a lane: row lane % 16,
 // chunk 4 kk + lane / 16; with binary32 its four elements go to four instructions, the same
-// k order in both operands.  The first half of a step's fragments are read, then the next
-// step's loads are issued, then the second half's reads are dealt among the first half's
-// products.  4096 x 4096 x 11008 bf16 (the loop alone, binary32 out): 258 us, 1431 TFLOP/s, the
-// matrix pipes busy 72% of the time at the 1.9 GHz that the chip holds then; all fragments
-// read before the products 266; the loads first and each half read before its products
-// 286; steps of half the length in four buffers 275; four waves of 128 x 128 each 315; two
-// groups of waves kept half a step apart 256 (not built).  32x32x16 instructions, free of bank
-// conflicts too, take the whole layer from 320 to 340.
+// k order in both operands.  A step's first half of fragments is in registers when it begins;
+// the second half's reads are dealt among the first half's products, then the waves meet, and
+// the next step's first half and the loads are dealt among the second half's.
+// The whole layer of 4096 x 11008 x 4096 bf16 takes 308 us so (20 of them the dequantization),
+// 319 with the waves meeting at the beginning of a step, all fragments read before the products
+// 8 us more, the loads first and each half read before its products 28 more.  The matrix pipes
+// are busy 78% of the cycles (67% with the waves meeting at the beginning), and the clock falls
+// as that rises, 1.75 to 1.6 GHz: what is left is power.  32x32x16 instructions 330; steps of half the
+// length in four buffers, four waves of 128 x 128 each, two groups of waves kept half a step apart:
+// equal or slower.
 // B's fragment is the first operand, so that a lane's four sums are four neighbouring
 // columns of C.
 
