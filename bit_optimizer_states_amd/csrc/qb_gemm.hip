@@ -460,24 +460,27 @@ constexpr int64_t kEveryColumn = int64_t(1) << 40;
 // Tile shapes (the cases of gemm_shape), and the time in us of a step of a workgroup where 1, 2, ..
 // of them share a CU: fitted to layers of 4096 and 11008 inputs and outputs with 1 .. 4096
 // rows, their weights just dequantized (bf16).  A CU's only workgroup waits for memory:
-// 256 rows of 4096 x 4096 take 48 us in all in shape 4 with three buffers, 35 with five; many
-// small workgroups a CU hide it as well (shape 5: 30).
+// 256 rows of 4096 x 4096 take 48 us in all in 64 x 64 tiles with three buffers, 35 with five; many
+// small workgroups a CU hide it as well (with two buffers: 30).  Binary32 is bound by the matrix
+// instructions and takes the third or the fourth (4096 x 4096 x 4096 1009 us and 1085; the first 979).  (128 x 256 tiles are never the best by more
+// than a percent.)
 struct TileShape {
     int bm, bn, per_cu;
     double us[5];
 };
-constexpr int kShapeCount = 6, kCus = 256;
+constexpr int kShapeCount = 5, kCus = 256;
 constexpr TileShape kShapes[kShapeCount] = {
-    {256, 256, 1, {1.6}}, {128, 256, 1, {0.97}}, {128, 128, 1, {0.77}}, {128, 128, 2, {0.80, 0.95}},
+    {256, 256, 1, {1.6}}, {128, 128, 1, {0.77}}, {128, 128, 2, {0.80, 0.95}},
     {64, 64, 2, {0.38, 0.44}}, {64, 64, 5, {0.50, 0.56, 0.70, 0.89, 0.93}}};
 
 // Estimated time of `groups` workgroups of `steps` steps: rounds that fill every CU, then the
-// rest.  Binary32 is bound by the matrix instructions (0.55 TFLOP/s a CU) in large tiles.
+// rest.  Binary32 is bound by the matrix instructions (0.55 TFLOP/s a CU, 0.51 in 64 x 64 tiles) where
+// several share a CU.
 // (32-bit numbers, since the host takes this estimate at every call.)
 double rounds_us(int xdt, const TileShape& t, uint32_t groups, uint32_t steps)
 {
     auto step_us = [&](uint32_t k) {
-        const double flops = 2.0 * t.bm * t.bn * gemm_step(DT_F32) * k / 0.55e6;
+        const double flops = 2.0 * t.bm * t.bn * gemm_step(DT_F32) * k / (t.bm == 64 ? 0.51e6 : 0.55e6);
         return xdt == DT_F32 && flops > t.us[k - 1] ? flops : t.us[k - 1];
     };
     const uint32_t round = kCus * t.per_cu, full = groups / round, rest = groups - full * round;
@@ -498,7 +501,8 @@ GemmPlan gemm_plan(int xdt, int64_t M, int64_t R, uint32_t steps, bool may_split
     const double sums = (double)M * (double)R;
     const uint32_t fit = sums * kSplitMax <= (double)kPartMax ? (uint32_t)kSplitMax : (uint32_t)((double)kPartMax / sums);
     const uint32_t most = may_split ? (steps / 4 < fit ? steps / 4 : fit) : 1;
-    for (int i = 0; i < kShapeCount; ++i) {
+    const int first = xdt == DT_F32 ? 2 : 0, end = xdt == DT_F32 ? 4 : kShapeCount;
+    for (int i = first; i < end; ++i) {
         const TileShape& t = kShapes[i];
         const uint32_t tiles = (uint32_t)((M + t.bm - 1) / t.bm * ((R + t.bn - 1) / t.bn));
         for (uint32_t split = 1; split == 1 || (split <= most && split * tiles <= 5u * kCus); ++split) {
@@ -513,13 +517,17 @@ GemmPlan gemm_plan(int xdt, int64_t M, int64_t R, uint32_t steps, bool may_split
 template <int XDT, bool GATED>
 hipError_t gemm_shape(int shape, const GemmParams& p, int64_t n_first, int64_t columns, hipStream_t s)
 {
-    switch (shape) {
-    case 0: return gemm_as<XDT, 256, 256, 2, 4, 2, GATED>(p, n_first, columns, s);
-    case 1: return gemm_as<XDT, 128, 256, 2, 4, 3, GATED>(p, n_first, columns, s);
-    case 2: return gemm_as<XDT, 128, 128, 2, 4, 4, GATED>(p, n_first, columns, s);
-    case 3: return gemm_as<XDT, 128, 128, 2, 4, 2, GATED>(p, n_first, columns, s);
-    case 4: return gemm_as<XDT, 64, 64, 2, 2, 5, GATED>(p, n_first, columns, s);
-    default: return gemm_as<XDT, 64, 64, 2, 2, 2, GATED>(p, n_first, columns, s);
+    if constexpr (XDT == DT_F32) {
+        return shape == 2 ? gemm_as<XDT, 128, 128, 2, 4, 2, GATED>(p, n_first, columns, s)
+                          : gemm_as<XDT, 64, 64, 2, 2, 5, GATED>(p, n_first, columns, s);
+    } else {
+        switch (shape) {
+        case 0: return gemm_as<XDT, 256, 256, 2, 4, 2, GATED>(p, n_first, columns, s);
+        case 1: return gemm_as<XDT, 128, 128, 2, 4, 4, GATED>(p, n_first, columns, s);
+        case 2: return gemm_as<XDT, 128, 128, 2, 4, 2, GATED>(p, n_first, columns, s);
+        case 3: return gemm_as<XDT, 64, 64, 2, 2, 5, GATED>(p, n_first, columns, s);
+        default: return gemm_as<XDT, 64, 64, 2, 2, 2, GATED>(p, n_first, columns, s);
+        }
     }
 }
 
@@ -531,7 +539,7 @@ hipError_t gemm_tiles(GemmParams p, hipStream_t s)
     // or: the columns that whole rounds of 256 x 256 tiles cover, and the rest in the shape that suits it best (4096
     // rows of a gated block of 2 x 11008, 5.4 rounds: 709 us in 256 x 256 tiles alone, 662 so)
     const int64_t rows = tiles_over(M, 256), columns = tiles_over(R, 256), whole = rows * columns / kCus * kCus / rows;
-    if (whole > 0 && whole < columns) {
+    if (XDT != DT_F32 && whole > 0 && whole < columns) {
         p.split = 1;
         p.per_split = p.steps;
         const GemmPlan rest = gemm_plan(XDT, M, R - whole * 256, p.steps, false);

@@ -229,7 +229,7 @@ def test_no_rows_and_refusals():
 
 
 @pytest.mark.parametrize("M,K,N", [(3600, 160, 1751), (3601, 3520, 67), (1500, 224, 1055), (1499, 2112, 49)])
-@pytest.mark.parametrize("xdt", [BF16, F32])
+@pytest.mark.parametrize("xdt", [BF16, F16, F32])
 def test_large_tiles(M, K, N, xdt):
     L = qb()
     w = pair(N, K, NF4, 64, True, xdt, seed=M)

@@ -15,7 +15,7 @@ from gpu_helpers import DEV, qb
 
 pytestmark = pytest.mark.gpu
 
-F32, BF16 = torch.float32, torch.bfloat16
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
 ROWS, DIM, WIDE, EPS = 90, 160, 352, 1e-5
 
 
@@ -226,13 +226,13 @@ def test_tokens_one_and_a_few_at_a_time(xdt):
 
 
 # products that take each tile shape, whole and ragged, in one piece and split over their length, with and without
-# columns left over whole rounds; a last half step in the last piece
+# columns left over whole rounds (the last ones); a last half step in the last piece
 PLANS = [(65, 8192, 64), (65, 32, 64), (97, 4128, 129), (256, 1120, 4096), (300, 2080, 1000), (512, 1056, 4099),
-         (700, 4000, 700), (1030, 96, 5000), (2048, 160, 2049), (4100, 64, 4352)]
+         (700, 4000, 700), (1030, 96, 5000), (2048, 160, 2049), (4100, 64, 4352), (2000, 1120, 8500)]
 
 
 @pytest.mark.parametrize("M,K,N", PLANS)
-@pytest.mark.parametrize("xdt", [BF16, F32])
+@pytest.mark.parametrize("xdt", [BF16, F16, F32])
 def test_product_plans(M, K, N, xdt):
     """About fifty rows of products of many sizes, of every tile row, against 64 bits."""
     L = qb()
@@ -274,8 +274,8 @@ def test_few_rows_of_long_layers(M, K, N, nested, blocksize, xdt):
 
 
 @pytest.mark.parametrize("M,K,N", [(66, 8192, 700), (130, 4096, 3001), (200, 6144, 1100), (300, 2080, 2000),
-                                   (520, 1056, 3000), (1025, 96, 2500), (2050, 160, 1025), (4100, 64, 2200)])
-@pytest.mark.parametrize("xdt", [BF16, F32])
+                                   (520, 1056, 3000), (1025, 96, 2500), (2050, 160, 1025), (4100, 64, 2200), (2000, 1120, 4250)])
+@pytest.mark.parametrize("xdt", [BF16, F16, F32])
 def test_gated_plans(M, K, N, xdt):
     L = qb()
     print(f"[gated plan] {M} {K} {N} {xdt}", flush=True)
@@ -289,3 +289,19 @@ def test_gated_plans(M, K, N, xdt):
     dx = gated.backward(L, dy, g, u, w)[0]
     gated.check_backward(L, dy[at], g[at], u[at], w, "SILU", dx[at])
     assert dx.isfinite().all()
+
+
+@pytest.mark.parametrize("M", [3, 7, 12, 30, 45, 60])
+@pytest.mark.parametrize("N", [40, 6150])
+@pytest.mark.parametrize("nested", [False, True])
+@pytest.mark.parametrize("xdt", [BF16, F16, F32])
+def test_rows_kernels(M, N, nested, xdt):
+    """Every number of rows a workgroup takes, with 8 and with 16 waves, one weight and two, in every type."""
+    L = qb()
+    w = gated.pair(N, 160, oracle.FP4, 128, nested, xdt, M)
+    x = ref.normal((M, 160), M, 0.8, dtype=xdt)
+    y, g, u = gated.forward(L, x, w, "GELU", keep=True)
+    gated.check_forward(L, x, w, "GELU", y, g, u)
+    bias = ref.normal((N,), 1, dtype=xdt)
+    y, z = linear.forward(L, x, w[0], bias, "RELU", keep=True)
+    linear.check_forward(L, x, w[0], bias, "RELU", None, y, z)

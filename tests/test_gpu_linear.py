@@ -370,7 +370,7 @@ LARGE = [(3600, 160, 3501), (3601, 3520, 130), (1500, 224, 2111), (1499, 2112, 9
 
 
 @pytest.mark.parametrize("M,K,N", LARGE)
-@pytest.mark.parametrize("xdt", [BF16, F32])
+@pytest.mark.parametrize("xdt", [BF16, F16, F32])
 def test_large_tiles(M, K, N, xdt):
     L = qb()
     w = ref.Weight(N, K, NF4, 64, True, xdt, seed=M)
