@@ -462,8 +462,8 @@ constexpr int64_t kEveryColumn = int64_t(1) << 40;
 // rows, their weights just dequantized (bf16).  A CU's only workgroup waits for memory:
 // 256 rows of 4096 x 4096 take 48 us in all in 64 x 64 tiles with three buffers, 35 with five; many
 // small workgroups a CU hide it as well (with two buffers: 30).  Binary32 is bound by the matrix
-// instructions and takes the third or the fourth (4096 x 4096 x 4096 1009 us and 1085; the first 979).  (128 x 256 tiles are never the best by more
-// than a percent.)
+// instructions and takes the third or the fourth (4096 x 4096 x 4096 1009 us and 1085; in the
+// first 979).  128 x 256 tiles are never the best by more than a percent.
 struct TileShape {
     int bm, bn, per_cu;
     double us[5];
