@@ -39,7 +39,7 @@ __device__ __forceinline__ void store_up_to4(void* p, int64_t i, int cnt, const 
 {
     if (cnt >= 4) {
         if constexpr (DT == DT_F32) *(QB_G f32x4_e4*)(static_cast<float*>(p) + i) = v;
-        else *(QB_G u32x2_e2*)(static_cast<uint16_t*>(p) + i) = u32x2{pack_pair<DT>(v.x, v.y), pack_pair<DT>(v.z, v.w)};
+        else *(QB_G u32x2_e2*)(static_cast<uint16_t*>(p) + i) = u32x2{pack_two<DT>(v.x, v.y), pack_two<DT>(v.z, v.w)};
     } else {
 #pragma unroll
         for (int j = 0; j < 3; ++j)
@@ -107,8 +107,8 @@ __device__ __forceinline__ void store_up_to8(void* p, int64_t i, int cnt, const 
             store_up_to4<DT>(p, i + 4, 4, f32x4{v[4], v[5], v[6], v[7]});
         } else {
             *(QB_G u32x4_e2*)(static_cast<uint16_t*>(p) + i) =
-                u32x4{pack_pair<DT>(v[0], v[1]), pack_pair<DT>(v[2], v[3]), pack_pair<DT>(v[4], v[5]),
-                      pack_pair<DT>(v[6], v[7])};
+                u32x4{pack_two<DT>(v[0], v[1]), pack_two<DT>(v[2], v[3]), pack_two<DT>(v[4], v[5]),
+                      pack_two<DT>(v[6], v[7])};
         }
     } else {
 #pragma unroll

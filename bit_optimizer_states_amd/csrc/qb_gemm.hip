@@ -1,5 +1,4 @@
-// qb_gemm.hip -- the tiled matrix product behind the 4-bit layers of many rows, and the
-// kernels that lay its weights out.
+// qb_gemm.hip -- the tiled matrix product behind the 4-bit layers of many rows.
 //
 // From a few hundred rows on the products bound the layer, not the weights: each
 // weight is dequantized once into a workspace in the compute dtype (N K elements written
@@ -14,89 +13,6 @@ namespace qb {
 namespace {
 
 int64_t tiles_over(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
-
-// ---------------------------------------------------------------------------
-// weights into the compute dtype
-// ---------------------------------------------------------------------------
-
-struct Weights2 {
-    Weight4 w[2];
-};
-
-// Transposed, into out[k][n]: a workgroup takes 64 rows n and 128 columns k, 8 weights of two
-// neighbouring rows a thread at a time into LDS, and writes rows k of 64 n (128 bytes, 256 in
-// binary32).  16-byte chunk c of LDS row k lies at chunk c ^ spread(k): the threads of a
-// wave, which hold 16 k eight apart and 4 row pairs, write to different banks but for two
-// each.  (Rows padded by 16 bytes instead fell into one bank: 4096 x 4096 15.1 us.)
-template <int XDT, bool DQ>
-__global__ __launch_bounds__(256) void k_unpack_transposed(const Weights2 ws, int64_t N, int64_t K, int64_t pitch,
-                                                           int64_t np, const Weight4Format f, void* __restrict__ out,
-                                                           const QbTables* __restrict__ tab)
-{
-    constexpr int ES = XDT == DT_F32 ? 4 : 2;
-    constexpr int LP = 64 * ES, CPR = LP / 16;                // bytes and chunks of an LDS row of 64 n
-    __shared__ __attribute__((aligned(16))) char s_t[128 * LP];
-    __shared__ float s_val[16];
-    __shared__ float s_dyn[DQ ? 256 : 1];
-    const int tid = threadIdx.x, kl = (tid & 15) * 8;
-    const int64_t k0 = (int64_t)blockIdx.x * 128, n0 = (int64_t)blockIdx.y * 64;
-    const Weight4 w = ws.w[blockIdx.z];
-    // row pairs tid / 16 and tid / 16 + 16 of the tile: codes and constants of 8 weights of each row
-    uint32_t code[2][2], c2[2][2];
-    float a[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t n = n0 + 2 * ((tid >> 4) + 16 * i) + h, e = n * K + k0 + kl, blk = e >> f.log2B;
-            code[i][h] = c2[i][h] = 0u;
-            a[i][h] = 0.0f;
-            if (n < N && k0 + kl < K) {
-                code[i][h] = gld<uint32_t>(w.codes + e / 2);
-                if constexpr (DQ) {
-                    c2[i][h] = gld<uint8_t>(w.c2 + blk);
-                    a[i][h] = gld<float>(w.absmax2 + (blk >> f.log2B2));
-                } else {
-                    a[i][h] = gld<float>(w.absmax + blk);
-                }
-            }
-        }
-    const float mu = DQ ? gld<float>(w.offset) : 0.0f;
-    if (tid < 16) s_val[tid] = (f.code4 == 0 ? tab->nf4 : tab->fp4)[tid];
-    if constexpr (DQ) s_dyn[tid] = tab->dyn8[tid];
-    __syncthreads();
-    auto spread = [](int k) { return XDT == DT_F32 ? ((k >> 3) & 7) * 2 : (k >> 3) & 7; };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int pr = (tid >> 4) + 16 * i;
-        Frag<DT_F32> v[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t n = n0 + 2 * pr + h;
-            const float c = DQ ? s_dyn[c2[i][h]] * a[i][h] + mu : a[i][h];       // two rounded operations
-            dequant_frag<DT_F32>(code[i][h], n < N ? c : 0.0f, s_val, v[h]);     // zeros beyond the last row
-        }
-        const int at = 2 * pr * ES;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            char* const p = s_t + (kl + j) * LP + ((at / 16) ^ spread(kl)) * 16 + at % 16;
-            if constexpr (XDT == DT_F32) {
-                typedef float f32x2_t __attribute__((ext_vector_type(2)));
-                *reinterpret_cast<f32x2_t*>(p) = f32x2_t{v[0].w[j], v[1].w[j]};
-            } else {
-                *reinterpret_cast<uint32_t*>(p) = pack_pair<XDT>(v[0].w[j], v[1].w[j]);
-            }
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 128 * CPR / 256; ++i) {
-        const int o = tid + 256 * i, row = o / CPR, c = o % CPR;
-        if (k0 + row < K && n0 + c * (16 / ES) < np)
-            gst<u32x4>(static_cast<char*>(out) + ((k0 + row) * pitch + blockIdx.z * np + n0) * ES + 16 * c,
-                       *reinterpret_cast<const u32x4*>(s_t + row * LP + (c ^ spread(row)) * 16));
-    }
-}
 
 // ---------------------------------------------------------------------------
 // C = A B^T
@@ -568,26 +484,6 @@ hipError_t gemm_rows(const GemmParams& p, hipStream_t s)
     return hipSuccess;
 }
 
-template <int XDT, bool DQ>
-hipError_t transposed_as(const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
-                         hipStream_t s)
-{
-    const QbTables* tab = device_tables();
-    if (!tab) return hipErrorNotInitialized;
-    const Weights2 ws{{w[0], w[count - 1]}};
-    const int64_t np = gemm_pitch(XDT, N), pitch = np * count;
-    const dim3 grid((unsigned)tiles_over(K, 128), (unsigned)tiles_over(np, 64), (unsigned)count);
-    return launch_grid(k_unpack_transposed<XDT, DQ>, grid, 256, 0, s, ws, N, K, pitch, np, f, out, tab);
-}
-
-template <int XDT>
-hipError_t transposed_dq(const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
-                         hipStream_t s)
-{
-    return f.nested ? transposed_as<XDT, true>(w, count, N, K, f, out, s)
-                    : transposed_as<XDT, false>(w, count, N, K, f, out, s);
-}
-
 }  // namespace
 
 hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
@@ -598,16 +494,6 @@ hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_
         d[i] = DequantDesc{w[i].codes,   w[i].absmax, w[i].c2, w[i].absmax2,
                            w[i].offset, static_cast<char*>(out) + i * each, N * K, 0};
     return launch_dequant4_kept(d, count, f.code4, 1 << f.log2B, 1 << f.log2B2, f.nested != 0, xdt, s);
-}
-
-hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f,
-                                    void* out, hipStream_t s)
-{
-    switch (xdt) {
-    case DT_F32: return transposed_dq<DT_F32>(w, count, N, K, f, out, s);
-    case DT_F16: return transposed_dq<DT_F16>(w, count, N, K, f, out, s);
-    default: return transposed_dq<DT_BF16>(w, count, N, K, f, out, s);
-    }
 }
 
 double gemm_us(int xdt, int64_t M, int64_t R, int64_t len)

@@ -68,10 +68,15 @@ constexpr int64_t gated_rows(int64_t n) { return (n + 15) / 16 * 32; }
 // behind the first.
 hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f, void* out,
                          size_t each, hipStream_t s);
-// Transposed: out[k][n], for two weights next to each other (columns n of the second at
-// gemm_pitch(N) + n); the pitch is count * gemm_pitch(N), its padding zero.
-hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format& f,
-                                    void* out, hipStream_t s);
+// One or two weights [N, K] transposed: out[k][n], the second's columns n at np + n, np =
+// gemm_pitch(N); the pitch is count * np, its padding zero.
+struct TransposedWeights {
+    Weight4 w[2];
+    Weight4Format f;
+    void* out;
+    int64_t N, K, np;
+    int32_t count;
+};
 
 // C = epilogue(A B^T).  A [M, len] in one or two pieces of columns (a0: the first len0, a1
 // the others; both of `lda` elements a row, 16-byte aligned rows), B [R, len] of ldb
@@ -102,9 +107,11 @@ constexpr int64_t gemm_part_floats(int64_t M, int64_t R)
 
 // dz = dy act'(z) [M, N] into `dz` of pitch `pitch` (its padding zero; nullptr: not
 // wanted) and into `dz_out` [M, N] (nullptr: not wanted), and per slice of rows the sums of
-// dz over its rows, part[slice][N] (nullptr: not wanted).  z == nullptr: dz = dy.
-hipError_t launch_linear_dz(int xdt, const void* dy, const void* z, int act, int64_t M, int64_t N, void* dz,
-                            int64_t pitch, void* dz_out, float* part, int slices, hipStream_t s);
+// dz over its rows, part[slice][N] (nullptr: not wanted).  z == nullptr: dz = dy.  dz_too false:
+// none of this.  And the weights `t` (nullptr: not wanted).
+hipError_t launch_linear_grad(int xdt, bool dz_too, const void* dy, const void* z, int act, int64_t M, int64_t N, void* dz,
+                              int64_t pitch, void* dz_out, float* part, int slices, const TransposedWeights* t,
+                              hipStream_t s);
 constexpr int kDzCols = 512, kDzWaves = 4;
 // Slices of rows: enough workgroups for the chip (2048 over the blocks of columns), four rows a
 // wave at least, two where that leaves fewer than 64 slices (301 rows of 2731 columns in binary32:
@@ -120,8 +127,10 @@ inline int linear_dz_slices(int64_t M, int64_t N)
 hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool accumulate, void* db, int bias_dt,
                            hipStream_t s);
 // dg = dh u act'(g) and du = dh act(g) into `dz` ([M, pitch] each, du behind dg; nullptr:
-// not wanted) and into dg_out, du_out [M, N] (nullptr: not wanted).
-hipError_t launch_gated_dz(int xdt, const void* dh, const void* g, const void* u, int act, int64_t M, int64_t N,
-                           void* dz, int64_t pitch, void* dg_out, void* du_out, hipStream_t s);
+// not wanted) and into dg_out, du_out [M, N] (nullptr: not wanted).  And the weights `t`
+// (nullptr: not wanted).
+hipError_t launch_gated_grad(int xdt, const void* dh, const void* g, const void* u, int act, int64_t M, int64_t N,
+                             void* dz, int64_t pitch, void* dg_out, void* du_out, const TransposedWeights* t,
+                             hipStream_t s);
 
 }  // namespace qb

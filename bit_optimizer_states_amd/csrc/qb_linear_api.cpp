@@ -152,18 +152,20 @@ BackwardLayout backward_layout(int xdt, int64_t M, int64_t K, int64_t N, int cou
 
 bool whole_steps(int xdt, int64_t n) { return n % gemm_step(xdt) == 0; }
 
-// dx = [dz_0 dz_1] [W_0; W_1] for dz of rows of `lda` elements.
-hipError_t input_gradient(int xdt, const void* dz0, const void* dz1, int64_t lda, const Weight4* w, int count,
-                          const Weight4Format& f, int64_t M, int64_t K, int64_t N, void* dx, void* ws, float* part,
-                          hipStream_t s)
+TransposedWeights transposed(int xdt, const Weight4* w, int count, const Weight4Format& f, int64_t K, int64_t N, void* ws)
 {
-    const int64_t pitch = gemm_pitch(xdt, N);
-    hipError_t e = launch_unpack_transposed(xdt, w, count, N, K, f, ws, s);
-    if (e != hipSuccess) return e;
-    const GemmArgs g{dz0, dz1, ws, nullptr, M, K, pitch, pitch * count, lda, pitch * count};
+    return TransposedWeights{{w[0], w[count - 1]}, f, ws, N, K, gemm_pitch(xdt, N), count};
+}
+
+// dx = [dz_0 dz_1] [W_0; W_1] for dz of rows of `lda` elements and the weights `t`.
+hipError_t input_gradient(int xdt, const void* dz0, const void* dz1, int64_t lda, const TransposedWeights& t, int64_t M,
+                          void* dx, float* part, hipStream_t s)
+{
+    const int64_t pitch = t.np * t.count;
+    const GemmArgs g{dz0, dz1, t.out, nullptr, M, t.K, t.np, pitch, lda, pitch};
     Epilogue out{};
     out.y = dx;
-    out.N = K;
+    out.N = t.K;
     return launch_gemm(xdt, false, g, out, part, s);
 }
 
@@ -235,16 +237,17 @@ qb_status qb_dequant_linear_backward(const void* dy, const void* z, qb_dtype xdt
     hipStream_t s = static_cast<hipStream_t>(stream);
     char* const wp = static_cast<char*>(ws);
     const int64_t pitch = gemm_pitch(xdt, N);
+    const TransposedWeights t = transposed(xdt, &w, 1, f, K, N, wp);
     const void* a = dy;
     int64_t lda = N;
     hipError_t e = hipSuccess;
     if (M > 0) {
         const bool own = dx && (act != QB_ACT_NONE || !whole_steps(xdt, N));     // dx reads a padded dz
         const bool given = own && dz && whole_steps(xdt, N);                     // ... which the caller's dz is
-        const int slices = linear_dz_slices(M, N);
-        if (own || dz || dbias)
-            e = launch_linear_dz(xdt, dy, act != QB_ACT_NONE ? z : nullptr, act, M, N, own && !given ? wp + l.dz : nullptr,
-                                 pitch, dz, dbias ? reinterpret_cast<float*>(wp + l.part) : nullptr, slices, s);
+        e = launch_linear_grad(xdt, own || dz || dbias, dy, act != QB_ACT_NONE ? z : nullptr, act, M, N,
+                               own && !given ? wp + l.dz : nullptr, pitch, dz,
+                               dbias ? reinterpret_cast<float*>(wp + l.part) : nullptr, linear_dz_slices(M, N),
+                               dx ? &t : nullptr, s);
         if (own) {
             a = given ? dz : wp + l.dz;
             lda = pitch;
@@ -253,7 +256,7 @@ qb_status qb_dequant_linear_backward(const void* dy, const void* z, qb_dtype xdt
     if (e == hipSuccess && dbias)
         e = launch_bias_sum(reinterpret_cast<float*>(wp + l.part), M > 0 ? linear_dz_slices(M, N) : 0, N,
                             accumulate != 0, dbias, bdt, s);
-    if (e == hipSuccess && dx && M > 0) e = input_gradient(xdt, a, nullptr, lda, &w, 1, f, M, K, N, dx, wp,
+    if (e == hipSuccess && dx && M > 0) e = input_gradient(xdt, a, nullptr, lda, t, M, dx,
                                                               reinterpret_cast<float*>(wp + l.split), s);
     return hip_status(e);
 }
@@ -320,12 +323,13 @@ qb_status qb_dequant_gated_backward(const void* dy, const void* gate_out, const 
     char* const wp = static_cast<char*>(ws);
     const int64_t pitch = gemm_pitch(xdt, N);
     const bool given = dgate && dup && whole_steps(xdt, N);       // dx reads the caller's arrays
-    hipError_t e = launch_gated_dz(xdt, dy, gate_out, up_out, act, M, N, dx && !given ? wp + l.dz : nullptr, pitch,
-                                   dgate, dup, s);
+    const TransposedWeights t = transposed(xdt, w, 2, f, K, N, wp);
+    hipError_t e = launch_gated_grad(xdt, dy, gate_out, up_out, act, M, N, dx && !given ? wp + l.dz : nullptr, pitch, dgate,
+                                     dup, dx ? &t : nullptr, s);
     if (e == hipSuccess && dx) {
         const void* const dg = given ? dgate : wp + l.dz;
         const void* const du = given ? dup : wp + l.dz + (size_t)M * pitch * dtype_bytes(xdt);
-        e = input_gradient(xdt, dg, du, pitch, w, 2, f, M, K, N, dx, wp, reinterpret_cast<float*>(wp + l.split), s);
+        e = input_gradient(xdt, dg, du, pitch, t, M, dx, reinterpret_cast<float*>(wp + l.split), s);
     }
     return hip_status(e);
 }

@@ -91,7 +91,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 // Two binary32 values rounded to nearest even into one word of the compute
 // dtype, a in the low half.
 template <int XDT>
-__device__ __forceinline__ uint32_t pack_pair(float a, float b)
+__device__ __forceinline__ uint32_t pack_two(float a, float b)
 {
     if constexpr (XDT == DT_BF16) {
         const bf16x2 h = __builtin_convertvector((f32x2{a, b}), bf16x2);    // one v_cvt_pk_bf16_f32
@@ -126,7 +126,7 @@ __device__ __forceinline__ void dequant_frag(uint32_t word, float a, const float
             f.w[2 * j] = hi;
             f.w[2 * j + 1] = lo;
         } else {
-            f.w[j] = pack_pair<XDT>(hi, lo);
+            f.w[j] = pack_two<XDT>(hi, lo);
         }
     }
 }
@@ -153,7 +153,7 @@ __device__ __forceinline__ void scaled(const float* v, float a, Frag<XDT>& f)
             f.w[2 * j] = v[2 * j] * a;
             f.w[2 * j + 1] = v[2 * j + 1] * a;
         } else {
-            f.w[j] = pack_pair<XDT>(v[2 * j] * a, v[2 * j + 1] * a);
+            f.w[j] = pack_two<XDT>(v[2 * j] * a, v[2 * j + 1] * a);
         }
     }
 }

@@ -792,8 +792,8 @@ size_t qb_dequant_linear_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int
  *           is left as it is, and zero otherwise.
  * dz is rounded to xdt before it is multiplied by W (the matrix instructions take
  * that type; for binary32 nothing is rounded); dbias sums the unrounded dz.  N >= 1.
- * The workspace is needed for dx and dbias.  Up to six kernels: dz, dbias, the weights
- * transposed, the product in one or two launches, its pieces joined.
+ * The workspace is needed for dx and dbias.  Up to five kernels: dz and the weights
+ * transposed, dbias, the product in one or two launches, its pieces joined.
  */
 qb_status qb_dequant_linear_backward(const void* dy, const void* z, qb_dtype xdt, int64_t M, int64_t K,
                                      const uint8_t* codes, const float* absmax, const qb_dq* dq, qb_code code,
@@ -820,7 +820,7 @@ size_t qb_dequant_gated_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int6
  *   dy, gate_out, up_out   [M, N]: the gradient of y; g and u as qb_dequant_gated wrote them.
  *   dx          [M, K] out, dgate, dup [M, N] out: each may be NULL (not wanted).
  * dg and du are rounded to xdt before they are multiplied.  N >= 1.  The workspace is needed
- * for dx.  Up to five kernels: dg and du, the weights transposed, the product in one or two
+ * for dx.  Up to four kernels: dg, du and the weights transposed, the product in one or two
  * launches, its pieces joined.
  */
 qb_status qb_dequant_gated_backward(const void* dy, const void* gate_out, const void* up_out, qb_dtype xdt, int64_t M,

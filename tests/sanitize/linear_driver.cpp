@@ -61,14 +61,13 @@ hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_
     weights_end = offset_of(out) + (count - 1) * (double)each + bytes;
     return done();
 }
-hipError_t launch_unpack_transposed(int xdt, const Weight4* w, int count, int64_t N, int64_t K, const Weight4Format&,
-                                    void* out, hipStream_t)
+static void transposed(int xdt, const TransposedWeights* t)
 {
-    if (!w[0].codes || !w[count - 1].codes) ++failures;
-    const double bytes = (double)K * (double)gemm_pitch(xdt, N) * count * es(xdt);
-    inside(out, bytes);
-    weights_end = offset_of(out) + bytes;
-    return done();
+    if (!t) return;
+    if (!t->w[0].codes || !t->w[t->count - 1].codes || t->np != gemm_pitch(xdt, t->N)) ++failures;
+    const double bytes = (double)t->K * (double)t->np * t->count * es(xdt);
+    inside(t->out, bytes);
+    weights_end = offset_of(t->out) + bytes;
 }
 hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t)
 {
@@ -81,13 +80,16 @@ hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e
     dz_end = 0;
     return done();
 }
-hipError_t launch_linear_dz(int xdt, const void*, const void*, int, int64_t M, int64_t N, void* dz, int64_t pitch, void*,
-                            float* part, int slices, hipStream_t)
+hipError_t launch_linear_grad(int xdt, bool dz_too, const void*, const void*, int, int64_t M, int64_t N, void* dz,
+                              int64_t pitch, void* dz_out, float* part, int slices, const TransposedWeights* t, hipStream_t)
 {
+    if (!dz_too && (dz || dz_out || part)) ++failures;
+    transposed(xdt, t);
     if (dz) inside(dz, (double)M * (double)pitch * es(xdt));
+    if (dz && (!t || offset_of(dz) < weights_end)) ++failures;
     if (part) inside(part, 4.0 * slices * (double)N);
     dz_end = dz ? offset_of(dz) + (double)M * (double)pitch * es(xdt) : 0;
-    if (part && dz && offset_of(part) < dz_end) ++failures;
+    if (part && (offset_of(part) < dz_end || (t && offset_of(part) < weights_end))) ++failures;
     return done();
 }
 hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool, void*, int, hipStream_t)
@@ -95,11 +97,12 @@ hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool, void*
     if (slices) inside(part, 4.0 * slices * (double)N);
     return done();
 }
-hipError_t launch_gated_dz(int xdt, const void*, const void*, const void*, int, int64_t M, int64_t N, void* dz,
-                           int64_t pitch, void*, void*, hipStream_t)
+hipError_t launch_gated_grad(int xdt, const void*, const void*, const void*, int, int64_t M, int64_t, void* dz,
+                             int64_t pitch, void*, void*, const TransposedWeights* t, hipStream_t)
 {
-    (void)N;
+    transposed(xdt, t);
     if (dz) inside(dz, 2.0 * (double)M * (double)pitch * es(xdt));
+    if (dz && (!t || offset_of(dz) < weights_end)) ++failures;
     dz_end = dz ? offset_of(dz) + 2.0 * (double)M * (double)pitch * es(xdt) : 0;
     return done();
 }
