@@ -368,13 +368,23 @@ int32_t tiles_of(const qb_grad& g)
     return (int32_t)((g.n + tile - 1) / tile);
 }
 
-// The next launch's gradients, empty ones left out: from *at on ...
+const char* end_of(const void* p, const qb_grad& g) { return static_cast<const char*>(p) + g.n * dtype_bytes(g.dtype); }
+
+// Whether gradient b, and its output, begin where those of a end, as neighbours of a bucket do.
+bool joins(const qb_grad& a, const qb_grad& b, bool out)
+{
+    return a.dtype == b.dtype && a.n + b.n < kGradMax && end_of(a.g, a) == b.g && (!out || end_of(a.out, a) == b.out);
+}
+
+// The next launch's gradients, empty ones left out and neighbours joined into one (448 views of a
+// bucket, 65536 binary32 each: 60 us for norm and clipping, 73 in entries of their own): from *at on ...
 void next_table(const qb_grad* grads, int32_t count, int32_t* at, NormTable* t)
 {
     t->count = t->tiles = 0;
-    for (; t->count < kNormGrads && *at < count; ++*at) {
-        const qb_grad& g = grads[*at];
+    while (t->count < kNormGrads && *at < count) {
+        qb_grad g = grads[(*at)++];
         if (g.n == 0) continue;
+        for (; *at < count && (grads[*at].n == 0 || joins(g, grads[*at], false)); ++*at) g.n += grads[*at].n;
         t->g[t->count] = g.g;
         t->size[t->count++] = size_of(g);
         t->tiles += tiles_of(g);
@@ -385,9 +395,16 @@ void next_table(const qb_grad* grads, int32_t count, int32_t* at, NormTable* t)
 void next_table(const qb_grad* grads, int32_t* at, ScaleTable* t)
 {
     t->count = t->tiles = 0;
-    for (; t->count < kScaleGrads && *at >= 0; --*at) {
-        const qb_grad& g = grads[*at];
+    while (t->count < kScaleGrads && *at >= 0) {
+        qb_grad g = grads[(*at)--];
         if (g.n == 0) continue;
+        for (; *at >= 0 && (grads[*at].n == 0 || joins(grads[*at], g, true)); --*at) {
+            const qb_grad& before = grads[*at];
+            if (before.n == 0) continue;
+            g.g = before.g;
+            g.out = before.out;
+            g.n += before.n;
+        }
         t->g[t->count] = g.g;
         t->out[t->count] = g.out;
         t->size[t->count++] = size_of(g);

@@ -851,8 +851,8 @@ typedef struct {
  *   norm    [1] fp32 out, 16-byte aligned; 0 without gradients.
  *   ws      device workspace of qb_multi_tensor_grad_norm_workspace_bytes(count) bytes, 16-byte
  *           aligned; holds nothing between calls.
- * The same bits on every run.  One launch per 224 gradients and one more (a few small
- * gradients: one in all); no memory operations, so the call may be captured.  Several
+ * The same bits on every run.  One launch per 224 gradients (neighbours in memory, of one
+ * type and in order, count as one) and one more (a few small gradients: one in all); no memory operations, so the call may be captured.  Several
  * ranks' norms of their own gradients make the global one as sqrt(sum of norm^2).
  */
 qb_status qb_multi_tensor_grad_norm(const qb_grad* grads, int32_t count, float* norm, void* ws, size_t ws_bytes,
@@ -866,7 +866,8 @@ size_t qb_multi_tensor_grad_norm_workspace_bytes(int32_t count);
  *   norm       device [1] fp32, 16-byte aligned: what qb_multi_tensor_grad_norm wrote, or a
  *              norm over several ranks.  An infinite norm makes s 0, a NaN s NaN.
  * With s = 1 and out = g a gradient is left as it is (not read).  Gradients must not overlap
- * each other, nor appear twice.  One launch per 150 gradients; may be captured.
+ * each other, nor appear twice.  One launch per 150 gradients (neighbours count as
+ * one); may be captured.
  */
 qb_status qb_multi_tensor_clip_grads(const qb_grad* grads, int32_t count, double max_norm, const float* norm,
                                      void* stream);

@@ -181,6 +181,19 @@ int main()
         EXPECT(qb_multi_tensor_clip_grads(grads.data(), count, 1.0, F, nullptr), QB_OK);
         EXPECT(seen_elements, total);
     }
+    {
+        // neighbours are one entry, up to the longest gradient there may be
+        std::vector<qb_grad> grads;
+        const int64_t n = int64_t(1) << 30;
+        for (int64_t i = 0; i < 300; ++i) grads.push_back(qb_grad{D + 4 * n * i, D + 4 * n * i, n, QB_F32});
+        const int start = launches;
+        seen_elements = 0;
+        ws_bytes = qb_multi_tensor_grad_norm_workspace_bytes(300);
+        EXPECT(qb_multi_tensor_grad_norm(grads.data(), 300, F, ws_begin, ws_bytes, nullptr), QB_OK);
+        EXPECT(qb_multi_tensor_clip_grads(grads.data(), 300, 1.0, F, nullptr), QB_OK);
+        EXPECT(seen_elements, 600 * n);
+        EXPECT(launches - start, 3);
+    }
     const int before = launches;
     ws_bytes = qb_dequant_linear_workspace_bytes(QB_BF16, 100, 64, 64);
     EXPECT(qb_dequant_linear(A, QB_BF16, 100, 64, U, F, nullptr, QB_NF4, 64, 64, nullptr, QB_F32, QB_ACT_NONE, nullptr,

@@ -236,3 +236,50 @@ def test_overlapping_gradients_are_measured_and_not_clipped():
     one = torch.ones(1, device=DEV)             # the scale is 1 / (1 + 1e-6): a was clipped twice in place, b once
     assert torch.equal(a, expected(expected(torch.full_like(a, 3.0), 1.0, one), 1.0, one))
     assert torch.equal(b, expected(torch.full_like(b, 4.0), 1.0, one))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lengths", [[64] * 500, [1, 2, 3, 4097, 5, 0, 8192, 1, 0, 30001], [70000, 1, 70000], [4096, 0, 0, 4096]])
+def test_neighbours_of_a_bucket(lengths, in_place):
+    """Views that lie next to each other, in order, backwards and with their outputs apart: the norm of the whole,
+    every element scaled once, nothing around them written."""
+    L = qb()
+    total = sum(lengths)
+    for dt in (F32, F16, BF16):
+        for order in ("forward", "backward", "outputs apart"):
+            flat = ref.normal((total + 32,), 1, 0.1, dt)
+            out = flat if in_place else torch.full((total + 16 * len(lengths) + 32,), 7.0, dtype=dt, device=DEV)
+            before, entries, at, to = flat.clone(), [], 16, 16
+            gap = 8 if order == "outputs apart" and not in_place else 0
+            places = []
+            for n in lengths:
+                entries.append((flat[at:at + n], out[to:to + n]))
+                places.append((at, to, n))
+                at, to = at + n, to + n + gap
+            if order == "backward":
+                entries.reverse()
+            table = L.grad_table(entries)
+            norm = norm_of(L, table, len(entries))
+            want = exact_norm([before[16:16 + total]])
+            assert abs(norm.item() - want) <= want * 2.0 ** -24 * 1.001
+            L.qb_multi_tensor_clip_grads(table, len(entries), want / 2, norm)
+            torch.cuda.synchronize()
+            whole = torch.full_like(out, 7.0) if not in_place else before.clone()
+            for at, to, n in places:
+                whole[to:to + n] = expected(before[at:at + n], want / 2, norm)
+            assert torch.equal(out, whole) and (in_place or torch.equal(flat, before)), (dt, order)
+
+
+def test_neighbours_of_two_types():
+    """A bf16 gradient whose end is where an fp32 one begins."""
+    L = qb()
+    raw = torch.zeros(4096, dtype=torch.uint8, device=DEV)
+    a, b = raw[:2048].view(BF16), raw[2048:].view(F32)
+    a.copy_(ref.normal((1024,), 1, dtype=BF16))
+    b.copy_(ref.normal((512,), 2))
+    old = [a.clone(), b.clone()]
+    table = L.grad_table([a, b])
+    norm = norm_of(L, table, 2)
+    assert abs(norm.item() - exact_norm(old)) <= exact_norm(old) * 2.0 ** -24 * 1.001
+    L.qb_multi_tensor_clip_grads(table, 2, 1.0, norm)
+    assert torch.equal(a, expected(old[0], 1.0, norm)) and torch.equal(b, expected(old[1], 1.0, norm))
