@@ -496,6 +496,20 @@ hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_
     return launch_dequant4_kept(d, count, f.code4, 1 << f.log2B, 1 << f.log2B2, f.nested != 0, xdt, s);
 }
 
+hipError_t launch_join(int xdt, const float* part, int pieces, int64_t M, const Epilogue& e, hipStream_t s)
+{
+    GemmParams p{};
+    p.g.M = M;
+    p.g.R = e.N;
+    p.e = e;
+    p.part = const_cast<float*>(part);
+    p.split = pieces;
+    const int64_t groups = (e.N + 3) / 4;
+    const int grid = (int)tiles_over(M * groups, 256);
+    return xdt == DT_F16 ? launch_kernel(k_join_split<DT_F16, false>, grid, s, p, groups)
+                         : launch_kernel(k_join_split<DT_BF16, false>, grid, s, p, groups);
+}
+
 double gemm_us(int xdt, int64_t M, int64_t R, int64_t len)
 {
     return gemm_plan(xdt, M, R, (uint32_t)tiles_over(len, gemm_step(xdt)), true).us;

@@ -93,6 +93,10 @@ struct GemmArgs {
 // (a product of few tiles is not split without it).
 hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t s);
 
+// The join of a split product alone: the epilogue of the sum of `pieces` pieces, part[piece][M][e.N],
+// 16-bit types.
+hipError_t launch_join(int xdt, const float* part, int pieces, int64_t M, const Epilogue& e, hipStream_t s);
+
 // Estimated times in us: of launch_linear_rows, and of launch_gemm of M x R x len.
 double rows_us(int xdt, int64_t M, int64_t K, int64_t N, int count);
 double gemm_us(int xdt, int64_t M, int64_t R, int64_t len);
@@ -132,5 +136,10 @@ hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool accumu
 hipError_t launch_gated_grad(int xdt, const void* dh, const void* g, const void* u, int act, int64_t M, int64_t N,
                              void* dz, int64_t pitch, void* dg_out, void* du_out, const TransposedWeights* t,
                              hipStream_t s);
+
+// dz W for up to kRowsMax rows in a 16-bit type, the weights from their codes: part[slice][M][K] of
+// `*slices` slices of the n (t.out is not used).
+hipError_t launch_few_rows_back(int xdt, const void* dz0, const void* dz1, int64_t ldz, int64_t M,
+                                const TransposedWeights& t, float* part, int* slices, hipStream_t s);
 
 }  // namespace qb

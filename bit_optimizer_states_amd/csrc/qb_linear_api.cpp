@@ -157,15 +157,29 @@ TransposedWeights transposed(int xdt, const Weight4* w, int count, const Weight4
     return TransposedWeights{{w[0], w[count - 1]}, f, ws, N, K, gemm_pitch(xdt, N), count};
 }
 
+// Whether dx is taken from the codes, without the transposed weights in the workspace: up to 48 rows,
+// and up to 64 of a layer of more than 2^24 weights (64 rows, us: 1024 x 1000 17.6 so and 14.8 by the
+// tiled product, 4096 x 4096 24.8 and 24.3, 4096 x 11008 34.5 and 46).  Its slices' sums have to fit
+// the room for partial sums.
+bool few_rows(int xdt, int64_t M, int64_t K, int64_t N, int count)
+{
+    return xdt != QB_F32 && M <= kRowsMax && (M <= 48 || count * N * K > int64_t(1) << 24) && M * K <= kPartMax;
+}
+
 // dx = [dz_0 dz_1] [W_0; W_1] for dz of rows of `lda` elements and the weights `t`.
 hipError_t input_gradient(int xdt, const void* dz0, const void* dz1, int64_t lda, const TransposedWeights& t, int64_t M,
                           void* dx, float* part, hipStream_t s)
 {
     const int64_t pitch = t.np * t.count;
-    const GemmArgs g{dz0, dz1, t.out, nullptr, M, t.K, t.np, pitch, lda, pitch};
     Epilogue out{};
     out.y = dx;
     out.N = t.K;
+    if (few_rows(xdt, M, t.K, t.N, t.count)) {
+        int slices = 0;
+        const hipError_t e = launch_few_rows_back(xdt, dz0, dz1, lda, M, t, part, &slices, s);
+        return e != hipSuccess ? e : launch_join(xdt, part, slices, M, out, s);
+    }
+    const GemmArgs g{dz0, dz1, t.out, nullptr, M, t.K, t.np, pitch, lda, pitch};
     return launch_gemm(xdt, false, g, out, part, s);
 }
 
@@ -247,7 +261,7 @@ qb_status qb_dequant_linear_backward(const void* dy, const void* z, qb_dtype xdt
         e = launch_linear_grad(xdt, own || dz || dbias, dy, act != QB_ACT_NONE ? z : nullptr, act, M, N,
                                own && !given ? wp + l.dz : nullptr, pitch, dz,
                                dbias ? reinterpret_cast<float*>(wp + l.part) : nullptr, linear_dz_slices(M, N),
-                               dx ? &t : nullptr, s);
+                               dx && !few_rows(xdt, M, K, N, 1) ? &t : nullptr, s);
         if (own) {
             a = given ? dz : wp + l.dz;
             lda = pitch;
@@ -325,7 +339,7 @@ qb_status qb_dequant_gated_backward(const void* dy, const void* gate_out, const 
     const bool given = dgate && dup && whole_steps(xdt, N);       // dx reads the caller's arrays
     const TransposedWeights t = transposed(xdt, w, 2, f, K, N, wp);
     hipError_t e = launch_gated_grad(xdt, dy, gate_out, up_out, act, M, N, dx && !given ? wp + l.dz : nullptr, pitch, dgate,
-                                     dup, dx ? &t : nullptr, s);
+                                     dup, dx && !few_rows(xdt, M, K, N, 2) ? &t : nullptr, s);
     if (e == hipSuccess && dx) {
         const void* const dg = given ? dgate : wp + l.dz;
         const void* const du = given ? dup : wp + l.dz + (size_t)M * pitch * dtype_bytes(xdt);

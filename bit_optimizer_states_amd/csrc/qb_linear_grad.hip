@@ -72,78 +72,186 @@ struct GatedDz {
     int32_t act, blocks;
 };
 
-// Transposed, into out[k][n]: a workgroup takes 64 rows n and 128 columns k, 8 weights of two
-// neighbouring rows a thread at a time into LDS, and writes rows k of 64 n (128 bytes, 256 in
-// binary32).  16-byte chunk c of LDS row k lies at chunk c ^ spread(k): the threads of a
-// wave, which hold 16 k eight apart and 4 row pairs, write to different banks but for two
-// each.  (Rows padded by 16 bytes instead fell into one bank: 4096 x 4096 15.1 us.)
+// 64 rows n and 128 columns k of a weight, transposed into LDS rows k of 64 n (128 bytes, 256 in
+// binary32), by 256 threads: 8 weights of two neighbouring rows a thread at a time.  16-byte
+// chunk c of LDS row k lies at chunk c ^ spread(k): the threads of a wave, which hold 16 k eight
+// apart and 4 row pairs, write to different banks but for two each, and 16 rows' equal chunks
+// (16-bit types) are in different banks too.  (Rows padded by 16 bytes instead fell into one
+// bank: 4096 x 4096 15.1 us for 9.6.)
+template <int XDT, bool DQ>
+struct TransposedTile {
+    static constexpr int ES = XDT == DT_F32 ? 4 : 2;
+    static constexpr int LP = 64 * ES, CPR = LP / 16;          // bytes and chunks of an LDS row
+    uint32_t code[2][2], c2[2][2];                             // row pairs tid / 16 and tid / 16 + 16
+    float a[2][2], mu;
+
+    static __device__ __forceinline__ int spread(int k)
+    {
+        return XDT == DT_F32 ? ((k >> 3) & 7) * 2 : ((k >> 3) ^ k) & 7;
+    }
+    // Codes and constants of rows n0 .., columns k0 ..
+    __device__ __forceinline__ void load(const TransposedWeights& t, const Weight4& w, int64_t n0, int64_t k0)
+    {
+        const int tid = threadIdx.x, kl = (tid & 15) * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = n0 + 2 * ((tid >> 4) + 16 * i) + h, e = n * t.K + k0 + kl, blk = e >> t.f.log2B;
+                code[i][h] = c2[i][h] = 0u;
+                a[i][h] = 0.0f;
+                if (n < t.N && k0 + kl < t.K) {
+                    code[i][h] = gld<uint32_t>(w.codes + e / 2);
+                    if constexpr (DQ) {
+                        c2[i][h] = gld<uint8_t>(w.c2 + blk);
+                        a[i][h] = gld<float>(w.absmax2 + (blk >> t.f.log2B2));
+                    } else {
+                        a[i][h] = gld<float>(w.absmax + blk);
+                    }
+                }
+            }
+        mu = DQ ? gld<float>(w.offset) : 0.0f;
+    }
+    // .. into s_t, zeros beyond the last row.
+    __device__ __forceinline__ void fill(int64_t left, char* s_t, const float* s_val, const float* s_dyn) const
+    {
+        const int tid = threadIdx.x, kl = (tid & 15) * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int pr = (tid >> 4) + 16 * i;
+            Frag<DT_F32> v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float c = DQ ? s_dyn[c2[i][h]] * a[i][h] + mu : a[i][h];       // two rounded operations
+                dequant_frag<DT_F32>(code[i][h], 2 * pr + h < left ? c : 0.0f, s_val, v[h]);
+            }
+            const int at = 2 * pr * ES;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                char* const p = s_t + (kl + j) * LP + ((at / 16) ^ spread(kl + j)) * 16 + at % 16;
+                if constexpr (XDT == DT_F32) {
+                    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+                    *reinterpret_cast<f32x2_t*>(p) = f32x2_t{v[0].w[j], v[1].w[j]};
+                } else {
+                    *reinterpret_cast<uint32_t*>(p) = pack_two<XDT>(v[0].w[j], v[1].w[j]);
+                }
+            }
+        }
+    }
+};
+
+template <bool DQ>
+__device__ __forceinline__ void stage_tables(const Weight4Format& f, const QbTables* tab, float* s_val, float* s_dyn)
+{
+    const int tid = threadIdx.x;
+    if (tid < 16) s_val[tid] = (f.code4 == 0 ? tab->nf4 : tab->fp4)[tid];
+    if constexpr (DQ) s_dyn[tid] = tab->dyn8[tid];
+}
+
+// A tile into out[k][n].
 template <int XDT, bool DQ>
 __device__ __forceinline__ void unpack_transposed(const TransposedWeights& t, int64_t bx, int64_t by, int bz, char* s_t,
                                                   const QbTables* tab)
 {
-    constexpr int ES = XDT == DT_F32 ? 4 : 2;
-    constexpr int LP = 64 * ES, CPR = LP / 16;                // bytes and chunks of an LDS row of 64 n
+    using Tile = TransposedTile<XDT, DQ>;
+    constexpr int ES = Tile::ES, LP = Tile::LP, CPR = Tile::CPR;
     __shared__ float s_val[16];
     __shared__ float s_dyn[DQ ? 256 : 1];
-    const int tid = threadIdx.x, kl = (tid & 15) * 8;
-    const int64_t k0 = bx * 128, n0 = by * 64, N = t.N, K = t.K, np = t.np, pitch = t.np * t.count;
-    const Weight4 w = t.w[bz];
-    const Weight4Format f = t.f;
-    // row pairs tid / 16 and tid / 16 + 16 of the tile: codes and constants of 8 weights of each row
-    uint32_t code[2][2], c2[2][2];
-    float a[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t n = n0 + 2 * ((tid >> 4) + 16 * i) + h, e = n * K + k0 + kl, blk = e >> f.log2B;
-            code[i][h] = c2[i][h] = 0u;
-            a[i][h] = 0.0f;
-            if (n < N && k0 + kl < K) {
-                code[i][h] = gld<uint32_t>(w.codes + e / 2);
-                if constexpr (DQ) {
-                    c2[i][h] = gld<uint8_t>(w.c2 + blk);
-                    a[i][h] = gld<float>(w.absmax2 + (blk >> f.log2B2));
-                } else {
-                    a[i][h] = gld<float>(w.absmax + blk);
-                }
-            }
-        }
-    const float mu = DQ ? gld<float>(w.offset) : 0.0f;
-    if (tid < 16) s_val[tid] = (f.code4 == 0 ? tab->nf4 : tab->fp4)[tid];
-    if constexpr (DQ) s_dyn[tid] = tab->dyn8[tid];
+    const int tid = threadIdx.x;
+    const int64_t k0 = bx * 128, n0 = by * 64, pitch = t.np * t.count;
+    Tile tile;
+    tile.load(t, t.w[bz], n0, k0);
+    stage_tables<DQ>(t.f, tab, s_val, s_dyn);
     __syncthreads();
-    auto spread = [](int k) { return XDT == DT_F32 ? ((k >> 3) & 7) * 2 : (k >> 3) & 7; };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int pr = (tid >> 4) + 16 * i;
-        Frag<DT_F32> v[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t n = n0 + 2 * pr + h;
-            const float c = DQ ? s_dyn[c2[i][h]] * a[i][h] + mu : a[i][h];       // two rounded operations
-            dequant_frag<DT_F32>(code[i][h], n < N ? c : 0.0f, s_val, v[h]);     // zeros beyond the last row
-        }
-        const int at = 2 * pr * ES;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            char* const p = s_t + (kl + j) * LP + ((at / 16) ^ spread(kl)) * 16 + at % 16;
-            if constexpr (XDT == DT_F32) {
-                typedef float f32x2_t __attribute__((ext_vector_type(2)));
-                *reinterpret_cast<f32x2_t*>(p) = f32x2_t{v[0].w[j], v[1].w[j]};
-            } else {
-                *reinterpret_cast<uint32_t*>(p) = pack_two<XDT>(v[0].w[j], v[1].w[j]);
-            }
-        }
-    }
+    tile.fill(t.N - n0, s_t, s_val, s_dyn);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 128 * CPR / 256; ++i) {
         const int o = tid + 256 * i, row = o / CPR, c = o % CPR;
-        if (k0 + row < K && n0 + c * (16 / ES) < np)
-            gst<u32x4>(static_cast<char*>(t.out) + ((k0 + row) * pitch + bz * np + n0) * ES + 16 * c,
-                       *reinterpret_cast<const u32x4*>(s_t + row * LP + (c ^ spread(row)) * 16));
+        if (k0 + row < t.K && n0 + c * (16 / ES) < t.np)
+            gst<u32x4>(static_cast<char*>(t.out) + ((k0 + row) * pitch + bz * t.np + n0) * ES + 16 * c,
+                       *reinterpret_cast<const u32x4*>(s_t + row * LP + (c ^ Tile::spread(row)) * 16));
     }
+}
+
+// Few rows (16 MT, 16-bit types): dx = dz W without the transposed weights in memory.  A workgroup
+// takes 128 columns k of dx and a slice of the n (of both weights' n in a row): 64 of them at a time
+// it transposes the weights' tile into LDS as above, beside it dz's rows, by direct loads, and its
+// four waves multiply 32 columns each.  The slices' sums go to part[slice][M][K].  One row through
+// 4096 x 4096 17 us in all (26 with the transposed weights in memory and the tiled product), 16 through
+// a gated block of 4096 x 2 x 11008 43 (86), 64 through it 52 (92).
+struct FewRows {
+    const void* dz[2];
+    int64_t M, ldz;
+    float* part;
+    int32_t tiles, per_slice;            // tiles of 64 n, of all weights; of a slice
+};
+
+template <int XDT, bool DQ, int MT>
+__global__ __launch_bounds__(256) void k_few_rows_back(const FewRows a, const TransposedWeights t,
+                                                       const QbTables* __restrict__ tab)
+{
+    using Tile = TransposedTile<XDT, DQ>;
+    __shared__ __attribute__((aligned(16))) char s_t[128 * 128], s_a[16 * MT * 128];
+    __shared__ float s_val[16];
+    __shared__ float s_dyn[DQ ? 256 : 1];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int64_t k0 = (int64_t)blockIdx.x * 128, M = a.M, K = t.K;
+    const int per_weight = (int)(t.np / 64), begin = blockIdx.y * a.per_slice,
+              end = a.tiles - begin < a.per_slice ? a.tiles : begin + a.per_slice;
+    stage_tables<DQ>(t.f, tab, s_val, s_dyn);
+    f32x4 acc[2][MT];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = begin; i < end; ++i) {
+        const int bz = i / per_weight;
+        const int64_t n0 = (int64_t)(i - bz * per_weight) * 64;
+        Tile tile;
+        tile.load(t, t.w[bz], n0, k0);
+        __syncthreads();                                 // the tile before has been read
+        const char* const dz = static_cast<const char*>(a.dz[bz]) + n0 * 2;
+#pragma unroll
+        for (int l = 0; l < (2 * MT + 3) / 4; ++l) {     // 8 rows a load; chunk p of row i holds chunk p ^ (i % 8)
+            const int at = l * 4 + wave;
+            if (at < 2 * MT) {
+                const int row = at * 8 + (lane >> 3), c = (lane & 7) ^ (row & 7);
+                const int64_t m = row < M ? row : M - 1;
+                __builtin_amdgcn_global_load_lds((gptr_t)(dz + m * a.ldz * 2 + c * 16), (lptr_t)(s_a + at * 1024), 16, 0, 0);
+            }
+        }
+        tile.fill(t.N - n0, s_t, s_val, s_dyn);
+        wait_loads<0>();
+        __syncthreads();
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            u32x4 b[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = 32 * wave + 16 * j + r;
+                b[j] = *reinterpret_cast<const u32x4*>(s_t + row * 128 + ((4 * kk + g) ^ Tile::spread(row)) * 16);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                Frag<XDT> fa, fb;
+                __builtin_memcpy(fa.w, s_a + (16 * m + r) * 128 + ((4 * kk + g) ^ (r & 7)) * 16, 16);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    __builtin_memcpy(fb.w, &b[j], 16);
+                    mma<XDT>(fb, fa, acc[j][m]);         // a lane's four sums: four columns of one row
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int64_t row = 16 * m + r, k = k0 + 32 * wave + 16 * j + 4 * g;
+            if (row < M && k < K) gst<f32x4>(a.part + ((int64_t)blockIdx.y * M + row) * K + k, acc[j][m]);
+        }
 }
 
 // Workgroup (block of columns, slice of rows); its waves take the slice's rows in turn, the
@@ -298,8 +406,8 @@ hipError_t grad_inputs_as(const Dz& a, int groups, const TransposedWeights& t, h
 {
     const QbTables* tab = device_tables();
     if (!tab) return hipErrorNotInitialized;
+    if (groups == 0 && !t.out) return hipSuccess;
     const int64_t x = t.out ? (t.K + 127) / 128 : groups, rows = (groups + x - 1) / x, y = t.out ? (t.np + 63) / 64 : 0;
-    if (x == 0) return hipSuccess;
     return launch_grid(k_grad_inputs<XDT, DQ, TAIL, Dz>, dim3((unsigned)x, (unsigned)(rows + y), t.out ? t.count : 1), 256,
                        0, s, a, groups, (int)rows, t, tab);
 }
@@ -349,6 +457,41 @@ hipError_t launch_gated_grad(int xdt, const void* dh, const void* g, const void*
     const int64_t want = (4096 + blocks - 1) / blocks, take = row_groups < want ? row_groups : want;
     const GatedDz a{dh, g, u, dz, dg_out, du_out, M, N, pitch, act, (int32_t)blocks};
     return grad_inputs(xdt, a, blocks * take, t, s);
+}
+
+namespace {
+
+template <int XDT, bool DQ>
+hipError_t few_rows_as(const FewRows& a, const TransposedWeights& t, dim3 grid, const QbTables* tab, hipStream_t s)
+{
+    if (a.M <= 16) return launch_grid(k_few_rows_back<XDT, DQ, 1>, grid, 256, 0, s, a, t, tab);
+    if (a.M <= 32) return launch_grid(k_few_rows_back<XDT, DQ, 2>, grid, 256, 0, s, a, t, tab);
+    return launch_grid(k_few_rows_back<XDT, DQ, 4>, grid, 256, 0, s, a, t, tab);
+}
+
+template <int XDT>
+hipError_t few_rows_dq(const FewRows& a, const TransposedWeights& t, dim3 grid, const QbTables* tab, hipStream_t s)
+{
+    return t.f.nested ? few_rows_as<XDT, true>(a, t, grid, tab, s) : few_rows_as<XDT, false>(a, t, grid, tab, s);
+}
+
+}  // namespace
+
+hipError_t launch_few_rows_back(int xdt, const void* dz0, const void* dz1, int64_t ldz, int64_t M,
+                                const TransposedWeights& t, float* part, int* slices, hipStream_t s)
+{
+    const QbTables* tab = device_tables();
+    if (!tab) return hipErrorNotInitialized;
+    const int64_t tiles = t.np / 64 * t.count, x = (t.K + 127) / 128, fit = gemm_part_floats(M, t.K) / (M * t.K);
+    // four workgroups a CU, as far as the slices go
+    int64_t n = 1024 / x < tiles ? 1024 / x : tiles;
+    n = n < 1 ? 1 : n > kSplitMax ? kSplitMax : n;
+    n = n < fit ? n : fit;
+    const int64_t per = (tiles + n - 1) / n;
+    *slices = (int)((tiles + per - 1) / per);
+    const FewRows a{{dz0, dz1}, M, ldz, part, (int32_t)tiles, (int32_t)per};
+    const dim3 grid((unsigned)x, (unsigned)*slices);
+    return xdt == DT_F16 ? few_rows_dq<DT_F16>(a, t, grid, tab, s) : few_rows_dq<DT_BF16>(a, t, grid, tab, s);
 }
 
 hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool accumulate, void* db, int bias_dt,

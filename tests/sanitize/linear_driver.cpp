@@ -86,10 +86,24 @@ hipError_t launch_linear_grad(int xdt, bool dz_too, const void*, const void*, in
     if (!dz_too && (dz || dz_out || part)) ++failures;
     transposed(xdt, t);
     if (dz) inside(dz, (double)M * (double)pitch * es(xdt));
-    if (dz && (!t || offset_of(dz) < weights_end)) ++failures;
+    if (dz && t && offset_of(dz) < weights_end) ++failures;
     if (part) inside(part, 4.0 * slices * (double)N);
     dz_end = dz ? offset_of(dz) + (double)M * (double)pitch * es(xdt) : 0;
     if (part && (offset_of(part) < dz_end || (t && offset_of(part) < weights_end))) ++failures;
+    return done();
+}
+hipError_t launch_few_rows_back(int xdt, const void* dz0, const void*, int64_t ldz, int64_t M, const TransposedWeights& t,
+                                float* part, int* slices, hipStream_t)
+{
+    if (!dz0 || xdt == 0 || M > kRowsMax || ldz * 2 % 16 || !t.w[t.count - 1].codes) ++failures;
+    *slices = (int)(gemm_part_floats(M, t.K) / (M * t.K));
+    inside(part, 4.0 * *slices * (double)M * (double)t.K);
+    if (*slices < 1 || offset_of(part) < dz_end) ++failures;
+    return done();
+}
+hipError_t launch_join(int, const float* part, int pieces, int64_t M, const Epilogue& e, hipStream_t)
+{
+    inside(part, 4.0 * pieces * (double)M * (double)e.N);
     return done();
 }
 hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool, void*, int, hipStream_t)
@@ -102,7 +116,7 @@ hipError_t launch_gated_grad(int xdt, const void*, const void*, const void*, int
 {
     transposed(xdt, t);
     if (dz) inside(dz, 2.0 * (double)M * (double)pitch * es(xdt));
-    if (dz && (!t || offset_of(dz) < weights_end)) ++failures;
+    if (dz && t && offset_of(dz) < weights_end) ++failures;
     dz_end = dz ? offset_of(dz) + 2.0 * (double)M * (double)pitch * es(xdt) : 0;
     return done();
 }

@@ -305,3 +305,18 @@ def test_rows_kernels(M, N, nested, xdt):
     bias = ref.normal((N,), 1, dtype=xdt)
     y, z = linear.forward(L, x, w[0], bias, "RELU", keep=True)
     linear.check_forward(L, x, w[0], bias, "RELU", None, y, z)
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 32, 33, 48, 49, 64])
+@pytest.mark.parametrize("K,N", [(160, 70), (4096, 4200), (1056, 129)])
+@pytest.mark.parametrize("nested", [False, True])
+@pytest.mark.parametrize("xdt", [BF16, F16])
+def test_gradients_of_few_rows(M, K, N, nested, xdt):
+    """Both sides of the rows and sizes up to which no transposed weights are written; slices of one tile and many."""
+    L = qb()
+    w = gated.pair(N, K, oracle.NF4, 64, nested, xdt, M)
+    dy, z, u = (ref.normal((M, N), i, 0.5, xdt) for i in range(3))
+    linear.check_backward(L, dy, w[0], None, "NONE", linear.backward(L, dy, w[0])[0], None, None)
+    dx, _, db = linear.backward(L, dy, w[0], z, "SILU", bias_dt=F32)
+    linear.check_backward(L, dy, w[0], z, "SILU", dx, None, db)
+    gated.check_backward(L, dy, z, u, w, "GELU", gated.backward(L, dy, z, u, w, "GELU")[0])
