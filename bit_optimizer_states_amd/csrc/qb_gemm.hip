@@ -314,10 +314,51 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(const GemmParams p)
     }
 }
 
-// The pieces of a split product added in order, then the epilogue: four columns a thread.
-template <int XDT, bool GATED>
-__global__ __launch_bounds__(256) void k_join_split(const GemmParams p, int64_t groups)
+// 64 columns of the bias's gradient: the slices dealt to 16 sums, joined in order; WAVES waves (4 or
+// 16, with the same result) keep 16 / WAVES of them each.
+template <int WAVES>
+__device__ __forceinline__ void bias_sum(const BiasSum& b, int64_t group)
 {
+    constexpr int EACH = 16 / WAVES;
+    __shared__ float s_sum[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = group * 64 + lane;
+    float v[EACH] = {};
+    if (n < b.N) {
+        // (slices past the last read it again, so that no load waits for another)
+#pragma unroll 4
+        for (int s = wave; s < b.slices; s += 16)
+#pragma unroll
+            for (int q = 0; q < EACH; ++q) {
+                const int at = s + q * WAVES;
+                const float x = b.part[(int64_t)(at < b.slices ? at : b.slices - 1) * b.N + n];
+                v[q] += at < b.slices ? x : 0.0f;
+            }
+    }
+#pragma unroll
+    for (int q = 0; q < EACH; ++q) s_sum[wave + q * WAVES][lane] = v[q];
+    __syncthreads();
+    if (wave != 0 || n >= b.N) return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) sum += s_sum[w][lane];
+    if (b.dt == DT_F32) store1<DT_F32>(b.db, n, b.accumulate ? sum + load1<DT_F32>(b.db, n) : sum);
+    else if (b.dt == DT_F16) store1<DT_F16>(b.db, n, b.accumulate ? sum + load1<DT_F16>(b.db, n) : sum);
+    else store1<DT_BF16>(b.db, n, b.accumulate ? sum + load1<DT_BF16>(b.db, n) : sum);
+}
+
+// (4096 columns of 128 slices: with one thread a column 7 us, with four waves 5.5, with 16 4.7)
+__global__ __launch_bounds__(1024) void k_bias_sum(const BiasSum b) { bias_sum<16>(b, blockIdx.x); }
+
+// The pieces of a split product added in order, then the epilogue: four columns a thread.  The
+// workgroups from `blocks` on take the bias's gradient (a launch of its own 3 us more).
+template <int XDT, bool GATED>
+__global__ __launch_bounds__(256) void k_join_split(const GemmParams p, int64_t groups, int blocks, const BiasSum b)
+{
+    if ((int)blockIdx.x >= blocks) {
+        bias_sum<4>(b, blockIdx.x - blocks);
+        return;
+    }
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t m = i / groups, n = (i - m * groups) * 4;
     if (m >= p.g.M) return;
@@ -335,6 +376,14 @@ __global__ __launch_bounds__(256) void k_join_split(const GemmParams p, int64_t 
     } else {
         finish_linear4<XDT>(p.e, m, n, sum(n));
     }
+}
+
+template <int XDT, bool GATED>
+hipError_t join_as(const GemmParams& p, const BiasSum* b, hipStream_t s)
+{
+    const int64_t groups = (p.e.N + 3) / 4;
+    const int blocks = (int)tiles_over(p.g.M * groups, 256), more = b ? (int)tiles_over(b->N, 64) : 0;
+    return launch_kernel(k_join_split<XDT, GATED>, blocks + more, s, p, groups, blocks, b ? *b : BiasSum{});
 }
 
 // `rows` rows of an array of `width` elements further on.
@@ -447,8 +496,9 @@ hipError_t gemm_shape(int shape, const GemmParams& p, int64_t n_first, int64_t c
     }
 }
 
+// bias: the gradient that the call computes as well, or nullptr.
 template <int XDT, bool GATED>
-hipError_t gemm_tiles(GemmParams p, hipStream_t s)
+hipError_t gemm_tiles(GemmParams p, const BiasSum* bias, hipStream_t s)
 {
     const int64_t M = p.g.M, R = p.g.R;
     const GemmPlan plan = gemm_plan(XDT, M, R, p.steps, p.part != nullptr);
@@ -460,25 +510,26 @@ hipError_t gemm_tiles(GemmParams p, hipStream_t s)
         p.per_split = p.steps;
         const GemmPlan rest = gemm_plan(XDT, M, R - whole * 256, p.steps, false);
         if (rounds_us(XDT, kShapes[0], (uint32_t)(rows * whole), p.steps) + 4.0 + rest.us < plan.us && rest.shape != 0) {
-            const hipError_t e = gemm_shape<XDT, GATED>(0, p, 0, whole, s);
-            return e != hipSuccess ? e : gemm_shape<XDT, GATED>(rest.shape, p, whole * 256, kEveryColumn, s);
+            hipError_t e = gemm_shape<XDT, GATED>(0, p, 0, whole, s);
+            if (e == hipSuccess) e = gemm_shape<XDT, GATED>(rest.shape, p, whole * 256, kEveryColumn, s);
+            return e == hipSuccess && bias ? launch_bias_sum(*bias, s) : e;
         }
     }
     p.per_split = (int)tiles_over(p.steps, plan.split);
     p.split = (int)tiles_over(p.steps, p.per_split);
     const hipError_t e = gemm_shape<XDT, GATED>(plan.shape, p, 0, kEveryColumn, s);
-    if (e != hipSuccess || p.split == 1) return e;
-    const int64_t groups = (p.e.N + 3) / 4;
-    return launch_kernel(k_join_split<XDT, GATED>, (int)tiles_over(M * groups, 256), s, p, groups);
+    if (e != hipSuccess) return e;
+    if (p.split > 1) return join_as<XDT, GATED>(p, bias, s);
+    return bias ? launch_bias_sum(*bias, s) : hipSuccess;
 }
 
 // One product, or several of fewer rows where a grid would not hold them.
 template <int XDT, bool GATED>
-hipError_t gemm_rows(const GemmParams& p, hipStream_t s)
+hipError_t gemm_rows(const GemmParams& p, const BiasSum* bias, hipStream_t s)
 {
     const int64_t M = p.g.M, most = (int64_t(1) << 21) / tiles_over(p.g.R, 64) * 256;
     for (int64_t m = 0; m < M; m += most) {
-        const hipError_t e = gemm_tiles<XDT, GATED>(rows_of<XDT>(p, m, M - m < most ? M - m : most), s);
+        const hipError_t e = gemm_tiles<XDT, GATED>(rows_of<XDT>(p, m, M - m < most ? M - m : most), m == 0 ? bias : nullptr, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -496,7 +547,13 @@ hipError_t launch_unpack(int xdt, const Weight4* w, int count, int64_t N, int64_
     return launch_dequant4_kept(d, count, f.code4, 1 << f.log2B, 1 << f.log2B2, f.nested != 0, xdt, s);
 }
 
-hipError_t launch_join(int xdt, const float* part, int pieces, int64_t M, const Epilogue& e, hipStream_t s)
+hipError_t launch_bias_sum(const BiasSum& b, hipStream_t s)
+{
+    return launch_kernel_nt(k_bias_sum, (int)tiles_over(b.N, 64), 1024, s, b);
+}
+
+hipError_t launch_join(int xdt, const float* part, int pieces, int64_t M, const Epilogue& e, const BiasSum* bias,
+                       hipStream_t s)
 {
     GemmParams p{};
     p.g.M = M;
@@ -504,10 +561,7 @@ hipError_t launch_join(int xdt, const float* part, int pieces, int64_t M, const 
     p.e = e;
     p.part = const_cast<float*>(part);
     p.split = pieces;
-    const int64_t groups = (e.N + 3) / 4;
-    const int grid = (int)tiles_over(M * groups, 256);
-    return xdt == DT_F16 ? launch_kernel(k_join_split<DT_F16, false>, grid, s, p, groups)
-                         : launch_kernel(k_join_split<DT_BF16, false>, grid, s, p, groups);
+    return xdt == DT_F16 ? join_as<DT_F16, false>(p, bias, s) : join_as<DT_BF16, false>(p, bias, s);
 }
 
 double gemm_us(int xdt, int64_t M, int64_t R, int64_t len)
@@ -515,7 +569,8 @@ double gemm_us(int xdt, int64_t M, int64_t R, int64_t len)
     return gemm_plan(xdt, M, R, (uint32_t)tiles_over(len, gemm_step(xdt)), true).us;
 }
 
-hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t s)
+hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, const BiasSum* bias,
+                       hipStream_t s)
 {
     const int64_t step = gemm_step(xdt);
     GemmParams p{};
@@ -526,9 +581,9 @@ hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e
     p.steps0 = (int32_t)((g.len0 + step - 1) / step);
     p.half = g.len % step ? 1 : 0;
     switch (xdt) {
-    case DT_F32: return gated ? gemm_rows<DT_F32, true>(p, s) : gemm_rows<DT_F32, false>(p, s);
-    case DT_F16: return gated ? gemm_rows<DT_F16, true>(p, s) : gemm_rows<DT_F16, false>(p, s);
-    default: return gated ? gemm_rows<DT_BF16, true>(p, s) : gemm_rows<DT_BF16, false>(p, s);
+    case DT_F32: return gated ? gemm_rows<DT_F32, true>(p, bias, s) : gemm_rows<DT_F32, false>(p, bias, s);
+    case DT_F16: return gated ? gemm_rows<DT_F16, true>(p, bias, s) : gemm_rows<DT_F16, false>(p, bias, s);
+    default: return gated ? gemm_rows<DT_BF16, true>(p, bias, s) : gemm_rows<DT_BF16, false>(p, bias, s);
     }
 }
 

@@ -89,13 +89,25 @@ struct GemmArgs {
     const void* b1;
     int64_t M, R, len0, len, lda, ldb;
 };
+// The gradient of a bias from dz's sums over slices of rows: db[n] = the sum of part[.][n] in order
+// (plus what it holds).
+struct BiasSum {
+    const float* part;
+    void* db;
+    int64_t N;
+    int32_t slices, accumulate, dt;
+};
+hipError_t launch_bias_sum(const BiasSum& b, hipStream_t s);
+
 // part: room for the partial sums of a product split over its length, gemm_part_floats()
-// (a product of few tiles is not split without it).
-hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t s);
+// (a product of few tiles is not split without it).  bias: computed as well, nullptr none.
+hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, const BiasSum* bias,
+                       hipStream_t s);
 
 // The join of a split product alone: the epilogue of the sum of `pieces` pieces, part[piece][M][e.N],
 // 16-bit types.
-hipError_t launch_join(int xdt, const float* part, int pieces, int64_t M, const Epilogue& e, hipStream_t s);
+hipError_t launch_join(int xdt, const float* part, int pieces, int64_t M, const Epilogue& e, const BiasSum* bias,
+                       hipStream_t s);
 
 // Estimated times in us: of launch_linear_rows, and of launch_gemm of M x R x len.
 double rows_us(int xdt, int64_t M, int64_t K, int64_t N, int count);
@@ -127,9 +139,6 @@ inline int linear_dz_slices(int64_t M, int64_t N)
     const int64_t most = fours > 64 ? fours : twos < 64 ? twos : 64, n = want < most ? want : most;
     return (int)(n < 1 ? 1 : n);
 }
-// db[n] = the sum of part[.][n] in order (plus what it holds).
-hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool accumulate, void* db, int bias_dt,
-                           hipStream_t s);
 // dg = dh u act'(g) and du = dh act(g) into `dz` ([M, pitch] each, du behind dg; nullptr:
 // not wanted) and into dg_out, du_out [M, N] (nullptr: not wanted).  And the weights `t`
 // (nullptr: not wanted).

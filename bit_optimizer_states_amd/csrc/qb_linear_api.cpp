@@ -128,7 +128,7 @@ hipError_t unpack_and_multiply(int xdt, const void* x, int64_t M, int64_t K, con
     const hipError_t err = launch_unpack(xdt, w, count, N, K, f, b, each, s);
     if (err != hipSuccess) return err;
     const GemmArgs g{x, nullptr, b, b + (count - 1) * each, M, count == 2 ? gated_rows(N) : N, K, K, K, K};
-    return launch_gemm(xdt, count == 2, g, e, reinterpret_cast<float*>(b + count * each), s);
+    return launch_gemm(xdt, count == 2, g, e, reinterpret_cast<float*>(b + count * each), nullptr, s);
 }
 
 // Workspace of a gradient: the weights transposed, dz (dg and du) padded, the partial
@@ -166,9 +166,10 @@ bool few_rows(int xdt, int64_t M, int64_t K, int64_t N, int count)
     return xdt != QB_F32 && M <= kRowsMax && (M <= 48 || count * N * K > int64_t(1) << 24) && M * K <= kPartMax;
 }
 
-// dx = [dz_0 dz_1] [W_0; W_1] for dz of rows of `lda` elements and the weights `t`.
+// dx = [dz_0 dz_1] [W_0; W_1] for dz of rows of `lda` elements and the weights `t`; the bias's gradient
+// with it (nullptr: none).
 hipError_t input_gradient(int xdt, const void* dz0, const void* dz1, int64_t lda, const TransposedWeights& t, int64_t M,
-                          void* dx, float* part, hipStream_t s)
+                          void* dx, float* part, const BiasSum* bias, hipStream_t s)
 {
     const int64_t pitch = t.np * t.count;
     Epilogue out{};
@@ -177,10 +178,10 @@ hipError_t input_gradient(int xdt, const void* dz0, const void* dz1, int64_t lda
     if (few_rows(xdt, M, t.K, t.N, t.count)) {
         int slices = 0;
         const hipError_t e = launch_few_rows_back(xdt, dz0, dz1, lda, M, t, part, &slices, s);
-        return e != hipSuccess ? e : launch_join(xdt, part, slices, M, out, s);
+        return e != hipSuccess ? e : launch_join(xdt, part, slices, M, out, bias, s);
     }
     const GemmArgs g{dz0, dz1, t.out, nullptr, M, t.K, t.np, pitch, lda, pitch};
-    return launch_gemm(xdt, false, g, out, part, s);
+    return launch_gemm(xdt, false, g, out, part, bias, s);
 }
 
 }  // namespace
@@ -267,11 +268,12 @@ qb_status qb_dequant_linear_backward(const void* dy, const void* z, qb_dtype xdt
             lda = pitch;
         }
     }
-    if (e == hipSuccess && dbias)
-        e = launch_bias_sum(reinterpret_cast<float*>(wp + l.part), M > 0 ? linear_dz_slices(M, N) : 0, N,
-                            accumulate != 0, dbias, bdt, s);
-    if (e == hipSuccess && dx && M > 0) e = input_gradient(xdt, a, nullptr, lda, t, M, dx,
-                                                              reinterpret_cast<float*>(wp + l.split), s);
+    const BiasSum bias{reinterpret_cast<float*>(wp + l.part), dbias, N, M > 0 ? linear_dz_slices(M, N) : 0, accumulate,
+                       (int32_t)bdt};
+    if (e == hipSuccess && dx && M > 0)
+        e = input_gradient(xdt, a, nullptr, lda, t, M, dx, reinterpret_cast<float*>(wp + l.split), dbias ? &bias : nullptr, s);
+    else if (e == hipSuccess && dbias)
+        e = launch_bias_sum(bias, s);
     return hip_status(e);
 }
 
@@ -343,7 +345,7 @@ qb_status qb_dequant_gated_backward(const void* dy, const void* gate_out, const 
     if (e == hipSuccess && dx) {
         const void* const dg = given ? dgate : wp + l.dz;
         const void* const du = given ? dup : wp + l.dz + (size_t)M * pitch * dtype_bytes(xdt);
-        e = input_gradient(xdt, dg, du, pitch, t, M, dx, reinterpret_cast<float*>(wp + l.split), s);
+        e = input_gradient(xdt, dg, du, pitch, t, M, dx, reinterpret_cast<float*>(wp + l.split), nullptr, s);
     }
     return hip_status(e);
 }

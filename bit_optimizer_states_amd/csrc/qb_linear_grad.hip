@@ -1,6 +1,6 @@
 // qb_linear_grad.hip -- what the product of the 4-bit layers' gradients takes: the gradient
 // at the pre-activation, padded to the product's steps, and the weights transposed, by one
-// launch of two kinds of workgroups (neither needs the other); and the bias's gradient.
+// launch of two kinds of workgroups (neither needs the other).
 //
 //   linear: dz = dy act'(z), db = sum over rows of dz;
 //   gated:  dg = dh u act'(g), du = dh act(g).
@@ -306,31 +306,6 @@ __device__ __forceinline__ void linear_dz(const LinearDz& a, int group, float (*
     }
 }
 
-// 64 columns a workgroup; the slices dealt to 16 waves, joined in wave order (4096 columns
-// of 128 slices: one thread a column takes 7 us).
-constexpr int kSumWaves = 16;
-
-__global__ __launch_bounds__(64 * kSumWaves) void k_bias_sum(const float* __restrict__ part, int slices, int64_t N,
-                                                             int accumulate, void* __restrict__ db, int bias_dt)
-{
-    __shared__ float s_sum[kSumWaves][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n = (int64_t)blockIdx.x * 64 + lane;
-    float v = 0.0f;
-    if (n < N) {
-#pragma unroll 8
-        for (int s = wave; s < slices; s += kSumWaves) v += part[(int64_t)s * N + n];
-    }
-    s_sum[wave][lane] = v;
-    __syncthreads();
-    if (wave != 0 || n >= N) return;
-    float sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kSumWaves; ++w) sum += s_sum[w][lane];
-    if (accumulate) sum += load1_rt(bias_dt, db, n);
-    store1_rt(bias_dt, db, n, sum);
-}
-
 template <int XDT, int TAIL>
 __device__ __forceinline__ void gated_dz(const GatedDz& a, int group, int groups)
 {
@@ -492,12 +467,6 @@ hipError_t launch_few_rows_back(int xdt, const void* dz0, const void* dz1, int64
     const FewRows a{{dz0, dz1}, M, ldz, part, (int32_t)tiles, (int32_t)per};
     const dim3 grid((unsigned)x, (unsigned)*slices);
     return xdt == DT_F16 ? few_rows_dq<DT_F16>(a, t, grid, tab, s) : few_rows_dq<DT_BF16>(a, t, grid, tab, s);
-}
-
-hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool accumulate, void* db, int bias_dt,
-                           hipStream_t s)
-{
-    return launch_kernel_nt(k_bias_sum, (int)((N + 63) / 64), 64 * kSumWaves, s, part, slices, N, accumulate ? 1 : 0, db, bias_dt);
 }
 
 }  // namespace qb

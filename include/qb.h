@@ -792,8 +792,8 @@ size_t qb_dequant_linear_workspace_bytes(qb_dtype xdt, int64_t M, int64_t K, int
  *           is left as it is, and zero otherwise.
  * dz is rounded to xdt before it is multiplied by W (the matrix instructions take
  * that type; for binary32 nothing is rounded); dbias sums the unrounded dz.  N >= 1.
- * The workspace is needed for dx and dbias.  Up to five kernels: dz and the weights
- * transposed, dbias, the product in one or two launches, its pieces joined.  Few rows are
+ * The workspace is needed for dx and dbias.  Up to four kernels: dz and the weights
+ * transposed, the product in one or two launches, its pieces joined or dbias.  Few rows are
  * multiplied by weights transposed on the way, without a copy of them.
  */
 qb_status qb_dequant_linear_backward(const void* dy, const void* z, qb_dtype xdt, int64_t M, int64_t K,

@@ -44,6 +44,12 @@ static int es(int dt) { return dt == 0 ? 4 : 2; }
 static double dz_end = 0, weights_end = 0;
 static bool rows_cheap = false;           // which of the two forms the estimates favour
 
+static void bias_inside(const BiasSum& b)
+{
+    if (!b.db) ++failures;
+    if (b.slices) inside(b.part, 4.0 * b.slices * (double)b.N);
+}
+
 hipError_t launch_linear_rows(int, const void*, int64_t M, int64_t K, const Weight4*, int, const Weight4Format&,
                               const Epilogue& e, hipStream_t)
 {
@@ -69,12 +75,13 @@ static void transposed(int xdt, const TransposedWeights* t)
     inside(t->out, bytes);
     weights_end = offset_of(t->out) + bytes;
 }
-hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, hipStream_t)
+hipError_t launch_gemm(int xdt, bool gated, const GemmArgs& g, const Epilogue& e, float* part, const BiasSum* bias, hipStream_t)
 {
     inside(part, 4.0 * (double)gemm_part_floats(g.M, g.R));
     if (offset_of(part) < weights_end || offset_of(part) < dz_end) ++failures;       // behind what it reads
     if (g.len < gemm_step(xdt) || g.lda * es(xdt) % 16 || g.ldb * es(xdt) % 16) ++failures;
     if (g.len0 != g.len && (g.len0 % gemm_step(xdt) || !g.a1)) ++failures;
+    if (bias) bias_inside(*bias);
     if (gated && (!g.b1 || g.R != gated_rows(e.N))) ++failures;
     if (!gated && g.R != e.N) ++failures;
     dz_end = 0;
@@ -101,14 +108,15 @@ hipError_t launch_few_rows_back(int xdt, const void* dz0, const void*, int64_t l
     if (*slices < 1 || offset_of(part) < dz_end) ++failures;
     return done();
 }
-hipError_t launch_join(int, const float* part, int pieces, int64_t M, const Epilogue& e, hipStream_t)
+hipError_t launch_join(int, const float* part, int pieces, int64_t M, const Epilogue& e, const BiasSum* bias, hipStream_t)
 {
+    if (bias) bias_inside(*bias);
     inside(part, 4.0 * pieces * (double)M * (double)e.N);
     return done();
 }
-hipError_t launch_bias_sum(const float* part, int slices, int64_t N, bool, void*, int, hipStream_t)
+hipError_t launch_bias_sum(const BiasSum& b, hipStream_t)
 {
-    if (slices) inside(part, 4.0 * slices * (double)N);
+    bias_inside(b);
     return done();
 }
 hipError_t launch_gated_grad(int xdt, const void*, const void*, const void*, int, int64_t M, int64_t, void* dz,
