@@ -111,7 +111,7 @@ __global__ __launch_bounds__(64 * WAVES, rows_waves(XDT, G, XR, WAVES)) void k_l
     // A wave's loads: of a column tile's step one of 16 rows (4 lanes a row), of x RPL rows each.
     // Chunk p of row i holds chunk p ^ (i / 4) (codes), p ^ (i % 16) (x) of the row's step, so that
     // 16 rows' equal chunks lie in different banks.  Rows past the end are the last one again; chunks
-    // past K the step's first one (x is read as zeros there).
+    // past K the step's first one (x and the weights are taken as zeros there).
     const int cc = (lane & 3) ^ (lane >> 4);
     const uint32_t c_off = (uint32_t)min(lane >> 2, rows_n) * (uint32_t)(K / 2) + 16 * cc;
     uint32_t x_off[XL];
@@ -238,7 +238,9 @@ __global__ __launch_bounds__(64 * WAVES, rows_waves(XDT, G, XR, WAVES)) void k_l
 #pragma unroll
             for (int i = 0; i < G; ++i) {
                 code[i] = *reinterpret_cast<const u32x4*>(slot + i * 1024 + r * 64 + (g ^ (r >> 2)) * 16);
-                constant[i] = s_const[(i * 16 + r) * pitch + ((zeros ? first - 32 * g : first) >> a.f.log2B)];
+                // lanes past K: weights of zero too (an infinite constant times x's zero would be NaN)
+                const float c = s_const[(i * 16 + r) * pitch + ((zeros ? first - 32 * g : first) >> a.f.log2B)];
+                constant[i] = zeros ? 0.0f : c;
             }
 #pragma unroll
             for (int t = 0; t < MT; ++t)
