@@ -7,6 +7,9 @@
 // Their derivatives, with s' = s(x) s(-x) and p the normal density:
 //   silu s + x s',  gelu P + x p,  gelu_tanh s(q) + x s'(q) q'.
 // 1 - s(x) is taken as s(-x), which keeps its digits where s(x) is near 1.
+// At the infinities both are their limits (a 16-bit pre-activation may have become one): the factor
+// of a probability is held above -infinity, whose product with a probability of 0 would be NaN.
+// At NaN both are NaN.
 #pragma once
 #include "qb_device.h"
 
@@ -29,15 +32,19 @@ __device__ __forceinline__ float exp_f32(float x)
 
 __device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
 
+// x, -infinity as the lowest number.
+__device__ __forceinline__ float above_minus_infinity(float x) { return __builtin_fmaxf(x, -__FLT_MAX__); }
+
 constexpr float kGeluA = 1.59576917f, kGeluB = 0.044715f;      // 2 sqrt(2 / pi)
 
 __device__ __forceinline__ float act_value(int act, float x)
 {
     switch (act) {
     case ACT_RELU: return x < 0.0f ? 0.0f : x;
-    case ACT_GELU: return 0.5f * x * erfcf(x * -0.707106769f);
-    case ACT_GELU_TANH: return x * sigmoid_f32(kGeluA * __builtin_fmaf(kGeluB * x * x, x, x));
-    case ACT_SILU: return x * sigmoid_f32(x);
+    case ACT_GELU: return 0.5f * above_minus_infinity(x) * erfcf(x * -0.707106769f);
+    case ACT_GELU_TANH:
+        return above_minus_infinity(x) * sigmoid_f32(kGeluA * __builtin_fmaf(kGeluB * x * x, x, x));
+    case ACT_SILU: return above_minus_infinity(x) * sigmoid_f32(x);
     default: return x;
     }
 }
@@ -80,24 +87,24 @@ __device__ __forceinline__ void act_both(int act, float x, float& value, float& 
     switch (act) {
     case ACT_RELU:
         value = x < 0.0f ? 0.0f : x;
-        slope = x > 0.0f ? 1.0f : 0.0f;
+        slope = x > 0.0f ? 1.0f : x == x ? 0.0f : x;
         return;
     case ACT_GELU: {
         const float cdf = 0.5f * erfcf(x * -0.707106769f), p = 0.398942292f * exp_f32(-0.5f * x * x);
-        value = x * cdf;
+        value = above_minus_infinity(x) * cdf;
         slope = p == 0.0f ? cdf : __builtin_fmaf(x, p, cdf);
         return;
     }
     case ACT_GELU_TANH: {
         const float q = kGeluA * __builtin_fmaf(kGeluB * x * x, x, x);
         const float s = sigmoid_f32(q), dq = kGeluA * __builtin_fmaf(3.0f * kGeluB * x, x, 1.0f);
-        value = x * s;
+        value = above_minus_infinity(x) * s;
         slope = s + times_slope(x * dq, s, sigmoid_f32(-q));
         return;
     }
     case ACT_SILU: {
         const float s = sigmoid_f32(x);
-        value = x * s;
+        value = above_minus_infinity(x) * s;
         slope = s + times_slope(x, s, sigmoid_f32(-x));
         return;
     }

@@ -736,7 +736,8 @@ size_t qb_stable_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim)
  *   - Products of two xdt values are summed in binary32, in an order of the kernel's own that
  *     depends on the sizes alone (the same bits on every run); bias, activation, product and
  *     residual are binary32 too, and each output is rounded once.  NaN and infinities
- *     propagate as in the formulas, into the rows that they enter.
+ *     propagate as in the formulas, into the rows that they enter; activations and their
+ *     derivatives are their limits at the infinities, and NaN at NaN.
  *   - Outputs must not overlap inputs or each other, unless said otherwise.
  *   - ws: device workspace, 16-byte aligned, of the *_workspace_bytes size (0: none, ws may be
  *     NULL), which never shrinks when M, K or N grows: the weights in the compute dtype, and up
