@@ -54,7 +54,7 @@ qb_status check_weight(const Weight4& w, int* nested)
     if (mode) {
         if (w.absmax || !w.absmax2 || !w.offset) return QB_EINVAL;
         if (!aligned16(w.c2) || !aligned16(w.absmax2) || !aligned16(w.offset)) return QB_EALIGN;
-    } else if (!w.absmax) {
+    } else if (!w.absmax || w.absmax2 || w.offset) {     // (nested constants without their codes)
         return QB_EINVAL;
     }
     return aligned16(w.codes) && aligned16(w.absmax) ? QB_OK : QB_EALIGN;
