@@ -226,12 +226,21 @@ void stage_tile_map(std::vector<unsigned char>& staging, size_t at, const std::v
                          reinterpret_cast<const int32_t*>(w + dbytes + bbytes), used, shift};
 }
 
-// One copy of the staged tables to ws on stream s (from pageable memory: the
-// copy has read the host buffer when hipMemcpyAsync returns).
+// One copy of `bytes` (a multiple of 4) of host memory, which is the caller's again when this
+// returns, to device memory on stream s: hipMemcpyAsync has read pageable memory then.  Into a
+// captured graph it would record the address alone, to be read at every replay; the bytes go
+// with kernels there.
+qb_status upload(const void* from, size_t bytes, void* to, hipStream_t s)
+{
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    if (s && hipStreamIsCapturing(s, &capture) == hipSuccess && capture == hipStreamCaptureStatusActive)
+        return store_by_value && store_by_value(to, from, bytes, s) == hipSuccess ? QB_OK : QB_EHIP;
+    return hipMemcpyAsync(to, from, bytes, hipMemcpyHostToDevice, s) == hipSuccess ? QB_OK : QB_EHIP;
+}
+
 qb_status copy_staging(const std::vector<unsigned char>& staging, void* ws, hipStream_t s)
 {
-    return hipMemcpyAsync(ws, staging.data(), staging.size(), hipMemcpyHostToDevice, s) == hipSuccess ? QB_OK
-                                                                                                       : QB_EHIP;
+    return upload(staging.data(), staging.size(), ws, s);
 }
 
 // Bytes of one multi-tensor table region (qb_multi_tensor_workspace_bytes).
@@ -660,11 +669,7 @@ qb_status qb_prepare_code(const float* values, void* table, void* stream)
     std::memcpy(staged.values, values, sizeof(staged.values));
     if (user_code_thresholds(staged.values, staged.thr) != 0) return QB_EINVAL;
     user_code_first(staged.thr, staged.first);
-    // from pageable memory: the copy has read `staged` when hipMemcpyAsync returns
-    return hipMemcpyAsync(table, &staged, sizeof(staged), hipMemcpyHostToDevice, static_cast<hipStream_t>(stream)) ==
-                   hipSuccess
-               ? QB_OK
-               : QB_EHIP;
+    return upload(&staged, sizeof(staged), table, static_cast<hipStream_t>(stream));
 }
 
 qb_status qb_quantize_code(const void* x, qb_dtype xdt, int64_t n, const void* table, int32_t blocksize,

@@ -128,6 +128,12 @@ static_assert((size_t)kScratchMaxTensors * 64 + ((size_t)kScratchMaxTensors + 1)
               "scratch holds the tables of kScratchMaxTensors tensors");
 void* device_scratch();
 
+// Writes `bytes` (a multiple of 4) from host memory to device memory `to` by kernels that carry
+// them as arguments: what a captured graph replays does not lie in host memory any more, where a
+// copy node would read the address again.  Set by qb_runtime.hip (a pointer, so that the host
+// code links without the device code).
+inline hipError_t (*store_by_value)(void* to, const void* from, size_t bytes, hipStream_t s) = nullptr;
+
 // CUs x resident workgroups per CU of a kernel, cached per (device, kernel);
 // `query` returns the kernel's resident workgroups per CU.
 int persistent_grid_cap(const void* kernel, int (*query)(const void*));

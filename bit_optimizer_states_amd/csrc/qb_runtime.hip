@@ -1,4 +1,5 @@
 // qb_runtime.hip -- per-device constant tables, launch sizing, small kernels.
+#include <cstring>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -102,5 +103,34 @@ hipError_t launch_clear_bins(unsigned long long* bins, int sets, hipStream_t s)
     const int64_t grid = (nwords + 1023) / 1024;
     return launch_kernel(k_clear_bins, (int)(grid < 1024 ? grid : 1024), s, bins, nwords);
 }
+
+namespace {
+
+// Words of a launch of store_by_value: kernel arguments are at most 4 KB, the hidden ones among them.
+struct StoredWords {
+    uint32_t w[896];
+};
+
+__global__ __launch_bounds__(256) void k_store_words(uint32_t* __restrict__ to, int count, const StoredWords words)
+{
+    for (int i = threadIdx.x; i < count; i += 256) to[i] = words.w[i];
+}
+
+hipError_t store_words(void* to, const void* from, size_t bytes, hipStream_t s)
+{
+    StoredWords words{};
+    for (size_t at = 0; at < bytes; at += sizeof(words)) {
+        const size_t part = bytes - at < sizeof(words) ? bytes - at : sizeof(words);
+        std::memcpy(&words, static_cast<const char*>(from) + at, part);
+        const hipError_t e = launch_kernel(k_store_words, 1, s, reinterpret_cast<uint32_t*>(static_cast<char*>(to) + at),
+                                           (int)(part / 4), words);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+const bool store_set = (store_by_value = &store_words, true);
+
+}  // namespace
 
 }  // namespace qb

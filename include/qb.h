@@ -420,6 +420,11 @@ qb_status qb_adamw8bit_step(float* p, const void* g, qb_dtype gdt, int64_t n, ui
  *             into it on `stream`, so ws must not be reused by another stream
  *             until the step has run.
  * Tensors with n == 0 are skipped.  count == 0 is a no-op.
+ * Under graph capture (this call and every other one that uploads a table: the
+ * other multi-tensor and grouped calls, qb_prepare_code) the table goes into the
+ * graph itself, as arguments of small kernels (3.5 KB each) that write it into ws,
+ * so a replay reads no host memory; hp is the capture's as well.  Make one call on
+ * the device before: the first one uploads the library's constant tables.
  */
 qb_status qb_multi_tensor_step(const qb_tensor* tensors, int32_t count, qb_dtype gdt, int32_t blocksize,
                                const qb_adamw_hparams* hp, void* ws, size_t ws_bytes, void* stream);
