@@ -131,6 +131,29 @@ hipError_t unpack_and_multiply(int xdt, const void* x, int64_t M, int64_t K, con
     return launch_gemm(xdt, count == 2, g, e, reinterpret_cast<float*>(b + count * each), nullptr, s);
 }
 
+// Whether dx is taken from the codes, without the transposed weights in the workspace: up to 48 rows,
+// and up to 64 of a layer of more than 2^24 weights (64 rows, us: 1024 x 1000 17.6 so and 14.8 by the
+// tiled product, 4096 x 4096 24.8 and 24.3, 4096 x 11008 34.5 and 46).  Its slices' sums have to fit
+// the room for partial sums.
+constexpr int64_t kFewWeights = int64_t(1) << 24;
+bool may_be_few(int xdt, int64_t M, int64_t K) { return xdt != QB_F32 && M <= kRowsMax && M * K <= kPartMax; }
+bool few_rows(int xdt, int64_t M, int64_t K, int64_t N, int count)
+{
+    return may_be_few(xdt, M, K) && (M <= 48 || count * N * K > kFewWeights);
+}
+
+// Room for a gradient's transposed weights: none up to 48 rows of few; up to 64, where the smaller layers
+// take them, no more than the largest of these does (rows of N padded by less than a step), so that
+// it never shrinks.
+size_t transposed_bytes(int xdt, int64_t M, int64_t K, int64_t N, int count)
+{
+    const size_t all = (size_t)K * (size_t)gemm_pitch(xdt, N) * count * dtype_bytes(xdt);
+    if (!may_be_few(xdt, M, K)) return all;
+    if (M <= 48) return 0;
+    const size_t most = (size_t)(kFewWeights + gemm_step(xdt) * K * count) * dtype_bytes(xdt);
+    return all < most ? all : most;
+}
+
 // Workspace of a gradient: the weights transposed, dz (dg and du) padded, the partial
 // sums of a split product and of the bias's gradient.
 struct BackwardLayout {
@@ -143,7 +166,7 @@ BackwardLayout backward_layout(int xdt, int64_t M, int64_t K, int64_t N, int cou
     // the partial sums' slices shrink as columns are added: what is reserved never does
     const size_t most = (size_t)((M + 7) / 8) * (size_t)N, cap = (size_t)2048 * 512 + (size_t)N;
     BackwardLayout l;
-    l.dz = round_up((size_t)K * pitch, 256);
+    l.dz = round_up(transposed_bytes(xdt, M, K, N, count), 256);
     l.split = l.dz + round_up((size_t)M * pitch, 256);
     l.part = l.split + round_up((size_t)gemm_part_floats(M, K) * sizeof(float), 256);
     l.bytes = l.part + (count == 1 ? (most < cap ? most : cap) * sizeof(float) : 0);
@@ -155,15 +178,6 @@ bool whole_steps(int xdt, int64_t n) { return n % gemm_step(xdt) == 0; }
 TransposedWeights transposed(int xdt, const Weight4* w, int count, const Weight4Format& f, int64_t K, int64_t N, void* ws)
 {
     return TransposedWeights{{w[0], w[count - 1]}, f, ws, N, K, gemm_pitch(xdt, N), count};
-}
-
-// Whether dx is taken from the codes, without the transposed weights in the workspace: up to 48 rows,
-// and up to 64 of a layer of more than 2^24 weights (64 rows, us: 1024 x 1000 17.6 so and 14.8 by the
-// tiled product, 4096 x 4096 24.8 and 24.3, 4096 x 11008 34.5 and 46).  Its slices' sums have to fit
-// the room for partial sums.
-bool few_rows(int xdt, int64_t M, int64_t K, int64_t N, int count)
-{
-    return xdt != QB_F32 && M <= kRowsMax && (M <= 48 || count * N * K > int64_t(1) << 24) && M * K <= kPartMax;
 }
 
 // dx = [dz_0 dz_1] [W_0; W_1] for dz of rows of `lda` elements and the weights `t`; the bias's gradient

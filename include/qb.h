@@ -745,8 +745,9 @@ size_t qb_stable_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim)
  *     derivatives are their limits at the infinities, and NaN at NaN.
  *   - Outputs must not overlap inputs or each other, unless said otherwise.
  *   - ws: device workspace, 16-byte aligned, of the *_workspace_bytes size (0: none, ws may be
- *     NULL), which never shrinks when M, K or N grows: the weights in the compute dtype, and up
- *     to 80 MiB for partial sums of products split over their length.  It holds nothing
+ *     NULL), which never shrinks when M, K or N grows: the weights in the compute dtype (none for
+ *     a gradient of up to 48 rows in a 16-bit type, 32 MiB or little more up to 64), a gradient's
+ *     dz, and up to 80 MiB for partial sums of products split over their length.  It holds nothing
  *     between calls and must not be shared by calls that may overlap in time (two captured
  *     graphs that run at once among them).
  *   - No memory operations, so the calls may be captured; the first call on a device that
