@@ -405,8 +405,6 @@ GemmParams rows_of(const GemmParams& all, int64_t m, int64_t rows)
     return p;
 }
 
-
-
 // Columns n_first .. R - 1 of B in BN-wide tiles (`columns` tiles of them at most), the length
 // in p.split pieces.
 template <int XDT, int BM, int BN, int WM, int WN, int STAGES, bool GATED>

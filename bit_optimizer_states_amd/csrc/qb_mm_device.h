@@ -35,21 +35,6 @@ __device__ __forceinline__ T ldo(const void* base, uint32_t off)
     return *(const QB_G T*)(b + off);
 }
 
-// Eight consecutive activations at element offset e (a multiple of 8) of x.
-template <int XDT>
-__device__ __forceinline__ void load_frag(const void* x, int64_t e, Frag<XDT>& f)
-{
-    if constexpr (XDT == DT_F32) {
-        const f32x4 a = gld<f32x4>(static_cast<const float*>(x) + e);
-        const f32x4 b = gld<f32x4>(static_cast<const float*>(x) + e + 4);
-        f.w[0] = a.x; f.w[1] = a.y; f.w[2] = a.z; f.w[3] = a.w;
-        f.w[4] = b.x; f.w[5] = b.y; f.w[6] = b.z; f.w[7] = b.w;
-    } else {
-        const u32x4 a = gld<u32x4>(static_cast<const uint16_t*>(x) + e);
-        f.w[0] = a.x; f.w[1] = a.y; f.w[2] = a.z; f.w[3] = a.w;
-    }
-}
-
 // Eight activations at byte offset off from a uniform base.
 template <int XDT>
 __device__ __forceinline__ void load_frag_o(const void* base, uint32_t off, Frag<XDT>& f)
