@@ -183,3 +183,26 @@ def test_user_code():
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(t, want)
+
+
+@pytest.mark.parametrize("tokens", [40, 1100])
+@pytest.mark.parametrize("xdt", [BF16, F32])
+def test_whole_training_steps(tokens, xdt):
+    """Forward, backward, clipping and the optimizer's step in one graph, two of them in turn."""
+    from test_gpu_layer_step import ROWS, Block
+
+    L = qb()
+    blocks = [Block(L, tokens, xdt), Block(L, tokens + 30, xdt, nested=False)]
+    other = Optimizer(L, 300, L.QB_ADAMW, 1)
+    graphs = [capture(b.step) for b in blocks]
+
+    def change(turn):
+        for b in blocks:
+            b.ids.copy_(torch.randint(0, ROWS, b.ids.shape, device=DEV))
+
+    def others():
+        other.step()
+        for b in blocks:
+            b.ws.fill_(0xEE)
+
+    in_turns(graphs, [b.step for b in blocks], [b.results for b in blocks], change, others)
