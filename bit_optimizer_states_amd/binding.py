@@ -781,7 +781,8 @@ def qb_dequant_gated_backward(dy, gate_out, up_out, gate, up, code, blocksize, K
 
 def grad_table(grads):
     """ctypes array of qb_grad from tensors, or from (g, out) pairs for clipping out of place (a tensor alone is clipped
-    in place).  A program whose gradients stay where they are builds it once."""
+    in place).  A program whose gradients stay where they are (zero_grad(set_to_none=False), a bucket) builds it once:
+    it costs 1.7 us a gradient on the host, 0.8 ms for 448, where their norm and clipping take 0.06 to 0.08."""
     arr = (qb_grad * max(len(grads), 1))()
     device, spans = None, []
     for i, entry in enumerate(grads):

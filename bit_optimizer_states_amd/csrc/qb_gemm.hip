@@ -28,8 +28,8 @@ int64_t tiles_over(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 // k order in both operands.  A step's first half of fragments is in registers when it begins;
 // the second half's reads are dealt among the first half's products, then the waves meet, and
 // the next step's first half and the loads are dealt among the second half's.
-// The whole layer of 4096 x 11008 x 4096 bf16 takes 308 us so (20 of them the dequantization),
-// 319 with the waves meeting at the beginning of a step, all fragments read before the products
+// The whole layer of 4096 x 11008 x 4096 bf16 takes 312 us so, 24 of them the dequantization.
+// Beside runs of 308: 319 with the waves meeting at the beginning of a step, all fragments read before the products
 // 8 us more, the loads first and each half read before its products 28 more.  The matrix pipes
 // are busy 78% of the cycles (67% with the waves meeting at the beginning), and the clock falls
 // as that rises, 1.75 to 1.6 GHz: what is left is power.  32x32x16 instructions 330; steps of half the
@@ -426,7 +426,10 @@ constexpr int64_t kEveryColumn = int64_t(1) << 40;
 // 256 rows of 4096 x 4096 take 48 us in all in 64 x 64 tiles with three buffers, 35 with five; many
 // small workgroups a CU hide it as well (with two buffers: 30).  Binary32 is bound by the matrix
 // instructions and takes the third or the fourth (4096 x 4096 x 4096 1009 us and 1085; in the
-// first 979).  128 x 256 tiles are never the best by more than a percent.
+// first 979).  128 x 256 tiles are not built: with three buffers they save 2 to 4% of the few products of 512 and
+// 1024 rows where they are the best (the gradient of 1024 rows of 4096 x 4096 split in two 55 us, 57 in 128 x 128
+// tiles).  The estimate's own choice can be further off: 61 there, 40 and not 34 for 300 rows (128 x 128 in two), 193 and
+// not 177 for 2048 rows of 4096 x 11008 (256 x 256 in two).
 struct TileShape {
     int bm, bn, per_cu;
     double us[5];

@@ -14,9 +14,10 @@
 // fragments' lanes touch 16 rows at once and the address unit takes them one row at a time (64
 // rows of 11008 x 4096: 47 us with loads to registers, 25 so; one row 10.0 both ways).  The
 // block constants of the tile's rows are decoded into LDS once, for up to 12288 k.  What
-// bounds it now: one row of 4096 x 11008 takes 10.4 us, 23.3 MB at 2.2 TB/s, where the
-// lookups and products of the 4-bit codes alone, 3 vector instructions and one LDS read a weight, take
-// 5 us of the SIMDs; at 64 rows (30 us) it is x through LDS, 688 times over.
+// bounds it now: one row of 11008 x 4096 takes 10.2 us, 23.3 MB at 2.3 TB/s (from HBM hardly more than
+// from the cache: 9.8 and 9.6 us a call), where the lookups and products of the 4-bit codes alone, 3 vector
+// instructions and one LDS read a weight, take 5 us of the SIMDs; at 64 rows of 4096 x 11008 (28 us, 32 with
+// the weights from HBM) it is x through LDS, 688 times over.
 #include "qb_epilogue.h"
 #include "qb_linear.h"
 #include "qb_mm_device.h"
