@@ -319,8 +319,9 @@ qb_status qb_dequantize(const uint8_t* codes, const float* absmax, const qb_dq* 
  * Performance: up to 64 rows of x one wave per 16 weight rows streams W once
  * (up to 8 16-bit rows of at most 64 KiB in all are staged in LDS first);
  * from 65 rows (xdt 16-bit, K a multiple of 128) an LDS-tiled kernel shares x
- * across 64- or 128-row tiles and dequantizes W once per tile.  With M in the
- * thousands, dequantizing once and calling a GEMM library is faster.
+ * across 64- or 128-row tiles and dequantizes W once per tile.  qb_dequant_linear
+ * without an epilogue is the same product (other last bits), faster up to 64 rows and
+ * from 512 on, with a workspace beyond 64 rows (K, N < 2^21 there).
  * Accuracy: each product of two xdt values is exact in binary32; the K-term
  * sums are added in an order of the kernel's own (fixed: the same bits on
  * every run), so y is within (K+2) 2^-23 sum_k |x_mk w_nk| of the exact
